@@ -47,6 +47,9 @@ __all__ = [
     "gemm_bounds_checked", "bounds_checked_requested",
     "GEMM_F16", "GEMM_BF16", "GEMM_EPI_NONE", "GEMM_EPI_GELU_TANH", "GEMM_EPI_RELU",
     "GEMM_PIPELINED", "GEMM_SINGLE_BUFFER",
+    "gated_ffn", "gated_ffn_backward", "GatedKept", "orthogonalize", "NEWTON_SCHULZ",
+    "token_logprobs", "token_logprobs_backward", "TokenLogprobs", "MAX_TOP_K",
+    "check_operators", "close_operators", "FfnArgs", "OrthogonalizeArgs", "LogprobsArgs",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -527,3 +530,9 @@ def matmul_nt(A, B, epilogue=None, stages: int = 6, variant: str = "pipelined", 
     plan = get_plan(M, N, K, dtype, epilogue, stages, variant, A.device.index or 0, **tuning)
     plan.run(A, B, out, bias=bias)
     return out
+
+
+from .operators import (  # noqa: E402 - they use the binding above
+    FfnArgs, GatedKept, LogprobsArgs, MAX_TOP_K, NEWTON_SCHULZ, OrthogonalizeArgs, TokenLogprobs,
+    check_operators, close_operators, gated_ffn, gated_ffn_backward, orthogonalize, token_logprobs,
+    token_logprobs_backward)

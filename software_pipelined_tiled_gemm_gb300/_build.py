@@ -33,7 +33,9 @@ STAMP_CHECKED = os.path.join(LIBDIR, "libspgemm_checked.stamp")
 CHECKED_FLAGS = ["-DSPGEMM_BOUNDS_CHECKS=1"]
 
 SOURCES = ["gemm_api.cu", "gemm_bn64.cu", "gemm_bn128.cu", "gemm_bn256.cu", "gemm_pair128.cu",
-           "gemm_pair256.cu", "pad.cu", "fill.cu", "noalloc.cu"]
+           "gemm_pair256.cu", "pad.cu", "fill.cu", "noalloc.cu", "ops_api.cu", "block_nt.cu",
+           "block_nn.cu", "block_tn.cu", "block_gated.cu", "block_gated_bwd.cu", "pack.cu", "ffn.cu",
+           "orthogonal.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", CSRC, "-I", INCLUDE]
@@ -53,8 +55,9 @@ def _digest(checked: bool = False) -> str:
         h.update(f.encode())
         with open(os.path.join(CSRC, f), "rb") as fh:
             h.update(fh.read())
-    with open(os.path.join(INCLUDE, "gemm.h"), "rb") as fh:
-        h.update(fh.read())
+    for f in sorted(os.listdir(INCLUDE)):
+        with open(os.path.join(INCLUDE, f), "rb") as fh:
+            h.update(fh.read())
     h.update(" ".join(ARCH + FLAGS + (CHECKED_FLAGS if checked else [])).encode())
     return h.hexdigest()
 

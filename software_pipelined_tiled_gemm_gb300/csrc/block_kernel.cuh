@@ -1,0 +1,748 @@
+// block_kernel.cuh -- the products of the gated feed-forward block and of the
+// Newton-Schulz iteration, on the roles of gemm_kernel.cuh (one TMA producer
+// thread, one tcgen05.mma issuer thread, four epilogue warps; see there for
+// the ring and accumulator protocol).  What differs:
+//
+//   operands    each K-major (rows of K) or MN-major (stored K x M / K x N).
+//               An MN-major slice of 64 K rows arrives as boxes of 64 columns
+//               x 64 rows, 8 KiB each: swizzle atoms of 8 K rows are 1024 B
+//               apart along K and 8 KiB apart along M/N.  Two-dimensional
+//               boxes are clipped at the matrix's own edge, so no extent has
+//               to be a multiple of 64.
+//   tiles       256 x 256 on a CTA pair with two K slices per ring slot, or
+//               128 x 128 on one CTA; of a batch of matrices; optionally only
+//               those on and above the diagonal of a symmetric product.
+//   gated       the tile's B rows are half gate rows, half up rows of the
+//               same output columns, so act(gate) * up needs no other tile.
+//               With a pair, the even CTA copies the gate rows and the odd
+//               one the up rows.
+//   last wave   stream-K with any number of walkers per tile: the walker
+//               holding a tile's first K slices owns it, the others publish
+//               fp32 partials (each at most one, in a slot of its own, as its
+//               first piece of work), and the owner adds them in walker order.
+//               Every sum has a fixed order, so results repeat bit for bit.
+#pragma once
+
+#include "block_math.cuh"
+#include "block_params.h"
+#include "gemm_kernel.cuh"
+#include "ptx_block.cuh"
+
+namespace spgemm {
+
+struct BlockTile {
+  int mb, nb, z;
+};
+
+// Tile t of the launch: which matrix of the batch, and where in it.
+__device__ __forceinline__ BlockTile block_tile(int t, const BlockParams& p) {
+  BlockTile x;
+  x.z = t / p.tiles_per;
+  const int r = t - x.z * p.tiles_per;
+  if (!p.symmetric) {
+    tile_coords(r, p, x.mb, x.nb);
+    return x;
+  }
+  // Upper triangle, row by row: row i starts at i n - i (i - 1) / 2.
+  const int n = p.tiles_n;
+  const float b = 2.0f * n + 1.0f;
+  int i = static_cast<int>((b - sqrtf(fmaxf(b * b - 8.0f * r, 0.0f))) * 0.5f);
+  i = min(max(i, 0), n - 1);
+  while (i > 0 && i * n - i * (i - 1) / 2 > r) --i;
+  while (i + 1 < n && (i + 1) * n - (i + 1) * i / 2 <= r) ++i;
+  x.mb = i;
+  x.nb = i + (r - (i * n - i * (i - 1) / 2));
+  return x;
+}
+
+// A piece of work: K slots [k0, k1) of a tile.
+struct BlockUnit {
+  int tile, k0, k1, role;
+};
+
+// A walker's pieces: first its contiguous share of the stream-K tiles' K
+// slots (its partial for another walker, if any, comes first of all), then
+// its whole tiles.
+struct BlockIter {
+  int u;
+  int64_t it, end;
+  __device__ BlockIter(int walker, const BlockParams& p) : u(walker) {
+    const int64_t total = static_cast<int64_t>(p.sk_tiles) * p.k_blocks;
+    it = total * walker / p.walkers;
+    end = total * (walker + 1) / p.walkers;
+  }
+  __device__ bool next(const BlockParams& p, BlockUnit& x) {
+    if (it < end) {
+      x.tile = static_cast<int>(it / p.k_blocks);
+      x.k0 = static_cast<int>(it - static_cast<int64_t>(x.tile) * p.k_blocks);
+      const int64_t left = end - it;
+      x.k1 = static_cast<int>(x.k0 + left < p.k_blocks ? x.k0 + left : p.k_blocks);
+      x.role = x.k0 > 0 ? kContrib : (x.k1 < p.k_blocks ? kOwner : kWhole);
+      it += x.k1 - x.k0;
+      return true;
+    }
+    if (u < p.dp_tiles) {
+      x.tile = p.sk_tiles + u;
+      x.k0 = 0;
+      x.k1 = p.k_blocks;
+      x.role = kWhole;
+      u += p.walkers;
+      return true;
+    }
+    return false;
+  }
+};
+
+// The walkers after `walker` that hold a piece of its last stream-K tile.
+__device__ __forceinline__ int block_contributors(int walker, const BlockUnit& x,
+                                                  const BlockParams& p) {
+  const int64_t total = static_cast<int64_t>(p.sk_tiles) * p.k_blocks;
+  const int64_t tile_end = static_cast<int64_t>(x.tile + 1) * p.k_blocks;
+  int n = 0;
+  while (walker + n + 1 < p.walkers && total * (walker + n + 1) / p.walkers < tile_end) ++n;
+  return n;
+}
+
+// One 32-row x 64-column block of a 16-bit output, as 32 words per lane
+// (lane = row): through the warp's staging buffer (already free) in the
+// layout of a 128-byte-swizzled box and out with one bulk store, or row by
+// row where the output's rows are not 16-byte aligned.  `cols` bounds the
+// columns written, for an output whose neighbour follows directly.
+__device__ __forceinline__ void block_store(const uint32_t (&w)[32], const BlockParams& p,
+                                            const BlockOut& o, const CUtensorMap& map, uint8_t* sb,
+                                            int lane, int row0, int col0, int z, int cols) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t off = lane * 128u + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4);
+    *reinterpret_cast<uint4*>(sb + off) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+  if (o.tma) {
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      ptx::tma_store_3d(&map, ptx::smem_addr(sb), col0, row0, z);
+      ptx::bulk_commit_group();
+    }
+    return;
+  }
+  __syncwarp();
+  const int ncols = min(64, cols - col0);
+  const int nrows = min(32, p.M - row0);
+  uint16_t* base = static_cast<uint16_t*>(o.ptr) + z * o.batch + static_cast<int64_t>(row0) * o.ld + col0;
+#pragma unroll 4
+  for (int r = 0; r < nrows; ++r) {
+    uint16_t* crow = base + r * o.ld;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int cc = lane + 32 * h;
+      const uint32_t byte = static_cast<uint32_t>(cc) * 2u;
+      const uint32_t off = static_cast<uint32_t>(r) * 128u +
+                           (((byte >> 4) ^ (static_cast<uint32_t>(r) & 7u)) << 4) + (byte & 15u);
+      if (cc < ncols) crow[cc] = *reinterpret_cast<const uint16_t*>(sb + off);
+    }
+  }
+  __syncwarp();
+}
+
+// The block's transpose, into the same output: column j of the block is 32
+// consecutive elements of row col0 + j.  Neighbouring lanes first exchange
+// words, so that each lane stores two rows' worth of one column at once.
+__device__ __forceinline__ void block_store_mirror(const uint32_t (&w)[32], const BlockParams& p,
+                                                   const BlockOut& o, int lane, int row0, int col0,
+                                                   int z) {
+  uint16_t* base = static_cast<uint16_t*>(o.ptr) + z * o.batch;
+  const bool odd = lane & 1;
+  const int r = row0 + (lane & ~1);  // this lane's pair of source rows
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    // w[j]: columns 2j, 2j + 1 of this row.  The even lane keeps column 2j
+    // and takes its neighbour's; the odd lane column 2j + 1.
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
+    const uint32_t pair = odd ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
+    const int c = col0 + 2 * j + (odd ? 1 : 0);
+    if (c < p.N) {
+      uint16_t* dst = base + static_cast<int64_t>(c) * o.ld + r;
+      if (r + 1 < p.M)
+        *reinterpret_cast<uint32_t*>(dst) = pair;  // r is even and the pitch a multiple of 8
+      else if (r < p.M)
+        *dst = static_cast<uint16_t>(pair);
+    }
+  }
+}
+
+// 32 accumulator columns at TMEM column `col`, with the contributors'
+// partials added in order.
+__device__ __forceinline__ void block_acc(uint32_t t_addr, uint32_t (&r)[32], const float* partial,
+                                          size_t partial_step, int parts, int col, int lane) {
+  ptx::tmem_ld_32x32b_x32(t_addr + col, r);
+  ptx::tmem_wait_ld();
+  for (int n = 0; n < parts; ++n) {
+    const float* src = partial + n * partial_step + static_cast<size_t>(col) * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __ldcg(src + j * 32));
+  }
+}
+
+// act(gate) * up of 32 columns, packed two to a word; gate and up are also
+// kept in fp32 where the caller asks for them.
+template <int ACT>
+__device__ __forceinline__ void gated32(const uint32_t (&g)[32], const uint32_t (&u)[32],
+                                        uint32_t* pk, bool bf16) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    pk[j] = pack2(gate_act<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
+                  gate_act<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]), bf16);
+}
+
+template <int ACT>
+__device__ __forceinline__ void gated_bwd32(const uint32_t (&dh)[32], const float (&g)[32],
+                                            const float (&u)[32], uint32_t* pg, uint32_t* pu,
+                                            bool bf16) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float dg[2], du[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a, d;
+      gate_act_grad<ACT>(g[2 * j + i], a, d);
+      const float h = __uint_as_float(dh[2 * j + i]);
+      dg[i] = h * u[2 * j + i] * d;
+      du[i] = h * a;
+    }
+    pg[j] = pack2(dg[0], dg[1], bf16);
+    pu[j] = pack2(du[0], du[1], bf16);
+  }
+}
+
+// CG: 2 for CTA pairs, 1 for single CTAs.  kAT: A stored K x M.  kBN: B
+// stored K x N.  kEpi: the epilogue (kEpiLinear, kEpiGated, kEpiGatedBwd).
+template <int CG, bool kAT, bool kBN, int kEpi>
+__global__ void __launch_bounds__(kBlockThreads, 1)
+    block_kernel(const __grid_constant__ BlockMaps maps, const __grid_constant__ BlockParams p) {
+  constexpr int BN = block_bn(CG);
+  constexpr int kSub = block_sub(CG);
+  constexpr int kBRows = BN / CG;                 // B rows this CTA copies
+  constexpr uint32_t kStageB = kBRows * kBK * 2;
+  constexpr int kTileM = kBM * CG;
+  constexpr int kOutN = kEpi == kEpiGated ? BN / 2 : BN;  // output columns of a tile
+  constexpr uint32_t kBoxBytes = 64u * kBK * 2u;          // MN-major box: 64 columns x 64 K rows
+  // K-major A of a single row of tiles: only the rows that exist are copied
+  // (see Params::a_box_rows); the MMA's other rows read what follows in the
+  // slot and feed output rows that are never stored.
+  const uint32_t slice_a = kAT ? kStageA : static_cast<uint32_t>(p.a_box_rows) * (kBK * 2u);
+  const uint32_t slot_a = slice_a * kSub;
+  const uint32_t slot_bytes = slot_a + kStageB * kSub;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const int S = p.stages;
+  const uint32_t ring_bytes = static_cast<uint32_t>(S) * slot_bytes;
+  uint8_t* staging = smem + ring_bytes;
+  constexpr uint32_t staging_bytes = 4u * 2u * kStoreBuf;
+  const uint32_t bar_base = sbase + ring_bytes + staging_bytes;
+  if (SPGEMM_OUT_OF_BOUNDS(S >= 1 && S <= kMaxStages &&
+                               (sbase - raw_addr) + ring_bytes + staging_bytes +
+                                       8u * (2 * kMaxStages + 5 + 2 * kEpiWarps) + 4u <=
+                                   ptx::dynamic_smem_bytes(),
+                           p, kCheckSmemLayout))
+    return;
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (kMaxStages + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + 2 + a); };
+  const uint32_t done_bar = bar_base + 8u * (2 * kMaxStages + 4);
+  auto d_bar = [&](int e, int b) { return bar_base + 8u * (2 * kMaxStages + 5 + 2 * e + b); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + ring_bytes + staging_bytes +
+                                                    8u * (2 * kMaxStages + 5 + 2 * kEpiWarps));
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t tmem_cols = 2u * BN;  // two accumulators
+  const uint32_t rank = (CG == 2) ? ptx::cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int walker = static_cast<int>(blockIdx.x) / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(tfull_bar(a), 1);
+      ptx::mbar_init(tempty_bar(a), 4 * CG);
+    }
+    ptx::mbar_init(done_bar, 1);
+    for (int e = 0; e < 4; ++e)
+      for (int b = 0; b < 2; ++b) ptx::mbar_init(d_bar(e, b), 1);
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&maps.a);
+    ptx::tma_prefetch_desc(&maps.b);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc<CG>(ptx::smem_addr(tmem_slot), tmem_cols);
+    ptx::tmem_relinquish<CG>();
+  }
+  ptx::tc_fence_before_sync();
+  if (CG == 2)
+    ptx::cluster_sync();
+  else
+    __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  ptx::pdl_launch_dependents();
+
+  // First B row of a tile for this CTA, and (gated, single CTA) of its up half.
+  auto b_first = [&](int nb) {
+    if constexpr (kEpi == kEpiGated)
+      return nb * kOutN + (CG == 2 && rank == 1 ? p.gate_rows : 0);
+    else
+      return nb * BN + static_cast<int>(rank) * kBRows;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0, issued_parity = 0;
+      const uint64_t pol_b = (CG == 1 && p.b_stream) ? ptx::l2_policy_evict_first() : 0;
+      bool ok = true;
+      const uint32_t bytes =
+          (slice_a + static_cast<uint32_t>(kStageB)) * static_cast<uint32_t>(CG * kSub);
+      BlockIter it(walker, p);
+      BlockUnit x;
+      // Warm L2 with the weights of the first slots while the previous kernel
+      // in the stream finishes (only lines move; the copies come after the wait).
+      if (CG == 1 && p.l2_prefetch_first) {
+        BlockIter it0(walker, p);
+        if (it0.next(p, x)) {
+          const BlockTile t = block_tile(x.tile, p);
+          for (int i = 0; i < S && x.k0 + i < x.k1; ++i) {
+            const int kx = (x.k0 + i) * kBK;
+            if constexpr (kBN) {
+              ptx::tma_prefetch_l2_3d(&maps.b, b_first(t.nb), kx, t.z);
+              ptx::tma_prefetch_l2_3d(&maps.b, b_first(t.nb) + 64, kx, t.z);
+            } else {
+              ptx::tma_prefetch_l2_3d(&maps.b, kx, b_first(t.nb), t.z);
+              if constexpr (kEpi == kEpiGated)
+                ptx::tma_prefetch_l2_3d(&maps.b, kx, b_first(t.nb) + p.gate_rows, t.z);
+            }
+          }
+        }
+      }
+      ptx::pdl_wait_prior_grid();
+      while (ok && it.next(p, x)) {
+        const BlockTile t = block_tile(x.tile, p);
+        if (SPGEMM_OUT_OF_BOUNDS(x.tile >= 0 && x.tile < p.num_tiles && t.z < p.batch &&
+                                     t.mb >= 0 && t.mb < p.tiles_m && t.nb >= 0 && t.nb < p.tiles_n,
+                                 p, kCheckTile) ||
+            SPGEMM_OUT_OF_BOUNDS(x.k0 >= 0 && x.k0 < x.k1 && x.k1 <= p.k_blocks, p, kCheckKSlice)) {
+          ok = false;
+          break;
+        }
+        const int a_row = t.mb * kTileM + static_cast<int>(rank) * kBM;
+        const int b_row = b_first(t.nb);
+        for (int kb = x.k0; kb < x.k1; ++kb) {
+          if (!wait_bounded(empty_bar(stage), phase ^ 1u, p, kDetailProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          if (SPGEMM_OUT_OF_BOUNDS(stage < S && (a_row & 7) == 0 && (!kBN || (b_row & 7) == 0), p,
+                                   kCheckTmaCoord)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = sbase + stage * slot_bytes;
+          uint32_t fb = full_bar(stage);
+          if constexpr (CG == 2) fb = ptx::map_shared_rank(fb, 0);
+          if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), bytes);
+#pragma unroll
+          for (int sub = 0; sub < kSub; ++sub) {
+            const int kx = (kb * kSub + sub) * kBK;
+            const uint32_t da = sa + sub * slice_a, db = sa + slot_a + sub * kStageB;
+            if constexpr (CG == 2) {
+              if constexpr (kAT) {
+                ptx::tma_load_3d_pair(da, &maps.a, a_row, kx, t.z, fb);
+                ptx::tma_load_3d_pair(da + kBoxBytes, &maps.a, a_row + 64, kx, t.z, fb);
+              } else {
+                ptx::tma_load_3d_pair(da, &maps.a, kx, a_row, t.z, fb);
+              }
+              if constexpr (kBN) {
+                ptx::tma_load_3d_pair(db, &maps.b, b_row, kx, t.z, fb);
+                ptx::tma_load_3d_pair(db + kBoxBytes, &maps.b, b_row + 64, kx, t.z, fb);
+              } else {
+                ptx::tma_load_3d_pair(db, &maps.b, kx, b_row, t.z, fb);
+              }
+            } else {
+              if constexpr (kAT) {
+                ptx::tma_load_3d(da, &maps.a, a_row, kx, t.z, fb);
+                ptx::tma_load_3d(da + kBoxBytes, &maps.a, a_row + 64, kx, t.z, fb);
+              } else {
+                ptx::tma_load_3d(da, &maps.a, kx, a_row, t.z, fb);
+              }
+              auto load_b = [&](uint32_t dst, int cx, int cy) {
+                if (p.b_stream)
+                  ptx::tma_load_3d_hint(dst, &maps.b, cx, cy, t.z, fb, pol_b);
+                else
+                  ptx::tma_load_3d(dst, &maps.b, cx, cy, t.z, fb);
+              };
+              if constexpr (kBN) {
+                load_b(db, b_row, kx);
+                load_b(db + kBoxBytes, b_row + 64, kx);
+              } else if constexpr (kEpi == kEpiGated) {  // 64 gate rows, then 64 up rows
+                load_b(db, kx, b_row);
+                load_b(db + kStageB / 2, kx, b_row + p.gate_rows);
+              } else {
+                load_b(db, kx, b_row);
+              }
+            }
+          }
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every copy this CTA (pair) started must have landed before it exits.
+      if (leader) {
+        for (int s = 0; s < S; ++s)
+          if (issued & (1u << s))
+            wait_bounded(full_bar(s), (issued_parity >> s) & 1u, p, kDetailProducerDrain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer --
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      BlockIter it(walker, p);
+      BlockUnit x;
+      while (ok && it.next(p, x)) {
+        if (!wait_bounded_cluster<CG>(tempty_bar(acc), acc_phase ^ 1u, p, kDetailMmaAccEmpty)) break;
+        ptx::tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        for (int kb = x.k0; kb < x.k1; ++kb) {
+          if (!wait_bounded(full_bar(stage), phase, p, kDetailMmaFull) ||
+              SPGEMM_OUT_OF_BOUNDS(stage >= 0 && stage < S, p, kCheckMmaSlot)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after_sync();
+          const uint32_t sa = sbase + stage * slot_bytes;
+          const uint64_t a_desc = kAT ? ptx::smem_desc_mn_sw128(sa, kBoxBytes, 1024u)
+                                      : ptx::smem_desc_k_sw128(sa);
+          const uint64_t b_desc = kBN ? ptx::smem_desc_mn_sw128(sa + slot_a, kBoxBytes, 1024u)
+                                      : ptx::smem_desc_k_sw128(sa + slot_a);
+          // A 16-wide K step is 32 B inside a K-major swizzle row, or two
+          // 1024-byte atoms of 8 K rows of an MN-major box.
+          constexpr uint32_t a_step = kAT ? 2048u / 16u : 2u, b_step = kBN ? 2048u / 16u : 2u;
+#pragma unroll
+          for (int k = 0; k < kSub * (kBK / kUmmaK); ++k) {
+            const uint32_t sub = static_cast<uint32_t>(k) / 4u, kk = static_cast<uint32_t>(k) % 4u;
+            ptx::mma_f16_ss<CG>(d_tmem, a_desc + sub * (slice_a / 16u) + a_step * kk,
+                                b_desc + sub * (kStageB / 16u) + b_step * kk, p.idesc,
+                                (kb != x.k0 || k != 0) ? 1u : 0u);
+          }
+          if constexpr (CG == 2)
+            ptx::mma_commit_multicast_pair(empty_bar(stage), 0x3);
+          else
+            ptx::mma_commit<1>(empty_bar(stage));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if constexpr (CG == 2)
+          ptx::mma_commit_multicast_pair(tfull_bar(acc), 0x3);
+        else
+          ptx::mma_commit<1>(tfull_bar(acc));
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      ptx::mma_commit<CG>(done_bar);
+      wait_bounded(done_bar, 0, p, kDetailMmaDrain);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------- epilogue --
+    ptx::pdl_wait_prior_grid();
+    const int q = warp & 3;
+    const int ew = warp - 2;
+    uint8_t* my_stage = staging + ew * 2 * kStoreBuf;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    uint32_t d_phase = 0;  // parity of the next fill of D buffer b in bit b
+    int buf = 0;
+    const bool bf16_out = p.out_bf16 != 0;
+    constexpr size_t kPartial = block_partial_bytes(CG) / 4;  // floats of a CTA's partial
+    BlockIter it(walker, p);
+    BlockUnit x;
+    while (it.next(p, x)) {
+      const BlockTile t = block_tile(x.tile, p);
+      const int row0 = t.mb * kTileM + static_cast<int>(rank) * kBM + q * 32;
+      const int n0 = t.nb * kOutN;
+      const bool rows = row0 < p.M;
+      const bool stores = x.role != kContrib && rows;
+      if (SPGEMM_OUT_OF_BOUNDS(row0 >= 0 && row0 < p.tiles_m * kTileM && n0 >= 0 && (n0 & 63) == 0,
+                               p, kCheckStore) ||
+          SPGEMM_OUT_OF_BOUNDS(x.role == kWhole || (p.sk_ws != nullptr && p.sk_flags != nullptr), p,
+                               kCheckPartial))
+        break;
+      // beta D: the tile's first chunk, fetched while the accumulator fills.
+      auto load_d = [&](int b, int col) {
+        if (lane == 0) {
+          ptx::bulk_wait_group_read<0>();  // the buffer's last store has been read out
+          ptx::fence_proxy_async_smem();   // (by the warp itself, where rows are stored one by one)
+          ptx::mbar_arrive_expect_tx(d_bar(ew, b), kStoreBuf);
+          ptx::tma_load_3d(ptx::smem_addr(my_stage + b * kStoreBuf), &maps.d, col, row0, t.z,
+                           d_bar(ew, b));
+        }
+      };
+      if (kEpi == kEpiLinear && p.use_d && stores) load_d(buf, n0);
+
+      int ready = 1;
+      if (lane == 0) ready = wait_bounded<true>(tfull_bar(acc), acc_phase, p, kDetailEpiFull) ? 1 : 0;
+      ready = __shfl_sync(0xffffffffu, ready, 0);
+      if (!ready) {
+        // A copy of D still in flight lands before this warp's memory goes.
+        if (kEpi == kEpiLinear && p.use_d && stores)
+          wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy);
+        break;
+      }
+      ptx::tc_fence_after_sync();
+      const uint32_t t_row =
+          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+
+      if (x.role == kContrib) {
+        if (rows) {
+          const int slot = walker * CG + static_cast<int>(rank);
+          float* partial = p.sk_ws + slot * kPartial + static_cast<size_t>(ew) * BN * 32;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            uint32_t v[32];
+            ptx::tmem_ld_32x32b_x32(t_row + c, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              __stcg(partial + (c + j) * 32 + lane, __uint_as_float(v[j]));
+          }
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) atomicExch(p.sk_flags + slot * 4 + ew, 1);
+        }
+      } else if (rows) {
+        // Partials of the walkers after this one.
+        int parts = 0;
+        const float* partial = nullptr;
+        if (x.role == kOwner) {
+          parts = block_contributors(walker, x, p);
+          const int slot = (walker + 1) * CG + static_cast<int>(rank);
+          partial = p.sk_ws + slot * kPartial + static_cast<size_t>(ew) * BN * 32;
+          int ok = 1;
+          if (lane == 0)
+            for (int n = 0; n < parts && ok; ++n)
+              ok = wait_flag(p.sk_flags + (slot + n * CG) * 4 + ew, p, kDetailSkFlag) ? 1 : 0;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            if (kEpi == kEpiLinear && p.use_d)
+              wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy);
+            break;
+          }
+          for (int n = 0; n < parts; ++n)  // every lane acquires the partials
+            (void)ld_acquire_gpu(p.sk_flags + (slot + n * CG) * 4 + ew);
+        }
+        constexpr size_t step = kPartial * CG;
+
+        bool failed = false;
+#pragma unroll 1
+        for (int cc = 0; cc < kOutN; cc += 64) {
+          const int col0 = n0 + cc;
+          if (col0 >= p.N) break;
+          uint32_t pk[32];
+          if constexpr (kEpi == kEpiGated) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t g[32], u[32];
+              block_acc(t_row, g, partial, step, parts, cc + 32 * h, lane);
+              block_acc(t_row, u, partial, step, parts, BN / 2 + cc + 32 * h, lane);
+              if (p.pre != nullptr) {
+                float* dst = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0 + 32 * h) * 32 + lane;
+                const int n = p.N - (col0 + 32 * h);  // columns that exist
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j < n) {
+                    __stcs(dst + j * 32, __uint_as_float(g[j]));
+                    __stcs(dst + p.pre_half + j * 32, __uint_as_float(u[j]));
+                  }
+              }
+              if (p.act == kActSilu)
+                gated32<kActSilu>(g, u, pk + 16 * h, bf16_out);
+              else if (p.act == kActGelu)
+                gated32<kActGelu>(g, u, pk + 16 * h, bf16_out);
+              else
+                gated32<kActRelu>(g, u, pk + 16 * h, bf16_out);
+            }
+            if (lane == 0) ptx::bulk_wait_group_read<1>();
+            block_store(pk, p, p.out0, maps.c0, my_stage + buf * kStoreBuf, lane, row0, col0, t.z, p.N);
+            buf ^= 1;
+          } else if constexpr (kEpi == kEpiGatedBwd) {
+            uint32_t pu[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float* src = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0 + 32 * h) * 32 + lane;
+              const int n = p.N - (col0 + 32 * h);
+              float g[32], u[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                g[j] = j < n ? __ldcs(src + j * 32) : 0.0f;
+                u[j] = j < n ? __ldcs(src + p.pre_half + j * 32) : 0.0f;
+              }
+              uint32_t dh[32];
+              block_acc(t_row, dh, partial, step, parts, cc + 32 * h, lane);
+              if (p.act == kActSilu)
+                gated_bwd32<kActSilu>(dh, g, u, pk + 16 * h, pu + 16 * h, bf16_out);
+              else if (p.act == kActGelu)
+                gated_bwd32<kActGelu>(dh, g, u, pk + 16 * h, pu + 16 * h, bf16_out);
+              else
+                gated_bwd32<kActRelu>(dh, g, u, pk + 16 * h, pu + 16 * h, bf16_out);
+            }
+            if (lane == 0) ptx::bulk_wait_group_read<0>();
+            block_store(pk, p, p.out0, maps.c0, my_stage, lane, row0, col0, t.z, p.N);
+            block_store(pu, p, p.out1, maps.c1, my_stage + kStoreBuf, lane, row0, col0, t.z, p.N);
+          } else {
+            uint8_t* sb = my_stage + buf * kStoreBuf;
+            const bool more = cc + 64 < kOutN && col0 + 64 < p.N;
+            if (p.use_d) {
+              if (!wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy)) failed = true;
+              d_phase ^= 1u << buf;
+              if (__any_sync(0xffffffffu, failed)) {
+                failed = true;
+                break;
+              }
+              if (more) load_d(buf ^ 1, col0 + 64);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              block_acc(t_row, r, partial, step, parts, cc + 32 * h, lane);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(p.alpha * __uint_as_float(r[j]));
+              if (p.use_d) {
+                // D is fp16 (the iterate's type), in the swizzled layout of the box.
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t c = static_cast<uint32_t>(4 * h + j);
+                  const uint4 v = *reinterpret_cast<const uint4*>(sb + lane * 128u + ((c ^ (lane & 7u)) << 4));
+                  const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&wd[e]));
+                    const int i = 8 * j + 2 * e;
+                    r[i] = __float_as_uint(fmaf(p.beta, f.x, __uint_as_float(r[i])));
+                    r[i + 1] = __float_as_uint(fmaf(p.beta, f.y, __uint_as_float(r[i + 1])));
+                  }
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                pk[16 * h + j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), bf16_out);
+            }
+            if (p.symmetric && t.mb != t.nb) block_store_mirror(pk, p, p.out0, lane, row0, col0, t.z);
+            if (!p.use_d && lane == 0) ptx::bulk_wait_group_read<1>();
+            block_store(pk, p, p.out0, maps.c0, sb, lane, row0, col0, t.z, p.N);
+            buf ^= 1;
+          }
+        }
+        if (failed) break;
+        if (x.role == kOwner) {
+          __syncwarp();  // every lane has read the partials
+          const int slot = (walker + 1) * CG + static_cast<int>(rank);
+          if (lane == 0)
+            for (int n = 0; n < parts; ++n) p.sk_flags[(slot + n * CG) * 4 + ew] = 0;
+        }
+      }
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          ptx::mbar_arrive_cluster(ptx::map_shared_rank(tempty_bar(acc), 0));
+        else
+          ptx::mbar_arrive(tempty_bar(acc));
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (lane == 0) ptx::bulk_wait_group_all();
+    __syncwarp();
+  }
+
+  ptx::tc_fence_before_sync();
+  if (CG == 2)
+    ptx::cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc<CG>(tmem_base, tmem_cols);
+  }
+}
+
+template <bool kAT, bool kBN, int kEpi>
+cudaError_t block_set_smem(size_t smem) {
+  const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(block_kernel<1, kAT, kBN, kEpi>, attr, static_cast<int>(smem));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(block_kernel<2, kAT, kBN, kEpi>, attr, static_cast<int>(smem));
+  return e;
+}
+
+// `grid` CTAs in clusters of `cg`; the launch may overlap the previous
+// kernel's tail (programmatic dependent launch).
+template <bool kAT, bool kBN, int kEpi>
+cudaError_t block_launch(const BlockMaps& m, const BlockParams& p, int cg, int grid, size_t smem,
+                         cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kBlockThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cg == 2 ? 2 : 1;
+  return cg == 2 ? cudaLaunchKernelEx(&cfg, block_kernel<2, kAT, kBN, kEpi>, m, p)
+                 : cudaLaunchKernelEx(&cfg, block_kernel<1, kAT, kBN, kEpi>, m, p);
+}
+
+}  // namespace spgemm
+
+#define SPGEMM_DEFINE_BLOCK(NAME, AT, BN, EPI)                                                 \
+  namespace spgemm {                                                                           \
+  cudaError_t block_set_smem_##NAME(size_t smem) { return block_set_smem<AT, BN, EPI>(smem); } \
+  cudaError_t block_launch_##NAME(const BlockMaps& m, const BlockParams& p, int cg, int grid,  \
+                                  size_t smem, cudaStream_t stream) {                          \
+    return block_launch<AT, BN, EPI>(m, p, cg, grid, smem, stream);                            \
+  }                                                                                            \
+  }

@@ -44,6 +44,15 @@ gemm_status_t cuda_fail(cudaError_t e, const char* what) {
   return fail(GEMM_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+}  // namespace
+
+// The other translation units of the C ABI report through the same string.
+namespace spgemm {
+void set_last_error(const char* text) { g_last_error = text; }
+}  // namespace spgemm
+
+namespace {
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,

@@ -1,0 +1,305 @@
+// ops_api.cu -- the operators' handle (include/gemm_ops.h) and the planning
+// and launch of their products.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+#include <mutex>
+#include <new>
+
+#include "ops_internal.h"
+#include "ptx.cuh"
+
+namespace spgemm {
+
+gemm_status_t ops_fail(gemm_status_t st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  try {
+    set_last_error(buf);
+  } catch (...) {  // out of host memory: the status still says what failed
+  }
+  return st;
+}
+
+gemm_status_t ops_cuda_fail(cudaError_t e, const char* what) {
+  return ops_fail(GEMM_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+OpsDevice::OpsDevice(int dev) {
+  err = cudaGetDevice(&prev);
+  if (err == cudaSuccess && prev != dev) {
+    err = cudaSetDevice(dev);
+    switched = err == cudaSuccess;
+  }
+}
+OpsDevice::~OpsDevice() {
+  if (switched) cudaSetDevice(prev);
+}
+
+namespace {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// A batch of row-major 16-bit matrices as a 3-D map, box `box_cols` x
+// `box_rows` of one matrix, 128-byte swizzle.
+gemm_status_t encode(CUtensorMap* map, bool bf16, const Matrix& m, int64_t batch, uint32_t box_cols,
+                     uint32_t box_rows, CUtensorMapL2promotion l2) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return ops_fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const int64_t step = batch > 1 ? m.batch_stride : m.rows * m.ld;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(m.ld) * 2u,
+                                 static_cast<cuuint64_t>(step) * 2u};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r =
+      enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+          const_cast<void*>(m.ptr), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return ops_fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for %lld x %lld x %lld",
+                    static_cast<int>(r), static_cast<long long>(batch),
+                    static_cast<long long>(m.rows), static_cast<long long>(m.cols));
+  return GEMM_OK;
+}
+
+// The bulk-store path needs every row (and matrix) of the output 16-byte
+// aligned.  A bulk store is clipped to whole 16-byte units (loads to single
+// elements), so the output must also own its rows (Matrix::cols) up to the
+// next multiple of 8 elements.
+BlockOut describe_out(const Matrix& m, int64_t N, int64_t batch) {
+  BlockOut o{};
+  o.ptr = const_cast<void*>(m.ptr);
+  o.ld = m.ld;
+  o.batch = m.batch_stride;
+  o.tma = copyable(m) && m.cols >= round8(N) && (batch == 1 || m.batch_stride % 8 == 0) ? 1 : 0;
+  return o;
+}
+
+constexpr size_t kStagingBytes = 4u * 2u * kStoreBuf;
+
+size_t block_smem(int cg, int stages, int a_rows) {
+  const size_t slice = static_cast<size_t>(a_rows) * kBK * 2 +
+                       static_cast<size_t>(block_bn(cg) / cg) * kBK * 2;
+  return kAlignSlack + slice * block_sub(cg) * stages + kStagingBytes + kBarrierBytes;
+}
+
+}  // namespace
+
+size_t block_workspace(const gemm_ops* ops) {
+  return static_cast<size_t>(ops->sm_count) *
+         std::max(block_partial_bytes(1), block_partial_bytes(2));
+}
+
+gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, cudaStream_t stream) {
+  const bool gated = pr.kind == BlockProblem::kGated;
+  const bool a_t = pr.kind == BlockProblem::kTN;
+  const bool b_n = pr.kind == BlockProblem::kNN || pr.kind == BlockProblem::kTN ||
+                   pr.kind == BlockProblem::kGatedBwd;
+  BlockMaps maps;
+  BlockParams p;
+  std::memset(&p, 0, sizeof(p));
+
+  auto tiles = [&](int cg, int64_t* tm, int64_t* tn) -> int64_t {
+    *tm = ceil_div(pr.M, static_cast<int64_t>(kBM) * cg);
+    *tn = ceil_div(pr.N, gated ? block_bn(cg) / 2 : block_bn(cg));
+    return (pr.symmetric ? *tn * (*tn + 1) / 2 : *tm * *tn) * pr.batch;
+  };
+  // A pair's 256 x 256 tile moves half the operand bytes per product of a
+  // single CTA's 128 x 128, so pairs run wherever each gets at least four
+  // slots of K (512); smaller problems spread over all SMs in small tiles.
+  int64_t tm, tn;
+  int cg = 1;
+  if (pr.M > kBM && ops->pairs > 0) {
+    const int64_t t2 = tiles(2, &tm, &tn);
+    if (t2 * ceil_div(pr.K, kBK * 2) >= 4 * static_cast<int64_t>(ops->pairs)) cg = 2;
+  }
+  const int64_t nt = tiles(cg, &tm, &tn);
+  const int64_t kb = ceil_div(pr.K, static_cast<int64_t>(kBK) * block_sub(cg));
+  if (nt > kOpsMaxDim) return ops_fail(GEMM_ERR_INVALID_ARG, "too many output tiles");
+  const int64_t most = cg == 2 ? ops->pairs : ops->sm_count;
+
+  // K slots are shared out evenly (stream-K) in the last one to two waves of
+  // tiles; fewer tiles than walkers are all shared, as long as each walker
+  // gets at least kMinShare slots.
+  constexpr int64_t kMinShare = 4;
+  int64_t walkers, sk;
+  if (nt >= most) {
+    walkers = most;
+    sk = nt % most == 0 || kb < kMinShare ? 0 : nt % most + most;
+  } else {
+    walkers = std::max(nt, std::min(most, nt * kb / kMinShare));
+    sk = walkers > nt ? nt : 0;
+  }
+
+  const int a_rows = a_t || cg == 2 || pr.M > 64 ? kBM : static_cast<int>(round8(pr.M));
+  int stages = kMaxStages;
+  while (stages > 1 && block_smem(cg, stages, a_rows) > ops->smem_optin) --stages;
+  const size_t smem = block_smem(cg, stages, a_rows);
+  if (smem > ops->smem_optin) return ops_fail(GEMM_ERR_SMEM_BUDGET, "no ring fits shared memory");
+
+  p.M = static_cast<int>(pr.M);
+  p.N = static_cast<int>(pr.N);
+  p.K = static_cast<int>(pr.K);
+  p.tiles_m = static_cast<int>(tm);
+  p.tiles_n = static_cast<int>(tn);
+  p.num_tiles = static_cast<int>(nt);
+  p.tiles_per = static_cast<int>(nt / pr.batch);
+  p.batch = static_cast<int>(pr.batch);
+  p.k_blocks = static_cast<int>(kb);
+  p.stages = stages;
+  p.raster_group = cg == 2 ? 8 : 16;
+  p.walkers = static_cast<int>(walkers);
+  p.sk_tiles = static_cast<int>(sk);
+  p.dp_tiles = static_cast<int>(nt - sk);
+  p.sk_ws = partials;
+  p.sk_flags = ops->d_flags;
+  p.a_box_rows = a_rows;
+  p.b_stream = pr.stream_b && tm == 1 ? 1 : 0;
+  p.l2_prefetch_first = p.b_stream;
+  p.bf16 = pr.bf16 ? 1 : 0;
+  p.idesc = ptx::instr_desc_f16(kBM * cg, block_bn(cg), pr.bf16, b_n) | (a_t ? 1u << 15 : 0u);
+  p.status = ops->d_status;
+  p.timeout_ns = ops->timeout_ns;
+  p.symmetric = pr.symmetric ? 1 : 0;
+  p.out_bf16 = pr.out_bf16 ? 1 : 0;
+  p.act = pr.act;
+  p.gate_rows = gated ? static_cast<int>(pr.N) : 0;
+  p.use_d = pr.d.ptr != nullptr ? 1 : 0;
+  p.alpha = pr.alpha;
+  p.beta = pr.beta;
+  p.out0 = describe_out(pr.out0, pr.N, pr.batch);
+  p.out1 = describe_out(pr.out1, pr.N, pr.batch);
+  p.pre = pr.pre;
+  p.pre_half = ceil_div(pr.M, 32) * 32 * pr.N;
+
+  const CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  const CUtensorMapL2promotion none = CU_TENSOR_MAP_L2_PROMOTION_NONE;
+  const uint32_t b_rows = gated && cg == 1 ? block_bn(1) / 2 : block_bn(cg) / cg;
+  gemm_status_t st = encode(&maps.a, pr.bf16, pr.a, pr.batch, kBK,
+                            a_t ? kBK : static_cast<uint32_t>(a_rows), l2);
+  if (st == GEMM_OK) st = encode(&maps.b, pr.bf16, pr.b, pr.batch, kBK, b_n ? kBK : b_rows, l2);
+  Matrix o0 = pr.out0, o1 = pr.out1;
+  o0.rows = o1.rows = pr.M;
+  o0.cols = o1.cols = pr.N;
+  maps.c0 = maps.c1 = maps.d = maps.a;  // valid maps where a product has no such operand
+  if (st == GEMM_OK && p.out0.tma) st = encode(&maps.c0, pr.out_bf16, o0, pr.batch, 64, 32, none);
+  if (st == GEMM_OK && p.out1.ptr && p.out1.tma)
+    st = encode(&maps.c1, pr.out_bf16, o1, pr.batch, 64, 32, none);
+  if (st == GEMM_OK && p.use_d) st = encode(&maps.d, false, pr.d, pr.batch, 64, 32, none);
+  if (st != GEMM_OK) return st;
+
+  const int grid = static_cast<int>(walkers) * cg;
+  cudaError_t e;
+  switch (pr.kind) {
+    case BlockProblem::kNT: e = block_launch_nt(maps, p, cg, grid, smem, stream); break;
+    case BlockProblem::kNN: e = block_launch_nn(maps, p, cg, grid, smem, stream); break;
+    case BlockProblem::kTN: e = block_launch_tn(maps, p, cg, grid, smem, stream); break;
+    case BlockProblem::kGated: e = block_launch_gated(maps, p, cg, grid, smem, stream); break;
+    default: e = block_launch_gated_bwd(maps, p, cg, grid, smem, stream); break;
+  }
+  return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "block product launch");
+}
+
+}  // namespace spgemm
+
+using namespace spgemm;
+
+extern "C" {
+
+gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
+  ops_fail(GEMM_OK, "%s", "");
+  if (!out) return ops_fail(GEMM_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (device < 0) return ops_fail(GEMM_ERR_INVALID_ARG, "device %d < 0", device);
+  int ndev = 0;
+  cudaError_t e = cudaGetDeviceCount(&ndev);
+  if (e != cudaSuccess) return ops_cuda_fail(e, "cudaGetDeviceCount");
+  if (device >= ndev)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "device %d >= count %d", device, ndev);
+  gemm_device_desc_t desc;
+  const gemm_status_t st = gemm_device_query(device, &desc);
+  if (st != GEMM_OK) return st;
+  OpsDevice guard(device);
+  if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
+  gemm_ops* ops = new (std::nothrow) gemm_ops();
+  if (!ops) return ops_fail(GEMM_ERR_INVALID_ARG, "out of host memory");
+  ops->device = device;
+  ops->sm_count = desc.sm_count;
+  ops->pairs = desc.pair_clusters;
+  ops->smem_optin = static_cast<size_t>(desc.smem_optin);
+  ops->l2_bytes = desc.l2_bytes;
+  ops->timeout_ns = 2000000000ull;
+  for (auto set : {block_set_smem_nt, block_set_smem_nn, block_set_smem_tn, block_set_smem_gated,
+                   block_set_smem_gated_bwd})
+    if (e == cudaSuccess) e = set(ops->smem_optin);
+  const size_t flags = static_cast<size_t>(ops->sm_count) * 4 * sizeof(int);
+  if (e == cudaSuccess) e = cudaMalloc(&ops->d_status, 4 * sizeof(int));
+  if (e == cudaSuccess) e = cudaMemset(ops->d_status, 0, 4 * sizeof(int));
+  if (e == cudaSuccess) e = cudaMalloc(&ops->d_flags, flags);
+  if (e == cudaSuccess) e = cudaMemset(ops->d_flags, 0, flags);
+  // cudaMemset runs on the default stream; another stream's first call must not overtake it.
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  if (e != cudaSuccess) {
+    gemm_ops_destroy(ops);
+    return ops_cuda_fail(e, "operator handle set-up");
+  }
+  *out = ops;
+  return GEMM_OK;
+}
+
+void gemm_ops_destroy(gemm_ops_t* ops) {
+  if (!ops) return;
+  OpsDevice guard(ops->device);
+  cudaDeviceSynchronize();
+  if (ops->d_status) cudaFree(ops->d_status);
+  if (ops->d_flags) cudaFree(ops->d_flags);
+  delete ops;
+}
+
+gemm_status_t gemm_ops_check(gemm_ops_t* ops, int32_t* device_status, int32_t* detail) {
+  ops_fail(GEMM_OK, "%s", "");
+  if (!ops || !device_status) return ops_fail(GEMM_ERR_INVALID_ARG, "NULL argument");
+  OpsDevice guard(ops->device);
+  if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return ops_cuda_fail(e, "cudaDeviceSynchronize");
+  int h[4] = {0, 0, 0, 0};
+  e = cudaMemcpy(h, ops->d_status, sizeof(h), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemset(ops->d_status, 0, sizeof(h));
+  // A launch that gave up part-way may have left partial-ready flags raised.
+  if (e == cudaSuccess && h[0] != 0)
+    e = cudaMemset(ops->d_flags, 0, static_cast<size_t>(ops->sm_count) * 4 * sizeof(int));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  if (e != cudaSuccess) return ops_cuda_fail(e, "read or clear the status word");
+  *device_status = h[0];
+  if (detail) *detail = h[1];
+  return GEMM_OK;
+}
+
+}  // extern "C"

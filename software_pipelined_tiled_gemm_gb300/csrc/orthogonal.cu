@@ -1,0 +1,339 @@
+// orthogonal.cu -- the orthogonalised update by Newton-Schulz products.
+//
+// Two passes over G normalise it: the sum of squares (one partial per block),
+// then X = 2^8 G / max(|G|, eps) in fp16 (every block adds the partials in the
+// same order).  Each step is three block products: A = X X^T and
+// B = b A + c A^2 on the tiles on and above the diagonal only, and
+// X' = a X + B X.  On matrices with more rows than columns the products use
+// X^T X and X B instead, reading X as it lies.
+//
+// fp16 for the iterates: the step's map multiplies errors along small
+// singular values by up to a = 3.4 each time; with bf16's 8 bits five steps
+// end 1.1e-2 (relative, Frobenius) from exact arithmetic, with fp16's 11 bits
+// 1.3e-3, below the bf16 result's own rounding (1.7e-3).  The factor 2^8
+// lifts the elements of a normalised matrix (1 / sqrt(m n) in the mean) out
+// of fp16's subnormal range; elements stay below 2^8 x 1.3.
+#include <cuda_fp16.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "ops_internal.h"
+#include "ptx.cuh"
+
+using namespace spgemm;
+
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormVecs = 4;                                     // 8-element vectors per thread and step
+constexpr int kNormCols = kNormThreads * kNormVecs * 8;          // columns of a step
+constexpr int kNormBlocks = 608;                                 // at most, over the batch: four per SM
+constexpr float kIterateScale = 256.0f;
+
+struct NormArgs {
+  const void* g;
+  int64_t m, n, ld, batch_stride;
+  int chunks;          // steps per row
+  int64_t steps;       // steps per matrix
+  int aligned;         // vectors of 8 elements may be loaded whole
+  float* partial;      // batch x gridDim.x
+  uint16_t* x;
+  int64_t ldx;
+  float eps;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v);
+template <>
+__device__ __forceinline__ float to_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Elements [c, c + 8) of a row (0 at and past n).
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, bool aligned, float (&v)[8]) {
+  if (aligned && c + 8 <= n) {
+    constexpr int kWords = sizeof(T) * 8 / 16;
+    uint4 w[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
+    const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float<T>(e[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_float<T>(row[c + i]) : 0.0f;
+}
+
+// Sum over the block, the same in every thread.
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T* shared) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+  T s = 0;
+#pragma unroll
+  for (int i = 0; i < kNormThreads / 32; ++i) s += shared[i];
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) sum_squares_kernel(const NormArgs a) {
+  __shared__ float shared[kNormThreads / 32];
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
+  float sum = 0.0f;
+  for (int64_t s = blockIdx.x; s < a.steps; s += gridDim.x) {
+    const int64_t r = s / a.chunks;
+    const int64_t c0 = (s - r * a.chunks) * kNormCols + threadIdx.x * 8;
+    float v[kNormVecs][8];
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i)
+      load8<T>(g + r * a.ld, c0 + i * kNormThreads * 8, a.n, a.aligned != 0, v[i]);
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+  }
+  sum = block_sum<float>(sum, shared);
+  if (threadIdx.x == 0) a.partial[blockIdx.y * gridDim.x + blockIdx.x] = sum;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) normalize_kernel(const NormArgs a, int parts) {
+  __shared__ double shared[kNormThreads / 32];
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kNormThreads)
+    sum += static_cast<double>(__ldcg(a.partial + blockIdx.y * parts + i));
+  sum = block_sum<double>(sum, shared);
+  const float scale = kIterateScale / fmaxf(static_cast<float>(sqrt(sum)), a.eps);
+  const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
+  uint16_t* x = a.x + blockIdx.y * a.m * a.ldx;
+  for (int64_t s = blockIdx.x; s < a.steps; s += gridDim.x) {
+    const int64_t r = s / a.chunks;
+    const int64_t c0 = (s - r * a.chunks) * kNormCols + threadIdx.x * 8;
+    float v[kNormVecs][8];
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i)
+      load8<T>(g + r * a.ld, c0 + i * kNormThreads * 8, a.n, a.aligned != 0, v[i]);
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i) {
+      const int64_t c = c0 + i * kNormThreads * 8;
+      if (c < a.ldx) {
+        __half2 h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(v[i][2 * j] * scale, v[i][2 * j + 1] * scale);
+        *reinterpret_cast<uint4*>(x + r * a.ldx + c) = *reinterpret_cast<const uint4*>(h);
+      }
+    }
+  }
+}
+
+// Launch that may overlap the previous kernel's tail (both kernels wait for
+// it before they touch global memory).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kNormThreads, 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T>
+cudaError_t normalize(const NormArgs& a, int64_t batch, int blocks, cudaStream_t stream) {
+  const dim3 grid(blocks, static_cast<unsigned>(batch), 1);
+  cudaError_t e = launch_early(sum_squares_kernel<T>, grid, stream, a);
+  if (e == cudaSuccess) e = launch_early(normalize_kernel<T>, grid, stream, a, blocks);
+  return e;
+}
+
+struct Layout {
+  float* partials;
+  float* norms;
+  uint16_t* x[2];
+  uint16_t* a;
+  uint16_t* b;
+  int64_t np, s, sp;
+  int blocks;
+  size_t bytes;
+};
+
+Layout layout(const gemm_ops* ops, const gemm_orthogonalize_args_t* g, void* workspace) {
+  Layout l;
+  l.np = round8(g->n);
+  l.s = std::min(g->m, g->n);
+  l.sp = round8(l.s);
+  const int64_t steps = g->m * ceil_div(std::max<int64_t>(g->n, 1), kNormCols);
+  l.blocks = static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>(steps, kNormBlocks / std::max<int64_t>(1, std::min<int64_t>(g->batch, kNormBlocks)))));
+  const size_t x = static_cast<size_t>(g->batch) * g->m * l.np * 2;
+  const size_t a = static_cast<size_t>(g->batch) * l.s * l.sp * 2;
+  Carver c(workspace);
+  l.partials = static_cast<float*>(c.take(block_workspace(ops)));
+  l.norms = static_cast<float*>(c.take(static_cast<size_t>(g->batch) * l.blocks * sizeof(float)));
+  l.x[0] = static_cast<uint16_t*>(c.take(x));
+  l.x[1] = static_cast<uint16_t*>(c.take(x));
+  l.a = static_cast<uint16_t*>(c.take(a));
+  l.b = static_cast<uint16_t*>(c.take(a));
+  l.bytes = c.used;
+  return l;
+}
+
+size_t elem_bytes(gemm_in_t t) { return t == GEMM_IN_F32 ? 4 : 2; }
+
+gemm_status_t check(const gemm_orthogonalize_args_t* g) {
+  if (!g) return ops_fail(GEMM_ERR_INVALID_ARG, "args is NULL");
+  if (g->batch < 0 || g->m < 0 || g->n < 0)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "negative size batch=%lld m=%lld n=%lld", (long long)g->batch,
+                    (long long)g->m, (long long)g->n);
+  if (g->m > kOpsMaxDim || g->n > kOpsMaxDim || g->batch > 65535)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "m or n above 2^31-1, or batch above 65535");
+  if (g->dtype != GEMM_IN_F16 && g->dtype != GEMM_IN_BF16 && g->dtype != GEMM_IN_F32)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "dtype %d out of range", static_cast<int>(g->dtype));
+  if (g->steps < 1 || g->steps > 100)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "steps %d outside [1, 100]", g->steps);
+  if (!(g->eps > 0.0f) || !std::isfinite(g->a) || !std::isfinite(g->b) || !std::isfinite(g->c))
+    return ops_fail(GEMM_ERR_INVALID_ARG, "eps must be positive and a, b, c finite");
+  if (g->batch == 0 || g->m == 0 || g->n == 0) return GEMM_OK;
+  if (!g->g || !g->out) return ops_fail(GEMM_ERR_INVALID_ARG, "g or out is NULL");
+  if (g->ldg < g->n) return ops_fail(GEMM_ERR_INVALID_ARG, "ldg %lld < n", (long long)g->ldg);
+  if (g->batch > 1 && g->batch_stride < 0)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "negative batch_stride");
+  if ((reinterpret_cast<uintptr_t>(g->g) % elem_bytes(g->dtype)) || (reinterpret_cast<uintptr_t>(g->out) & 1u))
+    return ops_fail(GEMM_ERR_INVALID_ARG, "g or out is not aligned to its elements");
+  return GEMM_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_orthogonalize_workspace(gemm_ops_t* ops, const gemm_orthogonalize_args_t* args,
+                                           size_t* bytes) {
+  ops_fail(GEMM_OK, "%s", "");
+  if (!ops || !bytes) return ops_fail(GEMM_ERR_INVALID_ARG, "NULL argument");
+  const gemm_status_t st = check(args);
+  if (st == GEMM_OK) *bytes = layout(ops, args, nullptr).bytes;
+  return st;
+}
+
+gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_t* args,
+                                 void* workspace, size_t workspace_bytes, void* stream_handle) {
+  ops_fail(GEMM_OK, "%s", "");
+  if (!ops) return ops_fail(GEMM_ERR_INVALID_ARG, "ops is NULL");
+  gemm_status_t st = check(args);
+  if (st != GEMM_OK || args->batch == 0 || args->m == 0 || args->n == 0) return st;
+  const int64_t m = args->m, n = args->n, batch = args->batch;
+  const Layout l = layout(ops, args, workspace);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < l.bytes)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "workspace NULL, not 256-byte aligned or below %zu bytes", l.bytes);
+  const size_t g_bytes = (static_cast<size_t>(batch - 1) * (batch > 1 ? args->batch_stride : 0) +
+                          static_cast<size_t>(m - 1) * args->ldg + n) * elem_bytes(args->dtype);
+  const size_t o_bytes = static_cast<size_t>(batch) * m * n * 2;
+  if (overlap(args->out, o_bytes, args->g, g_bytes) || overlap(workspace, l.bytes, args->g, g_bytes) ||
+      overlap(workspace, l.bytes, args->out, o_bytes))
+    return ops_fail(GEMM_ERR_INVALID_ARG, "g, out and the workspace must not overlap");
+  OpsDevice guard(ops->device);
+  if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
+
+  NormArgs na{};
+  na.g = args->g;
+  na.m = m;
+  na.n = n;
+  na.ld = args->ldg;
+  na.batch_stride = batch > 1 ? args->batch_stride : 0;
+  na.chunks = static_cast<int>(ceil_div(n, kNormCols));
+  na.steps = m * na.chunks;
+  const int64_t vec = 16 / static_cast<int64_t>(elem_bytes(args->dtype));
+  na.aligned = (reinterpret_cast<uintptr_t>(args->g) & 15u) == 0 && args->ldg % vec == 0 &&
+               (batch == 1 || args->batch_stride % vec == 0);
+  na.partial = l.norms;
+  na.x = l.x[0];
+  na.ldx = l.np;
+  na.eps = args->eps;
+  cudaError_t e;
+  if (args->dtype == GEMM_IN_F32)
+    e = normalize<float>(na, batch, l.blocks, stream);
+  else if (args->dtype == GEMM_IN_BF16)
+    e = normalize<__nv_bfloat16>(na, batch, l.blocks, stream);
+  else
+    e = normalize<__half>(na, batch, l.blocks, stream);
+  if (e != cudaSuccess) return ops_cuda_fail(e, "normalisation launch");
+
+  const bool tall = m > n;
+  Matrix X{l.x[0], m, n, l.np, m * l.np}, Y{l.x[1], m, n, l.np, m * l.np};
+  const Matrix A{l.a, l.s, l.s, l.sp, l.s * l.sp}, B{l.b, l.s, l.s, l.sp, l.s * l.sp};
+  const float inv = 1.0f / kIterateScale;
+  for (int it = 0; it < args->steps; ++it) {
+    BlockProblem p;
+    p.batch = batch;
+    p.M = p.N = l.s;
+    p.symmetric = true;
+    p.kind = tall ? BlockProblem::kTN : BlockProblem::kNT;  // A = X^T X or X X^T
+    p.K = tall ? m : n;
+    p.a = p.b = X;
+    p.alpha = inv * inv;
+    p.out0 = A;  // the padded row is the iterate's own
+    p.out0.cols = l.sp;
+    st = run_block(ops, p, l.partials, stream);
+    if (st != GEMM_OK) return st;
+
+    p.kind = BlockProblem::kNT;  // B = c A A^T + b A
+    p.K = l.s;
+    p.a = p.b = p.d = A;
+    p.alpha = args->c;
+    p.beta = args->b;
+    p.out0 = B;
+    p.out0.cols = l.sp;
+    st = run_block(ops, p, l.partials, stream);
+    if (st != GEMM_OK) return st;
+
+    const bool last = it + 1 == args->steps;
+    p.symmetric = false;
+    p.M = m;
+    p.N = n;
+    if (tall) {  // X B, B symmetric
+      p.kind = BlockProblem::kNT;
+      p.a = X;
+      p.b = B;
+    } else {
+      p.kind = BlockProblem::kNN;
+      p.a = B;
+      p.b = X;
+    }
+    p.d = X;
+    p.alpha = last ? inv : 1.0f;
+    p.beta = last ? inv * args->a : args->a;
+    p.out_bf16 = last;
+    p.out0 = last ? Matrix{args->out, m, n, n, m * n} : Matrix{Y.ptr, m, l.np, l.np, m * l.np};
+    st = run_block(ops, p, l.partials, stream);
+    if (st != GEMM_OK) return st;
+    std::swap(X, Y);
+  }
+  return GEMM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,410 @@
+"""The operators built around the GEMM: the gated feed-forward block with its
+backward pass, the orthogonalised update of a gradient, and the log
+probabilities of tokens with their gradient.
+
+A thin ctypes binding over ``include/gemm_ops.h``.  As in :func:`matmul_nt`,
+tensors are CUDA tensors, work goes to the current stream of their device,
+nothing synchronises, and there is no fallback.  What a call needs besides
+its outputs (a workspace) comes from PyTorch's allocator on that stream.
+One library handle is kept per device and stream; :func:`check_operators`
+reports what a kernel recorded in them.
+"""
+from __future__ import annotations
+
+import collections
+import ctypes
+import threading
+
+__all__ = [
+    "gated_ffn", "gated_ffn_backward", "GatedKept", "orthogonalize", "check_operators",
+    "close_operators", "FfnArgs", "OrthogonalizeArgs", "NEWTON_SCHULZ", "token_logprobs",
+    "token_logprobs_backward", "TokenLogprobs", "LogprobsArgs", "MAX_TOP_K",
+]
+
+_vp, _i64, _ci, _f, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
+                           ctypes.c_size_t)
+
+GEMM_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 1, "relu": 2}
+
+# a, b, c of X <- a X + (b A + c A^2) X: steep at zero, so that five steps
+# bring every singular value above about 1e-3 of the norm close to one.
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+class FfnArgs(ctypes.Structure):
+    """gemm_ffn_args_t"""
+    _fields_ = [("tokens", _i64), ("d_model", _i64), ("d_inner", _i64), ("dtype", _ci),
+                ("act", _ci), ("x", _vp), ("ldx", _i64), ("w_in", _vp), ("w_out", _vp),
+                ("y", _vp), ("kept", _vp), ("dy", _vp), ("lddy", _i64), ("dx", _vp),
+                ("dw_in", _vp), ("dw_out", _vp)]
+
+
+class OrthogonalizeArgs(ctypes.Structure):
+    """gemm_orthogonalize_args_t"""
+    _fields_ = [("batch", _i64), ("m", _i64), ("n", _i64), ("dtype", _ci), ("g", _vp),
+                ("ldg", _i64), ("batch_stride", _i64), ("out", _vp), ("steps", _ci), ("a", _f),
+                ("b", _f), ("c", _f), ("eps", _f)]
+
+
+class LogprobsArgs(ctypes.Structure):
+    """gemm_logprobs_args_t"""
+    _fields_ = [("rows", _i64), ("vocab", _i64), ("dtype", _ci), ("logits", _vp), ("ld", _i64),
+                ("tokens", _vp), ("top_k", _ci), ("logprobs", _vp), ("entropy", _vp),
+                ("lse", _vp), ("top_logprobs", _vp), ("top_ids", _vp), ("d_logprobs", _vp),
+                ("d_entropy", _vp), ("d_logits", _vp), ("ldd", _i64)]
+
+
+MAX_TOP_K = 64   # GEMM_LOGPROBS_MAX_TOP_K
+
+_bound = None
+_handles: dict = {}
+_lock = threading.Lock()
+
+
+def _lib():
+    """The library, with the operators' signatures set."""
+    global _bound
+    if _bound is not None:
+        return _bound
+    from . import load_library
+    lib = load_library()
+    psz = ctypes.POINTER(_sz)
+    pi32 = ctypes.POINTER(ctypes.c_int32)
+    for name, args in {
+            "gemm_ops_create": [ctypes.POINTER(_vp), _ci],
+            "gemm_ops_check": [_vp, pi32, pi32],
+            "gemm_ffn_workspace": [_vp, ctypes.POINTER(FfnArgs), _ci, psz],
+            "gemm_ffn_run": [_vp, ctypes.POINTER(FfnArgs), _vp, _sz, _vp],
+            "gemm_ffn_backward": [_vp, ctypes.POINTER(FfnArgs), _vp, _sz, _vp],
+            "gemm_orthogonalize_workspace": [_vp, ctypes.POINTER(OrthogonalizeArgs), psz],
+            "gemm_orthogonalize": [_vp, ctypes.POINTER(OrthogonalizeArgs), _vp, _sz, _vp],
+            "gemm_token_logprobs": [_vp, ctypes.POINTER(LogprobsArgs), _vp],
+            "gemm_token_logprobs_backward": [_vp, ctypes.POINTER(LogprobsArgs), _vp]}.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, _ci
+    lib.gemm_ops_destroy.argtypes, lib.gemm_ops_destroy.restype = [_vp], None
+    lib.gemm_ffn_kept_bytes.argtypes, lib.gemm_ffn_kept_bytes.restype = [_i64, _i64], _sz
+    _bound = lib
+    return lib
+
+
+def _check(status, where):
+    if status:
+        from . import GemmError, gemm_last_error
+        raise GemmError(status, where, gemm_last_error())
+
+
+def _handle(device, stream):
+    """The handle of a device and stream (one handle serves one stream)."""
+    key = (device.index, stream)
+    h = _handles.get(key)
+    if h is None:
+        with _lock:
+            h = _handles.get(key)
+            if h is None:
+                out = _vp()
+                _check(_lib().gemm_ops_create(ctypes.byref(out), device.index), "gemm_ops_create")
+                h = _handles[key] = out.value
+    return h
+
+
+def check_operators() -> None:
+    """Synchronise and raise :class:`GemmError` if a kernel of any operator
+    recorded an error (a wait that ran out of time)."""
+    from . import GemmError, gemm_wait_detail_string
+    with _lock:
+        handles = list(_handles.values())
+    for h in handles:
+        ds, detail = ctypes.c_int32(0), ctypes.c_int32(0)
+        _check(_lib().gemm_ops_check(h, ctypes.byref(ds), ctypes.byref(detail)), "gemm_ops_check")
+        if ds.value:
+            raise GemmError(ds.value, "operators", gemm_wait_detail_string(detail.value))
+
+
+def close_operators() -> None:
+    """Close every handle (synchronises their devices).  Not while a CUDA
+    graph that captured a call is alive."""
+    with _lock:
+        while _handles:
+            _lib().gemm_ops_destroy(_handles.popitem()[1])
+
+
+def _rows(t, cols, name):
+    """(rows, row pitch) of `t` seen as a matrix of `cols` columns."""
+    if t.dim() == 0 or t.shape[-1] != cols:
+        raise ValueError("%s must have %d columns" % (name, cols))
+    rows = t.numel() // cols
+    if t.is_contiguous():
+        return rows, cols
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < cols:
+        raise ValueError("%s must be contiguous, or a matrix of contiguous rows" % name)
+    return rows, t.stride(0)
+
+
+def _on_cuda(first, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.device != first.device:
+            raise ValueError("all tensors must be on the same device (%s is not)" % name)
+
+
+def _output(out, shape, dtype, device, name="out"):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if (tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device
+            or not out.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on the inputs' device"
+                         % (name, dtype, tuple(shape)))
+    return out
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+# ------------------------------------------------ gated feed-forward block --
+
+# What a forward pass keeps for the backward pass: the fp32 gate and up
+# projections and the 16-bit product, in the kernels' own layout.
+GatedKept = collections.namedtuple("GatedKept", "buffer tokens d_model d_inner dtype act")
+
+
+def _ffn_args(x, w_in, w_out, act):
+    import torch
+    if act not in GEMM_ACT:
+        raise ValueError("act must be one of %s" % ", ".join(sorted(GEMM_ACT)))
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a CUDA tensor")
+    _on_cuda(x, x=x, w_in=w_in, w_out=w_out)
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("x must be float16 or bfloat16, got %s" % x.dtype)
+    if w_in.dtype != x.dtype or w_out.dtype != x.dtype:
+        raise TypeError("x, w_in and w_out must have the same dtype")
+    if w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1] or \
+            w_in.shape[1] != w_out.shape[0]:
+        raise ValueError("w_in must be (2 d_inner, d_model) and w_out (d_model, d_inner)")
+    if not (w_in.is_contiguous() and w_out.is_contiguous()):
+        raise ValueError("w_in and w_out must be contiguous")
+    d, i = w_out.shape
+    if d == 0 or i == 0:
+        raise ValueError("d_model and d_inner must be at least 1")
+    m, ldx = _rows(x, d, "x")
+    return FfnArgs(tokens=m, d_model=d, d_inner=i, dtype=1 if x.dtype == torch.bfloat16 else 0,
+                   act=GEMM_ACT[act], x=x.data_ptr(), ldx=ldx, w_in=w_in.data_ptr(),
+                   w_out=w_out.data_ptr(), lddy=d)
+
+
+def _run(name, device, args, query, run):
+    """Workspace from the caching allocator of the current stream, then the call."""
+    import torch
+    stream = torch.cuda.current_stream(device).cuda_stream
+    h = _handle(device, stream)
+    need = _sz()
+    _check(query(h, need), name + "_workspace")
+    with torch.cuda.device(device):
+        ws = torch.empty(max(1, need.value), dtype=torch.uint8, device=device)
+    _check(run(h, ws.data_ptr(), need.value, stream), name)
+
+
+def gated_ffn(x, w_in, w_out, act="silu", out=None, save=False):
+    """y = (act(x Wg^T) * (x Wu^T)) w_out^T on the current CUDA stream.
+
+    x: (..., d_model), float16 or bfloat16, contiguous or a matrix of
+    contiguous rows.  w_in: (2 d_inner, d_model), the rows of Wg followed by
+    those of Wu; w_out: (d_model, d_inner); both contiguous, of x's dtype.
+    act: "silu", "gelu" (tanh form) or "relu".  Returns y of x's shape and
+    dtype (``out`` if given), or ``(y, kept)`` with ``save=True``, kept being
+    what :func:`gated_ffn_backward` needs (10 bytes per token and inner
+    feature: the projections stay in fp32).
+    """
+    import torch
+    a = _ffn_args(x, w_in, w_out, act)
+    lib = _lib()
+    y = _output(out, x.shape, x.dtype, x.device)
+    a.y = y.data_ptr()
+    kept = None
+    if save:
+        buf = torch.empty(lib.gemm_ffn_kept_bytes(a.tokens, a.d_inner), dtype=torch.uint8,
+                          device=x.device)
+        a.kept = buf.data_ptr()
+        kept = GatedKept(buf, a.tokens, a.d_model, a.d_inner, x.dtype, act)
+    if a.tokens:
+        ref = ctypes.byref(a)
+        _run("gemm_ffn_run", x.device, a,
+             lambda h, n: lib.gemm_ffn_workspace(h, ref, 0, ctypes.byref(n)),
+             lambda h, w, n, s: lib.gemm_ffn_run(h, ref, w, n, s))
+    return (y, kept) if save else y
+
+
+def gated_ffn_backward(dy, x, w_in, w_out, kept, need=(True, True, True), out=(None, None, None)):
+    """Gradients (dx, dw_in, dw_out) of :func:`gated_ffn` from dy and what
+    the forward pass kept, with the same x, w_in and w_out.
+
+    dy: x's shape and dtype, contiguous or a matrix of contiguous rows.
+    need: which of the three to compute (None in the place of the others).
+    out: tensors to write them to.
+    """
+    if not isinstance(kept, GatedKept):
+        raise TypeError("kept must come from gated_ffn(..., save=True)")
+    a = _ffn_args(x, w_in, w_out, kept.act)
+    _on_cuda(x, dy=dy)
+    if dy.dtype != x.dtype or dy.shape != x.shape:
+        raise ValueError("dy must have x's shape and dtype")
+    if (a.tokens, a.d_model, a.d_inner, x.dtype) != kept[1:5] or kept.buffer.device != x.device:
+        raise ValueError("kept belongs to a forward pass of other sizes, dtype or device")
+    lib = _lib()
+    a.dy = dy.data_ptr()
+    a.lddy = _rows(dy, a.d_model, "dy")[1]
+    a.kept = kept.buffer.data_ptr()
+    shapes = ((x.shape, "dx"), (w_in.shape, "dw_in"), (w_out.shape, "dw_out"))
+    grads = [_output(o, shape, x.dtype, x.device, name) if want else None
+             for want, o, (shape, name) in zip(need, out, shapes)]
+    a.dx, a.dw_in, a.dw_out = map(_ptr, grads)
+    ref = ctypes.byref(a)
+    _run("gemm_ffn_backward", x.device, a,
+         lambda h, n: lib.gemm_ffn_workspace(h, ref, 1, ctypes.byref(n)),
+         lambda h, w, n, s: lib.gemm_ffn_backward(h, ref, w, n, s))
+    return tuple(grads)
+
+
+# --------------------------------------------------- orthogonalised update --
+
+def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
+    """The orthogonalised form of a matrix, by Newton-Schulz products.
+
+    X = g / max(|g|_F, eps), then `steps` times X <- a X + (b A + c A^2) X
+    with A = X X^T (on the shorter side).  g: (m, n) or a batch (b, m, n),
+    float32, float16 or bfloat16, rows contiguous.  Returns bfloat16 of g's
+    shape (``out`` if given): the update of a weight whose gradient or
+    momentum is g.
+    """
+    import torch
+    if not isinstance(g, torch.Tensor):
+        raise ValueError("g must be a CUDA tensor")
+    _on_cuda(g, g=g)
+    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    if g.dtype not in codes:
+        raise TypeError("g must be float32, float16 or bfloat16, got %s" % g.dtype)
+    if g.dim() not in (2, 3):
+        raise ValueError("g must be a matrix or a batch of matrices")
+    if len(coeffs) != 3:
+        raise ValueError("coeffs must be (a, b, c)")
+    b, m, n = (1,) * (3 - g.dim()) + tuple(g.shape)
+    ld, bs = n, m * n
+    if not g.is_contiguous():
+        ld, bs = g.stride(-2), (g.stride(0) if g.dim() == 3 else 0)
+        if g.stride(-1) != 1 or ld < n or (b > 1 and bs < 0):
+            raise ValueError("g must have contiguous rows")
+    y = _output(out, g.shape, torch.bfloat16, g.device)
+    a = OrthogonalizeArgs(batch=b, m=m, n=n, dtype=codes[g.dtype], g=g.data_ptr(), ldg=ld,
+                          batch_stride=bs, out=y.data_ptr(), steps=int(steps), a=coeffs[0],
+                          b=coeffs[1], c=coeffs[2], eps=eps)
+    lib = _lib()
+    ref = ctypes.byref(a)
+    _run("gemm_orthogonalize", g.device, a,
+         lambda h, need: lib.gemm_orthogonalize_workspace(h, ref, ctypes.byref(need)),
+         lambda h, w, need, s: lib.gemm_orthogonalize(h, ref, w, need, s))
+    return y
+
+
+# ----------------------------------------------- log probabilities of tokens --
+
+# Per row of logits (None where not asked for): log probability of the row's
+# token, entropy, log of the sum of exponentials, and the best alternatives.
+TokenLogprobs = collections.namedtuple("TokenLogprobs",
+                                       "logprobs entropy lse top_logprobs top_ids")
+
+
+def _logprobs_args(logits, tokens):
+    import torch
+    if not isinstance(logits, torch.Tensor):
+        raise ValueError("logits must be a CUDA tensor")
+    _on_cuda(logits, logits=logits)
+    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    if logits.dtype not in codes:
+        raise TypeError("logits must be float32, float16 or bfloat16, got %s" % logits.dtype)
+    if logits.dim() < 1 or logits.shape[-1] == 0:
+        raise ValueError("logits must have at least one column")
+    rows, ld = _rows(logits, logits.shape[-1], "logits")
+    if tokens is not None:
+        _on_cuda(logits, tokens=tokens)
+        if tokens.dtype != torch.int64:
+            raise TypeError("tokens must be int64, got %s" % tokens.dtype)
+        if tokens.shape != logits.shape[:-1] or not tokens.is_contiguous():
+            raise ValueError("tokens must be contiguous, one for each row of logits")
+    return LogprobsArgs(rows=rows, vocab=logits.shape[-1], dtype=codes[logits.dtype],
+                        logits=logits.data_ptr(), ld=ld, tokens=_ptr(tokens))
+
+
+def token_logprobs(logits, tokens=None, top_k=0):
+    """Log probabilities of `tokens` under rows of logits, in fp32.
+
+    logits: (..., vocab), float32, float16 or bfloat16, contiguous or a
+    matrix of contiguous rows (a slice of a padded vocabulary).  tokens:
+    int64 (...), or None; a negative one marks a position that does not
+    count (log probability 0).  top_k: how many of the best columns to
+    return, at most 64, equal ones by the lowest column.
+
+    Returns :class:`TokenLogprobs`: logprobs, entropy and lse of shape (...),
+    top_logprobs and top_ids (int64) of shape (..., top_k).  -inf masks a
+    column; a row of only masked columns has entropy 0, one with NaN or +inf
+    has NaN.
+    """
+    import torch
+    a = _logprobs_args(logits, tokens)
+    if not 0 <= top_k <= min(MAX_TOP_K, a.vocab):
+        raise ValueError("top_k must be in [0, min(%d, columns)]" % MAX_TOP_K)
+    a.top_k = top_k
+    shape, dev = logits.shape[:-1], logits.device
+    out = torch.empty((2 if tokens is None else 3,) + tuple(shape), dtype=torch.float32, device=dev)
+    lse, entropy = out[0], out[1]
+    logprobs = out[2] if tokens is not None else None
+    top_lp = top_ids = None
+    if top_k:
+        top_lp = torch.empty(tuple(shape) + (top_k,), dtype=torch.float32, device=dev)
+        top_ids = torch.empty(tuple(shape) + (top_k,), dtype=torch.int64, device=dev)
+    a.logprobs, a.entropy, a.lse, a.top_logprobs, a.top_ids = map(
+        _ptr, (logprobs, entropy, lse, top_lp, top_ids))
+    if a.rows:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _check(_lib().gemm_token_logprobs(_handle(dev, stream), ctypes.byref(a), stream),
+               "gemm_token_logprobs")
+    return TokenLogprobs(logprobs, entropy, lse, top_lp, top_ids)
+
+
+def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=None, out=None):
+    """Gradient of the logits from those of the log probabilities and the
+    entropies (float32, one for each row; None: zero).
+
+    logits, tokens: as given to :func:`token_logprobs`, and `result` what it
+    returned.  out: where to write it (logits itself is allowed); a new
+    contiguous tensor of logits' dtype otherwise.
+    """
+    import torch
+    a = _logprobs_args(logits, tokens)
+    if d_logprobs is not None and tokens is None:
+        raise ValueError("d_logprobs needs tokens")
+    for name, t in (("lse", result.lse), ("entropy", result.entropy), ("d_logprobs", d_logprobs),
+                    ("d_entropy", d_entropy)):
+        if t is None and name.startswith("d_"):
+            continue
+        _on_cuda(logits, **{name: t})
+        if t.dtype != torch.float32 or t.shape != logits.shape[:-1] or not t.is_contiguous():
+            raise ValueError("%s must be contiguous float32, one for each row of logits" % name)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _on_cuda(logits, out=out)
+    if out.dtype != logits.dtype or out.shape != logits.shape:
+        raise ValueError("out must have the logits' shape and dtype")
+    a.ldd = _rows(out, a.vocab, "out")[1]
+    a.lse, a.entropy, a.d_logprobs, a.d_entropy, a.d_logits = map(
+        _ptr, (result.lse, result.entropy, d_logprobs, d_entropy, out))
+    if a.rows:
+        dev = logits.device
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _check(_lib().gemm_token_logprobs_backward(_handle(dev, stream), ctypes.byref(a), stream),
+               "gemm_token_logprobs_backward")
+    return out
