@@ -16,6 +16,11 @@
 //               same output columns, so act(gate) * up needs no other tile.
 //               With a pair, the even CTA copies the gate rows and the odd
 //               one the up rows.
+//   split K     a product of few tiles gives each tile to a cluster of 2 or 4
+//               single CTAs, each with a share of K.  They stage their fp32
+//               partials in their idle rings, and each CTA then sums its own
+//               quarter (or half) of the tile's rows over the cluster, in CTA
+//               order, and stores it: the epilogue is shared out as well.
 //   last wave   stream-K with any number of walkers per tile: the walker
 //               holding a tile's first K slices owns it, the others publish
 //               fp32 partials (each at most one, in a slot of its own, as its
@@ -66,12 +71,28 @@ struct BlockUnit {
 struct BlockIter {
   int u;
   int64_t it, end;
+  int split;  // this CTA's share of a split tile, not yet taken; -1: none
   __device__ BlockIter(int walker, const BlockParams& p) : u(walker) {
+    split = p.splits > 1 ? walker % p.splits : -1;
+    if (p.splits > 1) {
+      u = walker / p.splits;
+      it = end = 0;
+      return;
+    }
     const int64_t total = static_cast<int64_t>(p.sk_tiles) * p.k_blocks;
     it = total * walker / p.walkers;
     end = total * (walker + 1) / p.walkers;
   }
   __device__ bool next(const BlockParams& p, BlockUnit& x) {
+    if (p.splits > 1) {
+      if (split < 0) return false;
+      x.tile = u;
+      x.k0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * split / p.splits);
+      x.k1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (split + 1) / p.splits);
+      x.role = kWhole;
+      split = -1;
+      return true;
+    }
     if (it < end) {
       x.tile = static_cast<int>(it / p.k_blocks);
       x.k0 = static_cast<int>(it - static_cast<int64_t>(x.tile) * p.k_blocks);
@@ -103,21 +124,26 @@ __device__ __forceinline__ int block_contributors(int walker, const BlockUnit& x
   return n;
 }
 
-// One 32-row x 64-column block of a 16-bit output, as 32 words per lane
-// (lane = row): through the warp's staging buffer (already free) in the
-// layout of a 128-byte-swizzled box and out with one bulk store, or row by
-// row where the output's rows are not 16-byte aligned.  `cols` bounds the
-// columns written, for an output whose neighbour follows directly.
-__device__ __forceinline__ void block_store(const uint32_t (&w)[32], const BlockParams& p,
-                                            const BlockOut& o, const CUtensorMap& map, uint8_t* sb,
-                                            int lane, int row0, int col0, int z, int cols) {
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t off = lane * 128u + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4);
-    *reinterpret_cast<uint4*>(sb + off) =
-        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  }
+// The epilogue works on 16 columns at a time (lane = row) in rolled loops: a
+// launch of a small product runs its epilogue once, on a cold instruction
+// cache, and straight-line code for 64 columns took two to three times as
+// long there as a loop whose later turns find their instructions.
+//
+// A 32-row x 64-column block of a 16-bit output goes through the warp's
+// staging buffer (already free) in the layout of a 128-byte-swizzled box.
+// stage16: columns [16 c, 16 c + 16) of the block, as 8 words of this row.
+__device__ __forceinline__ void stage16(uint8_t* sb, int lane, int c, const uint32_t (&w)[8]) {
+  uint8_t* row = sb + lane * 128u;
+  const uint32_t sw = lane & 7u, j = 2u * static_cast<uint32_t>(c);
+  *reinterpret_cast<uint4*>(row + ((j ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(row + (((j + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// The staged block, out with one bulk store, or row by row where the
+// output's rows are not 16-byte aligned (columns below `cols`).
+__device__ __forceinline__ void block_store(const BlockParams& p, const BlockOut& o,
+                                            const CUtensorMap& map, uint8_t* sb, int lane, int row0,
+                                            int col0, int z, int cols) {
   if (o.tma) {
     ptx::fence_proxy_async_smem();
     __syncwarp();
@@ -146,62 +172,69 @@ __device__ __forceinline__ void block_store(const uint32_t (&w)[32], const Block
   __syncwarp();
 }
 
-// The block's transpose, into the same output: column j of the block is 32
-// consecutive elements of row col0 + j.  Neighbouring lanes first exchange
-// words, so that each lane stores two rows' worth of one column at once.
-__device__ __forceinline__ void block_store_mirror(const uint32_t (&w)[32], const BlockParams& p,
-                                                   const BlockOut& o, int lane, int row0, int col0,
-                                                   int z) {
-  uint16_t* base = static_cast<uint16_t*>(o.ptr) + z * o.batch;
+// 16 columns of the block transposed, into the same output: a column is 32
+// consecutive elements of row col0 + column.  Neighbouring lanes first
+// exchange words, so that each lane stores two rows' worth of one column.
+__device__ __forceinline__ void mirror16(const uint32_t (&w)[8], const BlockParams& p,
+                                         const BlockOut& o, int lane, int row0, int col0, int z) {
   const bool odd = lane & 1;
   const int r = row0 + (lane & ~1);  // this lane's pair of source rows
+  uint16_t* dst = static_cast<uint16_t*>(o.ptr) + z * o.batch +
+                  static_cast<int64_t>(col0 + (odd ? 1 : 0)) * o.ld + r;
+  const int n = p.N - col0 - (odd ? 1 : 0);  // columns that exist from this lane's first
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
+  for (int j = 0; j < 8; ++j) {
     // w[j]: columns 2j, 2j + 1 of this row.  The even lane keeps column 2j
     // and takes its neighbour's; the odd lane column 2j + 1.
     const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
     const uint32_t pair = odd ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
-    const int c = col0 + 2 * j + (odd ? 1 : 0);
-    if (c < p.N) {
-      uint16_t* dst = base + static_cast<int64_t>(c) * o.ld + r;
+    if (2 * j < n) {
       if (r + 1 < p.M)
         *reinterpret_cast<uint32_t*>(dst) = pair;  // r is even and the pitch a multiple of 8
       else if (r < p.M)
         *dst = static_cast<uint16_t>(pair);
     }
+    dst += 2 * o.ld;
   }
 }
 
-// 32 accumulator columns at TMEM column `col`, with the contributors'
-// partials added in order.
-__device__ __forceinline__ void block_acc(uint32_t t_addr, uint32_t (&r)[32], const float* partial,
-                                          size_t partial_step, int parts, int col, int lane) {
-  ptx::tmem_ld_32x32b_x32(t_addr + col, r);
-  ptx::tmem_wait_ld();
-  for (int n = 0; n < parts; ++n) {
-    const float* src = partial + n * partial_step + static_cast<size_t>(col) * 32 + lane;
+// Adds the contributors' partials to a tile's accumulator in TMEM, in order.
+__device__ __forceinline__ void block_add_partials(uint32_t t_row, const float* partial,
+                                                   size_t partial_step, int parts, int columns,
+                                                   int lane) {
+#pragma unroll 1
+  for (int c = 0; c < columns; c += 32) {
+    uint32_t r[32];
+    ptx::tmem_ld_32x32b_x32(t_row + c, r);
+    ptx::tmem_wait_ld();
+    const float* src = partial + static_cast<size_t>(c) * 32 + lane;
+#pragma unroll 1
+    for (int n = 0; n < parts; ++n, src += partial_step)
 #pragma unroll
-    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __ldcg(src + j * 32));
+      for (int j = 0; j < 32; ++j)
+        r[j] = __float_as_uint(__uint_as_float(r[j]) + __ldcg(src + j * 32));
+    ptx::tmem_st_32x32b_x32(t_row + c, r);
   }
+  ptx::tmem_wait_st();
 }
 
-// act(gate) * up of 32 columns, packed two to a word; gate and up are also
-// kept in fp32 where the caller asks for them.
+// act(gate) * up of 16 columns, packed two to a word.
 template <int ACT>
-__device__ __forceinline__ void gated32(const uint32_t (&g)[32], const uint32_t (&u)[32],
-                                        uint32_t* pk, bool bf16) {
+__device__ __forceinline__ void gated16(const uint32_t (&g)[16], const uint32_t (&u)[16],
+                                        uint32_t (&pk)[8], bool bf16) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int j = 0; j < 8; ++j)
     pk[j] = pack2(gate_act<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
                   gate_act<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]), bf16);
 }
 
+// dGate and dUp of 16 columns.
 template <int ACT>
-__device__ __forceinline__ void gated_bwd32(const uint32_t (&dh)[32], const float (&g)[32],
-                                            const float (&u)[32], uint32_t* pg, uint32_t* pu,
-                                            bool bf16) {
+__device__ __forceinline__ void gated_bwd16(const uint32_t (&dh)[16], const float (&g)[16],
+                                            const float (&u)[16], uint32_t (&pg)[8],
+                                            uint32_t (&pu)[8], bool bf16) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 8; ++j) {
     float dg[2], du[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -303,6 +336,15 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       return nb * kOutN + (CG == 2 && rank == 1 ? p.gate_rows : 0);
     else
       return nb * BN + static_cast<int>(rank) * kBRows;
+  };
+
+  // Split K: the two points at which all warps of the cluster meet (partials
+  // staged; partials read).  Every warp passes both, whatever its role met.
+  auto split_syncs = [&]() {
+    if (CG == 1 && p.splits > 1) {
+      ptx::cluster_sync();
+      ptx::cluster_sync();
+    }
   };
 
   if (warp == 0) {
@@ -419,6 +461,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       }
     }
     __syncwarp();
+    split_syncs();
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer --
     if (lane == 0 && leader) {
@@ -478,6 +521,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       wait_bounded(done_bar, 0, p, kDetailMmaDrain);
     }
     __syncwarp();
+    split_syncs();
   } else {
     // --------------------------------------------------------- epilogue --
     ptx::pdl_wait_prior_grid();
@@ -490,8 +534,213 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     int buf = 0;
     const bool bf16_out = p.out_bf16 != 0;
     constexpr size_t kPartial = block_partial_bytes(CG) / 4;  // floats of a CTA's partial
+    // beta D: one chunk into staging buffer b.
+    auto load_d = [&](int b, int row0, int col, int z) {
+      if (lane == 0) {
+        ptx::bulk_wait_group_read<0>();  // the buffer's last store has been read out
+        ptx::fence_proxy_async_smem();   // (by the warp itself, where rows are stored one by one)
+        ptx::mbar_arrive_expect_tx(d_bar(ew, b), kStoreBuf);
+        ptx::tma_load_3d(ptx::smem_addr(my_stage + b * kStoreBuf), &maps.d, col, row0, z,
+                         d_bar(ew, b));
+      }
+    };
+    auto wait_d = [&]() { return wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy); };
+
+    // 32 rows x 64 output columns from column n0 + cc: acc(c, r) gives the 16
+    // accumulator columns from tile column c for this lane's row.  more: the
+    // next chunk of these rows follows (its D is fetched meanwhile).
+    auto chunk = [&](auto&& acc_cols, int row0, int n0, int cc, int z, bool more) -> bool {
+      const int col0 = n0 + cc;
+      uint8_t* sb = my_stage + buf * kStoreBuf;
+      if constexpr (kEpi == kEpiGated) {
+        if (lane == 0) ptx::bulk_wait_group_read<1>();
+        __syncwarp();
+        float* dst = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0) * 32 + lane;
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+          uint32_t g[16], u[16], pk[8];
+          acc_cols(cc + 16 * s, g);
+          acc_cols(BN / 2 + cc + 16 * s, u);
+          if (p.pre != nullptr) {
+            const int n = p.N - (col0 + 16 * s);  // columns that exist
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j < n) {
+                __stcs(dst + j * 32, __uint_as_float(g[j]));
+                __stcs(dst + p.pre_half + j * 32, __uint_as_float(u[j]));
+              }
+            dst += 16 * 32;
+          }
+          if (p.act == kActSilu)
+            gated16<kActSilu>(g, u, pk, bf16_out);
+          else if (p.act == kActGelu)
+            gated16<kActGelu>(g, u, pk, bf16_out);
+          else
+            gated16<kActRelu>(g, u, pk, bf16_out);
+          stage16(sb, lane, s, pk);
+        }
+        block_store(p, p.out0, maps.c0, sb, lane, row0, col0, z, p.N);
+        buf ^= 1;
+      } else if constexpr (kEpi == kEpiGatedBwd) {
+        if (lane == 0) ptx::bulk_wait_group_read<0>();
+        __syncwarp();
+        const float* src = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0) * 32 + lane;
+        const int n = p.N - col0;
+        float g[2][16], u[2][16];  // this step's and the next one's
+        auto load_pre = [&](int s, float (&gs)[16], float (&us)[16]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const bool in = 16 * s + j < n;
+            gs[j] = in ? __ldcs(src + (16 * s + j) * 32) : 0.0f;
+            us[j] = in ? __ldcs(src + p.pre_half + (16 * s + j) * 32) : 0.0f;
+          }
+        };
+        auto step = [&](int s, const float (&gs)[16], const float (&us)[16]) {
+          uint32_t dh[16], pg[8], pu[8];
+          acc_cols(cc + 16 * s, dh);
+          if (p.act == kActSilu)
+            gated_bwd16<kActSilu>(dh, gs, us, pg, pu, bf16_out);
+          else if (p.act == kActGelu)
+            gated_bwd16<kActGelu>(dh, gs, us, pg, pu, bf16_out);
+          else
+            gated_bwd16<kActRelu>(dh, gs, us, pg, pu, bf16_out);
+          stage16(my_stage, lane, s, pg);
+          stage16(my_stage + kStoreBuf, lane, s, pu);
+        };
+        load_pre(0, g[0], u[0]);
+#pragma unroll 1
+        for (int s = 0; s < 4; s += 2) {
+          load_pre(s + 1, g[1], u[1]);
+          step(s, g[0], u[0]);
+          if (s + 2 < 4) load_pre(s + 2, g[0], u[0]);
+          step(s + 1, g[1], u[1]);
+        }
+        block_store(p, p.out0, maps.c0, my_stage, lane, row0, col0, z, p.N);
+        block_store(p, p.out1, maps.c1, my_stage + kStoreBuf, lane, row0, col0, z, p.N);
+      } else {
+        if (p.use_d) {
+          const bool got = wait_d();
+          d_phase ^= 1u << buf;
+          if (!__all_sync(0xffffffffu, got)) return false;
+          if (more) load_d(buf ^ 1, row0, col0 + 64, z);
+        } else {
+          if (lane == 0) ptx::bulk_wait_group_read<1>();
+          __syncwarp();
+        }
+        const bool mirror = p.symmetric && row0 / kTileM != col0 / BN;
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+          uint32_t r[16], pk[8];
+          acc_cols(cc + 16 * s, r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(p.alpha * __uint_as_float(r[j]));
+          if (p.use_d) {
+            // D is fp16 (the iterate's type), in the swizzled layout of the box.
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t c = static_cast<uint32_t>(2 * s + j);
+              const uint4 v = *reinterpret_cast<const uint4*>(sb + lane * 128u + ((c ^ (lane & 7u)) << 4));
+              const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&wd[e]));
+                const int i = 8 * j + 2 * e;
+                r[i] = __float_as_uint(fmaf(p.beta, f.x, __uint_as_float(r[i])));
+                r[i + 1] = __float_as_uint(fmaf(p.beta, f.y, __uint_as_float(r[i + 1])));
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            pk[j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), bf16_out);
+          if (mirror) mirror16(pk, p, p.out0, lane, row0, col0 + 16 * s, z);
+          stage16(sb, lane, s, pk);
+        }
+        block_store(p, p.out0, maps.c0, sb, lane, row0, col0, z, p.N);
+        buf ^= 1;
+      }
+      return true;
+    };
+
     BlockIter it(walker, p);
     BlockUnit x;
+    if (CG == 1 && p.splits > 1) {
+      // ------------------------------------------ a share of a split tile --
+      const int part = walker % p.splits;
+      it.next(p, x);
+      const BlockTile t = block_tile(x.tile, p);
+      const int n0 = t.nb * kOutN;
+      // This CTA's rows of the tile, in blocks of 32, and of those the
+      // chunks that exist: (block, chunk) units, taken by the warps in turn.
+      const int row_blocks = 4 / p.splits;
+      constexpr int kChunks = kOutN / 64;
+      const int first_row = t.mb * kTileM + part * row_blocks * 32;
+      auto unit_exists = [&](int u) {
+        return u < row_blocks * kChunks && first_row + (u / kChunks) * 32 < p.M &&
+               n0 + (u % kChunks) * 64 < p.N;
+      };
+      if (kEpi == kEpiLinear && p.use_d && unit_exists(ew))
+        load_d(buf, first_row + (ew / kChunks) * 32, n0 + (ew % kChunks) * 64, t.z);
+      float* own = reinterpret_cast<float*>(smem);  // [column][row of the tile]
+      int ok = SPGEMM_OUT_OF_BOUNDS(kSplitBytes <= ring_bytes, p, kCheckFixup) ? 0 : 1;
+      if (lane == 0 && ok) ok = wait_bounded<true>(tfull_bar(0), 0, p, kDetailEpiFull) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok) {
+        // The accumulator is full, so every copy into the ring has been
+        // consumed and the ring is free.
+        ptx::tc_fence_after_sync();
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(t_row + c, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) own[(c + j) * kBM + q * 32 + lane] = __uint_as_float(v[j]);
+        }
+      }
+      ptx::cluster_sync();  // all partials are staged
+      if (first_row < p.M) {
+        // Sum the shares of this CTA's rows, four rows of a column at a time,
+        // into its own partial (which no other CTA reads there).
+        const int log_quads = p.splits == 2 ? 4 : 3;  // float4s of a column
+        const int total = BN << log_quads;
+        uint32_t peer[kMaxSplits];
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+          peer[s] = ptx::map_shared_rank(sbase, static_cast<uint32_t>(s < p.splits ? s : 0));
+#pragma unroll 4
+        for (int i = threadIdx.x - 64; i < total; i += 128) {
+          const uint32_t off =
+              static_cast<uint32_t>(i >> log_quads) * (kBM * 4u) +
+              static_cast<uint32_t>((part << log_quads) + (i & ((1 << log_quads) - 1))) * 16u;
+          float4 v[kMaxSplits];
+#pragma unroll
+          for (int s = 0; s < kMaxSplits; ++s)
+            if (s < p.splits) v[s] = ptx::ld_cluster_f32x4(peer[s] + off);
+          float4 sum = v[0];
+#pragma unroll
+          for (int s = 1; s < kMaxSplits; ++s)
+            if (s < p.splits) {
+              sum.x += v[s].x;
+              sum.y += v[s].y;
+              sum.z += v[s].z;
+              sum.w += v[s].w;
+            }
+          *reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(own) + off) = sum;
+        }
+      }
+      ptx::named_barrier_sync(1, 128);  // the epilogue warps
+      for (int u = ew; unit_exists(u); u += 4) {
+        const int rb = part * row_blocks + u / kChunks;
+        auto from_smem = [&](int c, uint32_t (&r)[16]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(own[(c + j) * kBM + rb * 32 + lane]);
+        };
+        if (!chunk(from_smem, t.mb * kTileM + rb * 32, n0, (u % kChunks) * 64, t.z, false)) break;
+      }
+      ptx::cluster_sync();  // no CTA leaves while another reads its partial
+    } else
     while (it.next(p, x)) {
       const BlockTile t = block_tile(x.tile, p);
       const int row0 = t.mb * kTileM + static_cast<int>(rank) * kBM + q * 32;
@@ -503,25 +752,21 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           SPGEMM_OUT_OF_BOUNDS(x.role == kWhole || (p.sk_ws != nullptr && p.sk_flags != nullptr), p,
                                kCheckPartial))
         break;
-      // beta D: the tile's first chunk, fetched while the accumulator fills.
-      auto load_d = [&](int b, int col) {
-        if (lane == 0) {
-          ptx::bulk_wait_group_read<0>();  // the buffer's last store has been read out
-          ptx::fence_proxy_async_smem();   // (by the warp itself, where rows are stored one by one)
-          ptx::mbar_arrive_expect_tx(d_bar(ew, b), kStoreBuf);
-          ptx::tma_load_3d(ptx::smem_addr(my_stage + b * kStoreBuf), &maps.d, col, row0, t.z,
-                           d_bar(ew, b));
-        }
-      };
-      if (kEpi == kEpiLinear && p.use_d && stores) load_d(buf, n0);
+      // The tile's first chunk of D arrives while the accumulator fills.
+      const bool d_first = kEpi == kEpiLinear && p.use_d && stores;
+      if (d_first) load_d(buf, row0, n0, t.z);
+      // The kept projections of these rows, a contiguous run each, into L2.
+      if (kEpi == kEpiGatedBwd && stores && lane < 2) {
+        const uint32_t n = static_cast<uint32_t>(min(BN, p.N - n0));
+        ptx::bulk_prefetch_l2(p.pre + lane * p.pre_half + (static_cast<int64_t>(row0 / 32) * p.N + n0) * 32,
+                              n * 128u);
+      }
 
       int ready = 1;
       if (lane == 0) ready = wait_bounded<true>(tfull_bar(acc), acc_phase, p, kDetailEpiFull) ? 1 : 0;
       ready = __shfl_sync(0xffffffffu, ready, 0);
       if (!ready) {
-        // A copy of D still in flight lands before this warp's memory goes.
-        if (kEpi == kEpiLinear && p.use_d && stores)
-          wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy);
+        if (d_first) wait_d();  // a copy in flight lands before this warp's memory goes
         break;
       }
       ptx::tc_fence_after_sync();
@@ -549,9 +794,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
         // Partials of the walkers after this one.
         int parts = 0;
         const float* partial = nullptr;
+        const int slot = (walker + 1) * CG + static_cast<int>(rank);
         if (x.role == kOwner) {
           parts = block_contributors(walker, x, p);
-          const int slot = (walker + 1) * CG + static_cast<int>(rank);
           partial = p.sk_ws + slot * kPartial + static_cast<size_t>(ew) * BN * 32;
           int ok = 1;
           if (lane == 0)
@@ -559,119 +804,24 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
               ok = wait_flag(p.sk_flags + (slot + n * CG) * 4 + ew, p, kDetailSkFlag) ? 1 : 0;
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) {
-            if (kEpi == kEpiLinear && p.use_d)
-              wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy);
+            if (d_first) wait_d();
             break;
           }
           for (int n = 0; n < parts; ++n)  // every lane acquires the partials
             (void)ld_acquire_gpu(p.sk_flags + (slot + n * CG) * 4 + ew);
         }
-        constexpr size_t step = kPartial * CG;
-
-        bool failed = false;
+        if (parts > 0) block_add_partials(t_row, partial, kPartial * CG, parts, BN, lane);
+        auto from_tmem = [&](int c, uint32_t (&r)[16]) {
+          ptx::tmem_ld_32x32b_x16(t_row + c, r);
+          ptx::tmem_wait_ld();
+        };
+        bool ok = true;
 #pragma unroll 1
-        for (int cc = 0; cc < kOutN; cc += 64) {
-          const int col0 = n0 + cc;
-          if (col0 >= p.N) break;
-          uint32_t pk[32];
-          if constexpr (kEpi == kEpiGated) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t g[32], u[32];
-              block_acc(t_row, g, partial, step, parts, cc + 32 * h, lane);
-              block_acc(t_row, u, partial, step, parts, BN / 2 + cc + 32 * h, lane);
-              if (p.pre != nullptr) {
-                float* dst = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0 + 32 * h) * 32 + lane;
-                const int n = p.N - (col0 + 32 * h);  // columns that exist
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (j < n) {
-                    __stcs(dst + j * 32, __uint_as_float(g[j]));
-                    __stcs(dst + p.pre_half + j * 32, __uint_as_float(u[j]));
-                  }
-              }
-              if (p.act == kActSilu)
-                gated32<kActSilu>(g, u, pk + 16 * h, bf16_out);
-              else if (p.act == kActGelu)
-                gated32<kActGelu>(g, u, pk + 16 * h, bf16_out);
-              else
-                gated32<kActRelu>(g, u, pk + 16 * h, bf16_out);
-            }
-            if (lane == 0) ptx::bulk_wait_group_read<1>();
-            block_store(pk, p, p.out0, maps.c0, my_stage + buf * kStoreBuf, lane, row0, col0, t.z, p.N);
-            buf ^= 1;
-          } else if constexpr (kEpi == kEpiGatedBwd) {
-            uint32_t pu[32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float* src = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0 + 32 * h) * 32 + lane;
-              const int n = p.N - (col0 + 32 * h);
-              float g[32], u[32];
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                g[j] = j < n ? __ldcs(src + j * 32) : 0.0f;
-                u[j] = j < n ? __ldcs(src + p.pre_half + j * 32) : 0.0f;
-              }
-              uint32_t dh[32];
-              block_acc(t_row, dh, partial, step, parts, cc + 32 * h, lane);
-              if (p.act == kActSilu)
-                gated_bwd32<kActSilu>(dh, g, u, pk + 16 * h, pu + 16 * h, bf16_out);
-              else if (p.act == kActGelu)
-                gated_bwd32<kActGelu>(dh, g, u, pk + 16 * h, pu + 16 * h, bf16_out);
-              else
-                gated_bwd32<kActRelu>(dh, g, u, pk + 16 * h, pu + 16 * h, bf16_out);
-            }
-            if (lane == 0) ptx::bulk_wait_group_read<0>();
-            block_store(pk, p, p.out0, maps.c0, my_stage, lane, row0, col0, t.z, p.N);
-            block_store(pu, p, p.out1, maps.c1, my_stage + kStoreBuf, lane, row0, col0, t.z, p.N);
-          } else {
-            uint8_t* sb = my_stage + buf * kStoreBuf;
-            const bool more = cc + 64 < kOutN && col0 + 64 < p.N;
-            if (p.use_d) {
-              if (!wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy)) failed = true;
-              d_phase ^= 1u << buf;
-              if (__any_sync(0xffffffffu, failed)) {
-                failed = true;
-                break;
-              }
-              if (more) load_d(buf ^ 1, col0 + 64);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[32];
-              block_acc(t_row, r, partial, step, parts, cc + 32 * h, lane);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(p.alpha * __uint_as_float(r[j]));
-              if (p.use_d) {
-                // D is fp16 (the iterate's type), in the swizzled layout of the box.
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint32_t c = static_cast<uint32_t>(4 * h + j);
-                  const uint4 v = *reinterpret_cast<const uint4*>(sb + lane * 128u + ((c ^ (lane & 7u)) << 4));
-                  const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&wd[e]));
-                    const int i = 8 * j + 2 * e;
-                    r[i] = __float_as_uint(fmaf(p.beta, f.x, __uint_as_float(r[i])));
-                    r[i + 1] = __float_as_uint(fmaf(p.beta, f.y, __uint_as_float(r[i + 1])));
-                  }
-                }
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                pk[16 * h + j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), bf16_out);
-            }
-            if (p.symmetric && t.mb != t.nb) block_store_mirror(pk, p, p.out0, lane, row0, col0, t.z);
-            if (!p.use_d && lane == 0) ptx::bulk_wait_group_read<1>();
-            block_store(pk, p, p.out0, maps.c0, sb, lane, row0, col0, t.z, p.N);
-            buf ^= 1;
-          }
-        }
-        if (failed) break;
+        for (int cc = 0; ok && cc < kOutN && n0 + cc < p.N; cc += 64)
+          ok = chunk(from_tmem, row0, n0, cc, t.z, cc + 64 < kOutN && n0 + cc + 64 < p.N);
+        if (!ok) break;
         if (x.role == kOwner) {
           __syncwarp();  // every lane has read the partials
-          const int slot = (walker + 1) * CG + static_cast<int>(rank);
           if (lane == 0)
             for (int n = 0; n < parts; ++n) p.sk_flags[(slot + n * CG) * 4 + ew] = 0;
         }
@@ -713,7 +863,7 @@ cudaError_t block_set_smem(size_t smem) {
   return e;
 }
 
-// `grid` CTAs in clusters of `cg`; the launch may overlap the previous
+// `grid` CTAs, in clusters of a pair or of a tile's K splits; the launch may overlap the previous
 // kernel's tail (programmatic dependent launch).
 template <bool kAT, bool kBN, int kEpi>
 cudaError_t block_launch(const BlockMaps& m, const BlockParams& p, int cg, int grid, size_t smem,
@@ -727,11 +877,12 @@ cudaError_t block_launch(const BlockMaps& m, const BlockParams& p, int cg, int g
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  const int cluster = cg == 2 ? 2 : p.splits;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cg == 2 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cg == 2 ? cudaLaunchKernelEx(&cfg, block_kernel<2, kAT, kBN, kEpi>, m, p)
                  : cudaLaunchKernelEx(&cfg, block_kernel<1, kAT, kBN, kEpi>, m, p);
 }

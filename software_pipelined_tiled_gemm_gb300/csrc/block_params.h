@@ -37,6 +37,7 @@ struct BlockParams : Params {
   int tiles_per;       // tiles of one matrix of the batch
   int batch;
   int walkers;         // CTAs, or CTA pairs
+  int splits;          // > 1: each tile's K is split over a cluster of this many single CTAs
   int symmetric;       // 1: only tiles on and above the diagonal run; each off-diagonal one is
                        // also written transposed (square output)
   int out_bf16;        // type of the 16-bit output(s)
@@ -66,6 +67,10 @@ __host__ __device__ constexpr int block_sub(int cg) { return cg == 2 ? 2 : 1; }
 __host__ __device__ constexpr size_t block_partial_bytes(int cg) {
   return static_cast<size_t>(kBM) * block_bn(cg) * 4;
 }
+
+// A split tile's fp32 partial, staged in the CTA's idle ring.
+constexpr uint32_t kSplitBytes = kBM * kSoloBN * 4u;
+constexpr int kMaxSplits = 4;
 
 constexpr int kBlockThreads = kernel_threads(1);
 

@@ -130,32 +130,54 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
     *tn = ceil_div(pr.N, gated ? block_bn(cg) / 2 : block_bn(cg));
     return (pr.symmetric ? *tn * (*tn + 1) / 2 : *tm * *tn) * pr.batch;
   };
-  // A pair's 256 x 256 tile moves half the operand bytes per product of a
-  // single CTA's 128 x 128, so pairs run wherever each gets at least four
-  // slots of K (512); smaller problems spread over all SMs in small tiles.
-  int64_t tm, tn;
-  int cg = 1;
-  if (pr.M > kBM && ops->pairs > 0) {
-    const int64_t t2 = tiles(2, &tm, &tn);
-    if (t2 * ceil_div(pr.K, kBK * 2) >= 4 * static_cast<int64_t>(ops->pairs)) cg = 2;
+  // The cheapest of three schedules, by a model of their times in us.  A pair
+  // multiplies a 256 x 256 x 128 slot in kPairSlot; a single CTA's 128 x 128
+  // x 64 slot moves twice the operand bytes per product, and with every SM
+  // at it is bound by L2 at kSoloSlot.  Splitting K costs its exchange:
+  // kSplitCost through a cluster's shared memory, kStreamCost through the
+  // workspace.
+  constexpr double kPairSlot = 0.55, kSoloSlot = 0.27, kSplitCost = 1.5, kStreamCost = 5.0;
+  constexpr double kHbmBytesPerUs = 6.5e6;
+  int64_t tm, tn, walkers = 0, sk = 0;
+  int cg = 1, splits = 1;
+  double best = 1e300;
+  auto offer = [&](double cost, int c, int s, int64_t w, int64_t k) {
+    if (cost < best) {
+      best = cost;
+      cg = c;
+      splits = s;
+      walkers = w;
+      sk = k;
+    }
+  };
+  for (int c = 1; c <= 2; ++c) {
+    if (c == 2 && (pr.M <= kBM || ops->pairs < 1)) break;
+    const int64_t most = c == 2 ? ops->pairs : ops->sm_count;
+    const int64_t nt = tiles(c, &tm, &tn);
+    const int64_t kb = ceil_div(pr.K, static_cast<int64_t>(kBK) * block_sub(c));
+    const double slot = c == 2 ? kPairSlot : kSoloSlot;
+    offer(ceil_div(nt, most) * kb * slot, c, 1, std::min(nt, most), 0);
+    // Stream-K: the last one to two waves' slots shared out evenly.  The
+    // walkers are then at different places along K, so operands beyond L2
+    // are read from HBM once per tile instead of once per wave.
+    const int64_t shared = nt < most ? nt : nt % most + most;
+    if (nt % most != 0 && nt * kb >= 2 * most) {
+      double cost = static_cast<double>(nt) * kb / most * slot + kStreamCost;
+      const double operands = 2.0 * (pr.M + pr.N * (gated ? 2 : 1)) * pr.K * pr.batch;
+      if (operands > 0.75 * ops->l2_bytes && pr.M > kBM) {
+        const double reads = 2.0 * shared * (kBM * c + block_bn(c)) * pr.K / kHbmBytesPerUs;
+        cost += std::max(0.0, reads - static_cast<double>(shared) * kb / most * slot);
+      }
+      offer(cost, c, 1, most, shared);
+    }
+    if (c == 1)
+      for (int s = 2; s <= kMaxSplits; s *= 2)
+        if (nt * s <= most && kb >= 2 * s)
+          offer(ceil_div(kb, s) * slot + kSplitCost, c, s, nt * s, 0);
   }
   const int64_t nt = tiles(cg, &tm, &tn);
   const int64_t kb = ceil_div(pr.K, static_cast<int64_t>(kBK) * block_sub(cg));
   if (nt > kOpsMaxDim) return ops_fail(GEMM_ERR_INVALID_ARG, "too many output tiles");
-  const int64_t most = cg == 2 ? ops->pairs : ops->sm_count;
-
-  // K slots are shared out evenly (stream-K) in the last one to two waves of
-  // tiles; fewer tiles than walkers are all shared, as long as each walker
-  // gets at least kMinShare slots.
-  constexpr int64_t kMinShare = 4;
-  int64_t walkers, sk;
-  if (nt >= most) {
-    walkers = most;
-    sk = nt % most == 0 || kb < kMinShare ? 0 : nt % most + most;
-  } else {
-    walkers = std::max(nt, std::min(most, nt * kb / kMinShare));
-    sk = walkers > nt ? nt : 0;
-  }
 
   const int a_rows = a_t || cg == 2 || pr.M > 64 ? kBM : static_cast<int>(round8(pr.M));
   int stages = kMaxStages;
@@ -175,6 +197,7 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.stages = stages;
   p.raster_group = cg == 2 ? 8 : 16;
   p.walkers = static_cast<int>(walkers);
+  p.splits = splits;
   p.sk_tiles = static_cast<int>(sk);
   p.dp_tiles = static_cast<int>(nt - sk);
   p.sk_ws = partials;
