@@ -17,10 +17,12 @@
 //               With a pair, the even CTA copies the gate rows and the odd
 //               one the up rows.
 //   split K     a product of few tiles gives each tile to a cluster of 2 or 4
-//               single CTAs, each with a share of K.  They stage their fp32
-//               partials in their idle rings, and each CTA then sums its own
-//               quarter (or half) of the tile's rows over the cluster, in CTA
-//               order, and stores it: the epilogue is shared out as well.
+//               single CTAs, each with a share of K.  Once a CTA's own
+//               products are done its ring is idle: it stages its fp32
+//               partial there, bulk-copies each CTA of the cluster the rows
+//               that one will store (a quarter or half of the tile), and adds
+//               what it receives itself in CTA order while it stores its
+//               rows: the epilogue is shared out as well.
 //   last wave   stream-K with any number of walkers per tile: the walker
 //               holding a tile's first K slices owns it, the others publish
 //               fp32 partials (each at most one, in a slot of its own, as its
@@ -139,21 +141,19 @@ __device__ __forceinline__ void stage16(uint8_t* sb, int lane, int c, const uint
   *reinterpret_cast<uint4*>(row + (((j + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// The staged block, out with one bulk store, or row by row where the
-// output's rows are not 16-byte aligned (columns below `cols`).
+// The staged block (visible to the warp and the copy engine), out with one
+// bulk store, or row by row where the output's rows are not 16-byte aligned
+// (columns below `cols`).
 __device__ __forceinline__ void block_store(const BlockParams& p, const BlockOut& o,
                                             const CUtensorMap& map, uint8_t* sb, int lane, int row0,
                                             int col0, int z, int cols) {
   if (o.tma) {
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
     if (lane == 0) {
       ptx::tma_store_3d(&map, ptx::smem_addr(sb), col0, row0, z);
       ptx::bulk_commit_group();
     }
     return;
   }
-  __syncwarp();
   const int ncols = min(64, cols - col0);
   const int nrows = min(32, p.M - row0);
   uint16_t* base = static_cast<uint16_t*>(o.ptr) + z * o.batch + static_cast<int64_t>(row0) * o.ld + col0;
@@ -169,7 +169,6 @@ __device__ __forceinline__ void block_store(const BlockParams& p, const BlockOut
       if (cc < ncols) crow[cc] = *reinterpret_cast<const uint16_t*>(sb + off);
     }
   }
-  __syncwarp();
 }
 
 // 16 columns of the block transposed, into the same output: a column is 32
@@ -182,28 +181,37 @@ __device__ __forceinline__ void mirror16(const uint32_t (&w)[8], const BlockPara
   uint16_t* dst = static_cast<uint16_t*>(o.ptr) + z * o.batch +
                   static_cast<int64_t>(col0 + (odd ? 1 : 0)) * o.ld + r;
   const int n = p.N - col0 - (odd ? 1 : 0);  // columns that exist from this lane's first
+  uint32_t pair[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     // w[j]: columns 2j, 2j + 1 of this row.  The even lane keeps column 2j
     // and takes its neighbour's; the odd lane column 2j + 1.
     const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
-    const uint32_t pair = odd ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
+    pair[j] = odd ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
+  }
+  if (row0 + 32 <= p.M && col0 + 16 <= p.N) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)  // r is even and the pitch a multiple of 8
+      *reinterpret_cast<uint32_t*>(dst + 2 * j * o.ld) = pair[j];
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
     if (2 * j < n) {
       if (r + 1 < p.M)
-        *reinterpret_cast<uint32_t*>(dst) = pair;  // r is even and the pitch a multiple of 8
+        *reinterpret_cast<uint32_t*>(dst + 2 * j * o.ld) = pair[j];
       else if (r < p.M)
-        *dst = static_cast<uint16_t>(pair);
+        dst[2 * j * o.ld] = static_cast<uint16_t>(pair[j]);
     }
-    dst += 2 * o.ld;
-  }
 }
 
-// Adds the contributors' partials to a tile's accumulator in TMEM, in order.
+// Adds the contributors' partials to a tile's accumulator in TMEM, in order:
+// columns [c, c + 32) for c = first, first + stride, ...
 __device__ __forceinline__ void block_add_partials(uint32_t t_row, const float* partial,
-                                                   size_t partial_step, int parts, int columns,
-                                                   int lane) {
+                                                   size_t partial_step, int parts, int first,
+                                                   int columns, int stride, int lane) {
 #pragma unroll 1
-  for (int c = 0; c < columns; c += 32) {
+  for (int c = first; c < columns; c += stride) {
     uint32_t r[32];
     ptx::tmem_ld_32x32b_x32(t_row + c, r);
     ptx::tmem_wait_ld();
@@ -251,8 +259,10 @@ __device__ __forceinline__ void gated_bwd16(const uint32_t (&dh)[16], const floa
 
 // CG: 2 for CTA pairs, 1 for single CTAs.  kAT: A stored K x M.  kBN: B
 // stored K x N.  kEpi: the epilogue (kEpiLinear, kEpiGated, kEpiGatedBwd).
-template <int CG, bool kAT, bool kBN, int kEpi>
-__global__ void __launch_bounds__(kBlockThreads, 1)
+// kG: epilogue warps per TMEM lane quarter.  With two, they share the
+// quarter's staging buffers and each takes 32 of a chunk's 64 columns.
+template <int CG, bool kAT, bool kBN, int kEpi, int kG>
+__global__ void __launch_bounds__(kernel_threads(kG), 1)
     block_kernel(const __grid_constant__ BlockMaps maps, const __grid_constant__ BlockParams p) {
   constexpr int BN = block_bn(CG);
   constexpr int kSub = block_sub(CG);
@@ -288,6 +298,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + a); };
   auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + 2 + a); };
   const uint32_t done_bar = bar_base + 8u * (2 * kMaxStages + 4);
+  const uint32_t inbox_bar = bar_base + 8u * (2 * kMaxStages + 13);
   auto d_bar = [&](int e, int b) { return bar_base + 8u * (2 * kMaxStages + 5 + 2 * e + b); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + ring_bytes + staging_bytes +
                                                     8u * (2 * kMaxStages + 5 + 2 * kEpiWarps));
@@ -306,11 +317,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(tfull_bar(a), 1);
-      ptx::mbar_init(tempty_bar(a), 4 * CG);
+      ptx::mbar_init(tempty_bar(a), 4 * kG * CG);
     }
     ptx::mbar_init(done_bar, 1);
     for (int e = 0; e < 4; ++e)
       for (int b = 0; b < 2; ++b) ptx::mbar_init(d_bar(e, b), 1);
+    ptx::mbar_init(inbox_bar, 1);
     ptx::fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -338,8 +350,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       return nb * BN + static_cast<int>(rank) * kBRows;
   };
 
-  // Split K: the two points at which all warps of the cluster meet (partials
-  // staged; partials read).  Every warp passes both, whatever its role met.
+  // Split K: the two points that all warps of the cluster pass, whatever
+  // their role met (rings free; partials received).
   auto split_syncs = [&]() {
     if (CG == 1 && p.splits > 1) {
       ptx::cluster_sync();
@@ -525,8 +537,27 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   } else {
     // --------------------------------------------------------- epilogue --
     ptx::pdl_wait_prior_grid();
-    const int q = warp & 3;
-    const int ew = warp - 2;
+    const int q = warp & 3;         // TMEM lane quarter
+    const int ew = (warp - 2) & 3;  // index of the quarter's staging, partials and flags
+    const int g = (warp - 2) >> 2;  // which of the quarter's warps
+    const bool lead = g == 0 && lane == 0;
+    // Sub-steps of 16 columns of a chunk that this warp takes.
+    constexpr int kSteps = 4 / kG;
+    const int s0 = g * kSteps;
+    auto quarter_sync = [&]() {  // the quarter's warps
+      if constexpr (kG == 2)
+        ptx::named_barrier_sync(2 + q, 64);
+      else
+        __syncwarp();
+    };
+    // Whether every wait of the quarter's warps ended well: they leave a
+    // unit together, or one would wait for the other at their barrier.
+    auto quarter_all = [&](bool ok) -> bool {
+      if constexpr (kG == 2)
+        return ptx::named_barrier_all(2 + q, 64, ok);
+      else
+        return __all_sync(0xffffffffu, ok);
+    };
     uint8_t* my_stage = staging + ew * 2 * kStoreBuf;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -536,7 +567,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     constexpr size_t kPartial = block_partial_bytes(CG) / 4;  // floats of a CTA's partial
     // beta D: one chunk into staging buffer b.
     auto load_d = [&](int b, int row0, int col, int z) {
-      if (lane == 0) {
+      if (lead) {
         ptx::bulk_wait_group_read<0>();  // the buffer's last store has been read out
         ptx::fence_proxy_async_smem();   // (by the warp itself, where rows are stored one by one)
         ptx::mbar_arrive_expect_tx(d_bar(ew, b), kStoreBuf);
@@ -546,6 +577,14 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     };
     auto wait_d = [&]() { return wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy); };
 
+    // The staged block out, once the quarter's warps have written it.
+    auto store = [&](const BlockOut& o, const CUtensorMap& map, uint8_t* sb, int row0, int col0, int z) {
+      if (o.tma) ptx::fence_proxy_async_smem();
+      quarter_sync();
+      if (g == 0) block_store(p, o, map, sb, lane, row0, col0, z, p.N);
+      if (!o.tma) quarter_sync();  // the buffer has been read
+    };
+
     // 32 rows x 64 output columns from column n0 + cc: acc(c, r) gives the 16
     // accumulator columns from tile column c for this lane's row.  more: the
     // next chunk of these rows follows (its D is fetched meanwhile).
@@ -553,40 +592,40 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       const int col0 = n0 + cc;
       uint8_t* sb = my_stage + buf * kStoreBuf;
       if constexpr (kEpi == kEpiGated) {
-        if (lane == 0) ptx::bulk_wait_group_read<1>();
-        __syncwarp();
-        float* dst = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0) * 32 + lane;
+        if (lead) ptx::bulk_wait_group_read<1>();
+        quarter_sync();
+        float* dst = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0 + 16 * s0) * 32 + lane;
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
-          uint32_t g[16], u[16], pk[8];
-          acc_cols(cc + 16 * s, g);
-          acc_cols(BN / 2 + cc + 16 * s, u);
+        for (int s = s0; s < s0 + kSteps; ++s) {
+          uint32_t gate[16], up[16], pk[8];
+          acc_cols(cc + 16 * s, gate);
+          acc_cols(BN / 2 + cc + 16 * s, up);
           if (p.pre != nullptr) {
             const int n = p.N - (col0 + 16 * s);  // columns that exist
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               if (j < n) {
-                __stcs(dst + j * 32, __uint_as_float(g[j]));
-                __stcs(dst + p.pre_half + j * 32, __uint_as_float(u[j]));
+                __stcs(dst + j * 32, __uint_as_float(gate[j]));
+                __stcs(dst + p.pre_half + j * 32, __uint_as_float(up[j]));
               }
             dst += 16 * 32;
           }
           if (p.act == kActSilu)
-            gated16<kActSilu>(g, u, pk, bf16_out);
+            gated16<kActSilu>(gate, up, pk, bf16_out);
           else if (p.act == kActGelu)
-            gated16<kActGelu>(g, u, pk, bf16_out);
+            gated16<kActGelu>(gate, up, pk, bf16_out);
           else
-            gated16<kActRelu>(g, u, pk, bf16_out);
+            gated16<kActRelu>(gate, up, pk, bf16_out);
           stage16(sb, lane, s, pk);
         }
-        block_store(p, p.out0, maps.c0, sb, lane, row0, col0, z, p.N);
+        store(p.out0, maps.c0, sb, row0, col0, z);
         buf ^= 1;
       } else if constexpr (kEpi == kEpiGatedBwd) {
-        if (lane == 0) ptx::bulk_wait_group_read<0>();
-        __syncwarp();
+        if (lead) ptx::bulk_wait_group_read<0>();
+        quarter_sync();
         const float* src = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0) * 32 + lane;
         const int n = p.N - col0;
-        float g[2][16], u[2][16];  // this step's and the next one's
+        float gate[2][16], up[2][16];  // this step's and the next one's
         auto load_pre = [&](int s, float (&gs)[16], float (&us)[16]) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -607,29 +646,29 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           stage16(my_stage, lane, s, pg);
           stage16(my_stage + kStoreBuf, lane, s, pu);
         };
-        load_pre(0, g[0], u[0]);
+        load_pre(s0, gate[0], up[0]);
 #pragma unroll 1
-        for (int s = 0; s < 4; s += 2) {
-          load_pre(s + 1, g[1], u[1]);
-          step(s, g[0], u[0]);
-          if (s + 2 < 4) load_pre(s + 2, g[0], u[0]);
-          step(s + 1, g[1], u[1]);
+        for (int s = s0; s < s0 + kSteps; s += 2) {
+          load_pre(s + 1, gate[1], up[1]);
+          step(s, gate[0], up[0]);
+          if (s + 2 < s0 + kSteps) load_pre(s + 2, gate[0], up[0]);
+          step(s + 1, gate[1], up[1]);
         }
-        block_store(p, p.out0, maps.c0, my_stage, lane, row0, col0, z, p.N);
-        block_store(p, p.out1, maps.c1, my_stage + kStoreBuf, lane, row0, col0, z, p.N);
+        store(p.out0, maps.c0, my_stage, row0, col0, z);
+        store(p.out1, maps.c1, my_stage + kStoreBuf, row0, col0, z);
       } else {
         if (p.use_d) {
           const bool got = wait_d();
           d_phase ^= 1u << buf;
-          if (!__all_sync(0xffffffffu, got)) return false;
+          if (!quarter_all(got)) return false;
           if (more) load_d(buf ^ 1, row0, col0 + 64, z);
         } else {
-          if (lane == 0) ptx::bulk_wait_group_read<1>();
-          __syncwarp();
+          if (lead) ptx::bulk_wait_group_read<1>();
+          quarter_sync();
         }
         const bool mirror = p.symmetric && row0 / kTileM != col0 / BN;
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
+        for (int s = s0; s < s0 + kSteps; ++s) {
           uint32_t r[16], pk[8];
           acc_cols(cc + 16 * s, r);
 #pragma unroll
@@ -656,7 +695,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           if (mirror) mirror16(pk, p, p.out0, lane, row0, col0 + 16 * s, z);
           stage16(sb, lane, s, pk);
         }
-        block_store(p, p.out0, maps.c0, sb, lane, row0, col0, z, p.N);
+        store(p.out0, maps.c0, sb, row0, col0, z);
         buf ^= 1;
       }
       return true;
@@ -681,65 +720,69 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       };
       if (kEpi == kEpiLinear && p.use_d && unit_exists(ew))
         load_d(buf, first_row + (ew / kChunks) * 32, n0 + (ew % kChunks) * 64, t.z);
-      float* own = reinterpret_cast<float*>(smem);  // [column][row of the tile]
-      int ok = SPGEMM_OUT_OF_BOUNDS(kSplitBytes <= ring_bytes, p, kCheckFixup) ? 0 : 1;
+      // The idle ring: this CTA's partial, [quarter][column][row], then what it
+      // receives, [CTA][quarter of this CTA's][column][row].
+      constexpr uint32_t kQuarter = kSplitBytes / 4;
+      const uint32_t inbox = sbase + kSplitBytes;
+      const int expected = [&]() {  // quarters of this CTA's rows that exist
+        int n = 0;
+        for (int i = 0; i < row_blocks; ++i) n += first_row + i * 32 < p.M ? 1 : 0;
+        return n;
+      }();
+      int ok = SPGEMM_OUT_OF_BOUNDS(2 * kSplitBytes <= ring_bytes, p, kCheckFixup) ? 0 : 1;
       if (lane == 0 && ok) ok = wait_bounded<true>(tfull_bar(0), 0, p, kDetailEpiFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (lead && ew == 0 && expected > 0)
+        ptx::mbar_arrive_expect_tx(inbox_bar, static_cast<uint32_t>(expected * p.splits) * kQuarter);
+      __syncwarp();
+      // The accumulator is full, so every copy into the ring has been
+      // consumed: this CTA's ring is free.
+      ptx::cluster_arrive();
+      const uint32_t mine = sbase + static_cast<uint32_t>(q) * kQuarter;
       if (ok) {
-        // The accumulator is full, so every copy into the ring has been
-        // consumed and the ring is free.
         ptx::tc_fence_after_sync();
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        float* own = reinterpret_cast<float*>(smem) + q * (kQuarter / 4);
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
+        for (int c = 32 * g; c < BN; c += 32 * kG) {
           uint32_t v[32];
           ptx::tmem_ld_32x32b_x32(t_row + c, v);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) own[(c + j) * kBM + q * 32 + lane] = __uint_as_float(v[j]);
+          for (int j = 0; j < 32; ++j) own[(c + j) * 32 + lane] = __uint_as_float(v[j]);
         }
+        ptx::fence_proxy_async_smem();
       }
-      ptx::cluster_sync();  // all partials are staged
-      if (first_row < p.M) {
-        // Sum the shares of this CTA's rows, four rows of a column at a time,
-        // into its own partial (which no other CTA reads there).
-        const int log_quads = p.splits == 2 ? 4 : 3;  // float4s of a column
-        const int total = BN << log_quads;
-        uint32_t peer[kMaxSplits];
+      ptx::cluster_wait();  // every ring of the cluster is free
+      if (quarter_all(ok != 0) && lead && t.mb * kTileM + q * 32 < p.M) {
+        const uint32_t to = static_cast<uint32_t>(q / row_blocks);
+        ptx::bulk_copy_to_peer(
+            ptx::map_shared_rank(inbox + static_cast<uint32_t>(part * row_blocks + q % row_blocks) * kQuarter, to),
+            mine, kQuarter, ptx::map_shared_rank(inbox_bar, to));
+      }
+      int got = 1;
+      if (expected > 0 && lane == 0) got = wait_bounded_cluster<2>(inbox_bar, 0, p, kDetailSkCopy) ? 1 : 0;
+      got = __shfl_sync(0xffffffffu, got, 0);
+      if (expected > 0 && got) (void)ptx::mbar_try_wait_cluster(inbox_bar, 0);  // every lane acquires
+      // Received; a CTA may leave when all have (its copies then are read out).
+      ptx::cluster_arrive();
+      if (quarter_all(got != 0))
+        for (int u = ew; unit_exists(u); u += 4) {
+          const float* in = reinterpret_cast<const float*>(smem + kSplitBytes) + (u / kChunks) * (kQuarter / 4) + lane;
+          const int step = row_blocks * (kQuarter / 4);
+          auto from_inbox = [&](int c, uint32_t (&r)[16]) {
+            float v[16];
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-          peer[s] = ptx::map_shared_rank(sbase, static_cast<uint32_t>(s < p.splits ? s : 0));
-#pragma unroll 4
-        for (int i = threadIdx.x - 64; i < total; i += 128) {
-          const uint32_t off =
-              static_cast<uint32_t>(i >> log_quads) * (kBM * 4u) +
-              static_cast<uint32_t>((part << log_quads) + (i & ((1 << log_quads) - 1))) * 16u;
-          float4 v[kMaxSplits];
+            for (int j = 0; j < 16; ++j) v[j] = in[(c + j) * 32];
+            for (int n = 1; n < p.splits; ++n)
 #pragma unroll
-          for (int s = 0; s < kMaxSplits; ++s)
-            if (s < p.splits) v[s] = ptx::ld_cluster_f32x4(peer[s] + off);
-          float4 sum = v[0];
+              for (int j = 0; j < 16; ++j) v[j] += in[n * step + (c + j) * 32];
 #pragma unroll
-          for (int s = 1; s < kMaxSplits; ++s)
-            if (s < p.splits) {
-              sum.x += v[s].x;
-              sum.y += v[s].y;
-              sum.z += v[s].z;
-              sum.w += v[s].w;
-            }
-          *reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(own) + off) = sum;
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(v[j]);
+          };
+          if (!chunk(from_inbox, first_row + (u / kChunks) * 32, n0, (u % kChunks) * 64, t.z, false)) break;
         }
-      }
-      ptx::named_barrier_sync(1, 128);  // the epilogue warps
-      for (int u = ew; unit_exists(u); u += 4) {
-        const int rb = part * row_blocks + u / kChunks;
-        auto from_smem = [&](int c, uint32_t (&r)[16]) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(own[(c + j) * kBM + rb * 32 + lane]);
-        };
-        if (!chunk(from_smem, t.mb * kTileM + rb * 32, n0, (u % kChunks) * 64, t.z, false)) break;
-      }
-      ptx::cluster_sync();  // no CTA leaves while another reads its partial
+      ptx::cluster_wait();
     } else
     while (it.next(p, x)) {
       const BlockTile t = block_tile(x.tile, p);
@@ -756,7 +799,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       const bool d_first = kEpi == kEpiLinear && p.use_d && stores;
       if (d_first) load_d(buf, row0, n0, t.z);
       // The kept projections of these rows, a contiguous run each, into L2.
-      if (kEpi == kEpiGatedBwd && stores && lane < 2) {
+      if (kEpi == kEpiGatedBwd && stores && g == 0 && lane < 2) {
         const uint32_t n = static_cast<uint32_t>(min(BN, p.N - n0));
         ptx::bulk_prefetch_l2(p.pre + lane * p.pre_half + (static_cast<int64_t>(row0 / 32) * p.N + n0) * 32,
                               n * 128u);
@@ -765,7 +808,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       int ready = 1;
       if (lane == 0) ready = wait_bounded<true>(tfull_bar(acc), acc_phase, p, kDetailEpiFull) ? 1 : 0;
       ready = __shfl_sync(0xffffffffu, ready, 0);
-      if (!ready) {
+      if (!quarter_all(ready != 0)) {
         if (d_first) wait_d();  // a copy in flight lands before this warp's memory goes
         break;
       }
@@ -778,7 +821,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           const int slot = walker * CG + static_cast<int>(rank);
           float* partial = p.sk_ws + slot * kPartial + static_cast<size_t>(ew) * BN * 32;
 #pragma unroll 1
-          for (int c = 0; c < BN; c += 32) {
+          for (int c = 32 * g; c < BN; c += 32 * kG) {
             uint32_t v[32];
             ptx::tmem_ld_32x32b_x32(t_row + c, v);
             ptx::tmem_wait_ld();
@@ -787,8 +830,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
               __stcg(partial + (c + j) * 32 + lane, __uint_as_float(v[j]));
           }
           __threadfence();
-          __syncwarp();
-          if (lane == 0) atomicExch(p.sk_flags + slot * 4 + ew, 1);
+          quarter_sync();
+          if (lead) atomicExch(p.sk_flags + slot * 4 + ew, 1);
         }
       } else if (rows) {
         // Partials of the walkers after this one.
@@ -803,14 +846,14 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
             for (int n = 0; n < parts && ok; ++n)
               ok = wait_flag(p.sk_flags + (slot + n * CG) * 4 + ew, p, kDetailSkFlag) ? 1 : 0;
           ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
+          if (!quarter_all(ok != 0)) {
             if (d_first) wait_d();
             break;
           }
           for (int n = 0; n < parts; ++n)  // every lane acquires the partials
             (void)ld_acquire_gpu(p.sk_flags + (slot + n * CG) * 4 + ew);
         }
-        if (parts > 0) block_add_partials(t_row, partial, kPartial * CG, parts, BN, lane);
+        if (parts > 0) block_add_partials(t_row, partial, kPartial * CG, parts, 32 * g, BN, 32 * kG, lane);
         auto from_tmem = [&](int c, uint32_t (&r)[16]) {
           ptx::tmem_ld_32x32b_x16(t_row + c, r);
           ptx::tmem_wait_ld();
@@ -821,8 +864,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           ok = chunk(from_tmem, row0, n0, cc, t.z, cc + 64 < kOutN && n0 + cc + 64 < p.N);
         if (!ok) break;
         if (x.role == kOwner) {
-          __syncwarp();  // every lane has read the partials
-          if (lane == 0)
+          quarter_sync();  // every lane has read the partials
+          if (lead)
             for (int n = 0; n < parts; ++n) p.sk_flags[(slot + n * CG) * 4 + ew] = 0;
         }
       }
@@ -857,21 +900,22 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 template <bool kAT, bool kBN, int kEpi>
 cudaError_t block_set_smem(size_t smem) {
   const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(block_kernel<1, kAT, kBN, kEpi>, attr, static_cast<int>(smem));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(block_kernel<2, kAT, kBN, kEpi>, attr, static_cast<int>(smem));
+  const int bytes = static_cast<int>(smem);
+  cudaError_t e = cudaFuncSetAttribute(block_kernel<1, kAT, kBN, kEpi, 2>, attr, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(block_kernel<2, kAT, kBN, kEpi, 1>, attr, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(block_kernel<2, kAT, kBN, kEpi, 2>, attr, bytes);
   return e;
 }
 
-// `grid` CTAs, in clusters of a pair or of a tile's K splits; the launch may overlap the previous
-// kernel's tail (programmatic dependent launch).
+// `grid` CTAs, in clusters of a pair or of a tile's K splits; the launch may
+// overlap the previous kernel's tail (programmatic dependent launch).
 template <bool kAT, bool kBN, int kEpi>
 cudaError_t block_launch(const BlockMaps& m, const BlockParams& p, int cg, int grid, size_t smem,
                          cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kBlockThreads, 1, 1);
+  cfg.blockDim = dim3(kernel_threads(p.epi), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -883,8 +927,9 @@ cudaError_t block_launch(const BlockMaps& m, const BlockParams& p, int cg, int g
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cg == 2 ? cudaLaunchKernelEx(&cfg, block_kernel<2, kAT, kBN, kEpi>, m, p)
-                 : cudaLaunchKernelEx(&cfg, block_kernel<1, kAT, kBN, kEpi>, m, p);
+  if (cg == 1) return cudaLaunchKernelEx(&cfg, block_kernel<1, kAT, kBN, kEpi, 2>, m, p);
+  return p.epi == 2 ? cudaLaunchKernelEx(&cfg, block_kernel<2, kAT, kBN, kEpi, 2>, m, p)
+                    : cudaLaunchKernelEx(&cfg, block_kernel<2, kAT, kBN, kEpi, 1>, m, p);
 }
 
 }  // namespace spgemm

@@ -37,6 +37,7 @@ struct BlockParams : Params {
   int tiles_per;       // tiles of one matrix of the batch
   int batch;
   int walkers;         // CTAs, or CTA pairs
+  int epi;             // epilogue warps per TMEM lane quarter, 1 or 2
   int splits;          // > 1: each tile's K is split over a cluster of this many single CTAs
   int symmetric;       // 1: only tiles on and above the diagonal run; each off-diagonal one is
                        // also written transposed (square output)
@@ -71,8 +72,6 @@ __host__ __device__ constexpr size_t block_partial_bytes(int cg) {
 // A split tile's fp32 partial, staged in the CTA's idle ring.
 constexpr uint32_t kSplitBytes = kBM * kSoloBN * 4u;
 constexpr int kMaxSplits = 4;
-
-constexpr int kBlockThreads = kernel_threads(1);
 
 // Launchers, one per operand layout (block_*.cu): A K-major or MN-major
 // ("t": stored K x M), B likewise ("n": stored K x N).

@@ -198,6 +198,9 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.raster_group = cg == 2 ? 8 : 16;
   p.walkers = static_cast<int>(walkers);
   p.splits = splits;
+  // Two epilogue warps per lane quarter halve an epilogue that the main loop
+  // does not hide: single CTAs, and pairs whose K is short.
+  p.epi = cg == 1 || pr.K <= 1024 ? 2 : 1;
   p.sk_tiles = static_cast<int>(sk);
   p.dp_tiles = static_cast<int>(nt - sk);
   p.sk_ws = partials;
