@@ -1,25 +1,31 @@
 // logprobs.cu -- log probabilities of tokens under rows of logits, with the
 // row's entropy and best alternatives, and their gradient.
 //
-//   m = max x, s = sum e^(x - m), w = sum e^(x - m) (x - m)
-//   lse = m + ln s,  log p_t = x_t - lse,  H = ln s - w / s
+// One pass over the logits, bound by memory.  In base 2, with L = fp32(log2 e)
+// and an integer reference N near the largest x L,
+//   t_j = x_j L - N (one fused multiply-add, so nothing is lost for large x),
+//   s = sum 2^t,  w = sum 2^t t,
+//   log2 p_j = t_j - log2 s,  H = ln 2 (log2 s - w / s).
+// Each thread keeps N, s and w of its own elements in fp32; when a larger
+// element comes, N grows by an integer d and s' = 2^-d s, w' = 2^-d (w - d s)
+// (exact scalings).  Threads, warps and the blocks that share a row are
+// combined in a fixed order by the same step.
 //
-// One pass over the logits, bound by memory: each thread keeps m, s and w of
-// its own elements in fp32, rescaled when its maximum grows
-//   s' = f s,  w' = f (w + (m - m') s),  f = e^(m - m')
-// and the block (or, for few rows, the cluster of blocks that shares a row)
-// combines them in a fixed order.  Exponents are taken base 2 of
-// (x - m) log2 e, the difference first, so large logits lose nothing; the
-// exponent is cut at -200 (2^-200 is 0 in fp32), which keeps masked logits
-// (-inf, or the type's lowest value) from making 0 x inf.
+// A block's producer thread streams its rows through a shared-memory ring by
+// bulk copies, running ahead into the next row while the block still reduces
+// the last one.  Pairs of values go through the packed fp32 instructions;
+// masked logits (-inf, or the type's lowest value) are raised to a finite
+// floor first, so that 2^t t is 0 and not 0 x inf.  A row whose maximum is
+// within reach of that floor (all masked by a lowest value) or near the
+// type's top is summed again by the slow form (x - m).
 //
 // Alternatives.  While streaming, each thread also keeps the largest of its
 // elements and the first 16-byte vector that holds it.  The k-th largest of
 // these is a lower bound of the row's k-th largest element, so only the
 // threads at or above it (about k of them) have anything to offer: their
 // vectors are read again (from L2), the few elements at or above the bound
-// are collected and ranked.  A key of (value, index) orders equal values by
-// index, and the bound is a pair too, so a row of equal logits offers no
+// are collected and ranked.  A key of (value, column) orders equal values by
+// column, and the bound is a pair too, so a row of equal logits offers no
 // more than the first k vectors.  A row that offers more than the list holds
 // (its largest elements all in a few threads' vectors) is searched k times.
 #include <cuda_bf16.h>
@@ -30,19 +36,24 @@
 #include <cstdint>
 
 #include "ops_internal.h"
-#include "ptx.cuh"
+#include "ptx_block.cuh"
 
 using namespace spgemm;
 
 namespace {
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;       // that compute; one warp more copies
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpUnroll = 4;          // vectors a thread has in flight
+constexpr int kLpUnroll = 4;          // vectors of a thread in a chunk
+constexpr int kLpChunkVecs = kLpUnroll * kLpThreads;
+constexpr uint32_t kLpChunk = kLpChunkVecs * 16u;
+constexpr int kLpStages = 4;          // chunks of a block's ring
+constexpr int kLpBlocks = 3;          // blocks an SM holds
 constexpr int kLpCandidates = 1024;
 constexpr int kMaxTopK = GEMM_LOGPROBS_MAX_TOP_K;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kExpCut = -200.0f;
+constexpr float kExpCut = -200.0f;    // 2^-200 is 0 in fp32
+constexpr int kBwdThreads = 256;
 
 struct LpArgs {
   const void* logits;
@@ -56,6 +67,9 @@ struct LpArgs {
   const float *d_logprobs, *d_entropy;
   void* d_logits;
   int64_t ldd;
+  int64_t rows;
+  int* status;
+  unsigned long long timeout_ns;
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -139,76 +153,169 @@ struct Vec<__half> {
   static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
 };
 
-// A row of logits as 16-byte vectors from the aligned address at or before
-// its first element: element j of vector v is column v kN + j - shift.  The
-// first and last vector may hold columns that do not exist; those are read
-// one element at a time, and -inf stands in their place (and for a vector
-// -1, which no row has).
+// Two floats in one register pair, for the packed instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack_f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(F2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ F2 fma_f2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 add_f2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Per type: the largest of a vector's elements (NaN if one is), the vector
+// with its elements raised to the floor, and the range of row maxima for
+// which the fast sums hold: 2^((floor - m) L) is 0, and m L is far from
+// overflow.  kStart: the first reference, below any such maximum's and so far
+// above the floor's that masked elements add 0 from the start.
+template <typename T>
+struct Fast;
+template <>
+struct Fast<float> {
+  static constexpr float kFloor = -1e30f, kStart = -1.4e30f, kLow = -1e29f, kHigh = 1e38f;
+  static __device__ __forceinline__ float max(const uint4& w) {
+    return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                   max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+  static __device__ __forceinline__ void pairs(const uint4& w, F2 (&v)[2]) {
+    v[0] = pack_f2(fmaxf(__uint_as_float(w.x), kFloor), fmaxf(__uint_as_float(w.y), kFloor));
+    v[1] = pack_f2(fmaxf(__uint_as_float(w.z), kFloor), fmaxf(__uint_as_float(w.w), kFloor));
+  }
+};
+template <>
+struct Fast<__nv_bfloat16> {
+  static constexpr float kFloor = -1e30f, kStart = -1.4e30f, kLow = -1e29f, kHigh = 1e38f;
+  static __device__ __forceinline__ __nv_bfloat162 at(const uint32_t& w) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+  }
+  static __device__ __forceinline__ float max(const uint4& w) {
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(at(w.x), at(w.y)), __hmax2_nan(at(w.z), at(w.w)));
+    return max_nan(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ void pairs(const uint4& w, F2 (&v)[4]) {
+    const __nv_bfloat162 lo = __float2bfloat162_rn(kFloor);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 r = __hmax2(at(a[i]), lo);
+      const uint32_t b = *reinterpret_cast<const uint32_t*>(&r);
+      v[i] = pack_f2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    }
+  }
+};
+template <>
+struct Fast<__half> {
+  static constexpr float kFloor = -65504.0f, kStart = -94000.0f, kLow = -65000.0f, kHigh = 1e38f;
+  static __device__ __forceinline__ __half2 at(const uint32_t& w) {
+    return *reinterpret_cast<const __half2*>(&w);
+  }
+  static __device__ __forceinline__ float max(const uint4& w) {
+    const __half2 m = __hmax2_nan(__hmax2_nan(at(w.x), at(w.y)), __hmax2_nan(at(w.z), at(w.w)));
+    return max_nan(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ void pairs(const uint4& w, F2 (&v)[4]) {
+    const __half2 lo = __float2half2_rn(kFloor);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(__hmax2(at(a[i]), lo));
+      v[i] = pack_f2(f.x, f.y);
+    }
+  }
+};
+
+// A row of logits: `head` elements before the first 16-byte boundary, then
+// whole vectors (vector v from column head + v kN), then `tail` elements.
 template <typename T>
 struct Row {
   static constexpr int kN = Vec<T>::kN;
   const T* p;
-  int vocab, shift, vectors;
-  __device__ Row(const T* row, int v) : p(row), vocab(v) {
-    shift = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    vectors = static_cast<int>((static_cast<int64_t>(v) + shift + kN - 1) / kN);
+  int head, vectors, tail;
+  __device__ Row(const T* row, int vocab) : p(row) {
+    head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / sizeof(T));
+    head = min(head, vocab);
+    vectors = (vocab - head) / kN;
+    tail = vocab - head - vectors * kN;
   }
-  __device__ __forceinline__ bool whole(int v) const {
-    const int64_t c = static_cast<int64_t>(v) * kN - shift;
-    return c >= 0 && c + kN <= vocab;
-  }
-  __device__ __forceinline__ void load_edge(int v, float (&x)[kN]) const {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int64_t c = static_cast<int64_t>(v) * kN + j - shift;
-      x[j] = v >= 0 && c >= 0 && c < vocab ? Vec<T>::get(p[c]) : -INFINITY;
-    }
-  }
+  __device__ __forceinline__ int column(int v) const { return head + v * kN; }
   __device__ __forceinline__ const uint4* at(int v) const {
-    return reinterpret_cast<const uint4*>(p + (static_cast<int64_t>(v) * kN - shift));
+    return reinterpret_cast<const uint4*>(p + column(v));
   }
-  __device__ __forceinline__ void load(int v, float (&x)[kN]) const {
-    if (whole(v))
-      Vec<T>::unpack(__ldg(at(v)), x);
-    else
-      load_edge(v, x);
-  }
+  // Columns outside the vectors, by number: fewer than 2 kN of them.
+  __device__ __forceinline__ int edges() const { return head + tail; }
+  __device__ __forceinline__ int edge_column(int i) const { return i < head ? i : i + vectors * kN; }
 };
 
 struct Stats {
-  float m, s, w;  // w in units of ln 2
+  float m;        // the largest element, NaN if one is
+  float n, s, w;  // reference, sum 2^t, sum 2^t t
 };
 
-__device__ __forceinline__ Stats combine(const Stats& a, const Stats& b) {
+// s and w for a reference larger by d >= 0.
+__device__ __forceinline__ void lower(float d, float& s, float& w) {
+  const float e = fmaxf(-d, kExpCut), f = exp2_approx(e);
+  w = f * fmaf(e, s, w);
+  s *= f;
+}
+
+__device__ __forceinline__ Stats combine(Stats a, Stats b) {
   Stats r;
   r.m = max_nan(a.m, b.m);
-  const float da = fmaxf((a.m - r.m) * kLog2e, kExpCut), db = fmaxf((b.m - r.m) * kLog2e, kExpCut);
-  const float fa = exp2_approx(da), fb = exp2_approx(db);
-  r.s = fa * a.s + fb * b.s;
-  r.w = fa * fmaf(da, a.s, a.w) + fb * fmaf(db, b.s, b.w);
+  r.n = fmaxf(a.n, b.n);
+  lower(r.n - a.n, a.s, a.w);
+  lower(r.n - b.n, b.s, b.w);
+  r.s = a.s + b.s;
+  r.w = a.w + b.w;
   return r;
 }
 
 __device__ __forceinline__ Stats shuffle_xor(const Stats& a, int o) {
-  return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-          __shfl_xor_sync(0xffffffffu, a.w, o)};
+  return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.n, o),
+          __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.w, o)};
 }
 
 struct LpShared {
-  Stats warp[kLpWarps];
+  uint64_t full[kLpStages], empty[kLpStages];
+  Stats warp[2][kLpWarps];          // of this row and the last one
   Stats block;
   int count;
   uint64_t best[kMaxTopK];          // this block's best keys, best first
   uint64_t list[kLpCandidates];
   uint64_t reduce[kLpWarps];
 };
+constexpr size_t kLpSmem = 128 + kLpStages * static_cast<size_t>(kLpChunk) + sizeof(LpShared);
+
+// Barriers of the computing warps.
+__device__ __forceinline__ void compute_sync() { ptx::named_barrier_sync(1, kLpThreads); }
+__device__ __forceinline__ int compute_count(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.popc.u32 %0, 1, %2, p;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "n"(kLpThreads)
+      : "memory");
+  return static_cast<int>(r);
+}
 
 __device__ __forceinline__ uint64_t key_of(float x, int column) {
   return (static_cast<uint64_t>(order_of(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(column));
 }
 
-// Writes the k largest of sh.list[0, n) to out, in order, and 0 in places
-// that no key takes.
+// Writes the k largest of list[0, n) to out, in order, and 0 in places that
+// no key takes.
 __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, int k, uint64_t* out) {
   for (int i = threadIdx.x; i < k; i += kLpThreads)
     if (i >= n) out[i] = 0;
@@ -221,20 +328,22 @@ __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, int k, ui
 }
 
 // The k best of the columns this block streamed (vectors v0 + i kLpThreads +
-// thread), to sh.best.  top: order of this thread's largest element (0: it
-// has none); top_v: the first vector that holds it.
+// thread below v1, and, with `edges`, the columns outside the vectors, one
+// to a thread), to sh.best.  top: order of this thread's largest element (0:
+// it has none); top_c: the first column of the vector that holds it.
 template <typename T>
-__device__ void block_top(const Row<T>& row, int v0, int v1, int k, uint32_t top, int top_v,
-                          LpShared& sh) {
+__device__ __noinline__ void block_top(const Row<T>& row, int v0, int v1, int edge, int k,
+                                       uint32_t top, int top_c, LpShared& sh) {
+  constexpr int kN = Row<T>::kN;
   const int tid = threadIdx.x, lane = tid & 31;
   // The bound: the largest order that at least k threads reach (0 if fewer
   // have anything), or one that k to 2 k threads reach.
   uint32_t lo = 0, hi = 0xffffffffu;
   int reach = kLpThreads;
-  if (__syncthreads_count(top == 0xffffffffu) >= k) lo = hi;  // NaNs
+  if (compute_count(top == 0xffffffffu) >= k) lo = hi;  // NaNs
   while (hi - lo > 1) {
     const uint32_t mid = lo + (hi - lo) / 2;
-    const int c = __syncthreads_count(top >= mid);
+    const int c = compute_count(top >= mid);
     if (c >= k) {
       lo = mid;
       reach = c;
@@ -243,62 +352,63 @@ __device__ void block_top(const Row<T>& row, int v0, int v1, int k, uint32_t top
       hi = mid;
     }
   }
-  // Many threads end on the same value: of those, the first vectors only.
-  int last_v = v1;
+  // Many threads end on the same value: of those, the first columns only.
+  int last_c = 0x7fffffff;
   if (lo > 0 && reach > 2 * k) {
-    const int want = k - __syncthreads_count(top > lo);
-    int a = v0 - 1, b = v1;  // count(top_v <= a) < want <= count(top_v <= b)
+    const int want = k - compute_count(top > lo);
+    int a = -1, b = 0x7fffffff;  // count(top_c <= a) < want <= count(top_c <= b)
     while (b - a > 1) {
       const int mid = a + (b - a) / 2;
-      if (__syncthreads_count(top == lo && top_v <= mid) >= want)
+      if (compute_count(top == lo && top_c <= mid) >= want)
         b = mid;
       else
         a = mid;
     }
-    last_v = b;
+    last_c = b;
   }
   if (tid == 0) sh.count = 0;
-  __syncthreads();
-  const bool offers = top > lo || (top == lo && top != 0 && top_v <= last_v);
+  compute_sync();
+  auto take = [&](float x, int c, int first) {
+    const uint32_t o = order_of(x);
+    if (o > lo || (o == lo && first <= last_c)) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kLpCandidates) sh.list[at] = key_of(x, c);
+    }
+  };
+  if (edge >= 0) take(Vec<T>::get(row.p[edge]), edge, edge);
+  const bool offers = top > lo || (top == lo && top != 0 && top_c <= last_c);
   uint32_t ask = __ballot_sync(0xffffffffu, offers);
   while (ask) {  // the warp reads one offering thread's vectors together
     const int src = __ffs(ask) - 1;
     ask &= ask - 1;
     for (int v = v0 + (tid - lane + src) + lane * kLpThreads; v < v1; v += 32 * kLpThreads) {
-      float x[Row<T>::kN];
-      row.load(v, x);
+      float x[kN];
+      Vec<T>::unpack(__ldg(row.at(v)), x);
 #pragma unroll
-      for (int j = 0; j < Row<T>::kN; ++j) {
-        const int64_t c = static_cast<int64_t>(v) * Row<T>::kN + j - row.shift;
-        const uint32_t o = order_of(x[j]);
-        if (c >= 0 && c < row.vocab && (o > lo || (o == lo && v <= last_v))) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kLpCandidates) sh.list[at] = key_of(x[j], static_cast<int>(c));
-        }
-      }
+      for (int j = 0; j < kN; ++j) take(x[j], row.column(v) + j, row.column(v));
     }
   }
-  __syncthreads();
+  compute_sync();
   const int n = sh.count;
   if (n <= kLpCandidates) {
     rank_keys(sh.list, n, k, sh.best);
-    __syncthreads();
+    compute_sync();
     return;
   }
   // More than the list holds: the largest key below the last one, k times.
   uint64_t below = ~0ull;
   for (int i = 0; i < k; ++i) {
     uint64_t best = 0;
+    auto offer = [&](float x, int c) {
+      const uint64_t key = key_of(x, c);
+      if (key < below && key > best) best = key;
+    };
+    if (edge >= 0) offer(Vec<T>::get(row.p[edge]), edge);
     for (int v = v0 + tid; v < v1; v += kLpThreads) {
-      float x[Row<T>::kN];
-      row.load(v, x);
+      float x[kN];
+      Vec<T>::unpack(__ldg(row.at(v)), x);
 #pragma unroll
-      for (int j = 0; j < Row<T>::kN; ++j) {
-        const int64_t c = static_cast<int64_t>(v) * Row<T>::kN + j - row.shift;
-        if (c < 0 || c >= row.vocab) continue;
-        const uint64_t key = key_of(x[j], static_cast<int>(c));
-        if (key < below && key > best) best = key;
-      }
+      for (int j = 0; j < kN; ++j) offer(x[j], row.column(v) + j);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -306,11 +416,31 @@ __device__ void block_top(const Row<T>& row, int v0, int v1, int k, uint32_t top
       best = other > best ? other : best;
     }
     if (lane == 0) sh.reduce[tid >> 5] = best;
-    __syncthreads();
+    compute_sync();
     for (int j = 0; j < kLpWarps; ++j) best = sh.reduce[j] > best ? sh.reduce[j] : best;
     if (tid == 0) sh.best[i] = best;
     below = best;
-    __syncthreads();
+    compute_sync();
+  }
+}
+
+// The sums of this block's share of a row whose maximum m (finite) is outside
+// the fast form's range: t = (x - m) L, the difference first.  The reference
+// of the result is m itself.
+template <typename T>
+__device__ __noinline__ void slow_sums(const Row<T>& row, int v0, int v1, int edge, float m, Stats& t) {
+  t.s = t.w = 0.0f;
+  auto add = [&](float x) {
+    const float e2 = fmaxf((x - m) * kLog2e, kExpCut), e = exp2_approx(e2);
+    t.s += e;
+    t.w = fmaf(e, e2, t.w);
+  };
+  if (edge >= 0) add(Vec<T>::get(row.p[edge]));
+  for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kLpThreads) {
+    float x[Row<T>::kN];
+    Vec<T>::unpack(__ldg(row.at(v)), x);
+#pragma unroll
+    for (int j = 0; j < Row<T>::kN; ++j) add(x[j]);
   }
 }
 
@@ -330,148 +460,290 @@ __device__ __forceinline__ uint64_t peer_u64(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// One row per cluster (of one block or more; see launch below).
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const LpArgs a) {
-  constexpr int kN = Vec<T>::kN;
-  __shared__ LpShared sh;
-  const uint32_t blocks = cluster_size();
-  const uint32_t rank = blocks > 1 ? ptx::cluster_ctarank() : 0u;
-  const int64_t r = blockIdx.x / blocks;
-  const int tid = threadIdx.x;
-  ptx::pdl_launch_dependents();
-  ptx::pdl_wait_prior_grid();
-  const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
-  const int v0 = static_cast<int>(static_cast<int64_t>(row.vectors) * rank / blocks);
-  const int v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (rank + 1) / blocks);
-
-  Stats t = {-INFINITY, 0.0f, 0.0f};
-  uint32_t top = 0;
-  int top_v = 0;
-  for (int base = v0 + tid; base < v1; base += kLpUnroll * kLpThreads) {
-    uint4 w[kLpUnroll];
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      const int v = base + u * kLpThreads;
-      if (v < v1 && row.whole(v)) {
-        w[u] = __ldg(row.at(v));
-      } else {
-        float x[kN];
-        row.load_edge(v < v1 ? v : -1, x);
-        w[u] = Vec<T>::pack(x);
-      }
-    }
-    float m = t.m;
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      float x[kN];
-      Vec<T>::unpack(w[u], x);
-      float vm = x[0];
-#pragma unroll
-      for (int j = 1; j < kN; ++j) vm = max_nan(vm, x[j]);
-      if constexpr (kTop) {
-        const uint32_t o = order_of(vm);
-        if (o > top && base + u * kLpThreads < v1) {
-          top = o;
-          top_v = base + u * kLpThreads;
-        }
-      }
-      m = max_nan(m, vm);
-    }
-    const float d = fmaxf((t.m - m) * kLog2e, kExpCut), f = exp2_approx(d);
-    t.w = f * fmaf(d, t.s, t.w);
-    t.s *= f;
-    t.m = m;
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      float x[kN];
-      Vec<T>::unpack(w[u], x);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const float e2 = fmaxf((x[j] - m) * kLog2e, kExpCut);
-        const float e = exp2_approx(e2);
-        t.s += e;
-        t.w = fmaf(e, e2, t.w);
-      }
+// Bounded wait on a ring barrier; a wait that runs out is recorded.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const LpArgs& a, int detail) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (ptx::globaltimer_ns() - t0 > a.timeout_ns) {
+      if (atomicCAS(a.status, 0, kStatusTimeout) == 0) atomicExch(a.status + 1, detail);
+      return false;
     }
   }
-  // Block, in a fixed order.
+  return true;
+}
+
+// A row's sums over the block: into sh.block by warp 0, in a fixed order.
+__device__ __forceinline__ Stats block_stats(Stats t, LpShared& sh, int parity) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t = combine(t, shuffle_xor(t, o));
-  if ((tid & 31) == 0) sh.warp[tid >> 5] = t;
-  __syncthreads();
-  if (tid < 32) {
-    t = sh.warp[tid & (kLpWarps - 1)];
+  if ((threadIdx.x & 31) == 0) sh.warp[parity][threadIdx.x >> 5] = t;
+  compute_sync();
+  t = sh.warp[parity][threadIdx.x & (kLpWarps - 1)];
 #pragma unroll
-    for (int o = kLpWarps / 2; o > 0; o >>= 1) t = combine(t, shuffle_xor(t, o));
-    if (tid == 0) sh.block = t;
-  }
-  if constexpr (kTop) block_top<T>(row, v0, v1, a.top_k, top, top_v, sh);
-  __syncthreads();
-  t = sh.block;
+  for (int o = kLpWarps / 2; o > 0; o >>= 1) t = combine(t, shuffle_xor(t, o));
+  return t;
+}
 
-  if (blocks > 1) {
-    ptx::cluster_sync();
-    if (rank == 0) {
-      const uint32_t at = ptx::smem_addr(&sh.block);
-      for (uint32_t b = 1; b < blocks; ++b)
-        t = combine(t, Stats{peer_f32(at, b), peer_f32(at + 4, b), peer_f32(at + 8, b)});
-      if constexpr (kTop) {
-        const uint32_t best = ptx::smem_addr(sh.best);
-        const int n = static_cast<int>(blocks) * a.top_k;
-        for (int i = tid; i < n; i += kLpThreads)
-          sh.list[i] = peer_u64(best + 8u * (i % a.top_k), i / a.top_k);
-        __syncthreads();
-        rank_keys(sh.list, n, a.top_k, sh.best);
-        __syncthreads();
-      }
-    }
-    ptx::cluster_sync();  // no block leaves while another reads its memory
-    if (rank != 0) return;
-  }
-  // Infinite (or NaN) largest logit: no distribution.  All masked: nothing
-  // is possible, and there is nothing to choose between.  log p is taken as
-  // (x - m) - ln s, which for large logits keeps the digits x - lse loses.
-  const float ln_s = logf(t.s);
-  float lse = t.m + ln_s, h = ln_s - t.w * kLn2 / t.s;
-  if (t.m == -INFINITY) {
-    lse = -INFINITY;
-    h = 0.0f;
-  } else if (!(t.m < INFINITY)) {
-    lse = h = NAN;
-  }
+// Rows row0, row0 + step, ... with one block each; or, launched as clusters
+// (few rows), one row per cluster, each block taking a share of its vectors.
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(const LpArgs a) {
+  constexpr int kN = Vec<T>::kN;
+  extern __shared__ uint8_t lp_smem[];
+  uint8_t* ring = lp_smem + ((128u - (ptx::smem_addr(lp_smem) & 127u)) & 127u);
+  LpShared& sh = *reinterpret_cast<LpShared*>(ring + kLpStages * kLpChunk);
+  const uint32_t ring_addr = ptx::smem_addr(ring);
+  const uint32_t full = ptx::smem_addr(sh.full), empty = ptx::smem_addr(sh.empty);
+  const uint32_t blocks = cluster_size();
+  const uint32_t rank = blocks > 1 ? ptx::cluster_ctarank() : 0u;
+  const int64_t row0 = blockIdx.x / blocks, step = gridDim.x / blocks;
+  const int tid = threadIdx.x;
   if (tid == 0) {
-    if (a.lse) a.lse[r] = lse;
-    if (a.entropy) a.entropy[r] = h;
-    if (a.tokens && a.logprobs) {
-      const int64_t token = a.tokens[r];
-      float lp = 0.0f;  // negative: the position does not count
-      if (token >= a.vocab) {
-        lp = NAN;
-      } else if (token >= 0) {
-        const float x = Vec<T>::get(row.p[token]);
-        lp = x == -INFINITY ? x : (x - t.m) - ln_s;
-      }
-      a.logprobs[r] = lp;
+    for (int i = 0; i < kLpStages; ++i) {
+      ptx::mbar_init(full + 8u * i, 1);
+      ptx::mbar_init(empty + 8u * i, kLpWarps);
     }
+    ptx::fence_barrier_init();
   }
-  if constexpr (kTop) {
-    if (tid < a.top_k) {
-      const uint64_t key = sh.best[tid];
-      const float x = value_of(static_cast<uint32_t>(key >> 32));
-      a.top_ids[r * a.top_k + tid] = 0xffffffffu - static_cast<uint32_t>(key);
-      a.top_logprobs[r * a.top_k + tid] = x == -INFINITY ? x : (x - t.m) - ln_s;
+  __syncthreads();
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+
+  auto share = [&](const Row<T>& row, int& v0, int& v1) {
+    v0 = static_cast<int>(static_cast<int64_t>(row.vectors) * rank / blocks);
+    v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (rank + 1) / blocks);
+  };
+
+  if (tid >= kLpThreads) {
+    // ------------------------------------------------------------ producer --
+    if (tid == kLpThreads) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      uint32_t used = 0, parity = 0;
+      const uint64_t pol = ptx::l2_policy_evict_first();
+      for (int64_t r = row0; ok && r < a.rows; r += step) {
+        const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
+        int v0, v1;
+        share(row, v0, v1);
+        for (int v = v0; v < v1; v += kLpChunkVecs) {
+          if (!ring_wait(empty + 8u * stage, phase ^ 1u, a, kDetailProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bytes = static_cast<uint32_t>(min(v1 - v, kLpChunkVecs)) * 16u;
+          ptx::mbar_arrive_expect_tx(full + 8u * stage, bytes);
+          if constexpr (kTop)  // read again, in part
+            ptx::bulk_load(ring_addr + stage * kLpChunk, row.at(v), bytes, full + 8u * stage);
+          else
+            ptx::bulk_load_hint(ring_addr + stage * kLpChunk, row.at(v), bytes, full + 8u * stage, pol);
+          used |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kLpStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every copy lands before the block may leave.
+      for (int i = 0; i < kLpStages; ++i)
+        if (used & (1u << i)) ring_wait(full + 8u * i, (parity >> i) & 1u, a, kDetailProducerDrain);
+    }
+    __syncwarp();
+    if (blocks > 1) {
+      ptx::cluster_sync();
+      ptx::cluster_sync();
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- compute --
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  const F2 l2 = pack_f2(kLog2e, kLog2e);
+  bool ok = true;
+  for (int64_t r = row0; r < a.rows; r += step, turn ^= 1) {
+    const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
+    int v0, v1;
+    share(row, v0, v1);
+    // This thread's column outside the vectors, if it has one: the head's go
+    // with the first block's share, the tail's with the last one's.
+    const int edge = tid < row.edges() && rank == (tid < row.head ? 0u : blocks - 1u)
+                         ? row.edge_column(tid)
+                         : -1;
+    Stats t = {-INFINITY, Fast<T>::kStart, 0.0f, 0.0f};
+    F2 s2 = 0, w2 = 0;  // (0.0f, 0.0f)
+    uint32_t top = 0;
+    int top_c = 0;
+    // A larger element (its x L, not above the next integer) moves the reference.
+    auto reach = [&](float m) {
+      t.m = max_nan(t.m, m);
+      const float n = m * kLog2e;
+      if (n > t.n) {
+        const float up = ceilf(n);
+        float sa, sb, wa, wb;
+        unpack_f2(s2, sa, sb);
+        unpack_f2(w2, wa, wb);
+        lower(up - t.n, sa, wa);
+        lower(up - t.n, sb, wb);
+        s2 = pack_f2(sa, sb);
+        w2 = pack_f2(wa, wb);
+        t.n = up;
+      }
+    };
+    if (edge >= 0) {
+      const float x = Vec<T>::get(row.p[edge]);
+      top = order_of(x);
+      top_c = edge;
+      reach(x);
+      const float e2 = fmaf(fmaxf(x, Fast<T>::kFloor), kLog2e, -t.n), e = exp2_approx(e2);
+      s2 = add_f2(s2, pack_f2(e, 0.0f));
+      w2 = add_f2(w2, pack_f2(e * e2, 0.0f));
+    }
+    for (int v = v0; v < v1; v += kLpChunkVecs) {
+      if (ok) ok = ring_wait(full + 8u * stage, phase, a, kDetailMmaFull);
+      const uint32_t src = ring_addr + stage * kLpChunk + static_cast<uint32_t>(tid) * 16u;
+      const int left = v1 - v - tid;  // this thread's vectors: u kLpThreads < left
+      uint4 w[kLpUnroll];
+#pragma unroll
+      for (int u = 0; u < kLpUnroll; ++u)
+        if (u * kLpThreads < left) w[u] = ptx::ld_shared_v4(src + u * (kLpThreads * 16u));
+      // The slot goes back at once, and the next copy may land at once: these
+      // reads come before it only by a fence between the two proxies.
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if ((tid & 31) == 0) ptx::mbar_arrive(empty + 8u * stage);
+      if (++stage == kLpStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      float m = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kLpUnroll; ++u)
+        if (u * kLpThreads < left) {
+          const float vm = Fast<T>::max(w[u]);
+          m = max_nan(m, vm);
+          if constexpr (kTop) {
+            const uint32_t o = order_of(vm);
+            if (o > top) {
+              top = o;
+              top_c = row.column(v + tid + u * kLpThreads);
+            }
+          }
+        }
+      reach(m);
+      const F2 n2 = pack_f2(-t.n, -t.n);
+#pragma unroll
+      for (int u = 0; u < kLpUnroll; ++u)
+        if (u * kLpThreads < left) {
+          F2 x[kN / 2];
+          Fast<T>::pairs(w[u], x);
+#pragma unroll
+          for (int j = 0; j < kN / 2; ++j) {
+            const F2 e2 = fma_f2(x[j], l2, n2);
+            float ea, eb;
+            unpack_f2(e2, ea, eb);
+            const F2 e = pack_f2(exp2_approx(ea), exp2_approx(eb));
+            s2 = add_f2(s2, e);
+            w2 = fma_f2(e, e2, w2);
+          }
+        }
+    }
+    {
+      float sa, sb, wa, wb;
+      unpack_f2(s2, sa, sb);
+      unpack_f2(w2, wa, wb);
+      t.s = sa + sb;
+      t.w = wa + wb;
+    }
+    t = block_stats(t, sh, turn);  // the same in every warp
+    if constexpr (kTop) block_top<T>(row, v0, v1, edge, a.top_k, top, top_c, sh);
+
+    // The blocks of a cluster share their sums (their maxima, if the slow
+    // form is needed: then again).
+    if (blocks > 1) {
+      if (tid == 0) sh.block = t;
+      ptx::cluster_sync();
+      const uint32_t at = ptx::smem_addr(&sh.block);
+      Stats all = {peer_f32(at, 0), peer_f32(at + 4, 0), peer_f32(at + 8, 0), peer_f32(at + 12, 0)};
+      for (uint32_t b = 1; b < blocks; ++b)
+        all = combine(all, Stats{peer_f32(at, b), peer_f32(at + 4, b), peer_f32(at + 8, b), peer_f32(at + 12, b)});
+      t = all;
+      if constexpr (kTop) {
+        if (rank == 0) {
+          const uint32_t best = ptx::smem_addr(sh.best);
+          const int n = static_cast<int>(blocks) * a.top_k;
+          for (int i = tid; i < n; i += kLpThreads)
+            sh.list[i] = peer_u64(best + 8u * (i % a.top_k), i / a.top_k);
+          compute_sync();
+          rank_keys(sh.list, n, a.top_k, sh.best);
+          compute_sync();
+        }
+      }
+    }
+    const bool slow = t.m > -INFINITY && t.m < INFINITY && !(t.m > Fast<T>::kLow && t.m < Fast<T>::kHigh);
+    if (slow && rank == 0) {  // a cluster's first block sums the whole row
+      Stats u = {t.m, 0.0f, 0.0f, 0.0f};
+      slow_sums<T>(row, 0, row.vectors, tid < row.edges() ? row.edge_column(tid) : -1, t.m, u);
+      compute_sync();  // the last row's sums have been read
+      t = block_stats(u, sh, turn);
+    }
+    if (blocks > 1) {
+      ptx::cluster_sync();  // no block leaves while another reads its memory
+      if (rank != 0) return;
+    }
+    // Both are taken from the largest element, whose own term e_m the sums
+    // hold exactly: a row with one possible token has log p = 0 and H = 0.
+    const float t_m = slow ? 0.0f : fmaf(t.m, kLog2e, -t.n);
+    const float e_m = exp2_approx(t_m);
+    const float log_s = log2f(t.s / e_m);
+    auto log_p = [&](float x) {
+      if (x == -INFINITY) return x;
+      const float e2 = slow ? (x - t.m) * kLog2e : fmaf(x, kLog2e, -t.n) - t_m;
+      return (e2 - log_s) * kLn2;
+    };
+    float lse = t.m - log_p(t.m), h = t.s == e_m ? 0.0f : (log_s + (t_m - t.w / t.s)) * kLn2;
+    bool none = false;
+    if (t.m == -INFINITY) {  // all masked: nothing is possible, and nothing to choose between
+      lse = -INFINITY;
+      h = 0.0f;
+    } else if (!(t.m < INFINITY)) {  // NaN or +inf: no distribution
+      lse = h = NAN;
+      none = true;
+    }
+    if (tid == 0) {
+      if (a.lse) a.lse[r] = lse;
+      if (a.entropy) a.entropy[r] = h;
+      if (a.tokens && a.logprobs) {
+        const int64_t token = a.tokens[r];
+        float lp = 0.0f;  // negative: the position does not count
+        if (token >= a.vocab) {
+          lp = NAN;
+        } else if (token >= 0) {
+          const float x = Vec<T>::get(row.p[token]);
+          lp = none && x != -INFINITY ? NAN : log_p(x);
+        }
+        a.logprobs[r] = lp;
+      }
+    }
+    if constexpr (kTop) {
+      if (tid < a.top_k) {
+        const uint64_t key = sh.best[tid];
+        const float x = value_of(static_cast<uint32_t>(key >> 32));
+        a.top_ids[r * a.top_k + tid] = 0xffffffffu - static_cast<uint32_t>(key);
+        a.top_logprobs[r * a.top_k + tid] = none && x != -INFINITY ? NAN : log_p(x);
+      }
     }
   }
 }
 
 // dx_j = gl ([j = token] - p_j) - gh p_j (log p_j + H): one read of the
-// logits, one write of their gradient.  Grid: x over steps of a row, y over
-// rows.  The two may start at different offsets from a 16-byte boundary
-// (then, and at the ends of a row, elements go one by one).
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_backward_kernel(const LpArgs a, int64_t rows,
-                                                                          int chunks) {
+// logits, one write of their gradient.  Grid: steps of a row, rows.  Where
+// the two start at different offsets from a 16-byte boundary, elements go
+// one by one.
+template <typename T, bool kEntropy>
+__global__ void __launch_bounds__(kBwdThreads) logprobs_backward_kernel(const LpArgs a, int chunks) {
   constexpr int kN = Vec<T>::kN;
   ptx::pdl_launch_dependents();
   ptx::pdl_wait_prior_grid();
@@ -479,54 +751,58 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_backward_kernel(const 
   const int chunk = static_cast<int>(blockIdx.x - r * chunks);
   const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
   T* out = static_cast<T*>(a.d_logits) + r * a.ldd;
-  const bool same = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(row.p) & 15u);
   const int64_t token = a.tokens ? a.tokens[r] : -1;
   const float gl = token >= 0 && a.d_logprobs ? a.d_logprobs[r] : 0.0f;
-  const float gh = a.d_entropy ? a.d_entropy[r] : 0.0f;
+  const float gh = kEntropy ? a.d_entropy[r] : 0.0f;
   const float lse = a.lse[r];
-  const float h = a.d_entropy ? a.entropy[r] : 0.0f;
-  const int base = chunk * kLpUnroll * kLpThreads + threadIdx.x;
+  const float h = kEntropy ? a.entropy[r] : 0.0f;
+  auto gradient = [&](float x) {
+    const float lp = x == -INFINITY ? x : x - lse;  // an all-masked row: lse is -inf too
+    const float p = exp2_approx(lp * kLog2e);
+    // p (log p + H) is 0 where p is.
+    return kEntropy ? -p * fmaf(gh, fmaxf(lp, kExpCut) + h, gl) : -p * gl;
+  };
+  if (chunk == 0 && static_cast<int>(threadIdx.x) < row.edges()) {
+    const int c = row.edge_column(threadIdx.x);
+    out[c] = Vec<T>::put(gradient(Vec<T>::get(row.p[c])) + (c == token ? gl : 0.0f));
+  }
+  const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
+  const int base = chunk * kLpUnroll * kBwdThreads + threadIdx.x;
   uint4 w[kLpUnroll];
 #pragma unroll
-  for (int u = 0; u < kLpUnroll; ++u) {
-    const int v = base + u * kLpThreads;
-    if (v < row.vectors && row.whole(v)) w[u] = __ldcs(row.at(v));
-  }
+  for (int u = 0; u < kLpUnroll; ++u)
+    if (base + u * kBwdThreads < row.vectors) w[u] = __ldcs(row.at(base + u * kBwdThreads));
 #pragma unroll
   for (int u = 0; u < kLpUnroll; ++u) {
-    const int v = base + u * kLpThreads;
+    const int v = base + u * kBwdThreads;
     if (v >= row.vectors) break;
-    const bool whole = row.whole(v);
     float x[kN];
-    if (whole)
-      Vec<T>::unpack(w[u], x);
-    else
-      row.load_edge(v, x);
-    const int64_t c0 = static_cast<int64_t>(v) * kN - row.shift;
+    Vec<T>::unpack(w[u], x);
+    const int c0 = row.column(v);
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const float lp = x[j] == -INFINITY ? -INFINITY : x[j] - lse;
-      const float p = exp2_approx(lp * kLog2e);
-      // p (log p + H) is 0 where p is.
-      x[j] = -p * fmaf(gh, fmaxf(lp, kExpCut) + h, gl);
-      if (c0 + j == token) x[j] += gl;
+    for (int j = 0; j < kN; ++j) x[j] = gradient(x[j]);
+    if (token >= c0 && token < c0 + kN) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if (c0 + j == token) x[j] += gl;
     }
-    if (whole && same) {
+    if (same) {
       __stcs(reinterpret_cast<uint4*>(out + c0), Vec<T>::pack(x));
     } else {
 #pragma unroll
-      for (int j = 0; j < kN; ++j)
-        if (c0 + j >= 0 && c0 + j < a.vocab) out[c0 + j] = Vec<T>::put(x[j]);
+      for (int j = 0; j < kN; ++j) out[c0 + j] = Vec<T>::put(x[j]);
     }
   }
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_rows(void (*kernel)(P...), int64_t grid, int cluster, cudaStream_t stream, A... args) {
+cudaError_t launch_rows(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cluster,
+                        cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kLpThreads, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -540,16 +816,16 @@ cudaError_t launch_rows(void (*kernel)(P...), int64_t grid, int cluster, cudaStr
 }
 
 template <typename T>
-cudaError_t forward(const LpArgs& a, int64_t rows, int cluster, cudaStream_t stream) {
-  return a.top_k > 0 ? launch_rows(logprobs_kernel<T, true>, rows * cluster, cluster, stream, a)
-                     : launch_rows(logprobs_kernel<T, false>, rows * cluster, cluster, stream, a);
+cudaError_t forward(const LpArgs& a, int64_t grid, int cluster, cudaStream_t stream) {
+  return launch_rows(a.top_k > 0 ? logprobs_kernel<T, true> : logprobs_kernel<T, false>, grid,
+                     kLpThreads + 32, kLpSmem, cluster, stream, a);
 }
 
 template <typename T>
-cudaError_t backward(const LpArgs& a, int64_t rows, cudaStream_t stream) {
-  const int64_t vectors = ceil_div(a.vocab + Vec<T>::kN - 1, Vec<T>::kN);
-  const int chunks = static_cast<int>(ceil_div(vectors, kLpUnroll * kLpThreads));
-  return launch_rows(logprobs_backward_kernel<T>, rows * chunks, 1, stream, a, rows, chunks);
+cudaError_t backward(const LpArgs& a, cudaStream_t stream) {
+  const int chunks = static_cast<int>(std::max<int64_t>(1, ceil_div(a.vocab / Vec<T>::kN, kLpUnroll * kBwdThreads)));
+  return launch_rows(a.d_entropy ? logprobs_backward_kernel<T, true> : logprobs_backward_kernel<T, false>,
+                     a.rows * chunks, kBwdThreads, 0, 1, stream, a, chunks);
 }
 
 size_t elem_bytes(gemm_in_t t) { return t == GEMM_IN_F32 ? 4 : 2; }
@@ -559,10 +835,10 @@ gemm_status_t check(const gemm_ops* ops, const gemm_logprobs_args_t* g, bool bwd
   if (g->rows < 0 || g->vocab < 1)
     return ops_fail(GEMM_ERR_INVALID_ARG, "rows %lld < 0 or vocab %lld < 1", (long long)g->rows,
                     (long long)g->vocab);
-  // Columns are counted in 32 bits, blocks of a row (at most 8, or one per 8192
-  // columns) in the grid's 31.
-  if (g->vocab > kOpsMaxDim / 2 || g->rows > kOpsMaxDim / 8 ||
-      g->rows * ceil_div(g->vocab + 8, 4 * kLpUnroll * kLpThreads) > kOpsMaxDim)
+  // Columns are counted in 32 bits, the gradient's blocks (at most one for
+  // every 4096 columns of a row) in the grid's 31.
+  if (g->vocab > kOpsMaxDim / 2 || g->rows > kOpsMaxDim ||
+      g->rows * (1 + g->vocab / (4 * kLpUnroll * kBwdThreads)) > kOpsMaxDim)
     return ops_fail(GEMM_ERR_INVALID_ARG, "too many rows or columns");
   if (g->dtype != GEMM_IN_F16 && g->dtype != GEMM_IN_BF16 && g->dtype != GEMM_IN_F32)
     return ops_fail(GEMM_ERR_INVALID_ARG, "dtype %d out of range", static_cast<int>(g->dtype));
@@ -597,8 +873,11 @@ gemm_status_t check(const gemm_ops* ops, const gemm_logprobs_args_t* g, bool bwd
   return GEMM_OK;
 }
 
-LpArgs kernel_args(const gemm_logprobs_args_t* g) {
+LpArgs kernel_args(const gemm_ops* ops, const gemm_logprobs_args_t* g) {
   LpArgs a{};
+  a.rows = g->rows;
+  a.status = ops->d_status;
+  a.timeout_ns = ops->timeout_ns;
   a.logits = g->logits;
   a.ld = g->ld;
   a.vocab = static_cast<int>(g->vocab);
@@ -618,6 +897,19 @@ LpArgs kernel_args(const gemm_logprobs_args_t* g) {
 
 }  // namespace
 
+namespace spgemm {
+// More shared memory than a kernel gets by default (per device, once).
+cudaError_t logprobs_set_smem() {
+  cudaError_t e = cudaSuccess;
+  for (auto k : {logprobs_kernel<float, false>, logprobs_kernel<float, true>,
+                 logprobs_kernel<__nv_bfloat16, false>, logprobs_kernel<__nv_bfloat16, true>,
+                 logprobs_kernel<__half, false>, logprobs_kernel<__half, true>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLpSmem));
+  return e;
+}
+}  // namespace spgemm
+
 extern "C" {
 
 gemm_status_t gemm_token_logprobs(gemm_ops_t* ops, const gemm_logprobs_args_t* args, void* stream_handle) {
@@ -628,19 +920,20 @@ gemm_status_t gemm_token_logprobs(gemm_ops_t* ops, const gemm_logprobs_args_t* a
   if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
   // Few rows: each is shared by a cluster of blocks, as many as keep one
-  // step of vectors each, until the SMs are covered.
-  const int64_t steps = ceil_div(args->vocab * static_cast<int64_t>(elem_bytes(args->dtype)),
-                                 16 * kLpUnroll * kLpThreads);
+  // chunk of vectors each, until the SMs are covered.
+  const int64_t chunks = ceil_div(args->vocab * static_cast<int64_t>(elem_bytes(args->dtype)), kLpChunk);
   int cluster = 1;
-  while (cluster < 8 && args->rows * cluster * 2 <= ops->sm_count && cluster < steps) cluster *= 2;
-  const LpArgs a = kernel_args(args);
+  while (cluster < 8 && args->rows * cluster * 2 <= ops->sm_count && cluster < chunks) cluster *= 2;
+  const int64_t grid = cluster > 1 ? args->rows * cluster
+                                   : std::min<int64_t>(args->rows, static_cast<int64_t>(ops->sm_count) * kLpBlocks);
+  const LpArgs a = kernel_args(ops, args);
   cudaError_t e;
   if (args->dtype == GEMM_IN_F32)
-    e = forward<float>(a, args->rows, cluster, stream);
+    e = forward<float>(a, grid, cluster, stream);
   else if (args->dtype == GEMM_IN_BF16)
-    e = forward<__nv_bfloat16>(a, args->rows, cluster, stream);
+    e = forward<__nv_bfloat16>(a, grid, cluster, stream);
   else
-    e = forward<__half>(a, args->rows, cluster, stream);
+    e = forward<__half>(a, grid, cluster, stream);
   return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "log probability launch");
 }
 
@@ -652,14 +945,14 @@ gemm_status_t gemm_token_logprobs_backward(gemm_ops_t* ops, const gemm_logprobs_
   OpsDevice guard(ops->device);
   if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  const LpArgs a = kernel_args(args);
+  const LpArgs a = kernel_args(ops, args);
   cudaError_t e;
   if (args->dtype == GEMM_IN_F32)
-    e = backward<float>(a, args->rows, stream);
+    e = backward<float>(a, stream);
   else if (args->dtype == GEMM_IN_BF16)
-    e = backward<__nv_bfloat16>(a, args->rows, stream);
+    e = backward<__nv_bfloat16>(a, stream);
   else
-    e = backward<__half>(a, args->rows, stream);
+    e = backward<__half>(a, stream);
   return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "log probability gradient launch");
 }
 

@@ -284,6 +284,7 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
   for (auto set : {block_set_smem_nt, block_set_smem_nn, block_set_smem_tn, block_set_smem_gated,
                    block_set_smem_gated_bwd})
     if (e == cudaSuccess) e = set(ops->smem_optin);
+  if (e == cudaSuccess) e = logprobs_set_smem();
   const size_t flags = static_cast<size_t>(ops->sm_count) * 4 * sizeof(int);
   if (e == cudaSuccess) e = cudaMalloc(&ops->d_status, 4 * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(ops->d_status, 0, 4 * sizeof(int));

@@ -102,6 +102,8 @@ struct BlockProblem {
 // Workspace for the fp32 partials of split tiles, enough for any product.
 size_t block_workspace(const gemm_ops* ops);
 
+cudaError_t logprobs_set_smem();  // logprobs.cu
+
 gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, cudaStream_t stream);
 
 }  // namespace spgemm

@@ -94,6 +94,12 @@ def _check(status, where):
         raise GemmError(status, where, gemm_last_error())
 
 
+def _stream(device):
+    """The raw handle of the device's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _handle(device, stream):
     """The handle of a device and stream (one handle serves one stream)."""
     key = (device.index, stream)
@@ -141,13 +147,12 @@ def _rows(t, cols, name):
     return rows, t.stride(0)
 
 
-def _on_cuda(first, **tensors):
+def _on_cuda(device, tensor, name):
     import torch
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-        if t.device != first.device:
-            raise ValueError("all tensors must be on the same device (%s is not)" % name)
+    if not isinstance(tensor, torch.Tensor) or not tensor.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if tensor.device != device:
+        raise ValueError("all tensors must be on the same device (%s is not)" % name)
 
 
 def _output(out, shape, dtype, device, name="out"):
@@ -176,9 +181,9 @@ def _ffn_args(x, w_in, w_out, act):
     import torch
     if act not in GEMM_ACT:
         raise ValueError("act must be one of %s" % ", ".join(sorted(GEMM_ACT)))
-    if not isinstance(x, torch.Tensor):
-        raise ValueError("x must be a CUDA tensor")
-    _on_cuda(x, x=x, w_in=w_in, w_out=w_out)
+    _on_cuda(getattr(x, "device", None), x, "x")
+    _on_cuda(x.device, w_in, "w_in")
+    _on_cuda(x.device, w_out, "w_out")
     if x.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("x must be float16 or bfloat16, got %s" % x.dtype)
     if w_in.dtype != x.dtype or w_out.dtype != x.dtype:
@@ -197,16 +202,16 @@ def _ffn_args(x, w_in, w_out, act):
                    w_out=w_out.data_ptr(), lddy=d)
 
 
-def _run(name, device, args, query, run):
+def _run(name, device, query, run):
     """Workspace from the caching allocator of the current stream, then the call."""
     import torch
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _stream(device)
     h = _handle(device, stream)
     need = _sz()
-    _check(query(h, need), name + "_workspace")
-    with torch.cuda.device(device):
-        ws = torch.empty(max(1, need.value), dtype=torch.uint8, device=device)
-    _check(run(h, ws.data_ptr(), need.value, stream), name)
+    _check(query(h, ctypes.byref(need)), name)
+    n = need.value
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _check(run(h, ws.data_ptr(), n, stream), name)
 
 
 def gated_ffn(x, w_in, w_out, act="silu", out=None, save=False):
@@ -233,8 +238,7 @@ def gated_ffn(x, w_in, w_out, act="silu", out=None, save=False):
         kept = GatedKept(buf, a.tokens, a.d_model, a.d_inner, x.dtype, act)
     if a.tokens:
         ref = ctypes.byref(a)
-        _run("gemm_ffn_run", x.device, a,
-             lambda h, n: lib.gemm_ffn_workspace(h, ref, 0, ctypes.byref(n)),
+        _run("gemm_ffn_run", x.device, lambda h, n: lib.gemm_ffn_workspace(h, ref, 0, n),
              lambda h, w, n, s: lib.gemm_ffn_run(h, ref, w, n, s))
     return (y, kept) if save else y
 
@@ -250,7 +254,7 @@ def gated_ffn_backward(dy, x, w_in, w_out, kept, need=(True, True, True), out=(N
     if not isinstance(kept, GatedKept):
         raise TypeError("kept must come from gated_ffn(..., save=True)")
     a = _ffn_args(x, w_in, w_out, kept.act)
-    _on_cuda(x, dy=dy)
+    _on_cuda(x.device, dy, "dy")
     if dy.dtype != x.dtype or dy.shape != x.shape:
         raise ValueError("dy must have x's shape and dtype")
     if (a.tokens, a.d_model, a.d_inner, x.dtype) != kept[1:5] or kept.buffer.device != x.device:
@@ -264,8 +268,7 @@ def gated_ffn_backward(dy, x, w_in, w_out, kept, need=(True, True, True), out=(N
              for want, o, (shape, name) in zip(need, out, shapes)]
     a.dx, a.dw_in, a.dw_out = map(_ptr, grads)
     ref = ctypes.byref(a)
-    _run("gemm_ffn_backward", x.device, a,
-         lambda h, n: lib.gemm_ffn_workspace(h, ref, 1, ctypes.byref(n)),
+    _run("gemm_ffn_backward", x.device, lambda h, n: lib.gemm_ffn_workspace(h, ref, 1, n),
          lambda h, w, n, s: lib.gemm_ffn_backward(h, ref, w, n, s))
     return tuple(grads)
 
@@ -282,9 +285,7 @@ def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
     momentum is g.
     """
     import torch
-    if not isinstance(g, torch.Tensor):
-        raise ValueError("g must be a CUDA tensor")
-    _on_cuda(g, g=g)
+    _on_cuda(getattr(g, "device", None), g, "g")
     codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
     if g.dtype not in codes:
         raise TypeError("g must be float32, float16 or bfloat16, got %s" % g.dtype)
@@ -304,9 +305,8 @@ def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
                           b=coeffs[1], c=coeffs[2], eps=eps)
     lib = _lib()
     ref = ctypes.byref(a)
-    _run("gemm_orthogonalize", g.device, a,
-         lambda h, need: lib.gemm_orthogonalize_workspace(h, ref, ctypes.byref(need)),
-         lambda h, w, need, s: lib.gemm_orthogonalize(h, ref, w, need, s))
+    _run("gemm_orthogonalize", g.device, lambda h, n: lib.gemm_orthogonalize_workspace(h, ref, n),
+         lambda h, w, n, s: lib.gemm_orthogonalize(h, ref, w, n, s))
     return y
 
 
@@ -320,9 +320,7 @@ TokenLogprobs = collections.namedtuple("TokenLogprobs",
 
 def _logprobs_args(logits, tokens):
     import torch
-    if not isinstance(logits, torch.Tensor):
-        raise ValueError("logits must be a CUDA tensor")
-    _on_cuda(logits, logits=logits)
+    _on_cuda(getattr(logits, "device", None), logits, "logits")
     codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
     if logits.dtype not in codes:
         raise TypeError("logits must be float32, float16 or bfloat16, got %s" % logits.dtype)
@@ -330,7 +328,7 @@ def _logprobs_args(logits, tokens):
         raise ValueError("logits must have at least one column")
     rows, ld = _rows(logits, logits.shape[-1], "logits")
     if tokens is not None:
-        _on_cuda(logits, tokens=tokens)
+        _on_cuda(logits.device, tokens, "tokens")
         if tokens.dtype != torch.int64:
             raise TypeError("tokens must be int64, got %s" % tokens.dtype)
         if tokens.shape != logits.shape[:-1] or not tokens.is_contiguous():
@@ -359,17 +357,21 @@ def token_logprobs(logits, tokens=None, top_k=0):
         raise ValueError("top_k must be in [0, min(%d, columns)]" % MAX_TOP_K)
     a.top_k = top_k
     shape, dev = logits.shape[:-1], logits.device
-    out = torch.empty((2 if tokens is None else 3,) + tuple(shape), dtype=torch.float32, device=dev)
-    lse, entropy = out[0], out[1]
-    logprobs = out[2] if tokens is not None else None
+    out = torch.empty((2 if tokens is None else 3, *shape), dtype=torch.float32, device=dev)
+    logprobs = None
+    if tokens is None:
+        lse, entropy = out.unbind(0)
+    else:
+        lse, entropy, logprobs = out.unbind(0)
     top_lp = top_ids = None
     if top_k:
-        top_lp = torch.empty(tuple(shape) + (top_k,), dtype=torch.float32, device=dev)
-        top_ids = torch.empty(tuple(shape) + (top_k,), dtype=torch.int64, device=dev)
-    a.logprobs, a.entropy, a.lse, a.top_logprobs, a.top_ids = map(
-        _ptr, (logprobs, entropy, lse, top_lp, top_ids))
+        top_lp = torch.empty((*shape, top_k), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((*shape, top_k), dtype=torch.int64, device=dev)
+        a.top_logprobs, a.top_ids = top_lp.data_ptr(), top_ids.data_ptr()
+    a.lse, a.entropy = lse.data_ptr(), entropy.data_ptr()
+    a.logprobs = _ptr(logprobs)
     if a.rows:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _stream(dev)
         _check(_lib().gemm_token_logprobs(_handle(dev, stream), ctypes.byref(a), stream),
                "gemm_token_logprobs")
     return TokenLogprobs(logprobs, entropy, lse, top_lp, top_ids)
@@ -391,12 +393,12 @@ def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=N
                     ("d_entropy", d_entropy)):
         if t is None and name.startswith("d_"):
             continue
-        _on_cuda(logits, **{name: t})
+        _on_cuda(logits.device, t, name)
         if t.dtype != torch.float32 or t.shape != logits.shape[:-1] or not t.is_contiguous():
             raise ValueError("%s must be contiguous float32, one for each row of logits" % name)
     if out is None:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    _on_cuda(logits, out=out)
+    _on_cuda(logits.device, out, "out")
     if out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' shape and dtype")
     a.ldd = _rows(out, a.vocab, "out")[1]
@@ -404,7 +406,7 @@ def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=N
         _ptr, (result.lse, result.entropy, d_logprobs, d_entropy, out))
     if a.rows:
         dev = logits.device
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _stream(dev)
         _check(_lib().gemm_token_logprobs_backward(_handle(dev, stream), ctypes.byref(a), stream),
                "gemm_token_logprobs_backward")
     return out
