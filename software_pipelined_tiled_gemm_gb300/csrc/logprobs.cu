@@ -19,15 +19,17 @@
 // within reach of that floor (all masked by a lowest value) or near the
 // type's top is summed again by the slow form (x - m).
 //
-// Alternatives.  While streaming, each thread also keeps the largest of its
-// elements and the first 16-byte vector that holds it.  The k-th largest of
-// these is a lower bound of the row's k-th largest element, so only the
-// threads at or above it (about k of them) have anything to offer: their
-// vectors are read again (from L2), the few elements at or above the bound
-// are collected and ranked.  A key of (value, column) orders equal values by
-// column, and the bound is a pair too, so a row of equal logits offers no
-// more than the first k vectors.  A row that offers more than the list holds
-// (its largest elements all in a few threads' vectors) is searched k times.
+// Alternatives.  While streaming, each thread also keeps its largest element,
+// the first 16-byte vector that holds it and the largest of its other
+// vectors.  As keys (value, then lower column first), the k-th largest of 32,
+// 64 or 128 groups of threads (at least twice k) is a lower bound of the
+// row's k-th best, so only the threads at or above it (k to 2 k of them) have
+// anything to offer: each reads its best vector again (from L2), and the few
+// whose other vectors reach the bound too have all of theirs read by the
+// block.  The elements at or above the bound are collected and ranked.  The
+// column in the bound keeps a row of equal logits from offering more than its
+// first vectors.  A row that offers more than the list holds (its largest
+// elements all in a few threads' vectors) is searched k times.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,13 +44,17 @@ using namespace spgemm;
 
 namespace {
 
-constexpr int kLpThreads = 256;       // that compute; one warp more copies
-constexpr int kLpWarps = kLpThreads / 32;
+// Threads of a block that compute (one warp more copies): small blocks where
+// each takes whole rows, since a block's warps wait for one another several
+// times a row (8192 x 500 bf16: 128 threads and five blocks an SM 18 us, 256
+// and three 48 us); larger ones where a cluster shares a row (one row of
+// 131072, 20 alternatives: 256 threads 10 us, 128 threads 14 us).
+constexpr int kRowThreads = 128, kRowBlocks = 5;
+constexpr int kShareThreads = 256;
 constexpr int kLpUnroll = 4;          // vectors of a thread in a chunk
-constexpr int kLpChunkVecs = kLpUnroll * kLpThreads;
-constexpr uint32_t kLpChunk = kLpChunkVecs * 16u;
 constexpr int kLpStages = 4;          // chunks of a block's ring
-constexpr int kLpBlocks = 3;          // blocks an SM holds
+template <int kThreads>
+constexpr uint32_t kChunkBytes = kThreads * kLpUnroll * 16u;
 constexpr int kLpCandidates = 1024;
 constexpr int kMaxTopK = GEMM_LOGPROBS_MAX_TOP_K;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -269,142 +275,161 @@ __device__ __forceinline__ void lower(float d, float& s, float& w) {
   s *= f;
 }
 
-__device__ __forceinline__ Stats combine(Stats a, Stats b) {
-  Stats r;
-  r.m = max_nan(a.m, b.m);
-  r.n = fmaxf(a.n, b.n);
-  lower(r.n - a.n, a.s, a.w);
-  lower(r.n - b.n, b.s, b.w);
-  r.s = a.s + b.s;
-  r.w = a.w + b.w;
-  return r;
+// Combines the threads of each group of kLanes lanes, for all of them alike:
+// the largest reference first, then plain sums in a fixed order.
+template <int kLanes>
+__device__ __forceinline__ void warp_combine(Stats& t) {
+  float n = t.n;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    t.m = max_nan(t.m, __shfl_xor_sync(0xffffffffu, t.m, o));
+    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+  }
+  lower(n - t.n, t.s, t.w);
+  t.n = n;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
+    t.w += __shfl_xor_sync(0xffffffffu, t.w, o);
+  }
 }
 
-__device__ __forceinline__ Stats shuffle_xor(const Stats& a, int o) {
-  return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.n, o),
-          __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.w, o)};
-}
-
+template <int kThreads>
 struct LpShared {
   uint64_t full[kLpStages], empty[kLpStages];
-  Stats warp[2][kLpWarps];          // of this row and the last one
+  Stats warp[2][kThreads / 32];     // of this row and the last one
   Stats block;
-  int count;
+  int count, offering;
+  uint64_t bound;
   uint64_t best[kMaxTopK];          // this block's best keys, best first
   uint64_t list[kLpCandidates];
-  uint64_t reduce[kLpWarps];
+  uint64_t group[2 * kMaxTopK];     // the largest key of each group of threads
+  int2 offer[kThreads];           // threads with more than one vector to read, and their best
 };
-constexpr size_t kLpSmem = 128 + kLpStages * static_cast<size_t>(kLpChunk) + sizeof(LpShared);
+template <int kThreads>
+constexpr size_t kLpSmem = 128 + kLpStages * static_cast<size_t>(kChunkBytes<kThreads>) + sizeof(LpShared<kThreads>);
 
-// Barriers of the computing warps.
-__device__ __forceinline__ void compute_sync() { ptx::named_barrier_sync(1, kLpThreads); }
-__device__ __forceinline__ int compute_count(bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.popc.u32 %0, 1, %2, p;\n\t}"
-      : "=r"(r)
-      : "r"(pred ? 1u : 0u), "n"(kLpThreads)
-      : "memory");
-  return static_cast<int>(r);
-}
-
+// Barrier of the computing warps.
+template <int kThreads>
+__device__ __forceinline__ void compute_sync() { ptx::named_barrier_sync(1, kThreads); }
 __device__ __forceinline__ uint64_t key_of(float x, int column) {
   return (static_cast<uint64_t>(order_of(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(column));
 }
 
 // Writes the k largest of list[0, n) to out, in order, and 0 in places that
-// no key takes.
+// no key takes.  Eight lanes count for one key.
+template <int kThreads>
 __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, int k, uint64_t* out) {
-  for (int i = threadIdx.x; i < k; i += kLpThreads)
+  for (int i = threadIdx.x; i < k; i += kThreads)
     if (i >= n) out[i] = 0;
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
-    const uint64_t mine = list[i];
+  for (int base = 0; base < n; base += kThreads / 8) {
+    const int i = base + static_cast<int>(threadIdx.x) / 8;
+    const uint64_t mine = i < n ? list[i] : 0;
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += list[j] > mine ? 1 : 0;
-    if (rank < k) out[rank] = mine;
+#pragma unroll 4
+    for (int j = threadIdx.x % 8; j < n; j += 8) rank += list[j] > mine ? 1 : 0;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (i < n && rank < k && threadIdx.x % 8 == 0) out[rank] = mine;
   }
 }
 
-// The k best of the columns this block streamed (vectors v0 + i kLpThreads +
-// thread below v1, and, with `edges`, the columns outside the vectors, one
-// to a thread), to sh.best.  top: order of this thread's largest element (0:
-// it has none); top_c: the first column of the vector that holds it.
-template <typename T>
-__device__ __noinline__ void block_top(const Row<T>& row, int v0, int v1, int edge, int k,
-                                       uint32_t top, int top_c, LpShared& sh) {
+// The k best of the columns this block streamed (vectors v0 + i kThreads +
+// thread below v1, and `edge`, the thread's column outside the vectors or
+// -1), to sh.best.  top, top_v, second: this thread's largest element, the
+// first vector that holds it and the largest element of its other vectors.
+// nan: the row holds one, which these do not show.
+template <typename T, int kThreads>
+__device__ __noinline__ void block_top(const Row<T>& row, int v0, int v1, int edge, int k, float top,
+                                       int top_v, float second, bool nan, LpShared<kThreads>& sh) {
   constexpr int kN = Row<T>::kN;
-  const int tid = threadIdx.x, lane = tid & 31;
-  // The bound: the largest order that at least k threads reach (0 if fewer
-  // have anything), or one that k to 2 k threads reach.
-  uint32_t lo = 0, hi = 0xffffffffu;
-  int reach = kLpThreads;
-  if (compute_count(top == 0xffffffffu) >= k) lo = hi;  // NaNs
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const int c = compute_count(top >= mid);
-    if (c >= k) {
-      lo = mid;
-      reach = c;
-      if (c <= 2 * k) break;
-    } else {
-      hi = mid;
-    }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // 32, 64 or 128 groups of threads: at least two for each of the k.
+  const int span = kThreads / (k <= 16 ? 32 : (k <= 32 ? 64 : 128));
+  const uint64_t key = v0 + tid < v1 ? key_of(top, row.column(top_v)) : 0;
+  uint64_t best = key;
+  for (int o = span / 2; o > 0; o >>= 1) {
+    const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
+    best = other > best ? other : best;
   }
-  // Many threads end on the same value: of those, the first columns only.
-  int last_c = 0x7fffffff;
-  if (lo > 0 && reach > 2 * k) {
-    const int want = k - compute_count(top > lo);
-    int a = -1, b = 0x7fffffff;  // count(top_c <= a) < want <= count(top_c <= b)
-    while (b - a > 1) {
-      const int mid = a + (b - a) / 2;
-      if (compute_count(top == lo && top_c <= mid) >= want)
-        b = mid;
-      else
-        a = mid;
-    }
-    last_c = b;
+  if (tid % span == 0) sh.group[tid / span] = best;
+  if (tid == 0) {
+    sh.count = sh.offering = 0;
+    sh.bound = 0;
   }
-  if (tid == 0) sh.count = 0;
-  compute_sync();
-  auto take = [&](float x, int c, int first) {
-    const uint32_t o = order_of(x);
-    if (o > lo || (o == lo && first <= last_c)) {
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < kLpCandidates) sh.list[at] = key_of(x, c);
-    }
+  compute_sync<kThreads>();
+  // The bound: the k-th of the groups' keys (0 if fewer than k have one).  A
+  // group's threads share the counting of its rank.
+  {
+    const int groups = kThreads / span;
+    int rank = 0;
+#pragma unroll 4
+    for (int j = tid % span; j < groups; j += span) rank += sh.group[j] > best ? 1 : 0;
+    for (int o = span / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (rank == k - 1 && best != 0 && tid % span == 0) sh.bound = best;  // keys are distinct
+  }
+  compute_sync<kThreads>();
+  const uint64_t bound = sh.bound;
+  const float bound_x = value_of(static_cast<uint32_t>(bound >> 32));
+  const int bound_c = static_cast<int>(0xffffffffu - static_cast<uint32_t>(bound));
+  // Whether an element of the vector from column `first` is at or above it.
+  auto reaches = [&](float x, int first) {
+    return bound == 0 || x > bound_x || (x == bound_x && first <= bound_c);
   };
-  if (edge >= 0) take(Vec<T>::get(row.p[edge]), edge, edge);
-  const bool offers = top > lo || (top == lo && top != 0 && top_c <= last_c);
-  uint32_t ask = __ballot_sync(0xffffffffu, offers);
-  while (ask) {  // the warp reads one offering thread's vectors together
-    const int src = __ffs(ask) - 1;
-    ask &= ask - 1;
-    for (int v = v0 + (tid - lane + src) + lane * kLpThreads; v < v1; v += 32 * kLpThreads) {
-      float x[kN];
-      Vec<T>::unpack(__ldg(row.at(v)), x);
+  auto take = [&](const uint4& w, int first) {
+    float x[kN];
+    Vec<T>::unpack(w, x);
+    uint32_t mask = 0;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) take(x[j], row.column(v) + j, row.column(v));
+    for (int j = 0; j < kN; ++j) mask |= reaches(x[j], first) ? 1u << j : 0u;
+    if (mask == 0) return;
+    int at = atomicAdd(&sh.count, __popc(mask));
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      if ((mask >> j) & 1u) {
+        if (at < kLpCandidates) sh.list[at] = key_of(x[j], first + j);
+        ++at;
+      }
+  };
+  if (edge >= 0) {
+    const float x = Vec<T>::get(row.p[edge]);
+    if (reaches(x, edge)) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kLpCandidates) sh.list[at] = key_of(x, edge);
     }
   }
-  compute_sync();
+  if (key != 0 && key >= bound) {
+    take(__ldg(row.at(top_v)), row.column(top_v));
+    // Its other vectors lie at other columns, any of which may be within the bound's.
+    if (bound == 0 || second >= bound_x) sh.offer[atomicAdd(&sh.offering, 1)] = make_int2(tid, top_v);
+  }
+  compute_sync<kThreads>();
+  // The other vectors of the threads that have more to offer, a thread's by a warp.
+  const int offering = sh.offering;
+#pragma unroll 1
+  for (int o = warp; o < offering; o += (kThreads / 32)) {
+    const int2 who = sh.offer[o];
+#pragma unroll 1
+    for (int v = v0 + who.x + lane * kThreads; v < v1; v += 32 * kThreads)
+      if (v != who.y) take(__ldg(row.at(v)), row.column(v));
+  }
+  compute_sync<kThreads>();
   const int n = sh.count;
-  if (n <= kLpCandidates) {
-    rank_keys(sh.list, n, k, sh.best);
-    compute_sync();
+  if (n <= kLpCandidates && !nan) {
+    rank_keys<kThreads>(sh.list, n, k, sh.best);
+    compute_sync<kThreads>();
     return;
   }
-  // More than the list holds: the largest key below the last one, k times.
+  // More than the list holds, or NaN: the largest key below the last one, k times.
   uint64_t below = ~0ull;
   for (int i = 0; i < k; ++i) {
-    uint64_t best = 0;
+    best = 0;
     auto offer = [&](float x, int c) {
-      const uint64_t key = key_of(x, c);
-      if (key < below && key > best) best = key;
+      const uint64_t candidate = key_of(x, c);
+      if (candidate < below && candidate > best) best = candidate;
     };
     if (edge >= 0) offer(Vec<T>::get(row.p[edge]), edge);
-    for (int v = v0 + tid; v < v1; v += kLpThreads) {
+    for (int v = v0 + tid; v < v1; v += kThreads) {
       float x[kN];
       Vec<T>::unpack(__ldg(row.at(v)), x);
 #pragma unroll
@@ -415,19 +440,19 @@ __device__ __noinline__ void block_top(const Row<T>& row, int v0, int v1, int ed
       const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
       best = other > best ? other : best;
     }
-    if (lane == 0) sh.reduce[tid >> 5] = best;
-    compute_sync();
-    for (int j = 0; j < kLpWarps; ++j) best = sh.reduce[j] > best ? sh.reduce[j] : best;
+    if (lane == 0) sh.group[tid >> 5] = best;
+    compute_sync<kThreads>();
+    for (int j = 0; j < (kThreads / 32); ++j) best = sh.group[j] > best ? sh.group[j] : best;
     if (tid == 0) sh.best[i] = best;
     below = best;
-    compute_sync();
+    compute_sync<kThreads>();
   }
 }
 
 // The sums of this block's share of a row whose maximum m (finite) is outside
 // the fast form's range: t = (x - m) L, the difference first.  The reference
 // of the result is m itself.
-template <typename T>
+template <typename T, int kThreads>
 __device__ __noinline__ void slow_sums(const Row<T>& row, int v0, int v1, int edge, float m, Stats& t) {
   t.s = t.w = 0.0f;
   auto add = [&](float x) {
@@ -436,7 +461,7 @@ __device__ __noinline__ void slow_sums(const Row<T>& row, int v0, int v1, int ed
     t.w = fmaf(e, e2, t.w);
   };
   if (edge >= 0) add(Vec<T>::get(row.p[edge]));
-  for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kLpThreads) {
+  for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads) {
     float x[Row<T>::kN];
     Vec<T>::unpack(__ldg(row.at(v)), x);
 #pragma unroll
@@ -474,35 +499,38 @@ __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const L
 }
 
 // A row's sums over the block: into sh.block by warp 0, in a fixed order.
-__device__ __forceinline__ Stats block_stats(Stats t, LpShared& sh, int parity) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t = combine(t, shuffle_xor(t, o));
+template <int kThreads>
+__device__ __forceinline__ Stats block_stats(Stats t, LpShared<kThreads>& sh, int parity) {
+  warp_combine<32>(t);
   if ((threadIdx.x & 31) == 0) sh.warp[parity][threadIdx.x >> 5] = t;
-  compute_sync();
-  t = sh.warp[parity][threadIdx.x & (kLpWarps - 1)];
-#pragma unroll
-  for (int o = kLpWarps / 2; o > 0; o >>= 1) t = combine(t, shuffle_xor(t, o));
+  compute_sync<kThreads>();
+  t = sh.warp[parity][threadIdx.x & (kThreads / 32 - 1)];
+  warp_combine<kThreads / 32>(t);
   return t;
 }
 
 // Rows row0, row0 + step, ... with one block each; or, launched as clusters
 // (few rows), one row per cluster, each block taking a share of its vectors.
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(const LpArgs a) {
+template <typename T, bool kTop, int kThreads>
+__global__ void __launch_bounds__(kThreads + 32, kThreads == kRowThreads ? kRowBlocks : 1)
+    logprobs_kernel(const LpArgs a) {
+  constexpr bool kCluster = kThreads == kShareThreads;
+  constexpr int kWarps = kThreads / 32, kChunkVecs = kThreads * kLpUnroll;
+  constexpr uint32_t kChunk = kChunkBytes<kThreads>;
   constexpr int kN = Vec<T>::kN;
   extern __shared__ uint8_t lp_smem[];
   uint8_t* ring = lp_smem + ((128u - (ptx::smem_addr(lp_smem) & 127u)) & 127u);
-  LpShared& sh = *reinterpret_cast<LpShared*>(ring + kLpStages * kLpChunk);
+  LpShared<kThreads>& sh = *reinterpret_cast<LpShared<kThreads>*>(ring + kLpStages * kChunk);
   const uint32_t ring_addr = ptx::smem_addr(ring);
   const uint32_t full = ptx::smem_addr(sh.full), empty = ptx::smem_addr(sh.empty);
-  const uint32_t blocks = cluster_size();
-  const uint32_t rank = blocks > 1 ? ptx::cluster_ctarank() : 0u;
+  const uint32_t blocks = kCluster ? cluster_size() : 1u;
+  const uint32_t rank = kCluster ? ptx::cluster_ctarank() : 0u;
   const int64_t row0 = blockIdx.x / blocks, step = gridDim.x / blocks;
   const int tid = threadIdx.x;
   if (tid == 0) {
     for (int i = 0; i < kLpStages; ++i) {
       ptx::mbar_init(full + 8u * i, 1);
-      ptx::mbar_init(empty + 8u * i, kLpWarps);
+      ptx::mbar_init(empty + 8u * i, kWarps);
     }
     ptx::fence_barrier_init();
   }
@@ -515,9 +543,9 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
     v1 = static_cast<int>(static_cast<int64_t>(row.vectors) * (rank + 1) / blocks);
   };
 
-  if (tid >= kLpThreads) {
+  if (tid >= kThreads) {
     // ------------------------------------------------------------ producer --
-    if (tid == kLpThreads) {
+    if (tid == kThreads) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -527,17 +555,17 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
         const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
         int v0, v1;
         share(row, v0, v1);
-        for (int v = v0; v < v1; v += kLpChunkVecs) {
+        for (int v = v0; v < v1; v += kChunkVecs) {
           if (!ring_wait(empty + 8u * stage, phase ^ 1u, a, kDetailProducerEmpty)) {
             ok = false;
             break;
           }
-          const uint32_t bytes = static_cast<uint32_t>(min(v1 - v, kLpChunkVecs)) * 16u;
+          const uint32_t bytes = static_cast<uint32_t>(min(v1 - v, kChunkVecs)) * 16u;
           ptx::mbar_arrive_expect_tx(full + 8u * stage, bytes);
           if constexpr (kTop)  // read again, in part
-            ptx::bulk_load(ring_addr + stage * kLpChunk, row.at(v), bytes, full + 8u * stage);
+            ptx::bulk_load(ring_addr + stage * kChunk, row.at(v), bytes, full + 8u * stage);
           else
-            ptx::bulk_load_hint(ring_addr + stage * kLpChunk, row.at(v), bytes, full + 8u * stage, pol);
+            ptx::bulk_load_hint(ring_addr + stage * kChunk, row.at(v), bytes, full + 8u * stage, pol);
           used |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           if (++stage == kLpStages) {
@@ -551,7 +579,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
         if (used & (1u << i)) ring_wait(full + 8u * i, (parity >> i) & 1u, a, kDetailProducerDrain);
     }
     __syncwarp();
-    if (blocks > 1) {
+    if constexpr (kCluster) {
       ptx::cluster_sync();
       ptx::cluster_sync();
     }
@@ -563,7 +591,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
   uint32_t phase = 0;
   const F2 l2 = pack_f2(kLog2e, kLog2e);
   bool ok = true;
-  for (int64_t r = row0; r < a.rows; r += step, turn ^= 1) {
+  for (int64_t r = row0; r < a.rows; r += step, ++turn) {
     const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, a.vocab);
     int v0, v1;
     share(row, v0, v1);
@@ -572,10 +600,20 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
     const int edge = tid < row.edges() && rank == (tid < row.head ? 0u : blocks - 1u)
                          ? row.edge_column(tid)
                          : -1;
+    // One warp writes the row's results, another one each row: its first lane
+    // has the token's logit by then.
+    const bool writer = tid == (turn % kWarps) * 32;
+    int64_t token = -1;
+    float token_x = 0.0f;
+    if (writer && a.tokens && a.logprobs && rank == 0) {
+      token = a.tokens[r];
+      if (token >= 0 && token < a.vocab) token_x = Vec<T>::get(row.p[token]);
+    }
     Stats t = {-INFINITY, Fast<T>::kStart, 0.0f, 0.0f};
     F2 s2 = 0, w2 = 0;  // (0.0f, 0.0f)
-    uint32_t top = 0;
-    int top_c = 0;
+    float top = -INFINITY;  // the largest element of this thread's vectors,
+    int top_v = v0 + tid;   // the first that holds it,
+    float second = -INFINITY;  // and the largest of the others'
     // A larger element (its x L, not above the next integer) moves the reference.
     auto reach = [&](float m) {
       t.m = max_nan(t.m, m);
@@ -594,21 +632,19 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
     };
     if (edge >= 0) {
       const float x = Vec<T>::get(row.p[edge]);
-      top = order_of(x);
-      top_c = edge;
       reach(x);
       const float e2 = fmaf(fmaxf(x, Fast<T>::kFloor), kLog2e, -t.n), e = exp2_approx(e2);
       s2 = add_f2(s2, pack_f2(e, 0.0f));
       w2 = add_f2(w2, pack_f2(e * e2, 0.0f));
     }
-    for (int v = v0; v < v1; v += kLpChunkVecs) {
+    for (int v = v0; v < v1; v += kChunkVecs) {
       if (ok) ok = ring_wait(full + 8u * stage, phase, a, kDetailMmaFull);
-      const uint32_t src = ring_addr + stage * kLpChunk + static_cast<uint32_t>(tid) * 16u;
-      const int left = v1 - v - tid;  // this thread's vectors: u kLpThreads < left
+      const uint32_t src = ring_addr + stage * kChunk + static_cast<uint32_t>(tid) * 16u;
+      const int left = v1 - v - tid;  // this thread's vectors: u kThreads < left
       uint4 w[kLpUnroll];
 #pragma unroll
       for (int u = 0; u < kLpUnroll; ++u)
-        if (u * kLpThreads < left) w[u] = ptx::ld_shared_v4(src + u * (kLpThreads * 16u));
+        if (u * kThreads < left) w[u] = ptx::ld_shared_v4(src + u * (kThreads * 16u));
       // The slot goes back at once, and the next copy may land at once: these
       // reads come before it only by a fence between the two proxies.
       ptx::fence_proxy_async_smem();
@@ -621,14 +657,14 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
       float m = -INFINITY;
 #pragma unroll
       for (int u = 0; u < kLpUnroll; ++u)
-        if (u * kLpThreads < left) {
+        if (u * kThreads < left) {
           const float vm = Fast<T>::max(w[u]);
           m = max_nan(m, vm);
           if constexpr (kTop) {
-            const uint32_t o = order_of(vm);
-            if (o > top) {
-              top = o;
-              top_c = row.column(v + tid + u * kLpThreads);
+            second = fmaxf(second, fminf(vm, top));
+            if (vm > top) {
+              top = vm;
+              top_v = v + tid + u * kThreads;
             }
           }
         }
@@ -636,7 +672,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
       const F2 n2 = pack_f2(-t.n, -t.n);
 #pragma unroll
       for (int u = 0; u < kLpUnroll; ++u)
-        if (u * kLpThreads < left) {
+        if (u * kThreads < left) {
           F2 x[kN / 2];
           Fast<T>::pairs(w[u], x);
 #pragma unroll
@@ -657,44 +693,50 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
       t.s = sa + sb;
       t.w = wa + wb;
     }
-    t = block_stats(t, sh, turn);  // the same in every warp
-    if constexpr (kTop) block_top<T>(row, v0, v1, edge, a.top_k, top, top_c, sh);
+    t = block_stats(t, sh, turn & 1);  // the same in every warp
+    if constexpr (kTop)
+      block_top<T, kThreads>(row, v0, v1, edge, a.top_k, top, top_v, second, t.m != t.m, sh);
 
     // The blocks of a cluster share their sums (their maxima, if the slow
     // form is needed: then again).
-    if (blocks > 1) {
+    if constexpr (kCluster) {
       if (tid == 0) sh.block = t;
       ptx::cluster_sync();
-      const uint32_t at = ptx::smem_addr(&sh.block);
-      Stats all = {peer_f32(at, 0), peer_f32(at + 4, 0), peer_f32(at + 8, 0), peer_f32(at + 12, 0)};
-      for (uint32_t b = 1; b < blocks; ++b)
-        all = combine(all, Stats{peer_f32(at, b), peer_f32(at + 4, b), peer_f32(at + 8, b), peer_f32(at + 12, b)});
-      t = all;
+      const uint32_t at = ptx::smem_addr(&sh.block), peer = tid & 7;
+      t = {-INFINITY, -INFINITY, 0.0f, 0.0f};
+      if (peer < blocks)
+        t = {peer_f32(at, peer), peer_f32(at + 4, peer), peer_f32(at + 8, peer), peer_f32(at + 12, peer)};
+      warp_combine<8>(t);
       if constexpr (kTop) {
         if (rank == 0) {
           const uint32_t best = ptx::smem_addr(sh.best);
           const int n = static_cast<int>(blocks) * a.top_k;
-          for (int i = tid; i < n; i += kLpThreads)
-            sh.list[i] = peer_u64(best + 8u * (i % a.top_k), i / a.top_k);
-          compute_sync();
-          rank_keys(sh.list, n, a.top_k, sh.best);
-          compute_sync();
+          for (uint32_t b = tid / 32; b < blocks; b += kWarps)
+            for (int i = tid % 32; i < a.top_k; i += 32)
+              sh.list[b * a.top_k + i] = peer_u64(best + 8u * i, b);
+          compute_sync<kThreads>();
+          rank_keys<kThreads>(sh.list, n, a.top_k, sh.best);
+          compute_sync<kThreads>();
         }
       }
     }
     const bool slow = t.m > -INFINITY && t.m < INFINITY && !(t.m > Fast<T>::kLow && t.m < Fast<T>::kHigh);
     if (slow && rank == 0) {  // a cluster's first block sums the whole row
       Stats u = {t.m, 0.0f, 0.0f, 0.0f};
-      slow_sums<T>(row, 0, row.vectors, tid < row.edges() ? row.edge_column(tid) : -1, t.m, u);
-      compute_sync();  // the last row's sums have been read
-      t = block_stats(u, sh, turn);
+      slow_sums<T, kThreads>(row, 0, row.vectors, tid < row.edges() ? row.edge_column(tid) : -1, t.m, u);
+      compute_sync<kThreads>();  // the last row's sums have been read
+      t = block_stats(u, sh, turn & 1);
     }
-    if (blocks > 1) {
-      ptx::cluster_sync();  // no block leaves while another reads its memory
-      if (rank != 0) return;
+    if constexpr (kCluster) {  // no block leaves while another reads its memory
+      ptx::cluster_arrive();
+      if (rank != 0) {
+        ptx::cluster_wait();
+        return;
+      }
     }
-    // Both are taken from the largest element, whose own term e_m the sums
-    // hold exactly: a row with one possible token has log p = 0 and H = 0.
+    if (!writer && !(kTop && tid < a.top_k)) continue;
+    // log p and H are taken from the largest element, whose own term e_m the
+    // sums hold exactly: a row with one possible token has log p = 0, H = 0.
     const float t_m = slow ? 0.0f : fmaf(t.m, kLog2e, -t.n);
     const float e_m = exp2_approx(t_m);
     const float log_s = log2f(t.s / e_m);
@@ -712,18 +754,15 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
       lse = h = NAN;
       none = true;
     }
-    if (tid == 0) {
+    if (writer) {
       if (a.lse) a.lse[r] = lse;
       if (a.entropy) a.entropy[r] = h;
       if (a.tokens && a.logprobs) {
-        const int64_t token = a.tokens[r];
         float lp = 0.0f;  // negative: the position does not count
-        if (token >= a.vocab) {
+        if (token >= a.vocab)
           lp = NAN;
-        } else if (token >= 0) {
-          const float x = Vec<T>::get(row.p[token]);
-          lp = none && x != -INFINITY ? NAN : log_p(x);
-        }
+        else if (token >= 0)
+          lp = none && token_x != -INFINITY ? NAN : log_p(token_x);
         a.logprobs[r] = lp;
       }
     }
@@ -735,6 +774,10 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocks) logprobs_kernel(co
         a.top_logprobs[r * a.top_k + tid] = none && x != -INFINITY ? NAN : log_p(x);
       }
     }
+  }
+  if constexpr (kCluster) {
+    __syncwarp();
+    ptx::cluster_wait();
   }
 }
 
@@ -817,8 +860,13 @@ cudaError_t launch_rows(void (*kernel)(P...), int64_t grid, int threads, size_t 
 
 template <typename T>
 cudaError_t forward(const LpArgs& a, int64_t grid, int cluster, cudaStream_t stream) {
-  return launch_rows(a.top_k > 0 ? logprobs_kernel<T, true> : logprobs_kernel<T, false>, grid,
-                     kLpThreads + 32, kLpSmem, cluster, stream, a);
+  if (cluster > 1)
+    return launch_rows(a.top_k > 0 ? logprobs_kernel<T, true, kShareThreads>
+                                   : logprobs_kernel<T, false, kShareThreads>,
+                       grid, kShareThreads + 32, kLpSmem<kShareThreads>, cluster, stream, a);
+  return launch_rows(a.top_k > 0 ? logprobs_kernel<T, true, kRowThreads>
+                                 : logprobs_kernel<T, false, kRowThreads>,
+                     grid, kRowThreads + 32, kLpSmem<kRowThreads>, 1, stream, a);
 }
 
 template <typename T>
@@ -899,13 +947,23 @@ LpArgs kernel_args(const gemm_ops* ops, const gemm_logprobs_args_t* g) {
 
 namespace spgemm {
 // More shared memory than a kernel gets by default (per device, once).
+template <typename T, int kThreads>
+static cudaError_t set_smem_of() {
+  const int bytes = static_cast<int>(kLpSmem<kThreads>);
+  const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T, false, kThreads>, attr, bytes);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(logprobs_kernel<T, true, kThreads>, attr, bytes);
+}
+template <typename T>
+static cudaError_t set_smem_both() {
+  const cudaError_t e = set_smem_of<T, kRowThreads>();
+  return e != cudaSuccess ? e : set_smem_of<T, kShareThreads>();
+}
+
 cudaError_t logprobs_set_smem() {
-  cudaError_t e = cudaSuccess;
-  for (auto k : {logprobs_kernel<float, false>, logprobs_kernel<float, true>,
-                 logprobs_kernel<__nv_bfloat16, false>, logprobs_kernel<__nv_bfloat16, true>,
-                 logprobs_kernel<__half, false>, logprobs_kernel<__half, true>})
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLpSmem));
+  cudaError_t e = set_smem_both<float>();
+  if (e == cudaSuccess) e = set_smem_both<__nv_bfloat16>();
+  if (e == cudaSuccess) e = set_smem_both<__half>();
   return e;
 }
 }  // namespace spgemm
@@ -921,11 +979,11 @@ gemm_status_t gemm_token_logprobs(gemm_ops_t* ops, const gemm_logprobs_args_t* a
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
   // Few rows: each is shared by a cluster of blocks, as many as keep one
   // chunk of vectors each, until the SMs are covered.
-  const int64_t chunks = ceil_div(args->vocab * static_cast<int64_t>(elem_bytes(args->dtype)), kLpChunk);
+  const int64_t chunks = ceil_div(args->vocab * static_cast<int64_t>(elem_bytes(args->dtype)), kChunkBytes<kShareThreads>);
   int cluster = 1;
   while (cluster < 8 && args->rows * cluster * 2 <= ops->sm_count && cluster < chunks) cluster *= 2;
   const int64_t grid = cluster > 1 ? args->rows * cluster
-                                   : std::min<int64_t>(args->rows, static_cast<int64_t>(ops->sm_count) * kLpBlocks);
+                                   : std::min<int64_t>(args->rows, static_cast<int64_t>(ops->sm_count) * kRowBlocks);
   const LpArgs a = kernel_args(ops, args);
   cudaError_t e;
   if (args->dtype == GEMM_IN_F32)

@@ -2,7 +2,8 @@
 //
 // Two passes over G normalise it: the sum of squares (one partial per block),
 // then X = 2^8 G / max(|G|, eps) in fp16 (every block adds the partials in the
-// same order).  Each step is three block products: A = X X^T and
+// same order).  Elements below 2^-40 and above 2^40 are squared at another
+// scale, so that the norm is right for any fp32 gradient.  Each step is three block products: A = X X^T and
 // B = b A + c A^2 on the tiles on and above the diagonal only, and
 // X' = a X + B X.  On matrices with more rows than columns the products use
 // X^T X and X B instead, reading X as it lies.
@@ -20,6 +21,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "ops_internal.h"
 #include "ptx.cuh"
@@ -40,7 +42,7 @@ struct NormArgs {
   int chunks;          // steps per row
   int64_t steps;       // steps per matrix
   int aligned;         // vectors of 8 elements may be loaded whole
-  float* partial;      // batch x gridDim.x
+  double* partial;     // batch x gridDim.x
   uint16_t* x;
   int64_t ldx;
   float eps;
@@ -87,11 +89,11 @@ __device__ __forceinline__ T block_sum(T v, T* shared) {
 
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) sum_squares_kernel(const NormArgs a) {
-  __shared__ float shared[kNormThreads / 32];
+  __shared__ double shared[kNormThreads / 32];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait_prior_grid();
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
-  float sum = 0.0f;
+  float sum = 0.0f, small = 0.0f, large = 0.0f;  // small x 2^60, large x 2^-60
   for (int64_t s = blockIdx.x; s < a.steps; s += gridDim.x) {
     const int64_t r = s / a.chunks;
     const int64_t c0 = (s - r * a.chunks) * kNormCols + threadIdx.x * 8;
@@ -102,10 +104,22 @@ __global__ void __launch_bounds__(kNormThreads) sum_squares_kernel(const NormArg
 #pragma unroll
     for (int i = 0; i < kNormVecs; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+      for (int j = 0; j < 8; ++j) {
+        const float x = v[i][j], size = fabsf(x);
+        if (sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value) {  // fp16: within range
+          sum = fmaf(x, x, sum);
+          continue;
+        }
+        const float lo = size < 0x1p-40f ? x * 0x1p60f : 0.0f, hi = size > 0x1p40f ? x * 0x1p-60f : 0.0f;
+        const float mid = size < 0x1p-40f || size > 0x1p40f ? 0.0f : x;  // NaN is here
+        small = fmaf(lo, lo, small);
+        sum = fmaf(mid, mid, sum);
+        large = fmaf(hi, hi, large);
+      }
   }
-  sum = block_sum<float>(sum, shared);
-  if (threadIdx.x == 0) a.partial[blockIdx.y * gridDim.x + blockIdx.x] = sum;
+  const double total = block_sum<double>(
+      static_cast<double>(sum) + static_cast<double>(small) * 0x1p-120 + static_cast<double>(large) * 0x1p120, shared);
+  if (threadIdx.x == 0) a.partial[blockIdx.y * gridDim.x + blockIdx.x] = total;
 }
 
 template <typename T>
@@ -115,9 +129,11 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const NormArgs 
   ptx::pdl_wait_prior_grid();
   double sum = 0.0;
   for (int i = threadIdx.x; i < parts; i += kNormThreads)
-    sum += static_cast<double>(__ldcg(a.partial + blockIdx.y * parts + i));
+    sum += __ldcg(a.partial + blockIdx.y * parts + i);
   sum = block_sum<double>(sum, shared);
-  const float scale = kIterateScale / fmaxf(static_cast<float>(sqrt(sum)), a.eps);
+  // The scale in two factors, each within fp32's range.  (NaN: no comparison holds.)
+  const double norm = sqrt(sum) < static_cast<double>(a.eps) ? static_cast<double>(a.eps) : sqrt(sum);
+  const float scale = static_cast<float>(sqrt(static_cast<double>(kIterateScale) / norm));
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
   uint16_t* x = a.x + blockIdx.y * a.m * a.ldx;
   for (int64_t s = blockIdx.x; s < a.steps; s += gridDim.x) {
@@ -133,7 +149,7 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const NormArgs 
       if (c < a.ldx) {
         __half2 h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(v[i][2 * j] * scale, v[i][2 * j + 1] * scale);
+        for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(v[i][2 * j] * scale * scale, v[i][2 * j + 1] * scale * scale);
         *reinterpret_cast<uint4*>(x + r * a.ldx + c) = *reinterpret_cast<const uint4*>(h);
       }
     }
@@ -166,7 +182,7 @@ cudaError_t normalize(const NormArgs& a, int64_t batch, int blocks, cudaStream_t
 
 struct Layout {
   float* partials;
-  float* norms;
+  double* norms;
   uint16_t* x[2];
   uint16_t* a;
   uint16_t* b;
@@ -187,7 +203,7 @@ Layout layout(const gemm_ops* ops, const gemm_orthogonalize_args_t* g, void* wor
   const size_t a = static_cast<size_t>(g->batch) * l.s * l.sp * 2;
   Carver c(workspace);
   l.partials = static_cast<float*>(c.take(block_workspace(ops)));
-  l.norms = static_cast<float*>(c.take(static_cast<size_t>(g->batch) * l.blocks * sizeof(float)));
+  l.norms = static_cast<double*>(c.take(static_cast<size_t>(g->batch) * l.blocks * sizeof(double)));
   l.x[0] = static_cast<uint16_t*>(c.take(x));
   l.x[1] = static_cast<uint16_t*>(c.take(x));
   l.a = static_cast<uint16_t*>(c.take(a));
