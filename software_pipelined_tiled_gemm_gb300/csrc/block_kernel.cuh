@@ -21,7 +21,7 @@
 //               products are done its ring is idle: it stages its fp32
 //               partial there, bulk-copies each CTA of the cluster the rows
 //               that one will store (a quarter or half of the tile), and adds
-//               what it receives itself in CTA order while it stores its
+//               its own and what it receives in CTA order while it stores its
 //               rows: the epilogue is shared out as well.
 //   last wave   stream-K with any number of walkers per tile: the walker
 //               holding a tile's first K slices owns it, the others publish
@@ -217,10 +217,21 @@ __device__ __forceinline__ void block_add_partials(uint32_t t_row, const float* 
     ptx::tmem_wait_ld();
     const float* src = partial + static_cast<size_t>(c) * 32 + lane;
 #pragma unroll 1
-    for (int n = 0; n < parts; ++n, src += partial_step)
+    for (int n = 0; n < parts; n += 2, src += 2 * partial_step) {  // two partials' loads in flight
+      const bool both = n + 1 < parts;
+      float v[2][32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        r[j] = __float_as_uint(__uint_as_float(r[j]) + __ldcg(src + j * 32));
+      for (int j = 0; j < 32; ++j) {
+        v[0][j] = __ldcg(src + j * 32);
+        v[1][j] = both ? __ldcg(src + partial_step + j * 32) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float sum = __uint_as_float(r[j]) + v[0][j];
+        if (both) sum += v[1][j];
+        r[j] = __float_as_uint(sum);
+      }
+    }
     ptx::tmem_st_32x32b_x32(t_row + c, r);
   }
   ptx::tmem_wait_st();
@@ -621,8 +632,6 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
         store(p.out0, maps.c0, sb, row0, col0, z);
         buf ^= 1;
       } else if constexpr (kEpi == kEpiGatedBwd) {
-        if (lead) ptx::bulk_wait_group_read<0>();
-        quarter_sync();
         const float* src = p.pre + (static_cast<int64_t>(row0 / 32) * p.N + col0) * 32 + lane;
         const int n = p.N - col0;
         float gate[2][16], up[2][16];  // this step's and the next one's
@@ -647,12 +656,15 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
           stage16(my_stage + kStoreBuf, lane, s, pu);
         };
         load_pre(s0, gate[0], up[0]);
+        load_pre(s0 + 1, gate[1], up[1]);
+        if (lead) ptx::bulk_wait_group_read<0>();
+        quarter_sync();
 #pragma unroll 1
         for (int s = s0; s < s0 + kSteps; s += 2) {
-          load_pre(s + 1, gate[1], up[1]);
           step(s, gate[0], up[0]);
           if (s + 2 < s0 + kSteps) load_pre(s + 2, gate[0], up[0]);
           step(s + 1, gate[1], up[1]);
+          if (s + 3 < s0 + kSteps) load_pre(s + 3, gate[1], up[1]);
         }
         store(p.out0, maps.c0, my_stage, row0, col0, z);
         store(p.out1, maps.c1, my_stage + kStoreBuf, row0, col0, z);
@@ -733,7 +745,7 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
       if (lane == 0 && ok) ok = wait_bounded<true>(tfull_bar(0), 0, p, kDetailEpiFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (lead && ew == 0 && expected > 0)
-        ptx::mbar_arrive_expect_tx(inbox_bar, static_cast<uint32_t>(expected * p.splits) * kQuarter);
+        ptx::mbar_arrive_expect_tx(inbox_bar, static_cast<uint32_t>(expected * (p.splits - 1)) * kQuarter);
       __syncwarp();
       // The accumulator is full, so every copy into the ring has been
       // consumed: this CTA's ring is free.
@@ -754,12 +766,11 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
         ptx::fence_proxy_async_smem();
       }
       ptx::cluster_wait();  // every ring of the cluster is free
-      if (quarter_all(ok != 0) && lead && t.mb * kTileM + q * 32 < p.M) {
-        const uint32_t to = static_cast<uint32_t>(q / row_blocks);
+      const int to = q / row_blocks;  // the CTA that stores this quarter's rows
+      if (quarter_all(ok != 0) && lead && to != part && t.mb * kTileM + q * 32 < p.M)
         ptx::bulk_copy_to_peer(
             ptx::map_shared_rank(inbox + static_cast<uint32_t>(part * row_blocks + q % row_blocks) * kQuarter, to),
             mine, kQuarter, ptx::map_shared_rank(inbox_bar, to));
-      }
       int got = 1;
       if (expected > 0 && lane == 0) got = wait_bounded_cluster<2>(inbox_bar, 0, p, kDetailSkCopy) ? 1 : 0;
       got = __shfl_sync(0xffffffffu, got, 0);
@@ -768,15 +779,19 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
       ptx::cluster_arrive();
       if (quarter_all(got != 0))
         for (int u = ew; unit_exists(u); u += 4) {
-          const float* in = reinterpret_cast<const float*>(smem + kSplitBytes) + (u / kChunks) * (kQuarter / 4) + lane;
+          const int rb = u / kChunks;
+          const float* in = reinterpret_cast<const float*>(smem + kSplitBytes) + rb * (kQuarter / 4) + lane;
+          const float* own = reinterpret_cast<const float*>(smem) + (part * row_blocks + rb) * (kQuarter / 4) + lane;
           const int step = row_blocks * (kQuarter / 4);
           auto from_inbox = [&](int c, uint32_t (&r)[16]) {
             float v[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = in[(c + j) * 32];
-            for (int n = 1; n < p.splits; ++n)
+            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+            for (int n = 0; n < p.splits; ++n) {
+              const float* src = n == part ? own : in + n * step;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] += in[n * step + (c + j) * 32];
+              for (int j = 0; j < 16; ++j) v[j] += src[(c + j) * 32];
+            }
 #pragma unroll
             for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(v[j]);
           };

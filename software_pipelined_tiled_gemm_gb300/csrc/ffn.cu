@@ -123,7 +123,7 @@ size_t layout(const gemm_ops* ops, const gemm_ffn_args_t* a, bool backward, void
     const int64_t ldp = round8(m->cols);
     uint16_t* dst = static_cast<uint16_t*>(c.take(static_cast<size_t>(m->rows) * ldp * 2));
     f->pack.job[f->pack.count++] = {static_cast<const uint16_t*>(m->ptr), dst, m->rows, m->cols,
-                                    m->ld, ldp};
+                                    m->ld, ldp, 0};
     m->ptr = dst;
     m->ld = ldp;
   };
@@ -177,7 +177,7 @@ gemm_status_t gemm_ffn_run(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* w
   OpsDevice guard(ops->device);
   if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  const cudaError_t e = launch_pack(f.pack, stream);
+  const cudaError_t e = launch_pack(f.pack, ops->sm_count, stream);
   if (e != cudaSuccess) return ops_cuda_fail(e, "padding copy launch");
 
   BlockProblem g;
@@ -224,7 +224,7 @@ gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, vo
       e = cudaMemsetAsync(args->dw_out, 0, static_cast<size_t>(2) * I * D, stream);
     return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "cudaMemsetAsync(weight gradients)");
   }
-  const cudaError_t e = launch_pack(f.pack, stream);
+  const cudaError_t e = launch_pack(f.pack, ops->sm_count, stream);
   if (e != cudaSuccess) return ops_cuda_fail(e, "padding copy launch");
 
   if (args->dx || args->dw_in) {

@@ -130,13 +130,16 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
     *tn = ceil_div(pr.N, gated ? block_bn(cg) / 2 : block_bn(cg));
     return (pr.symmetric ? *tn * (*tn + 1) / 2 : *tm * *tn) * pr.batch;
   };
-  // The cheapest of three schedules, by a model of their times in us.  A pair
-  // multiplies a 256 x 256 x 128 slot in kPairSlot; a single CTA's 128 x 128
-  // x 64 slot moves twice the operand bytes per product, and with every SM
-  // at it is bound by L2 at kSoloSlot.  Splitting K costs its exchange:
-  // kSplitCost through a cluster's shared memory, kStreamCost through the
-  // workspace.
-  constexpr double kPairSlot = 0.55, kSoloSlot = 0.27, kSplitCost = 1.5, kStreamCost = 5.0;
+  // The cheapest of three schedules, by a model of their times in us (fitted
+  // to time stamps of launches between 3 and 600 us).  A pair multiplies a 256
+  // x 256 x 128 slot in kPairSlot; a single CTA's 128 x 128 x 64 slot moves
+  // twice the operand bytes per product and is bound by what an SM takes in,
+  // kSoloSlot.  A wave of tiles adds its start and its epilogue.  Splitting K
+  // costs its exchange: kSplitCost through a cluster's shared memory; through
+  // the workspace kStreamCost and, for every partial that a tile's owner adds
+  // one after another, kPairPart or kSoloPart.
+  constexpr double kPairSlot = 0.65, kSoloSlot = 0.30, kPairWave = 5.0, kSoloWave = 3.5;
+  constexpr double kSplitCost = 4.0, kStreamCost = 4.0, kPairPart = 2.5, kSoloPart = 1.5;
   constexpr double kHbmBytesPerUs = 6.5e6;
   int64_t tm, tn, walkers = 0, sk = 0;
   int cg = 1, splits = 1;
@@ -156,24 +159,33 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
     const int64_t nt = tiles(c, &tm, &tn);
     const int64_t kb = ceil_div(pr.K, static_cast<int64_t>(kBK) * block_sub(c));
     const double slot = c == 2 ? kPairSlot : kSoloSlot;
-    offer(ceil_div(nt, most) * kb * slot, c, 1, std::min(nt, most), 0);
-    // Stream-K: the last one to two waves' slots shared out evenly.  The
-    // walkers are then at different places along K, so operands beyond L2
-    // are read from HBM once per tile instead of once per wave.
-    const int64_t shared = nt < most ? nt : nt % most + most;
-    if (nt % most != 0 && nt * kb >= 2 * most) {
-      double cost = static_cast<double>(nt) * kb / most * slot + kStreamCost;
+    // Later waves' epilogues hide behind the next tiles' main loops where those are longer.
+    const double wave = c == 2 ? kPairWave : kSoloWave;
+    const double waves = static_cast<double>(ceil_div(nt, most));
+    offer(wave + kb * slot + (waves - 1) * std::max(kb * slot, 0.6 * wave), c, 1, std::min(nt, most), 0);
+    // Stream-K: the last one to two waves' slots shared out evenly, or fewer
+    // tiles than walkers over up to four walkers each.  The walkers are then
+    // at different places along K, so operands beyond L2 are read from HBM
+    // once per tile instead of once per wave.
+    for (int64_t per = 1; per <= 4 && nt % most != 0; ++per) {
+      const int64_t w = nt < most ? std::min(most, nt * (per + 1)) : most;
+      if (nt * kb < 2 * w) break;
+      const int64_t shared = nt < w ? nt : nt % w + w;
+      const double parts = static_cast<double>(nt < w ? ceil_div(w, nt) - 1 : 1);
+      double cost = wave + static_cast<double>(nt) * kb / w * slot + kStreamCost +
+                    parts * (c == 2 ? kPairPart : kSoloPart);
       const double operands = 2.0 * (pr.M + pr.N * (gated ? 2 : 1)) * pr.K * pr.batch;
       if (operands > 0.75 * ops->l2_bytes && pr.M > kBM) {
         const double reads = 2.0 * shared * (kBM * c + block_bn(c)) * pr.K / kHbmBytesPerUs;
-        cost += std::max(0.0, reads - static_cast<double>(shared) * kb / most * slot);
+        cost += std::max(0.0, reads - static_cast<double>(shared) * kb / w * slot);
       }
-      offer(cost, c, 1, most, shared);
+      offer(cost, c, 1, w, shared);
+      if (w == most) break;
     }
     if (c == 1)
       for (int s = 2; s <= kMaxSplits; s *= 2)
         if (nt * s <= most && kb >= 2 * s)
-          offer(ceil_div(kb, s) * slot + kSplitCost, c, s, nt * s, 0);
+          offer(wave + ceil_div(kb, s) * slot + kSplitCost, c, s, nt * s, 0);
   }
   const int64_t nt = tiles(cg, &tm, &tn);
   const int64_t kb = ceil_div(pr.K, static_cast<int64_t>(kBK) * block_sub(cg));
@@ -198,9 +210,9 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.raster_group = cg == 2 ? 8 : 16;
   p.walkers = static_cast<int>(walkers);
   p.splits = splits;
-  // Two epilogue warps per lane quarter halve an epilogue that the main loop
-  // does not hide: single CTAs, and pairs whose K is short.
-  p.epi = cg == 1 || pr.K <= 1024 ? 2 : 1;
+  // Two epilogue warps per lane quarter halve an epilogue that no main loop
+  // hides: single CTAs, pairs whose K is short, and one wave (or less) of tiles.
+  p.epi = cg == 1 || pr.K <= 1024 || nt <= walkers ? 2 : 1;
   p.sk_tiles = static_cast<int>(sk);
   p.dp_tiles = static_cast<int>(nt - sk);
   p.sk_ws = partials;

@@ -31,16 +31,16 @@ using namespace spgemm;
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormVecs = 4;                                     // 8-element vectors per thread and step
-constexpr int kNormCols = kNormThreads * kNormVecs * 8;          // columns of a step
-constexpr int kNormBlocks = 608;                                 // at most, over the batch: four per SM
+constexpr int kNormVecs = 4;       // 8-element vectors per thread and step
+constexpr int kNormStep = kNormThreads * kNormVecs;
+constexpr int kNormBlocks = 608;   // at most, over the batch: four per SM
 constexpr float kIterateScale = 256.0f;
 
 struct NormArgs {
   const void* g;
   int64_t m, n, ld, batch_stride;
-  int chunks;          // steps per row
-  int64_t steps;       // steps per matrix
+  int64_t per;         // vectors of 8 elements in a row (the last may be cut)
+  int64_t vectors;     // in a matrix
   int aligned;         // vectors of 8 elements may be loaded whole
   double* partial;     // batch x gridDim.x
   uint16_t* x;
@@ -56,6 +56,12 @@ template <>
 __device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
 template <>
 __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Row and first column of a matrix's vector v.
+__device__ __forceinline__ void place(const NormArgs& a, int64_t v, int64_t& r, int64_t& c) {
+  r = v < (int64_t{1} << 31) ? static_cast<uint32_t>(v) / static_cast<uint32_t>(a.per) : v / a.per;
+  c = (v - r * a.per) * 8;
+}
 
 // Elements [c, c + 8) of a row (0 at and past n).
 template <typename T>
@@ -94,13 +100,16 @@ __global__ void __launch_bounds__(kNormThreads) sum_squares_kernel(const NormArg
   ptx::pdl_wait_prior_grid();
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
   float sum = 0.0f, small = 0.0f, large = 0.0f;  // small x 2^60, large x 2^-60
-  for (int64_t s = blockIdx.x; s < a.steps; s += gridDim.x) {
-    const int64_t r = s / a.chunks;
-    const int64_t c0 = (s - r * a.chunks) * kNormCols + threadIdx.x * 8;
+  for (int64_t s = static_cast<int64_t>(blockIdx.x) * kNormStep + threadIdx.x; s < a.vectors;
+       s += static_cast<int64_t>(gridDim.x) * kNormStep) {
     float v[kNormVecs][8];
 #pragma unroll
-    for (int i = 0; i < kNormVecs; ++i)
-      load8<T>(g + r * a.ld, c0 + i * kNormThreads * 8, a.n, a.aligned != 0, v[i]);
+    for (int i = 0; i < kNormVecs; ++i) {
+      const int64_t at = s + i * kNormThreads;
+      int64_t r, c;
+      place(a, at < a.vectors ? at : 0, r, c);
+      load8<T>(g + r * a.ld, c, at < a.vectors ? a.n : 0, a.aligned != 0, v[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kNormVecs; ++i)
 #pragma unroll
@@ -136,23 +145,25 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const NormArgs 
   const float scale = static_cast<float>(sqrt(static_cast<double>(kIterateScale) / norm));
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
   uint16_t* x = a.x + blockIdx.y * a.m * a.ldx;
-  for (int64_t s = blockIdx.x; s < a.steps; s += gridDim.x) {
-    const int64_t r = s / a.chunks;
-    const int64_t c0 = (s - r * a.chunks) * kNormCols + threadIdx.x * 8;
+  for (int64_t s = static_cast<int64_t>(blockIdx.x) * kNormStep + threadIdx.x; s < a.vectors;
+       s += static_cast<int64_t>(gridDim.x) * kNormStep) {
     float v[kNormVecs][8];
-#pragma unroll
-    for (int i = 0; i < kNormVecs; ++i)
-      load8<T>(g + r * a.ld, c0 + i * kNormThreads * 8, a.n, a.aligned != 0, v[i]);
+    int64_t r[kNormVecs], c[kNormVecs];
 #pragma unroll
     for (int i = 0; i < kNormVecs; ++i) {
-      const int64_t c = c0 + i * kNormThreads * 8;
-      if (c < a.ldx) {
+      const int64_t at = s + i * kNormThreads;
+      place(a, at < a.vectors ? at : 0, r[i], c[i]);
+      load8<T>(g + r[i] * a.ld, c[i], at < a.vectors ? a.n : 0, a.aligned != 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kNormVecs; ++i)
+      if (s + i * kNormThreads < a.vectors) {
         __half2 h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(v[i][2 * j] * scale * scale, v[i][2 * j + 1] * scale * scale);
-        *reinterpret_cast<uint4*>(x + r * a.ldx + c) = *reinterpret_cast<const uint4*>(h);
+        for (int j = 0; j < 4; ++j)
+          h[j] = __floats2half2_rn(v[i][2 * j] * scale * scale, v[i][2 * j + 1] * scale * scale);
+        *reinterpret_cast<uint4*>(x + r[i] * a.ldx + c[i]) = *reinterpret_cast<const uint4*>(h);
       }
-    }
   }
 }
 
@@ -196,7 +207,7 @@ Layout layout(const gemm_ops* ops, const gemm_orthogonalize_args_t* g, void* wor
   l.np = round8(g->n);
   l.s = std::min(g->m, g->n);
   l.sp = round8(l.s);
-  const int64_t steps = g->m * ceil_div(std::max<int64_t>(g->n, 1), kNormCols);
+  const int64_t steps = ceil_div(g->m * (l.np / 8), kNormStep);
   l.blocks = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(steps, kNormBlocks / std::max<int64_t>(1, std::min<int64_t>(g->batch, kNormBlocks)))));
   const size_t x = static_cast<size_t>(g->batch) * g->m * l.np * 2;
@@ -281,8 +292,8 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
   na.n = n;
   na.ld = args->ldg;
   na.batch_stride = batch > 1 ? args->batch_stride : 0;
-  na.chunks = static_cast<int>(ceil_div(n, kNormCols));
-  na.steps = m * na.chunks;
+  na.per = l.np / 8;
+  na.vectors = m * na.per;
   const int64_t vec = 16 / static_cast<int64_t>(elem_bytes(args->dtype));
   na.aligned = (reinterpret_cast<uintptr_t>(args->g) & 15u) == 0 && args->ldg % vec == 0 &&
                (batch == 1 || args->batch_stride % vec == 0);
