@@ -123,7 +123,7 @@ size_t layout(const gemm_ops* ops, const gemm_ffn_args_t* a, bool backward, void
     const int64_t ldp = round8(m->cols);
     uint16_t* dst = static_cast<uint16_t*>(c.take(static_cast<size_t>(m->rows) * ldp * 2));
     f->pack.job[f->pack.count++] = {static_cast<const uint16_t*>(m->ptr), dst, m->rows, m->cols,
-                                    m->ld, ldp, 0};
+                                    m->ld, ldp};
     m->ptr = dst;
     m->ld = ldp;
   };

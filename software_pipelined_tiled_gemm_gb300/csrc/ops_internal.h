@@ -77,13 +77,12 @@ struct PackJob {
   const uint16_t* src;
   uint16_t* dst;
   int64_t rows, cols, ld, ldp;
-  int64_t vectors;  // of the copy, 16 bytes each (filled in by the launch)
 };
 struct PackJobs {
   PackJob job[kPackJobs];
   int count = 0;
 };
-cudaError_t launch_pack(PackJobs jobs, int sm_count, cudaStream_t stream);
+cudaError_t launch_pack(const PackJobs& jobs, int sm_count, cudaStream_t stream);
 
 // One product of the block kernels.
 struct BlockProblem {
