@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
           }
         }
       }
-      ptx::pdl_wait_prior_grid();
+      bool waited = false;  // on the previous kernel: finding the first tile overlaps it
       while (ok && it.next(p, x)) {
         const BlockTile t = block_tile(x.tile, p);
         if (SPGEMM_OUT_OF_BOUNDS(x.tile >= 0 && x.tile < p.num_tiles && t.z < p.batch &&
@@ -427,6 +427,10 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
           uint32_t fb = full_bar(stage);
           if constexpr (CG == 2) fb = ptx::map_shared_rank(fb, 0);
           if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), bytes);
+          if (!waited) {
+            ptx::pdl_wait_prior_grid();
+            waited = true;
+          }
 #pragma unroll
           for (int sub = 0; sub < kSub; ++sub) {
             const int kx = (kb * kSub + sub) * kBK;
