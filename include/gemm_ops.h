@@ -38,6 +38,13 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device);
 /* Wait for the handle's work to finish and free it.  NULL is allowed. */
 void gemm_ops_destroy(gemm_ops_t* ops);
 
+/* timeout_ns: the limit of each device-side wait of later calls, 0 for the
+ * default (2 s).  debug_fault: test hook, 0 in normal use; 1: the first copy
+ * of the first block of each kernel with a copy ring is announced but never
+ * made, so that the waits run out and gemm_ops_check reports
+ * GEMM_ERR_TIMEOUT.  Nothing faults or hangs. */
+gemm_status_t gemm_ops_configure(gemm_ops_t* ops, int64_t timeout_ns, int debug_fault);
+
 /* As gemm_plan_check: synchronise the device, read and clear the status word. */
 gemm_status_t gemm_ops_check(gemm_ops_t* ops, int32_t* device_status, int32_t* detail);
 

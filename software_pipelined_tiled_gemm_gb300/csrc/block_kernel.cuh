@@ -431,8 +431,11 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
             ptx::pdl_wait_prior_grid();
             waited = true;
           }
+          // Test hook: the first slot of the first CTA is announced but never copied.
+          const bool skip = p.inject_fault == 1 && blockIdx.x == 0 && issued == 0;
 #pragma unroll
           for (int sub = 0; sub < kSub; ++sub) {
+            if (skip) break;
             const int kx = (kb * kSub + sub) * kBK;
             const uint32_t da = sa + sub * slice_a, db = sa + slot_a + sub * kStageB;
             if constexpr (CG == 2) {

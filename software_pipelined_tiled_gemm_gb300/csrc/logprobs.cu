@@ -76,6 +76,7 @@ struct LpArgs {
   int64_t rows;
   int* status;
   unsigned long long timeout_ns;
+  int inject_fault;  // test hook, see gemm_ops_configure
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -566,7 +567,9 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == kRowThreads ? kRowB
           }
           const uint32_t bytes = static_cast<uint32_t>(min(v1 - v, kChunkVecs)) * 16u;
           ptx::mbar_arrive_expect_tx(full + 8u * stage, bytes);
-          if constexpr (kTop)  // read again, in part
+          if (a.inject_fault && blockIdx.x == 0 && used == 0)
+            ;  // announced but never copied
+          else if constexpr (kTop)  // read again, in part
             ptx::bulk_load(ring_addr + stage * kChunk, row.at(v), bytes, full + 8u * stage);
           else
             ptx::bulk_load_hint(ring_addr + stage * kChunk, row.at(v), bytes, full + 8u * stage, pol);
@@ -929,6 +932,7 @@ LpArgs kernel_args(const gemm_ops* ops, const gemm_logprobs_args_t* g) {
   a.rows = g->rows;
   a.status = ops->d_status;
   a.timeout_ns = ops->timeout_ns;
+  a.inject_fault = ops->debug_fault;
   a.logits = g->logits;
   a.ld = g->ld;
   a.vocab = static_cast<int>(g->vocab);

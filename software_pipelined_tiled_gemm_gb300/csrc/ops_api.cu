@@ -224,6 +224,7 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.idesc = ptx::instr_desc_f16(kBM * cg, block_bn(cg), pr.bf16, b_n) | (a_t ? 1u << 15 : 0u);
   p.status = ops->d_status;
   p.timeout_ns = ops->timeout_ns;
+  p.inject_fault = ops->debug_fault;
   p.symmetric = pr.symmetric ? 1 : 0;
   p.out_bf16 = pr.out_bf16 ? 1 : 0;
   p.act = pr.act;
@@ -292,7 +293,7 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
   ops->pairs = desc.pair_clusters;
   ops->smem_optin = static_cast<size_t>(desc.smem_optin);
   ops->l2_bytes = desc.l2_bytes;
-  ops->timeout_ns = 2000000000ull;
+  ops->timeout_ns = kOpsTimeoutNs;
   for (auto set : {block_set_smem_nt, block_set_smem_nn, block_set_smem_tn, block_set_smem_gated,
                    block_set_smem_gated_bwd})
     if (e == cudaSuccess) e = set(ops->smem_optin);
@@ -319,6 +320,17 @@ void gemm_ops_destroy(gemm_ops_t* ops) {
   if (ops->d_status) cudaFree(ops->d_status);
   if (ops->d_flags) cudaFree(ops->d_flags);
   delete ops;
+}
+
+gemm_status_t gemm_ops_configure(gemm_ops_t* ops, int64_t timeout_ns, int debug_fault) {
+  ops_fail(GEMM_OK, "%s", "");
+  if (!ops) return ops_fail(GEMM_ERR_INVALID_ARG, "ops is NULL");
+  if (timeout_ns < 0) return ops_fail(GEMM_ERR_INVALID_ARG, "negative timeout_ns");
+  if (debug_fault < 0 || debug_fault > 1)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "debug_fault %d not in {0, 1}", debug_fault);
+  ops->timeout_ns = timeout_ns > 0 ? static_cast<unsigned long long>(timeout_ns) : kOpsTimeoutNs;
+  ops->debug_fault = debug_fault;
+  return GEMM_OK;
 }
 
 gemm_status_t gemm_ops_check(gemm_ops_t* ops, int32_t* device_status, int32_t* detail) {

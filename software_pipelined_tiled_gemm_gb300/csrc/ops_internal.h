@@ -21,6 +21,7 @@ struct gemm_ops {
   size_t smem_optin = 0;
   int64_t l2_bytes = 0;
   unsigned long long timeout_ns = 0;
+  int debug_fault = 0;
   int* d_status = nullptr;       // [0] code, [1] detail
   int* d_flags = nullptr;        // 4 per CTA
 };
@@ -32,6 +33,7 @@ void set_last_error(const char* text);  // gemm_api.cu
 gemm_status_t ops_fail(gemm_status_t st, const char* fmt, ...);
 gemm_status_t ops_cuda_fail(cudaError_t e, const char* what);
 
+constexpr unsigned long long kOpsTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int64_t kOpsMaxDim = (int64_t{1} << 31) - 1;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -73,6 +73,7 @@ def _lib():
     for name, args in {
             "gemm_ops_create": [ctypes.POINTER(_vp), _ci],
             "gemm_ops_check": [_vp, pi32, pi32],
+            "gemm_ops_configure": [_vp, _i64, _ci],
             "gemm_ffn_workspace": [_vp, ctypes.POINTER(FfnArgs), _ci, psz],
             "gemm_ffn_run": [_vp, ctypes.POINTER(FfnArgs), _vp, _sz, _vp],
             "gemm_ffn_backward": [_vp, ctypes.POINTER(FfnArgs), _vp, _sz, _vp],
@@ -125,6 +126,13 @@ def check_operators() -> None:
         _check(_lib().gemm_ops_check(h, ctypes.byref(ds), ctypes.byref(detail)), "gemm_ops_check")
         if ds.value:
             raise GemmError(ds.value, "operators", gemm_wait_detail_string(detail.value))
+
+
+def _configure(device, timeout_ns=0, debug_fault=0) -> None:
+    """gemm_ops_configure for the handle of the device's current stream (tests)."""
+    stream = _stream(device)
+    _check(_lib().gemm_ops_configure(_handle(device, stream), timeout_ns, debug_fault),
+           "gemm_ops_configure")
 
 
 def close_operators() -> None:
