@@ -59,6 +59,8 @@ MAX_TOP_K = 64   # GEMM_LOGPROBS_MAX_TOP_K
 _bound = None
 _handles: dict = {}
 _lock = threading.Lock()
+_sixteen: dict = {}   # torch dtype -> gemm_dtype_t
+_inputs: dict = {}    # torch dtype -> gemm_in_t
 
 
 def _lib():
@@ -66,8 +68,11 @@ def _lib():
     global _bound
     if _bound is not None:
         return _bound
+    import torch
     from . import load_library
     lib = load_library()
+    _sixteen.update({torch.float16: 0, torch.bfloat16: 1})
+    _inputs.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
     psz = ctypes.POINTER(_sz)
     pi32 = ctypes.POINTER(ctypes.c_int32)
     for name, args in {
@@ -186,18 +191,19 @@ GatedKept = collections.namedtuple("GatedKept", "buffer tokens d_model d_inner d
 
 
 def _ffn_args(x, w_in, w_out, act):
-    import torch
-    if act not in GEMM_ACT:
+    act_code = GEMM_ACT.get(act)
+    if act_code is None:
         raise ValueError("act must be one of %s" % ", ".join(sorted(GEMM_ACT)))
     _on_cuda(getattr(x, "device", None), x, "x")
     _on_cuda(x.device, w_in, "w_in")
     _on_cuda(x.device, w_out, "w_out")
-    if x.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError("x must be float16 or bfloat16, got %s" % x.dtype)
-    if w_in.dtype != x.dtype or w_out.dtype != x.dtype:
+    dtype = x.dtype
+    code = _sixteen.get(dtype)
+    if code is None:
+        raise TypeError("x must be float16 or bfloat16, got %s" % dtype)
+    if w_in.dtype != dtype or w_out.dtype != dtype:
         raise TypeError("x, w_in and w_out must have the same dtype")
-    if w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1] or \
-            w_in.shape[1] != w_out.shape[0]:
+    if w_out.dim() != 2 or tuple(w_in.shape) != (2 * w_out.shape[1], w_out.shape[0]):
         raise ValueError("w_in must be (2 d_inner, d_model) and w_out (d_model, d_inner)")
     if not (w_in.is_contiguous() and w_out.is_contiguous()):
         raise ValueError("w_in and w_out must be contiguous")
@@ -205,21 +211,23 @@ def _ffn_args(x, w_in, w_out, act):
     if d == 0 or i == 0:
         raise ValueError("d_model and d_inner must be at least 1")
     m, ldx = _rows(x, d, "x")
-    return FfnArgs(tokens=m, d_model=d, d_inner=i, dtype=1 if x.dtype == torch.bfloat16 else 0,
-                   act=GEMM_ACT[act], x=x.data_ptr(), ldx=ldx, w_in=w_in.data_ptr(),
-                   w_out=w_out.data_ptr(), lddy=d)
+    return FfnArgs(m, d, i, code, act_code, x.data_ptr(), ldx, w_in.data_ptr(), w_out.data_ptr(),
+                   None, None, None, d)
 
 
-def _run(name, device, query, run):
+def _run(name, query, run, args, device, *which):
     """Workspace from the caching allocator of the current stream, then the call."""
     import torch
     stream = _stream(device)
     h = _handle(device, stream)
-    need = _sz()
-    _check(query(h, ctypes.byref(need)), name)
-    n = need.value
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _check(run(h, ws.data_ptr(), n, stream), name)
+    ref, need = ctypes.byref(args), _sz()
+    status = query(h, ref, *which, ctypes.byref(need))
+    if not status:
+        n = need.value
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        status = run(h, ref, ws.data_ptr(), n, stream)
+    if status:
+        _check(status, name)
 
 
 def gated_ffn(x, w_in, w_out, act="silu", out=None, save=False):
@@ -234,8 +242,8 @@ def gated_ffn(x, w_in, w_out, act="silu", out=None, save=False):
     feature: the projections stay in fp32).
     """
     import torch
-    a = _ffn_args(x, w_in, w_out, act)
     lib = _lib()
+    a = _ffn_args(x, w_in, w_out, act)
     y = _output(out, x.shape, x.dtype, x.device)
     a.y = y.data_ptr()
     kept = None
@@ -245,9 +253,7 @@ def gated_ffn(x, w_in, w_out, act="silu", out=None, save=False):
         a.kept = buf.data_ptr()
         kept = GatedKept(buf, a.tokens, a.d_model, a.d_inner, x.dtype, act)
     if a.tokens:
-        ref = ctypes.byref(a)
-        _run("gemm_ffn_run", x.device, lambda h, n: lib.gemm_ffn_workspace(h, ref, 0, n),
-             lambda h, w, n, s: lib.gemm_ffn_run(h, ref, w, n, s))
+        _run("gemm_ffn_run", lib.gemm_ffn_workspace, lib.gemm_ffn_run, a, x.device, 0)
     return (y, kept) if save else y
 
 
@@ -261,13 +267,13 @@ def gated_ffn_backward(dy, x, w_in, w_out, kept, need=(True, True, True), out=(N
     """
     if not isinstance(kept, GatedKept):
         raise TypeError("kept must come from gated_ffn(..., save=True)")
+    lib = _lib()
     a = _ffn_args(x, w_in, w_out, kept.act)
     _on_cuda(x.device, dy, "dy")
     if dy.dtype != x.dtype or dy.shape != x.shape:
         raise ValueError("dy must have x's shape and dtype")
     if (a.tokens, a.d_model, a.d_inner, x.dtype) != kept[1:5] or kept.buffer.device != x.device:
         raise ValueError("kept belongs to a forward pass of other sizes, dtype or device")
-    lib = _lib()
     a.dy = dy.data_ptr()
     a.lddy = _rows(dy, a.d_model, "dy")[1]
     a.kept = kept.buffer.data_ptr()
@@ -275,9 +281,7 @@ def gated_ffn_backward(dy, x, w_in, w_out, kept, need=(True, True, True), out=(N
     grads = [_output(o, shape, x.dtype, x.device, name) if want else None
              for want, o, (shape, name) in zip(need, out, shapes)]
     a.dx, a.dw_in, a.dw_out = map(_ptr, grads)
-    ref = ctypes.byref(a)
-    _run("gemm_ffn_backward", x.device, lambda h, n: lib.gemm_ffn_workspace(h, ref, 1, n),
-         lambda h, w, n, s: lib.gemm_ffn_backward(h, ref, w, n, s))
+    _run("gemm_ffn_backward", lib.gemm_ffn_workspace, lib.gemm_ffn_backward, a, x.device, 1)
     return tuple(grads)
 
 
@@ -294,8 +298,8 @@ def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
     """
     import torch
     _on_cuda(getattr(g, "device", None), g, "g")
-    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-    if g.dtype not in codes:
+    lib = _lib()
+    if g.dtype not in _inputs:
         raise TypeError("g must be float32, float16 or bfloat16, got %s" % g.dtype)
     if g.dim() not in (2, 3):
         raise ValueError("g must be a matrix or a batch of matrices")
@@ -308,13 +312,10 @@ def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
         if g.stride(-1) != 1 or ld < n or (b > 1 and bs < 0):
             raise ValueError("g must have contiguous rows")
     y = _output(out, g.shape, torch.bfloat16, g.device)
-    a = OrthogonalizeArgs(batch=b, m=m, n=n, dtype=codes[g.dtype], g=g.data_ptr(), ldg=ld,
+    a = OrthogonalizeArgs(batch=b, m=m, n=n, dtype=_inputs[g.dtype], g=g.data_ptr(), ldg=ld,
                           batch_stride=bs, out=y.data_ptr(), steps=int(steps), a=coeffs[0],
                           b=coeffs[1], c=coeffs[2], eps=eps)
-    lib = _lib()
-    ref = ctypes.byref(a)
-    _run("gemm_orthogonalize", g.device, lambda h, n: lib.gemm_orthogonalize_workspace(h, ref, n),
-         lambda h, w, n, s: lib.gemm_orthogonalize(h, ref, w, n, s))
+    _run("gemm_orthogonalize", lib.gemm_orthogonalize_workspace, lib.gemm_orthogonalize, a, g.device)
     return y
 
 
@@ -328,21 +329,24 @@ TokenLogprobs = collections.namedtuple("TokenLogprobs",
 
 def _logprobs_args(logits, tokens):
     import torch
-    _on_cuda(getattr(logits, "device", None), logits, "logits")
-    codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-    if logits.dtype not in codes:
+    device = getattr(logits, "device", None)
+    _on_cuda(device, logits, "logits")
+    _lib()
+    code = _inputs.get(logits.dtype)
+    if code is None:
         raise TypeError("logits must be float32, float16 or bfloat16, got %s" % logits.dtype)
-    if logits.dim() < 1 or logits.shape[-1] == 0:
+    shape = logits.shape
+    if len(shape) < 1 or shape[-1] == 0:
         raise ValueError("logits must have at least one column")
-    rows, ld = _rows(logits, logits.shape[-1], "logits")
+    rows, ld = _rows(logits, shape[-1], "logits")
     if tokens is not None:
-        _on_cuda(logits.device, tokens, "tokens")
+        _on_cuda(device, tokens, "tokens")
         if tokens.dtype != torch.int64:
             raise TypeError("tokens must be int64, got %s" % tokens.dtype)
-        if tokens.shape != logits.shape[:-1] or not tokens.is_contiguous():
+        if tokens.shape != shape[:-1] or not tokens.is_contiguous():
             raise ValueError("tokens must be contiguous, one for each row of logits")
-    return LogprobsArgs(rows=rows, vocab=logits.shape[-1], dtype=codes[logits.dtype],
-                        logits=logits.data_ptr(), ld=ld, tokens=_ptr(tokens))
+    return LogprobsArgs(rows, shape[-1], code, logits.data_ptr(), ld,
+                        None if tokens is None else tokens.data_ptr())
 
 
 def token_logprobs(logits, tokens=None, top_k=0):
