@@ -136,10 +136,11 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   // twice the operand bytes per product and is bound by what an SM takes in,
   // kSoloSlot.  A wave of tiles adds its start and its epilogue.  Splitting K
   // costs its exchange: kSplitCost through a cluster's shared memory; through
-  // the workspace kStreamCost and, for every partial that a tile's owner adds
-  // one after another, kPairPart or kSoloPart.
+  // the workspace kPairStream or kSoloStream and, for every partial that a
+  // tile's owner adds one after another, kPairPart or kSoloPart.
   constexpr double kPairSlot = 0.65, kSoloSlot = 0.30, kPairWave = 5.0, kSoloWave = 3.5;
-  constexpr double kSplitCost = 4.0, kStreamCost = 4.0, kPairPart = 2.5, kSoloPart = 1.5;
+  constexpr double kSplitCost = 4.0, kPairStream = 8.0, kSoloStream = 4.0;
+  constexpr double kPairPart = 2.5, kSoloPart = 1.5;
   constexpr double kHbmBytesPerUs = 6.5e6;
   int64_t tm, tn, walkers = 0, sk = 0;
   int cg = 1, splits = 1;
@@ -172,8 +173,8 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
       if (nt * kb < 2 * w) break;
       const int64_t shared = nt < w ? nt : nt % w + w;
       const double parts = static_cast<double>(nt < w ? ceil_div(w, nt) - 1 : 1);
-      double cost = wave + static_cast<double>(nt) * kb / w * slot + kStreamCost +
-                    parts * (c == 2 ? kPairPart : kSoloPart);
+      double cost = wave + static_cast<double>(nt) * kb / w * slot +
+                    (c == 2 ? kPairStream + parts * kPairPart : kSoloStream + parts * kSoloPart);
       const double operands = 2.0 * (pr.M + pr.N * (gated ? 2 : 1)) * pr.K * pr.batch;
       if (operands > 0.75 * ops->l2_bytes && pr.M > kBM) {
         const double reads = 2.0 * shared * (kBM * c + block_bn(c)) * pr.K / kHbmBytesPerUs;
@@ -210,9 +211,6 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.raster_group = cg == 2 ? 8 : 16;
   p.walkers = static_cast<int>(walkers);
   p.splits = splits;
-  // Two epilogue warps per lane quarter halve an epilogue that no main loop
-  // hides: single CTAs, pairs whose K is short, and one wave (or less) of tiles.
-  p.epi = cg == 1 || pr.K <= 1024 || nt <= walkers ? 2 : 1;
   p.sk_tiles = static_cast<int>(sk);
   p.dp_tiles = static_cast<int>(nt - sk);
   p.sk_ws = partials;
@@ -230,6 +228,16 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.act = pr.act;
   p.gate_rows = gated ? static_cast<int>(pr.N) : 0;
   p.use_d = pr.d.ptr != nullptr ? 1 : 0;
+  // Two epilogue warps per lane quarter halve an epilogue that no main loop
+  // hides: single CTAs, one wave (or less) of tiles, and pairs whose K is
+  // short next to what their epilogue moves (one warp a quarter -> two, in us:
+  // gated backward and dX of 2048 x 2048 x 8192 176 -> 161, the forward pass
+  // that keeps its projections 142 -> 138; updates of 2048 x 8192 552 -> 534;
+  // at K = 16384 no difference).
+  const int64_t short_k = pr.kind == BlockProblem::kGatedBwd ? 8192
+                          : gated || p.use_d                 ? 2048
+                                                             : 1024;
+  p.epi = cg == 1 || pr.K <= short_k || nt <= walkers ? 2 : 1;
   p.alpha = pr.alpha;
   p.beta = pr.beta;
   p.out0 = describe_out(pr.out0, pr.N, pr.batch);
