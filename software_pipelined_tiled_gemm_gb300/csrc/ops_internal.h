@@ -12,12 +12,19 @@
 #include "../../include/gemm_ops.h"
 #include "block_params.h"
 
+namespace spgemm {
+constexpr int kSmallCluster = 8;  // CTAs of a cluster of the on-chip iteration, at most
+}
+
 // What persists between calls: the device status word and the
 // partial-ready flags of split tiles (raised and reset within a launch).
 struct gemm_ops {
   int device = 0;
   int sm_count = 0;
   int pairs = 0;                 // co-resident CTA pairs
+  // Co-resident clusters of the on-chip iteration, by its row blocks (less
+  // one) and the cluster's CTAs.
+  int small_clusters[2][spgemm::kSmallCluster + 1] = {};
   size_t smem_optin = 0;
   int64_t l2_bytes = 0;
   unsigned long long timeout_ns = 0;

@@ -1,11 +1,13 @@
 // orthogonal.cu -- the orthogonalised update by Newton-Schulz products.
 //
+// Matrices with a short side of at most 256 that fit a cluster's shared memory
+// take one launch (orthogonal_small.cu).  The others:
+//
 // Two passes over G normalise it: the sum of squares (one partial per block),
 // then X = 2^8 G / max(|G|, eps) in fp16 (every block adds the partials in the
-// same order).  Elements below 2^-40 and above 2^40 are squared at another
-// scale, so that the norm is right for any fp32 gradient.  Each step is three block products: A = X X^T and
-// B = b A + c A^2 on the tiles on and above the diagonal only, and
-// X' = a X + B X.  On matrices with more rows than columns the products use
+// same order).  Each step is three block products: A = X X^T and B = b A + c
+// A^2 on the tiles on and above the diagonal only, and X' = a X + B X.  On
+// matrices with more rows than columns the products use
 // X^T X and X B instead, reading X as it lies.
 //
 // fp16 for the iterates: the step's map multiplies errors along small
@@ -14,16 +16,17 @@
 // 1.3e-3, below the bf16 result's own rounding (1.7e-3).  The factor 2^8
 // lifts the elements of a normalised matrix (1 / sqrt(m n) in the mean) out
 // of fp16's subnormal range; elements stay below 2^8 x 1.3.
-#include <cuda_fp16.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "ops_internal.h"
+#include "orthogonal_load.cuh"
+#include "orthogonal_small.h"
 #include "ptx.cuh"
 
 using namespace spgemm;
@@ -34,7 +37,6 @@ constexpr int kNormThreads = 256;
 constexpr int kNormVecs = 4;       // 8-element vectors per thread and step
 constexpr int kNormStep = kNormThreads * kNormVecs;
 constexpr int kNormBlocks = 608;   // at most, over the batch: four per SM
-constexpr float kIterateScale = 256.0f;
 
 struct NormArgs {
   const void* g;
@@ -48,49 +50,10 @@ struct NormArgs {
   float eps;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
 // Row and first column of a matrix's vector v.
 __device__ __forceinline__ void place(const NormArgs& a, int64_t v, int64_t& r, int64_t& c) {
   r = v < (int64_t{1} << 31) ? static_cast<uint32_t>(v) / static_cast<uint32_t>(a.per) : v / a.per;
   c = (v - r * a.per) * 8;
-}
-
-// Elements [c, c + 8) of a row (0 at and past n).
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, bool aligned, float (&v)[8]) {
-  if (aligned && c + 8 <= n) {
-    constexpr int kWords = sizeof(T) * 8 / 16;
-    uint4 w[kWords];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
-    const T* e = reinterpret_cast<const T*>(w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float<T>(e[i]);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_float<T>(row[c + i]) : 0.0f;
-}
-
-// Sum over the block, the same in every thread.
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* shared) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T s = 0;
-#pragma unroll
-  for (int i = 0; i < kNormThreads / 32; ++i) s += shared[i];
-  return s;
 }
 
 template <typename T>
@@ -99,50 +62,48 @@ __global__ void __launch_bounds__(kNormThreads) sum_squares_kernel(const NormArg
   ptx::pdl_launch_dependents();
   ptx::pdl_wait_prior_grid();
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
-  float sum = 0.0f, small = 0.0f, large = 0.0f;  // small x 2^60, large x 2^-60
-  for (int64_t s = static_cast<int64_t>(blockIdx.x) * kNormStep + threadIdx.x; s < a.vectors;
-       s += static_cast<int64_t>(gridDim.x) * kNormStep) {
-    float v[kNormVecs][8];
+  SquareSum sum;
+  auto pass = [&](auto&& add) {
+    for (int64_t s = static_cast<int64_t>(blockIdx.x) * kNormStep + threadIdx.x; s < a.vectors;
+         s += static_cast<int64_t>(gridDim.x) * kNormStep) {
+      float v[kNormVecs][8];
 #pragma unroll
-    for (int i = 0; i < kNormVecs; ++i) {
-      const int64_t at = s + i * kNormThreads;
-      int64_t r, c;
-      place(a, at < a.vectors ? at : 0, r, c);
-      load8<T>(g + r * a.ld, c, at < a.vectors ? a.n : 0, a.aligned != 0, v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kNormVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = v[i][j], size = fabsf(x);
-        if (sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value) {  // fp16: within range
-          sum = fmaf(x, x, sum);
-          continue;
-        }
-        const float lo = size < 0x1p-40f ? x * 0x1p60f : 0.0f, hi = size > 0x1p40f ? x * 0x1p-60f : 0.0f;
-        const float mid = size < 0x1p-40f || size > 0x1p40f ? 0.0f : x;  // NaN is here
-        small = fmaf(lo, lo, small);
-        sum = fmaf(mid, mid, sum);
-        large = fmaf(hi, hi, large);
+      for (int i = 0; i < kNormVecs; ++i) {
+        const int64_t at = s + i * kNormThreads;
+        int64_t r, c;
+        place(a, at < a.vectors ? at : 0, r, c);
+        load8<T>(g + r * a.ld, c, at < a.vectors ? a.n : 0, a.aligned != 0, v[i]);
       }
+#pragma unroll
+      for (int i = 0; i < kNormVecs; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add(v[i][j]);
+    }
+  };
+  pass([&](float x) { sum.mid = fmaf(x, x, sum.mid); });
+  double total = sum.block_total<kNormThreads>(shared);
+  if (!__syncthreads_and(threadIdx.x > 0 || plain_sum_holds(total))) {
+    sum = SquareSum();
+    pass([&](float x) { sum.add<T>(x); });
+    total = sum.block_total<kNormThreads>(shared);
   }
-  const double total = block_sum<double>(
-      static_cast<double>(sum) + static_cast<double>(small) * 0x1p-120 + static_cast<double>(large) * 0x1p120, shared);
   if (threadIdx.x == 0) a.partial[blockIdx.y * gridDim.x + blockIdx.x] = total;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const NormArgs a, int parts) {
-  __shared__ double shared[kNormThreads / 32];
+  __shared__ float shared;
   ptx::pdl_launch_dependents();
   ptx::pdl_wait_prior_grid();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kNormThreads)
-    sum += __ldcg(a.partial + blockIdx.y * parts + i);
-  sum = block_sum<double>(sum, shared);
-  // The scale in two factors, each within fp32's range.  (NaN: no comparison holds.)
-  const double norm = sqrt(sum) < static_cast<double>(a.eps) ? static_cast<double>(a.eps) : sqrt(sum);
-  const float scale = static_cast<float>(sqrt(static_cast<double>(kIterateScale) / norm));
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 32) sum += __ldcg(a.partial + blockIdx.y * parts + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (threadIdx.x == 0) shared = half_scale(sum, a.eps);
+  }
+  __syncthreads();
+  const float scale = shared;
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
   uint16_t* x = a.x + blockIdx.y * a.m * a.ldx;
   for (int64_t s = static_cast<int64_t>(blockIdx.x) * kNormStep + threadIdx.x; s < a.vectors;
@@ -199,11 +160,23 @@ struct Layout {
   uint16_t* b;
   int64_t np, s, sp;
   int blocks;
+  SmallPlan small;
+  float* parts;
+  uint16_t* gram;
   size_t bytes;
 };
 
 Layout layout(const gemm_ops* ops, const gemm_orthogonalize_args_t* g, void* workspace) {
-  Layout l;
+  Layout l{};
+  Carver c(workspace);
+  l.small = small_newton_plan(ops, g->m, g->n, g->batch);
+  if (l.small.rows > 0) {
+    l.norms = static_cast<double*>(c.take(l.small.norm_bytes));
+    l.parts = static_cast<float*>(c.take(l.small.part_bytes));
+    l.gram = static_cast<uint16_t*>(c.take(l.small.gram_bytes));
+    l.bytes = c.used;
+    return l;
+  }
   l.np = round8(g->n);
   l.s = std::min(g->m, g->n);
   l.sp = round8(l.s);
@@ -212,7 +185,6 @@ Layout layout(const gemm_ops* ops, const gemm_orthogonalize_args_t* g, void* wor
       1, std::min<int64_t>(steps, kNormBlocks / std::max<int64_t>(1, std::min<int64_t>(g->batch, kNormBlocks)))));
   const size_t x = static_cast<size_t>(g->batch) * g->m * l.np * 2;
   const size_t a = static_cast<size_t>(g->batch) * l.s * l.sp * 2;
-  Carver c(workspace);
   l.partials = static_cast<float*>(c.take(block_workspace(ops)));
   l.norms = static_cast<double*>(c.take(static_cast<size_t>(g->batch) * l.blocks * sizeof(double)));
   l.x[0] = static_cast<uint16_t*>(c.take(x));
@@ -274,7 +246,7 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
   if (st != GEMM_OK || args->batch == 0 || args->m == 0 || args->n == 0) return st;
   const int64_t m = args->m, n = args->n, batch = args->batch;
   const Layout l = layout(ops, args, workspace);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < l.bytes)
+  if ((!workspace && l.bytes > 0) || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < l.bytes)
     return ops_fail(GEMM_ERR_INVALID_ARG, "workspace NULL, not 256-byte aligned or below %zu bytes", l.bytes);
   const size_t g_bytes = (static_cast<size_t>(batch - 1) * (batch > 1 ? args->batch_stride : 0) +
                           static_cast<size_t>(m - 1) * args->ldg + n) * elem_bytes(args->dtype);
@@ -286,6 +258,33 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
   if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
 
+  const int64_t vec = 16 / static_cast<int64_t>(elem_bytes(args->dtype));
+  const bool aligned = (reinterpret_cast<uintptr_t>(args->g) & 15u) == 0 && args->ldg % vec == 0 &&
+                       (batch == 1 || args->batch_stride % vec == 0);
+  if (l.small.rows > 0) {
+    SmallNewton p{};
+    p.g = args->g;
+    p.ld = args->ldg;
+    p.g_batch = batch > 1 ? args->batch_stride : 0;
+    p.type = args->dtype;
+    p.tall = m > n;
+    p.aligned = aligned;
+    p.s = static_cast<int>(std::min(m, n));
+    p.l = static_cast<int>(std::max(m, n));
+    p.batch = static_cast<int>(batch);
+    p.steps = args->steps;
+    p.a = args->a;
+    p.b = args->b;
+    p.c = args->c;
+    p.eps = args->eps;
+    p.out = static_cast<uint16_t*>(args->out);
+    p.norms = l.norms;
+    p.parts = l.parts;
+    p.gram = l.gram;
+    const cudaError_t small = small_newton_launch(ops, l.small, p, stream);
+    return small == cudaSuccess ? GEMM_OK : ops_cuda_fail(small, "on-chip iteration launch");
+  }
+
   NormArgs na{};
   na.g = args->g;
   na.m = m;
@@ -294,9 +293,7 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
   na.batch_stride = batch > 1 ? args->batch_stride : 0;
   na.per = l.np / 8;
   na.vectors = m * na.per;
-  const int64_t vec = 16 / static_cast<int64_t>(elem_bytes(args->dtype));
-  na.aligned = (reinterpret_cast<uintptr_t>(args->g) & 15u) == 0 && args->ldg % vec == 0 &&
-               (batch == 1 || args->batch_stride % vec == 0);
+  na.aligned = aligned;
   na.partial = l.norms;
   na.x = l.x[0];
   na.ldx = l.np;

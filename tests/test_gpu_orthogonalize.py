@@ -179,3 +179,31 @@ def test_refusals():
         with pytest.raises(sg.GemmError) as e:
             sg.orthogonalize(g, **kw)
         assert e.value.status == sg.GEMM_ERR_INVALID_ARG
+
+
+# Both ways through the operator (a short side up to 256 stays on chip), wide and tall.
+@pytest.mark.parametrize("shape", [(96, 700), (700, 96), (200, 300), (310, 420)], ids=str)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_extreme_scales_of_the_gradient(shape, dt):
+    g = gradient(*shape, seed=11).to(DT[dt])
+    ref = sg.orthogonalize(g.cuda())
+    for k in (-105, -30, 30, 120):
+        got = sg.orthogonalize((g.double() * 2.0 ** k).to(DT[dt]).cuda(), eps=1e-38)
+        assert (got.double() - ref.double()).norm() <= 2.0 ** -9 * ref.double().norm(), k
+
+
+@pytest.mark.parametrize("shape", [(128, 512), (129, 192), (128, 513), (193, 129), (4096, 128), (128, 4097),
+                                   (256, 1536), (1537, 256), (255, 1001), (2, 4001), (4001, 100), (257, 64)], ids=str)
+def test_edges_of_the_chip(shape):
+    g = gradient(*shape, seed=12)
+    check(sg.orthogonalize(g.cuda()), g)
+
+
+@pytest.mark.parametrize("b,m,n", [(200, 20, 24), (40, 130, 200), (60, 200, 260), (30, 64, 1100), (3, 1000, 70)])
+def test_many_small_matrices(b, m, n):
+    gen = torch.Generator().manual_seed(b)
+    g = torch.randn(b, m, n, generator=gen)
+    got = sg.orthogonalize(g.cuda())
+    assert torch.equal(got, sg.orthogonalize(g.cuda()))
+    for i in (0, 1, b // 2, b - 1):
+        check(got[i], g[i])
