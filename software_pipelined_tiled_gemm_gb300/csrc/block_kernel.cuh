@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
   constexpr int kBRows = BN / CG;                 // B rows this CTA copies
   constexpr uint32_t kStageB = kBRows * kBK * 2;
   constexpr int kTileM = kBM * CG;
+  constexpr bool kUseD = kEpi >= kEpiDiagOut;
   constexpr int kOutN = kEpi == kEpiGated ? BN / 2 : BN;  // output columns of a tile
   constexpr uint32_t kBoxBytes = 64u * kBK * 2u;          // MN-major box: 64 columns x 64 K rows
   // K-major A of a single row of tiles: only the rows that exist are copied
@@ -595,6 +596,18 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
     };
     auto wait_d = [&]() { return wait_bounded(d_bar(ew, buf), (d_phase >> buf) & 1u, p, kDetailSkCopy); };
 
+    // The diagonal's elements for this lane's row, or for two of a chunk's
+    // columns: read a chunk (or a tile) before they are used.
+    float diag0 = 0.0f, diag1 = 0.0f;
+    auto load_diag = [&](int row0, int col0, int z) {
+      const float* diag = p.diag + z * p.diag_batch;
+      if constexpr (kEpi == kEpiDiagRows) diag0 = row0 + lane < p.M ? __ldcg(diag + row0 + lane) : 0.0f;
+      if constexpr (kEpi == kEpiDiagCols) {
+        diag0 = __ldcg(diag + col0 + lane);
+        diag1 = __ldcg(diag + col0 + 32 + lane);
+      }
+    };
+
     // The staged block out, once the quarter's warps have written it.
     auto store = [&](const BlockOut& o, const CUtensorMap& map, uint8_t* sb, int row0, int col0, int z) {
       if (o.tma) ptx::fence_proxy_async_smem();
@@ -676,7 +689,9 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
         store(p.out0, maps.c0, my_stage, row0, col0, z);
         store(p.out1, maps.c1, my_stage + kStoreBuf, row0, col0, z);
       } else {
-        if (p.use_d) {
+        const float beta = fmaf(p.alpha, diag0, p.beta), beta2 = fmaf(p.alpha, diag1, p.beta);
+        if (kEpi == kEpiDiagCols && more) load_diag(row0, col0 + 64, z);
+        if constexpr (kUseD) {
           const bool got = wait_d();
           d_phase ^= 1u << buf;
           if (!quarter_all(got)) return false;
@@ -692,7 +707,12 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
           acc_cols(cc + 16 * s, r);
 #pragma unroll
           for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(p.alpha * __uint_as_float(r[j]));
-          if (p.use_d) {
+          if constexpr (kUseD) {
+            auto weight = [&](int i) {
+              return kEpi == kEpiDiagCols
+                         ? __shfl_sync(0xffffffffu, s < 2 ? beta : beta2, 16 * (s & 1) + i)
+                         : beta;
+            };
             // D is fp16 (the iterate's type), in the swizzled layout of the box.
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -703,9 +723,21 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
               for (int e = 0; e < 4; ++e) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&wd[e]));
                 const int i = 8 * j + 2 * e;
-                r[i] = __float_as_uint(fmaf(p.beta, f.x, __uint_as_float(r[i])));
-                r[i + 1] = __float_as_uint(fmaf(p.beta, f.y, __uint_as_float(r[i + 1])));
+                r[i] = __float_as_uint(fmaf(weight(i), f.x, __uint_as_float(r[i])));
+                r[i + 1] = __float_as_uint(fmaf(weight(i + 1), f.y, __uint_as_float(r[i + 1])));
               }
+            }
+          }
+          if constexpr (kEpi == kEpiDiagOut) {
+            if ((col0 + 16 * s) >> 5 == row0 >> 5) {
+              float* diag = p.diag + z * p.diag_batch;
+              const int at = row0 + lane - (col0 + 16 * s);  // the diagonal's of these columns
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (j == at) {
+                  if (row0 + lane < p.M) __stcg(diag + row0 + lane, __uint_as_float(r[j]));
+                  r[j] = 0u;
+                }
             }
           }
 #pragma unroll
@@ -737,7 +769,7 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
         return u < row_blocks * kChunks && first_row + (u / kChunks) * 32 < p.M &&
                n0 + (u % kChunks) * 64 < p.N;
       };
-      if (kEpi == kEpiLinear && p.use_d && unit_exists(ew))
+      if (kUseD && unit_exists(ew))
         load_d(buf, first_row + (ew / kChunks) * 32, n0 + (ew % kChunks) * 64, t.z);
       // The idle ring: this CTA's partial, [quarter][column][row], then what it
       // receives, [CTA][quarter of this CTA's][column][row].
@@ -790,6 +822,7 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
           const float* in = reinterpret_cast<const float*>(smem + kSplitBytes) + rb * (kQuarter / 4) + lane;
           const float* own = reinterpret_cast<const float*>(smem) + (part * row_blocks + rb) * (kQuarter / 4) + lane;
           const int step = row_blocks * (kQuarter / 4);
+          if (kUseD) load_diag(first_row + rb * 32, n0 + (u % kChunks) * 64, t.z);
           auto from_inbox = [&](int c, uint32_t (&r)[16]) {
             float v[16];
 #pragma unroll
@@ -818,8 +851,11 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
                                kCheckPartial))
         break;
       // The tile's first chunk of D arrives while the accumulator fills.
-      const bool d_first = kEpi == kEpiLinear && p.use_d && stores;
-      if (d_first) load_d(buf, row0, n0, t.z);
+      const bool d_first = kUseD && stores;
+      if (d_first) {
+        load_d(buf, row0, n0, t.z);
+        load_diag(row0, n0, t.z);
+      }
       // The kept projections of these rows, a contiguous run each, into L2.
       if (kEpi == kEpiGatedBwd && stores && g == 0 && lane < 2) {
         const uint32_t n = static_cast<uint32_t>(min(BN, p.N - n0));

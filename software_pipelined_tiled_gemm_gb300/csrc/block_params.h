@@ -13,9 +13,14 @@
 namespace spgemm {
 
 // What the epilogue does with a tile's fp32 accumulator.
-constexpr int kEpiLinear = 0;     // C = alpha acc + beta D, optionally mirrored across the diagonal
+constexpr int kEpiLinear = 0;     // C = alpha acc, optionally mirrored across the diagonal
 constexpr int kEpiGated = 1;      // H = act(gate) * up, the tile holding both; keeps both in fp32
 constexpr int kEpiGatedBwd = 2;   // acc = dH: writes dGate and dUp from the kept gate and up
+
+// C = alpha acc + beta D, with a diagonal in fp32 beside a 16-bit matrix: C's is
+// moved there and 0 left in its place; or alpha diag[row] D or alpha
+// diag[column] D is added.
+constexpr int kEpiDiagOut = 3, kEpiDiagRows = 4, kEpiDiagCols = 5;
 
 // Activation of the gated block (gemm_act_t).
 constexpr int kActSilu = 0, kActGelu = 1, kActRelu = 2;
@@ -44,8 +49,9 @@ struct BlockParams : Params {
   int out_bf16;        // type of the 16-bit output(s)
   int act;
   int gate_rows;       // gated: rows of the gate half of w_in (the up half follows)
-  int use_d;           // linear: beta D is added
   float alpha, beta;
+  float* diag;         // kEpiDiagOut, kEpiDiagRows, kEpiDiagCols
+  int64_t diag_batch;  // of one matrix, elements
   BlockOut out0, out1;  // C or H or dGate; dUp
   // Gated: gate and up in fp32, [half][row block of 32][column][row in block],
   // so that an epilogue warp (lane = row) moves one 128-byte line a column;
@@ -82,6 +88,9 @@ constexpr int kMaxSplits = 4;
 SPGEMM_DECLARE_BLOCK(nt)         // linear, A M x K, B N x K
 SPGEMM_DECLARE_BLOCK(nn)         // linear, A M x K, B K x N
 SPGEMM_DECLARE_BLOCK(tn)         // linear, A K x M, B K x N
+SPGEMM_DECLARE_BLOCK(diag_out)   // kEpiDiagOut,  A M x K, B N x K
+SPGEMM_DECLARE_BLOCK(diag_rows)  // kEpiDiagRows, A M x K, B K x N
+SPGEMM_DECLARE_BLOCK(diag_cols)  // kEpiDiagCols, A M x K, B N x K
 SPGEMM_DECLARE_BLOCK(gated)      // gated,          A M x K, B 2N x K
 SPGEMM_DECLARE_BLOCK(gated_bwd)  // gated backward, A M x K, B K x N
 #undef SPGEMM_DECLARE_BLOCK

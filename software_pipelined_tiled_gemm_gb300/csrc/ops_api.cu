@@ -120,7 +120,10 @@ size_t block_workspace(const gemm_ops* ops) {
 gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, cudaStream_t stream) {
   const bool gated = pr.kind == BlockProblem::kGated;
   const bool a_t = pr.kind == BlockProblem::kTN;
+  const bool use_d = pr.kind == BlockProblem::kDiagOut || pr.kind == BlockProblem::kDiagRows ||
+                     pr.kind == BlockProblem::kDiagCols;
   const bool b_n = pr.kind == BlockProblem::kNN || pr.kind == BlockProblem::kTN ||
+                   pr.kind == BlockProblem::kDiagRows ||
                    pr.kind == BlockProblem::kGatedBwd;
   BlockMaps maps;
   BlockParams p;
@@ -228,7 +231,6 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.out_bf16 = pr.out_bf16 ? 1 : 0;
   p.act = pr.act;
   p.gate_rows = gated ? static_cast<int>(pr.N) : 0;
-  p.use_d = pr.d.ptr != nullptr ? 1 : 0;
   // Two epilogue warps per lane quarter halve an epilogue that no main loop
   // hides: single CTAs, one wave (or less) of tiles, and pairs whose K is
   // short next to what their epilogue moves (one warp a quarter -> two, in us:
@@ -236,11 +238,13 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   // that keeps its projections 142 -> 138; updates of 2048 x 8192 552 -> 534;
   // at K = 16384 no difference).
   const int64_t short_k = pr.kind == BlockProblem::kGatedBwd ? 8192
-                          : gated || p.use_d                 ? 2048
+                          : gated || use_d                   ? 2048
                                                              : 1024;
   p.epi = cg == 1 || pr.K <= short_k || nt <= walkers ? 2 : 1;
   p.alpha = pr.alpha;
   p.beta = pr.beta;
+  p.diag = pr.diag;
+  p.diag_batch = pr.diag_batch;
   p.out0 = describe_out(pr.out0, pr.N, pr.batch);
   p.out1 = describe_out(pr.out1, pr.N, pr.batch);
   p.pre = pr.pre;
@@ -259,7 +263,7 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   if (st == GEMM_OK && p.out0.tma) st = encode(&maps.c0, pr.out_bf16, o0, pr.batch, 64, 32, none);
   if (st == GEMM_OK && p.out1.ptr && p.out1.tma)
     st = encode(&maps.c1, pr.out_bf16, o1, pr.batch, 64, 32, none);
-  if (st == GEMM_OK && p.use_d) st = encode(&maps.d, false, pr.d, pr.batch, 64, 32, none);
+  if (st == GEMM_OK && use_d) st = encode(&maps.d, false, pr.d, pr.batch, 64, 32, none);
   if (st != GEMM_OK) return st;
 
   const int grid = static_cast<int>(walkers) * cg;
@@ -268,6 +272,9 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
     case BlockProblem::kNT: e = block_launch_nt(maps, p, cg, grid, smem, stream); break;
     case BlockProblem::kNN: e = block_launch_nn(maps, p, cg, grid, smem, stream); break;
     case BlockProblem::kTN: e = block_launch_tn(maps, p, cg, grid, smem, stream); break;
+    case BlockProblem::kDiagOut: e = block_launch_diag_out(maps, p, cg, grid, smem, stream); break;
+    case BlockProblem::kDiagRows: e = block_launch_diag_rows(maps, p, cg, grid, smem, stream); break;
+    case BlockProblem::kDiagCols: e = block_launch_diag_cols(maps, p, cg, grid, smem, stream); break;
     case BlockProblem::kGated: e = block_launch_gated(maps, p, cg, grid, smem, stream); break;
     default: e = block_launch_gated_bwd(maps, p, cg, grid, smem, stream); break;
   }
@@ -303,7 +310,8 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
   ops->smem_optin = static_cast<size_t>(desc.smem_optin);
   ops->l2_bytes = desc.l2_bytes;
   ops->timeout_ns = kOpsTimeoutNs;
-  for (auto set : {block_set_smem_nt, block_set_smem_nn, block_set_smem_tn, block_set_smem_gated,
+  for (auto set : {block_set_smem_nt, block_set_smem_nn, block_set_smem_tn, block_set_smem_diag_out,
+                   block_set_smem_diag_rows, block_set_smem_diag_cols, block_set_smem_gated,
                    block_set_smem_gated_bwd})
     if (e == cudaSuccess) e = set(ops->smem_optin);
   if (e == cudaSuccess) e = logprobs_set_smem();

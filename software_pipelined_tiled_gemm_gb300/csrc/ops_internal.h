@@ -95,13 +95,15 @@ cudaError_t launch_pack(const PackJobs& jobs, int sm_count, cudaStream_t stream)
 
 // One product of the block kernels.
 struct BlockProblem {
-  enum Kind { kNT, kNN, kTN, kGated, kGatedBwd } kind = kNT;
+  enum Kind { kNT, kNN, kTN, kDiagOut, kDiagRows, kDiagCols, kGated, kGatedBwd } kind = kNT;
   int64_t M = 0, N = 0, K = 0;   // output extent (gated: N columns of H) and reduction
   int64_t batch = 1;
-  Matrix a, b, d;                // d: added with weight beta (fp16)
+  Matrix a, b, d;                // d: added with weight beta (fp16; the kDiag kinds)
   bool bf16 = false, out_bf16 = false;
   bool symmetric = false;
   float alpha = 1.0f, beta = 0.0f;
+  float* diag = nullptr;         // the kDiag kinds: diag_batch elements a matrix, at least M
+  int64_t diag_batch = 0;        // (kDiagOut, kDiagRows) or N rounded up to 64 (kDiagCols)
   int act = 0;
   Matrix out0, out1;             // cols: the columns of each row that may be written (>= N)
   float* pre = nullptr;

@@ -11,6 +11,12 @@
 // and all read the fp16 sums back.  Only blocks on and above the diagonal are
 // multiplied, the rest is mirrored.
 //
+// Where six panels or fewer are a CTA's, what rounding the iterate to fp16
+// loses is kept beside it (kLow) and carried in the term a Z: its errors along
+// small singular values grow up to a^5 = 480 times, so that of 8 x 8 or 64 x 64
+// matrices a few end several times further off than the mean.  It costs 3 us;
+// 64 x 64 ends 1.9e-3 from the exact result, of which 1.65e-3 is bf16's.
+//
 // Latency is what bounds it: separate products spend 5 to 7.5 us a launch on
 // matrices of this size, nearly all of it launch, first copies and the last
 // store.  Here a step on one CTA is three bursts of tcgen05.mma with an
@@ -54,7 +60,9 @@ struct Small {
   static constexpr int kPanels = small_newton_panels(R);      // of Z in a CTA, at most
   static constexpr int kCols = R == 1 ? 128 : 384;            // accumulator columns of A's upper blocks
   static constexpr int kElems = kCols * 128;
-  static constexpr uint32_t kBytes = kSquare + kPanels * kPanel;
+  // As many as leave room for the iterate's low parts (kLow).
+  static constexpr int kLowPanels = R == 1 ? 6 : 0;
+  static constexpr uint32_t kBytes = kSquare + (R == 1 ? 2 * kLowPanels : kPanels) * kPanel;
 };
 
 // Byte offset of element (row, col) from the first panel.
@@ -75,6 +83,12 @@ __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// What two values rounded to `high` lost.
+__device__ __forceinline__ uint32_t low_half2(uint32_t high, float lo, float hi) {
+  const float2 f = unpack_half2(high);
+  return pack_half2(lo - f.x, hi - f.y);
 }
 
 // How a CTA's part of Z is read from G, in items of which neighbouring threads
@@ -226,15 +240,17 @@ __device__ __forceinline__ void add_partials(const float* parts, uint16_t* gram,
   }
 }
 
-template <int R>
+template <int R, bool kLow>
 __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_constant__ SmallNewton p) {
   using K = Small<R>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ double shared[kThreads / 32];
   __shared__ float shared_scale;
+  __shared__ float diag[K::kSide];  // of B, in fp32 (see orthogonal.cu); 0 in the square
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   uint8_t* square = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   uint8_t* z = square + K::kSquare;
+  uint8_t* z_low = z + K::kLowPanels * K::kPanel;
   const uint32_t square_addr = ptx::smem_addr(square), z_addr = square_addr + K::kSquare;
   const uint32_t bar = square_addr + K::kBytes;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(square + K::kBytes + 8u);
@@ -338,13 +354,23 @@ __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_
         uint8_t* dst = z + element<R>(row, col);
         constexpr int kCount = sizeof(v) / sizeof(float);
         if constexpr (kCount == 1) {
-          *reinterpret_cast<__half*>(dst) = __float2half_rn(v[0] * scale * scale);
+          const float x = v[0] * scale * scale;
+          const __half high = __float2half_rn(x);
+          *reinterpret_cast<__half*>(dst) = high;
+          if (kLow)
+            *reinterpret_cast<__half*>(z_low + element<R>(row, col)) = __float2half_rn(x - __half2float(high));
         } else {
 #pragma unroll
-          for (int j = 0; j < kCount; j += 4)
-            *reinterpret_cast<uint2*>(dst + 2 * j) =
-                make_uint2(pack_half2(v[j] * scale * scale, v[j + 1] * scale * scale),
-                           pack_half2(v[j + 2] * scale * scale, v[j + 3] * scale * scale));
+          for (int j = 0; j < kCount; j += 4) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = v[j + e] * scale * scale;
+            const uint2 high = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+            *reinterpret_cast<uint2*>(dst + 2 * j) = high;
+            if (kLow)
+              *reinterpret_cast<uint2*>(z_low + element<R>(row, col) + 2 * j) =
+                  make_uint2(low_half2(high.x, x[0], x[1]), low_half2(high.y, x[2], x[3]));
+          }
         }
       });
     });
@@ -463,6 +489,20 @@ __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_
             w[j] = pack_half2(fmaf(p.c, __uint_as_float(r[2 * j]), p.b * f.x),
                               fmaf(p.c, __uint_as_float(r[2 * j + 1]), p.b * f.y));
           }
+          if (col >> 5 == row >> 5) {  // the warp's rows meet the diagonal here
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 f = unpack_half2(old[j]);
+              if (row == col + 2 * j) {
+                diag[row] = fmaf(p.c, __uint_as_float(r[2 * j]), p.b * f.x);
+                w[j] &= 0xFFFF0000u;
+              }
+              if (row == col + 2 * j + 1) {
+                diag[row] = fmaf(p.c, __uint_as_float(r[2 * j + 1]), p.b * f.y);
+                w[j] &= 0x0000FFFFu;
+              }
+            }
+          }
           *at0 = make_uint4(w[0], w[1], w[2], w[3]);
           *at1 = make_uint4(w[4], w[5], w[6], w[7]);
           if (R == 2 && i == 0 && c >= 128) {
@@ -488,10 +528,11 @@ __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_
             }
           }
       });
-      const float wa = last ? inv * p.a : p.a, wm = last ? inv : 1.0f;
+      const float wm = last ? inv : 1.0f;
       uint16_t* out = p.out + static_cast<int64_t>(m) * p.s * p.l;
       for (int i = 0; i < R; ++i) {
         const int row = i * 128 + q * 32 + lane;
+        const float weight = p.a + diag[row], wa = wm * weight;
 #pragma unroll 1
         for (int c = group * 32; c < panels * 64; c += 32 * kGroups) {
           uint32_t r[32], w[16];
@@ -500,6 +541,20 @@ __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_
 #pragma unroll
           for (int j = 0; j < 4; ++j) old[j] = *reinterpret_cast<const uint4*>(z + element<R>(row, c + 8 * j));
           ptx::tmem_wait_ld();
+          if (kLow) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 o = *reinterpret_cast<const uint4*>(z_low + element<R>(row, c + 8 * j));
+              const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack_half2(ow[e]);
+                const int n = 8 * j + 2 * e;
+                r[n] = __float_as_uint(fmaf(weight, f.x, __uint_as_float(r[n])));
+                r[n + 1] = __float_as_uint(fmaf(weight, f.y, __uint_as_float(r[n + 1])));
+              }
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint4& o = old[j >> 2];
@@ -507,6 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_
             const float x = fmaf(wm, __uint_as_float(r[2 * j]), wa * f.x);
             const float y = fmaf(wm, __uint_as_float(r[2 * j + 1]), wa * f.y);
             w[j] = last ? pack_bf162(x, y) : pack_half2(x, y);
+            r[2 * j] = __float_as_uint(x);
+            r[2 * j + 1] = __float_as_uint(y);
           }
           if (last && p.tall) {  // a column of Z is a row of the output
 #pragma unroll
@@ -518,6 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_
             for (int j = 0; j < 4; ++j)
               *reinterpret_cast<uint4*>(z + element<R>(row, c + 8 * j)) =
                   make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            if (kLow && !last) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[j] = low_half2(w[j], __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(z_low + element<R>(row, c + 8 * j)) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            }
           }
         }
       }
@@ -539,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_newton_kernel(const __grid_
   if (warp == 0) ptx::tmem_dealloc<1>(tmem, 512u);
 }
 
-constexpr size_t kStaticBytes = 1024;  // left for the kernel's own static shared memory
+constexpr size_t kStaticBytes = 1536;  // left for the kernel's own static shared memory
 
 // The whole opt-in shared memory, whatever the panels need: a second CTA on
 // an SM could not have its TMEM.
@@ -563,14 +629,16 @@ void configure(const gemm_ops* ops, int cluster, int grid, cudaStream_t stream, 
 
 template <int R>
 cudaError_t init(gemm_ops* ops) {
-  cudaError_t e = cudaFuncSetAttribute(small_newton_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem_bytes(ops)));
+  const cudaFuncAttribute attribute = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const int bytes = static_cast<int>(smem_bytes(ops));
+  cudaError_t e = cudaFuncSetAttribute(small_newton_kernel<R, false>, attribute, bytes);
+  if (e == cudaSuccess && R == 1) e = cudaFuncSetAttribute(small_newton_kernel<R, R == 1>, attribute, bytes);
   ops->small_clusters[R - 1][1] = ops->sm_count;
   for (int c = 2; c <= kSmallCluster && e == cudaSuccess; ++c) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     configure(ops, c, c, nullptr, &cfg, attr);
-    e = cudaOccupancyMaxActiveClusters(&ops->small_clusters[R - 1][c], small_newton_kernel<R>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&ops->small_clusters[R - 1][c], small_newton_kernel<R, false>, &cfg);
   }
   return e;
 }
@@ -580,7 +648,9 @@ cudaError_t launch(const gemm_ops* ops, const SmallNewton& p, int grid, cudaStre
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   configure(ops, p.cluster, grid, stream, &cfg, attr);
-  return cudaLaunchKernelEx(&cfg, small_newton_kernel<R>, p);
+  if (R == 1 && ceil_div(ceil_div(p.l, 64), p.cluster) <= Small<R>::kLowPanels)
+    return cudaLaunchKernelEx(&cfg, small_newton_kernel<R, R == 1>, p);
+  return cudaLaunchKernelEx(&cfg, small_newton_kernel<R, false>, p);
 }
 
 }  // namespace

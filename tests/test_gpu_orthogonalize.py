@@ -207,3 +207,14 @@ def test_many_small_matrices(b, m, n):
     assert torch.equal(got, sg.orthogonalize(g.cuda()))
     for i in (0, 1, b // 2, b - 1):
         check(got[i], g[i])
+
+
+# The rows (or columns) of a matrix far from square have nearly equal norms,
+# so that the diagonals of the products share one rounding error.  The result
+# may be half as far again from the exact one as its own rounding to bf16.
+@pytest.mark.parametrize("shape", [(64, 7608), (7000, 48), (40, 3000), (100, 1000), (300, 9000)], ids=str)
+def test_far_from_square(shape):
+    g = gradient(*shape, seed=13)
+    exact = iterate(g)
+    once = float((exact.bfloat16().double() - exact).norm())
+    assert float((sg.orthogonalize(g.cuda()).double().cpu() - exact).norm()) <= 1.5 * once
