@@ -35,7 +35,7 @@ CHECKED_FLAGS = ["-DSPGEMM_BOUNDS_CHECKS=1"]
 SOURCES = ["gemm_api.cu", "gemm_bn64.cu", "gemm_bn128.cu", "gemm_bn256.cu", "gemm_pair128.cu",
            "gemm_pair256.cu", "pad.cu", "fill.cu", "noalloc.cu", "ops_api.cu", "block_nt.cu",
            "block_nn.cu", "block_tn.cu", "block_diag_out.cu", "block_diag_rows.cu",
-           "block_diag_cols.cu", "block_gated.cu", "block_gated_bwd.cu", "pack.cu", "ffn.cu",
+           "block_diag_cols.cu", "block_gated.cu", "block_gated_bwd.cu", "pack.cu", "ffn.cu", "few_tokens.cu",
            "orthogonal.cu", "orthogonal_small.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -8,6 +8,7 @@
 
 #include <cstdint>
 
+#include "few_tokens.h"
 #include "ops_internal.h"
 
 using namespace spgemm;
@@ -180,27 +181,61 @@ gemm_status_t gemm_ffn_run(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* w
   const cudaError_t e = launch_pack(f.pack, ops->sm_count, stream);
   if (e != cudaSuccess) return ops_cuda_fail(e, "padding copy launch");
 
-  BlockProblem g;
-  g.kind = BlockProblem::kGated;
-  g.M = f.M;
-  g.N = f.I;
-  g.K = f.D;
-  g.a = f.x;
-  g.b = f.w_in;
-  g.bf16 = g.out_bf16 = f.bf16;
-  g.act = static_cast<int>(args->act);
-  g.out0 = {f.h, f.M, f.Ip, f.Ip, 0};
-  g.pre = f.pre;
-  g.stream_b = true;
-  st = run_block(ops, g, f.partials, stream);
-  if (st != GEMM_OK) return st;
+  // A product of few tokens is a pass over its weights (few_tokens.cu).  The
+  // fault hook withholds a copy, of which that path has none.
+  auto few = [&](int64_t k, int64_t rows) {
+    return few_tokens_fits(ops, f.M, k, rows) && ops->debug_fault == 0;
+  };
+  const bool few_first = few(f.D, 2 * f.I);
+  if (few_first) {
+    FewTokens t{};
+    t.x = f.x;
+    t.w = f.w_in;
+    t.rows = f.I;
+    t.gated = true;
+    t.bf16 = f.bf16;
+    t.out = f.h;
+    t.ldo = f.Ip;
+    t.pre = f.pre;
+    t.act = static_cast<int>(args->act);
+    const cudaError_t err = few_tokens_launch(ops, t, stream);
+    if (err != cudaSuccess) return ops_cuda_fail(err, "few tokens launch");
+  } else {
+    BlockProblem g;
+    g.kind = BlockProblem::kGated;
+    g.M = f.M;
+    g.N = f.I;
+    g.K = f.D;
+    g.a = f.x;
+    g.b = f.w_in;
+    g.bf16 = g.out_bf16 = f.bf16;
+    g.act = static_cast<int>(args->act);
+    g.out0 = {f.h, f.M, f.Ip, f.Ip, 0};
+    g.pre = f.pre;
+    g.stream_b = true;
+    st = run_block(ops, g, f.partials, stream);
+    if (st != GEMM_OK) return st;
+  }
 
+  const Matrix h{f.h, f.M, f.I, f.Ip, 0};
+  if (few(f.I, f.D)) {
+    FewTokens t{};
+    t.x = h;
+    t.w = f.w_out;
+    t.rows = f.D;
+    t.bf16 = f.bf16;
+    t.weights_ready = few_first;
+    t.out = static_cast<uint16_t*>(args->y);
+    t.ldo = f.D;
+    const cudaError_t err = few_tokens_launch(ops, t, stream);
+    return err == cudaSuccess ? GEMM_OK : ops_cuda_fail(err, "few tokens launch");
+  }
   BlockProblem y;
   y.kind = BlockProblem::kNT;
   y.M = f.M;
   y.N = f.D;
   y.K = f.I;
-  y.a = {f.h, f.M, f.I, f.Ip, 0};
+  y.a = h;
   y.b = f.w_out;
   y.bf16 = y.out_bf16 = f.bf16;
   y.out0 = {args->y, f.M, f.D, f.D, 0};

@@ -10,6 +10,7 @@
 #include <mutex>
 #include <new>
 
+#include "few_tokens.h"
 #include "ops_internal.h"
 #include "orthogonal_small.h"
 #include "ptx.cuh"
@@ -316,6 +317,7 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
     if (e == cudaSuccess) e = set(ops->smem_optin);
   if (e == cudaSuccess) e = logprobs_set_smem();
   if (e == cudaSuccess) e = small_newton_init(ops);
+  if (e == cudaSuccess) e = few_tokens_init(ops);
   const size_t flags = static_cast<size_t>(ops->sm_count) * 4 * sizeof(int);
   if (e == cudaSuccess) e = cudaMalloc(&ops->d_status, 4 * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(ops->d_status, 0, 4 * sizeof(int));

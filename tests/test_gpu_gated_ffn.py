@@ -303,3 +303,56 @@ def test_refusals():
     assert e.value.status == sg.GEMM_ERR_INVALID_ARG and "overlaps" in str(e.value)
     with pytest.raises(sg.GemmError):
         sg.gated_ffn_backward(dy, x, w_in, w_out, kept, out=(None, w_in, None))
+
+
+# A few tokens take another path (passes over the weights), product by product
+# where their values fit on chip: token counts around its steps, widths around
+# its groups of 8 and 16 rows and 32 elements of K, and both mixed cases.
+FEW = [(1, 32, 8), (2, 33, 7), (3, 1, 300), (4, 255, 1), (7, 1000, 513), (8, 64, 2440), (9, 520, 1217), (15, 96, 1224),
+       (16, 1031, 136), (24, 160, 2433), (31, 72, 264), (32, 2050, 40), (33, 72, 264)]
+
+
+@pytest.mark.parametrize("size", FEW, ids=str)
+@pytest.mark.parametrize("act,dt", [("silu", "bf16"), ("gelu", "f16")])
+def test_few_tokens(size, act, dt):
+    ts = inputs(*size, dt, seed=sum(size))
+    want = reference(*ts, act, dt)
+    for k, v in run_all(*(t.cuda() for t in ts), act).items():
+        assert_within(v, want[k], (size, k))
+
+
+@pytest.mark.parametrize("size", [(1, 200, 40000), (6, 17000, 24), (7, 24, 17000), (32, 64, 3300), (32, 8200, 64),
+                                  (1, 120000, 8)], ids=str)
+def test_few_tokens_with_long_rows(size):
+    x, w_in, w_out, _ = inputs(*size, "bf16", seed=sum(size))
+    want = reference(x, w_in, w_out, torch.zeros_like(x), "relu", "bf16")["y"]
+    assert_within(sg.gated_ffn(x.cuda(), w_in.cuda(), w_out.cuda(), act="relu"), want, size)
+
+
+def test_few_tokens_do_not_meet():
+    x, w_in, w_out, _ = inputs(6, 100, 60, "bf16", seed=3)
+    xs, w_in, w_out = x.cuda(), w_in.cuda(), w_out.cuda()
+    ref = sg.gated_ffn(xs, w_in, w_out)
+    for bad in (float("inf"), float("nan")):
+        spoilt = xs.clone()
+        spoilt[2, 99] = bad
+        got = sg.gated_ffn(spoilt, w_in, w_out)
+        keep = [0, 1, 3, 4, 5]
+        assert torch.equal(got[keep], ref[keep]) and not torch.isfinite(got[2]).all()
+    buf = torch.full((6, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    buf[:, :100] = xs
+    assert torch.equal(sg.gated_ffn(buf[:, :100], w_in, w_out), ref)
+
+
+def test_few_tokens_follow_an_update_of_the_weights():
+    """The weights are read as the kernels before the call on the stream left them."""
+    x, w_in, w_out, _ = (t.cuda() for t in inputs(2, 2048, 4096, "bf16", seed=4))
+    w2, o2 = torch.zeros_like(w_in), torch.zeros_like(w_out)
+    want = sg.gated_ffn(x, w_in, w_out)
+    for _ in range(20):
+        w2.zero_()
+        o2.zero_()
+        sg.gated_ffn(x, w2, o2)
+        w2.copy_(w_in)
+        o2.copy_(w_out)
+        assert torch.equal(sg.gated_ffn(x, w2, o2), want)
