@@ -1,5 +1,5 @@
 // block_params.h -- launch parameters of the block products (block_kernel.cuh)
-// shared by the host planner (block_plan.cu) and the device kernels.
+// shared by the host planner (ops_api.cu) and the device kernels.
 #pragma once
 
 #include <cuda.h>

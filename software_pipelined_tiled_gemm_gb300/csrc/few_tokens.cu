@@ -20,7 +20,9 @@
 // A block takes a contiguous share of the rows, so the bytes are shared out
 // evenly; its warps take groups of those, or, where there are fewer groups than
 // warps, shares of a group's K (added in a fixed order).  The tokens lie in
-// shared memory; where they do not fit, a product takes the tiles.
+// shared memory; where they do not fit, a product takes the tiles.  Rows that
+// are not 16-byte aligned are read as they lie, a vector from the two words
+// around it.
 //
 // Forward pass in us, here and on tiles (bytes at 6780 GB/s): 4096 / 16384, 1
 // token 62 and 74 (59); 2048 / 4096, 1 token 12 and 27 (7), 8 tokens 14 and 27,
@@ -33,6 +35,7 @@
 #include <cstdint>
 
 #include "block_math.cuh"
+#include "byte_shift.cuh"
 #include "few_tokens.h"
 #include "ops_internal.h"
 #include "ptx.cuh"
@@ -42,7 +45,9 @@ namespace spgemm {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kSteps = 8;  // pairs of 16-byte words that a lane reads at a time
+// Steps (a vector of eight weights from each of two rows) that a lane has in
+// flight; a vector of an unaligned row takes two words.
+constexpr int steps_ahead(bool shifted) { return shifted ? 4 : 8; }
 
 struct Args {
   const uint16_t* x;   // M x K
@@ -93,10 +98,37 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// kTiles: groups of eight tokens.
-template <bool kBf16, int kTiles, bool kGated>
+// The eight elements from p on (`end`: past the array's last), as the aligned
+// words around them.  The second is read only if it holds an element of the
+// array; each has one, so both lie in its allocation.
+struct Window {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const uint16_t* p, const uint16_t* end, bool in) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), base = at & ~uintptr_t{15};
+    lo = hi = make_uint4(0u, 0u, 0u, 0u);
+    if (in) lo = __ldcg(reinterpret_cast<const uint4*>(base));
+    if (in && at != base && base + 16 < reinterpret_cast<uintptr_t>(end))
+      hi = __ldcg(reinterpret_cast<const uint4*>(base + 16));
+  }
+  // The first `count` of them, 0 after those.
+  __device__ __forceinline__ uint4 get(const uint16_t* p, int count) const {
+    const uint4 v = shift_window(lo, hi, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u));
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (count < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= count) w[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// kTiles: groups of eight tokens.  kShifted: rows of weights or tokens that
+// are not 16-byte aligned, or of no multiple of eight elements.
+template <bool kBf16, int kTiles, bool kGated, bool kShifted>
 __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
   constexpr int kGroup = kGated ? 8 : 16;  // rows of a group
+  constexpr int kSteps = steps_ahead(kShifted);
   extern __shared__ uint4 xs[];  // M rows of token_pitch(k)
   __shared__ float4 partial[kWarps][kTiles][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -112,7 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
   const int rounds = (groups + slots - 1) / slots;
 
   // Words of step s0 + i: row g of the group's first eight, and of its others.
-  uint4 w[2][kSteps];
+  uint4 w[2][kShifted ? 1 : kSteps];
+  Window window[2][kShifted ? kSteps : 1];
+  const uint16_t* w_end = a.w + (static_cast<int64_t>(kGated ? 2 : 1) * a.rows - 1) * a.ldw + a.k;
   auto each_word = [&](int round, int s0, auto&& f) {
     const int row = first_row + (round * slots + slot) * kGroup + g;
 #pragma unroll
@@ -122,26 +156,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const int v = 4 * (s0 + i) + t;
-        f(h, i, reinterpret_cast<const uint4*>(src) + v, exists && s0 + i < end && v < vecs);
+        // Sixteen bytes a step, so that the steps' loads share one address (src +
+        // 8 v made each its own: 1 to 2 us a call).
+        f(h, i, reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint4*>(src) + v),
+          exists && s0 + i < end && v < vecs);
       }
     }
   };
   auto load = [&](int round, int s0) {
-    each_word(round, s0, [&](int h, int i, const uint4* src, bool in) {
-      w[h][i] = in ? __ldcs(src) : make_uint4(0u, 0u, 0u, 0u);
+    each_word(round, s0, [&](int h, int i, const uint16_t* src, bool in) {
+      if constexpr (kShifted)
+        window[h][i].load(src, w_end, in);
+      else
+        w[h][i] = in ? __ldcs(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
     });
   };
-  // Eight elements of a token (0 past the last).
-  auto token = [&](int n, int v) {
-    const uint16_t* src = a.x + n * a.ldx + 8 * v;
-    if (8 * v + 8 <= a.k) return __ldcg(reinterpret_cast<const uint4*>(src));
-    uint32_t e[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (8 * v + j < a.k) e[j >> 1] |= static_cast<uint32_t>(__ldcg(src + j)) << (16 * (j & 1));
-    return make_uint4(e[0], e[1], e[2], e[3]);
-  };
-
   // The first weights come while the previous kernel ends: into registers
   // where that one is known to have waited for whatever writes them, otherwise
   // only into L2.  The next kernel may start once this one has waited.
@@ -150,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
     if (a.weights_ready)
       load(0, s0);
     else
-      each_word(0, s0, [](int, int, const uint4* src, bool in) {
+      each_word(0, s0, [](int, int, const uint16_t* src, bool in) {
         if (in) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
       });
   }
@@ -158,14 +187,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
   ptx::pdl_launch_dependents();
   if (rounds > 0 && !a.weights_ready) load(0, s0);
   const int pitch = token_pitch(a.k);
-  if (a.k % 8 == 0) {
+  if constexpr (kShifted) {
+    const uint16_t* x_end = a.x + (a.m - 1) * a.ldx + a.k;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < a.m * vecs; i += kThreads) {
+      const int n = i / vecs, v = i - n * vecs;
+      const uint16_t* src = a.x + n * a.ldx + 8 * v;
+      Window window;
+      window.load(src, x_end, true);
+      xs[n * pitch + v] = window.get(src, a.k - 8 * v);
+    }
+  } else {
 #pragma unroll 8
     for (int i = threadIdx.x; i < a.m * vecs; i += kThreads) {
       const int n = i / vecs, v = i - n * vecs;
       xs[n * pitch + v] = __ldcg(reinterpret_cast<const uint4*>(a.x + n * a.ldx) + v);
     }
-  } else {
-    for (int i = threadIdx.x; i < a.m * vecs; i += kThreads) xs[i / vecs * pitch + i % vecs] = token(i / vecs, i % vecs);
   }
   __syncthreads();
 
@@ -177,7 +214,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
   while (round < rounds) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const uint4 w0 = w[0][i], w1 = w[1][i];
+      uint4 w0, w1;
+      if constexpr (kShifted) {
+        const int row = first_row + (round * slots + slot) * kGroup + g, k = 8 * (4 * (s0 + i) + t);
+        const uint16_t* src = a.w + static_cast<int64_t>(row) * a.ldw + k;
+        w0 = window[0][i].get(src, a.k - k);
+        w1 = window[1][i].get(src + static_cast<int64_t>(kGated ? a.rows : 8) * a.ldw, a.k - k);
+      } else {
+        w0 = w[0][i];
+        w1 = w[1][i];
+      }
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
         // Past the end of a warp's share the weights are 0: no token is read there.
@@ -246,16 +292,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
 
 using Kernel = void (*)(const Args);
 
-template <bool kBf16, bool kGated>
+template <bool kBf16, bool kGated, bool kShifted>
 Kernel kernel_of(int64_t m) {
-  return m <= 8    ? few_tokens_kernel<kBf16, 1, kGated>
-         : m <= 16 ? few_tokens_kernel<kBf16, 2, kGated>
-                   : few_tokens_kernel<kBf16, 4, kGated>;
+  return m <= 8    ? few_tokens_kernel<kBf16, 1, kGated, kShifted>
+         : m <= 16 ? few_tokens_kernel<kBf16, 2, kGated, kShifted>
+                   : few_tokens_kernel<kBf16, 4, kGated, kShifted>;
 }
 
-Kernel kernel_of(bool bf16, bool gated, int64_t m) {
-  if (bf16) return gated ? kernel_of<true, true>(m) : kernel_of<true, false>(m);
-  return gated ? kernel_of<false, true>(m) : kernel_of<false, false>(m);
+Kernel kernel_of(bool bf16, bool gated, bool shifted, int64_t m) {
+  if (shifted) {
+    if (bf16) return gated ? kernel_of<true, true, true>(m) : kernel_of<true, false, true>(m);
+    return gated ? kernel_of<false, true, true>(m) : kernel_of<false, false, true>(m);
+  }
+  if (bf16) return gated ? kernel_of<true, true, false>(m) : kernel_of<true, false, false>(m);
+  return gated ? kernel_of<false, true, false>(m) : kernel_of<false, false, false>(m);
 }
 
 }  // namespace
@@ -273,10 +323,14 @@ size_t token_limit(int64_t m) {
 // then bound by those: 9 to 16 tokens up to 256 MB of weights (us here and on
 // tiles: 36 and 51 where gate and up are 108 MB, 73 and 74 at 268 MB, 135 to
 // 159 and 132 at 537 MB), 17 to 32 up to 48 MB (23 and 27 at 34 MB, 90 and 74
-// at 268 MB).
+// at 268 MB).  Rows that are not 16-byte aligned cost twice the loads, but on
+// tiles a padded copy of all weights (1 token of 2049 / 4095 24 and 51, 16
+// tokens 36 and 52); more than eight tokens of long rows do not gain (16 of
+// 6045 / 1617 68 and 57).
 bool few_tokens_fits(const gemm_ops* ops, int64_t m, int64_t k, int64_t rows) {
   const int64_t limit = int64_t{1} << 20;
   const int64_t most = m <= 8 ? kOpsMaxDim * limit : m <= 16 ? 256 * limit : 48 * limit;
+  if (k % 8 != 0 && m > 8 && token_bytes(m, k) > 128 * 1024) return false;
   return 2 * rows * k <= most && m >= 1 && m <= kFewTokens && k <= kOpsMaxDim - 64 && ops->smem_optin >= 227 * 1024 &&
          token_bytes(m, k) <= token_limit(m);
 }
@@ -284,9 +338,9 @@ bool few_tokens_fits(const gemm_ops* ops, int64_t m, int64_t k, int64_t rows) {
 cudaError_t few_tokens_init(const gemm_ops* ops) {
   cudaError_t e = cudaSuccess;
   if (ops->smem_optin < 227 * 1024) return e;  // not used
-  for (int n = 0; n < 12 && e == cudaSuccess; ++n) {
-    const int m = n < 4 ? 8 : n < 8 ? 16 : 32;
-    e = cudaFuncSetAttribute(kernel_of((n & 1) != 0, (n & 2) != 0, m), cudaFuncAttributeMaxDynamicSharedMemorySize,
+  for (int n = 0; n < 24 && e == cudaSuccess; ++n) {
+    const int m = n < 8 ? 8 : n < 16 ? 16 : 32;
+    e = cudaFuncSetAttribute(kernel_of((n & 1) != 0, (n & 2) != 0, (n & 4) != 0, m), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(token_limit(m)));
   }
   return e;
@@ -313,6 +367,7 @@ cudaError_t few_tokens_launch(const gemm_ops* ops, const FewTokens& f, cudaStrea
   a.share = 1;
   while (a.share < kWarps && groups * a.share * 2 <= kWarps && ceil_div(f.x.cols, 32) >= a.share * 2)
     a.share *= 2;
+  const bool shifted = f.x.cols % 8 != 0 || !copyable(f.x) || !copyable(f.w);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(ops->sm_count, 1, 1);
@@ -323,7 +378,7 @@ cudaError_t few_tokens_launch(const gemm_ops* ops, const FewTokens& f, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel_of(f.bf16, f.gated, f.x.rows), a);
+  return cudaLaunchKernelEx(&cfg, kernel_of(f.bf16, f.gated, shifted, f.x.rows), a);
 }
 
 }  // namespace spgemm

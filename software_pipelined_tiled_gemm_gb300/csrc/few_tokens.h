@@ -13,8 +13,8 @@ namespace spgemm {
 constexpr int kFewTokens = 32;
 
 struct FewTokens {
-  Matrix x;            // rows: the tokens; cols: K; rows 16-byte aligned
-  Matrix w;            // weights, rows of K, 16-byte aligned, zero from K to a multiple of 8
+  Matrix x;            // rows: the tokens; cols: K
+  Matrix w;            // weights, rows of K
   int64_t rows;        // outputs of a token (gated: rows of either half of w)
   bool gated, bf16;
   bool weights_ready;  // the launch before this one is another of these, and does not write w

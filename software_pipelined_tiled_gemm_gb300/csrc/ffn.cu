@@ -24,6 +24,7 @@ struct Ffn {
   uint16_t* dgu;       // backward: M x 2 I, pitch round8(2 I)
   float* partials;
   Matrix x, w_in, w_out, dy;
+  bool few_first, few_second;  // forward products that go over the weights as they lie (few_tokens.cu)
   PackJobs pack;
 };
 
@@ -128,9 +129,13 @@ size_t layout(const gemm_ops* ops, const gemm_ffn_args_t* a, bool backward, void
     m->ptr = dst;
     m->ld = ldp;
   };
-  padded(&f->w_out);
-  if (!backward || a->dx) padded(&f->w_in);
-  if (!backward || a->dw_in) padded(&f->x);
+  // (The fault hook withholds a copy, of which that path has none.)
+  const bool few = !backward && ops->debug_fault == 0;
+  f->few_first = few && few_tokens_fits(ops, f->M, f->D, 2 * f->I);
+  f->few_second = few && few_tokens_fits(ops, f->M, f->I, f->D);
+  if (!f->few_second) padded(&f->w_out);
+  if (!f->few_first && (!backward || a->dx)) padded(&f->w_in);
+  if (!f->few_first && (!backward || a->dw_in)) padded(&f->x);
   if (backward) padded(&f->dy);
   return c.used;
 }
@@ -181,13 +186,7 @@ gemm_status_t gemm_ffn_run(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* w
   const cudaError_t e = launch_pack(f.pack, ops->sm_count, stream);
   if (e != cudaSuccess) return ops_cuda_fail(e, "padding copy launch");
 
-  // A product of few tokens is a pass over its weights (few_tokens.cu).  The
-  // fault hook withholds a copy, of which that path has none.
-  auto few = [&](int64_t k, int64_t rows) {
-    return few_tokens_fits(ops, f.M, k, rows) && ops->debug_fault == 0;
-  };
-  const bool few_first = few(f.D, 2 * f.I);
-  if (few_first) {
+  if (f.few_first) {
     FewTokens t{};
     t.x = f.x;
     t.w = f.w_in;
@@ -218,13 +217,13 @@ gemm_status_t gemm_ffn_run(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* w
   }
 
   const Matrix h{f.h, f.M, f.I, f.Ip, 0};
-  if (few(f.I, f.D)) {
+  if (f.few_second) {
     FewTokens t{};
     t.x = h;
     t.w = f.w_out;
     t.rows = f.D;
     t.bf16 = f.bf16;
-    t.weights_ready = few_first;
+    t.weights_ready = f.few_first;
     t.out = static_cast<uint16_t*>(args->y);
     t.ldo = f.D;
     const cudaError_t err = few_tokens_launch(ops, t, stream);

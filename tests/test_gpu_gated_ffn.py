@@ -356,3 +356,21 @@ def test_few_tokens_follow_an_update_of_the_weights():
         w2.copy_(w_in)
         o2.copy_(w_out)
         assert torch.equal(sg.gated_ffn(x, w2, o2), want)
+
+
+@pytest.mark.parametrize("offsets", [(1, 3, 5), (0, 1, 0), (8, 8, 7)], ids=str)
+@pytest.mark.parametrize("size", [(1, 64, 48), (6, 129, 77), (20, 40, 23)], ids=str)
+def test_few_tokens_read_operands_where_they_lie(size, offsets):
+    m, d, i = size
+    x, w_in, w_out, _ = (t.cuda() for t in inputs(m, d, i, "bf16", seed=5))
+    ref = sg.gated_ffn(x, w_in, w_out)
+
+    def moved(t, k):
+        buf = torch.full((t.numel() + 32,), float("nan"), dtype=t.dtype, device="cuda")
+        out = buf[k:k + t.numel()].view(t.shape)
+        return out.copy_(t)
+    ts = [moved(t, k) for t, k in zip((x, w_in, w_out), offsets)]
+    assert torch.equal(sg.gated_ffn(*ts), ref)
+    rows = torch.full((m, d + 5), float("nan"), dtype=x.dtype, device="cuda")
+    rows[:, 2:2 + d] = x
+    assert torch.equal(sg.gated_ffn(rows[:, 2:2 + d], w_in, w_out), ref)
