@@ -805,6 +805,10 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
         ptx::fence_proxy_async_smem();
       }
       ptx::cluster_wait();  // every ring of the cluster is free
+      // The stores below are shared out by chunk, so a warp also reads what
+      // the other quarters' warps staged: their arrivals at the cluster's
+      // barrier came before that.
+      ptx::named_barrier_sync(1, 128 * kG);
       const int to = q / row_blocks;  // the CTA that stores this quarter's rows
       if (quarter_all(ok != 0) && lead && to != part && t.mb * kTileM + q * 32 < p.M)
         ptx::bulk_copy_to_peer(
