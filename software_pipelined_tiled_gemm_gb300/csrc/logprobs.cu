@@ -748,9 +748,8 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == kRowThreads ? kRowB
     const float e_m = exp2_approx(t_m);
     const float log_s = log2f(t.s / e_m);
     auto log_p = [&](float x) {
-      if (x == -INFINITY) return x;
-      const float e2 = slow ? (x - t.m) * kLog2e : fmaf(x, kLog2e, -t.n) - t_m;
-      return (e2 - log_s) * kLn2;
+      // The difference in the logits' own base: x L overflows near the type's lowest value.
+      return x == -INFINITY ? x : x - t.m - log_s * kLn2;
     };
     float lse = t.m - log_p(t.m), h = t.s == e_m ? 0.0f : (log_s + (t_m - t.w / t.s)) * kLn2;
     bool none = false;

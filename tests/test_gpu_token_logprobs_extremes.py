@@ -1,0 +1,74 @@
+"""Log probabilities and their gradient where logits are large, masked with
+finite values or not numbers, on the GPU against the definition in 64 bits.
+
+Tolerances are those of test_gpu_token_logprobs.py, which hold for logits of
+any size: log p is the difference of a logit and the row's largest (one
+rounding of its value) less ln s, and lse the sum of that largest and ln s
+(one rounding).
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import software_pipelined_tiled_gemm_gb300 as sg
+from tests.test_gpu_token_logprobs import DT, INF, close
+
+pytestmark = pytest.mark.gpu
+
+# One row shared by a cluster, a few rows, and more rows than blocks.
+SHAPES = [(1, 70001), (3, 2600), (900, 2600)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    sg.check_operators()
+
+
+def reference(logits, tokens, k):
+    """The definition in 64 bits, every difference from the row's largest logit
+    taken first: beyond 2^53 even 64 bits lose ln s beside it."""
+    x = logits.double().cpu()
+    m = x.amax(1, keepdim=True)
+    log_s = torch.logsumexp(x - m, 1, keepdim=True)
+    lp = (x - m) - log_s
+    p = lp.exp()
+    out = {"lse": (m + log_s)[:, 0], "entropy": -torch.where(p > 0, p * lp, torch.zeros_like(p)).sum(1), "p": p,
+           "lp": lp, "logprobs": lp.gather(1, tokens.cpu()[:, None])[:, 0]}
+    if k:
+        out["top_ids"] = x.sort(dim=1, descending=True, stable=True).indices[:, :k]
+        out["top_logprobs"] = lp.gather(1, out["top_ids"])
+    return out
+
+
+def check(logits, tokens, k):
+    r = sg.token_logprobs(logits, tokens, top_k=k)
+    want = reference(logits, tokens, k)
+    for name in ("lse", "entropy", "logprobs") + (("top_logprobs",) if k else ()):
+        close(getattr(r, name), want[name], name)
+    if k:
+        assert torch.equal(r.top_ids.cpu(), want["top_ids"])
+    return r, want
+
+
+def normal(t, v, seed):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(t, v, generator=gen) * 3, torch.randint(0, v, (t,), generator=gen).cuda()
+
+
+@pytest.mark.parametrize("t,v", SHAPES, ids=str)
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_log_probabilities_of_columns_masked_with_the_lowest_value(dt, t, v):
+    x, tokens = normal(t, v, seed=4)
+    low = torch.finfo(DT[dt]).min
+    y = x.to(DT[dt])
+    y[:, 4:] = low                # fewer possible columns than alternatives
+    tokens[:] = v - 2
+    r, want = check(y.cuda(), tokens, 8)
+    assert (r.logprobs == torch.finfo(DT[dt]).min).all() if dt != "f16" else torch.isfinite(r.logprobs).all()
+    assert torch.isfinite(r.top_logprobs).all() and r.top_ids[:, 4:].tolist() == [[4, 5, 6, 7]] * t
