@@ -3,7 +3,7 @@
 //
 // One pass over the logits, bound by memory.  In base 2, with L = fp32(log2 e)
 // and an integer reference N near the largest x L,
-//   t_j = x_j L - N (one fused multiply-add, so nothing is lost for large x),
+//   t_j = x_j L - N (one fused multiply-add: one rounding, of the difference),
 //   s = sum 2^t,  w = sum 2^t t,
 //   log2 p_j = t_j - log2 s,  H = ln 2 (log2 s - w / s).
 // Each thread keeps N, s and w of its own elements in fp32; when a larger
@@ -14,10 +14,11 @@
 // A block's producer thread streams its rows through a shared-memory ring by
 // bulk copies, running ahead into the next row while the block still reduces
 // the last one.  Pairs of values go through the packed fp32 instructions;
-// masked logits (-inf, or the type's lowest value) are raised to a finite
-// floor first, so that 2^t t is 0 and not 0 x inf.  A row whose maximum is
-// within reach of that floor (all masked by a lowest value) or near the
-// type's top is summed again by the slow form (x - m).
+// masked logits (-inf, or a large negative value) are raised to a finite
+// floor first (fp32 and bf16 -2^22, fp16 its lowest value), so that 2^t t is 0
+// and not 0 x inf.  A row whose maximum is within reach of that floor (all
+// masked by a finite value) or above 4e6 is summed again by the slow form
+// (x - m): there N would be too coarse beside it.
 //
 // Alternatives.  While streaming, each thread also keeps its largest element,
 // the first 16-byte vector that holds it and the largest of its other
@@ -183,14 +184,16 @@ __device__ __forceinline__ F2 add_f2(F2 a, F2 b) {
 
 // Per type: the largest of a vector's elements (NaN if one is), the vector
 // with its elements raised to the floor, and the range of row maxima for
-// which the fast sums hold: 2^((floor - m) L) is 0, and m L is far from
-// overflow.  kStart: the first reference, below any such maximum's and so far
-// above the floor's that masked elements add 0 from the start.
+// which the fast sums hold: 2^((floor - m) L) is 0, and |m| L is below 2^23, so
+// that the reference is at most 1 from m L (from 2^31 on the fp32 product is
+// more than 127 off, and 2^t inf or 0).  kStart: the first reference, below any
+// such maximum's and so far above the floor's that masked elements add 0 from
+// the start.  Every floor is exact in its type.
 template <typename T>
 struct Fast;
 template <>
 struct Fast<float> {
-  static constexpr float kFloor = -1e30f, kStart = -1.4e30f, kLow = -1e29f, kHigh = 1e38f;
+  static constexpr float kFloor = -4194304.0f, kStart = -6050000.0f, kLow = -4193000.0f, kHigh = 4e6f;
   static __device__ __forceinline__ float max(const uint4& w) {
     return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
                    max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
@@ -202,7 +205,7 @@ struct Fast<float> {
 };
 template <>
 struct Fast<__nv_bfloat16> {
-  static constexpr float kFloor = -1e30f, kStart = -1.4e30f, kLow = -1e29f, kHigh = 1e38f;
+  static constexpr float kFloor = -4194304.0f, kStart = -6050000.0f, kLow = -4193000.0f, kHigh = 4e6f;
   static __device__ __forceinline__ __nv_bfloat162 at(const uint32_t& w) {
     return *reinterpret_cast<const __nv_bfloat162*>(&w);
   }
@@ -223,7 +226,7 @@ struct Fast<__nv_bfloat16> {
 };
 template <>
 struct Fast<__half> {
-  static constexpr float kFloor = -65504.0f, kStart = -94000.0f, kLow = -65000.0f, kHigh = 1e38f;
+  static constexpr float kFloor = -65504.0f, kStart = -94000.0f, kLow = -65000.0f, kHigh = 65505.0f;
   static __device__ __forceinline__ __half2 at(const uint32_t& w) {
     return *reinterpret_cast<const __half2*>(&w);
   }

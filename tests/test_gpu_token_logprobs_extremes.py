@@ -72,3 +72,52 @@ def test_log_probabilities_of_columns_masked_with_the_lowest_value(dt, t, v):
     r, want = check(y.cuda(), tokens, 8)
     assert (r.logprobs == torch.finfo(DT[dt]).min).all() if dt != "f16" else torch.isfinite(r.logprobs).all()
     assert torch.isfinite(r.top_logprobs).all() and r.top_ids[:, 4:].tolist() == [[4, 5, 6, 7]] * t
+
+
+@pytest.mark.parametrize("t,v", SHAPES, ids=str)
+@pytest.mark.parametrize("mask", [-1e4, -4e6, -5e6, -1e10, -3e9, -1e12, -1e20, -1e30, -3e38])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_columns_masked_with_a_large_negative_value(dt, mask, t, v):
+    x, tokens = normal(t, v, seed=1)
+    tokens.clamp_(max=v // 2 - 1)
+    for columns in (slice(0, v // 3), slice(v // 2, v), slice(0, v, 2), slice(0, 0)):
+        y = x.clone()
+        y[:, columns] = mask
+        y = y.to(DT[dt]).cuda()
+        for k in (0, 6):
+            check(y, tokens, k)
+
+
+@pytest.mark.parametrize("t,v", SHAPES, ids=str)
+@pytest.mark.parametrize("mask", [-1e4, -4e6, -5e6, -1e10, -3e9, -1e12, -1e20, -1e30, -3e38])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_a_row_of_one_large_negative_value_is_uniform(dt, mask, t, v):
+    y = torch.full((t, v), mask).to(DT[dt]).cuda()
+    tokens = torch.full((t,), 5, device="cuda")
+    for k in (0, 6):
+        r, _ = check(y, tokens, k)
+        assert (r.logprobs + math.log(v)).abs().max() < 1e-5
+        assert (r.entropy - math.log(v)).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("t,v", SHAPES, ids=str)
+@pytest.mark.parametrize("offset", [1e4, 1e6, 3.9e6, 4.1e6, 1.7e7, 1e10, 1e20, 1e38, -1e4, -1e6, -4.1944e6, -1e10, -1e20])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rows_far_from_zero(dt, offset, t, v):
+    x, tokens = normal(t, v, seed=2)
+    y = (x + offset).to(DT[dt]).cuda()
+    y[:, v // 3] = offset - 4     # between rows' values wherever the type resolves it
+    for k in (0, 6):
+        check(y, tokens, k)
+
+
+@pytest.mark.parametrize("t,v", SHAPES, ids=str)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rows_across_the_whole_range(dt, t, v):
+    # Each thread meets elements of every size, the largest of them last or first.
+    x, tokens = normal(t, v, seed=3)
+    size = 10.0 ** (torch.arange(v) * 7919 % 38).float()
+    for sign in (-1.0, 1.0):
+        y = (x.abs() * sign * size).to(DT[dt]).cuda()
+        for k in (0, 6):
+            check(y, tokens, k)
