@@ -93,9 +93,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // Unsigned words in the order of the floats: -inf < ... < -0 = +0 < ... <
-// +inf < NaN (any).
+// +inf < NaN (any).  Between 0 and ~0, so that a key is neither 0 (none) nor
+// all ones (the search's start, which every key is below).
 __device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 0xffffffffu;
+  if (x != x) return 0xfffffffeu;
   const uint32_t b = __float_as_uint(x + 0.0f);
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }

@@ -121,3 +121,23 @@ def test_rows_across_the_whole_range(dt, t, v):
         y = (x.abs() * sign * size).to(DT[dt]).cuda()
         for k in (0, 6):
             check(y, tokens, k)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("t,v,k", [(1, 1, 1), (1, 20, 20), (600, 20, 20), (1, 131072, 64), (2, 2600, 5), (700, 2600, 33)])
+def test_nan_ranks_first_from_the_first_column_on(dt, t, v, k):
+    nan = float("nan")
+    x, _ = normal(t, v, seed=8)
+    for columns in ([0], [0, v - 1], list(range(v))):
+        y = x.clone()
+        y[:, columns] = nan
+        y = y.to(DT[dt])
+        if v > 2:
+            y[:, 1] = nan if len(columns) == v else -INF
+        r = sg.token_logprobs(y.cuda(), None, top_k=k)
+        want = (y.float() + 0.0).sort(dim=1, descending=True, stable=True).indices[:, :k]
+        assert torch.equal(r.top_ids.cpu(), want)
+        assert torch.isnan(r.lse).all() and torch.isnan(r.entropy).all()
+        picked = y.float().gather(1, want)
+        assert (torch.isnan(r.top_logprobs.cpu()) == (picked != -INF)).all()
+        assert (r.top_logprobs.cpu()[picked == -INF] == -INF).all()
