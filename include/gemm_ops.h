@@ -152,12 +152,15 @@ typedef struct {
   const float* d_entropy;
   void* d_logits;            /* rows x vocab, row pitch ldd; may be logits itself (ldd == ld) */
   int64_t ldd;
+  float* lse_low;            /* rows; what lse's rounding to fp32 lost.  Written by the forward pass,
+                                read by the backward pass; may be NULL in either (zero), at the cost
+                                of |lse| 2^-24 in log p there */
 } gemm_logprobs_args_t;
 
 gemm_status_t gemm_token_logprobs(gemm_ops_t* ops, const gemm_logprobs_args_t* args, void* stream);
 
 /* d_logits_j = g_l ([j = token] - p_j) - g_H p_j (log p_j + H), from the
- * forward pass's lse (and entropy). */
+ * forward pass's lse, lse_low (and entropy). */
 gemm_status_t gemm_token_logprobs_backward(gemm_ops_t* ops, const gemm_logprobs_args_t* args,
                                            void* stream);
 

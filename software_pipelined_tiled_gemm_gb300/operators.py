@@ -51,7 +51,7 @@ class LogprobsArgs(ctypes.Structure):
     _fields_ = [("rows", _i64), ("vocab", _i64), ("dtype", _ci), ("logits", _vp), ("ld", _i64),
                 ("tokens", _vp), ("top_k", _ci), ("logprobs", _vp), ("entropy", _vp),
                 ("lse", _vp), ("top_logprobs", _vp), ("top_ids", _vp), ("d_logprobs", _vp),
-                ("d_entropy", _vp), ("d_logits", _vp), ("ldd", _i64)]
+                ("d_entropy", _vp), ("d_logits", _vp), ("ldd", _i64), ("lse_low", _vp)]
 
 
 MAX_TOP_K = 64   # GEMM_LOGPROBS_MAX_TOP_K
@@ -322,9 +322,11 @@ def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
 # ----------------------------------------------- log probabilities of tokens --
 
 # Per row of logits (None where not asked for): log probability of the row's
-# token, entropy, log of the sum of exponentials, and the best alternatives.
+# token, entropy, log of the sum of exponentials, the best alternatives, and
+# what lse's rounding to fp32 lost (for the backward pass; None: zero).
 TokenLogprobs = collections.namedtuple("TokenLogprobs",
-                                       "logprobs entropy lse top_logprobs top_ids")
+                                       "logprobs entropy lse top_logprobs top_ids lse_low",
+                                       defaults=(None,))
 
 
 def _logprobs_args(logits, tokens):
@@ -358,8 +360,8 @@ def token_logprobs(logits, tokens=None, top_k=0):
     count (log probability 0).  top_k: how many of the best columns to
     return, at most 64, equal ones by the lowest column.
 
-    Returns :class:`TokenLogprobs`: logprobs, entropy and lse of shape (...),
-    top_logprobs and top_ids (int64) of shape (..., top_k).  -inf masks a
+    Returns :class:`TokenLogprobs`: logprobs, entropy, lse and lse_low of
+    shape (...), top_logprobs and top_ids (int64) of shape (..., top_k).  -inf masks a
     column; a row of only masked columns has entropy 0, one with NaN or +inf
     has NaN.
     """
@@ -369,24 +371,24 @@ def token_logprobs(logits, tokens=None, top_k=0):
         raise ValueError("top_k must be in [0, min(%d, columns)]" % MAX_TOP_K)
     a.top_k = top_k
     shape, dev = logits.shape[:-1], logits.device
-    out = torch.empty((2 if tokens is None else 3, *shape), dtype=torch.float32, device=dev)
+    out = torch.empty((3 if tokens is None else 4, *shape), dtype=torch.float32, device=dev)
     logprobs = None
     if tokens is None:
-        lse, entropy = out.unbind(0)
+        lse, entropy, lse_low = out.unbind(0)
     else:
-        lse, entropy, logprobs = out.unbind(0)
+        lse, entropy, lse_low, logprobs = out.unbind(0)
     top_lp = top_ids = None
     if top_k:
         top_lp = torch.empty((*shape, top_k), dtype=torch.float32, device=dev)
         top_ids = torch.empty((*shape, top_k), dtype=torch.int64, device=dev)
         a.top_logprobs, a.top_ids = top_lp.data_ptr(), top_ids.data_ptr()
-    a.lse, a.entropy = lse.data_ptr(), entropy.data_ptr()
+    a.lse, a.entropy, a.lse_low = lse.data_ptr(), entropy.data_ptr(), lse_low.data_ptr()
     a.logprobs = _ptr(logprobs)
     if a.rows:
         stream = _stream(dev)
         _check(_lib().gemm_token_logprobs(_handle(dev, stream), ctypes.byref(a), stream),
                "gemm_token_logprobs")
-    return TokenLogprobs(logprobs, entropy, lse, top_lp, top_ids)
+    return TokenLogprobs(logprobs, entropy, lse, top_lp, top_ids, lse_low)
 
 
 def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=None, out=None):
@@ -401,9 +403,9 @@ def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=N
     a = _logprobs_args(logits, tokens)
     if d_logprobs is not None and tokens is None:
         raise ValueError("d_logprobs needs tokens")
-    for name, t in (("lse", result.lse), ("entropy", result.entropy), ("d_logprobs", d_logprobs),
-                    ("d_entropy", d_entropy)):
-        if t is None and name.startswith("d_"):
+    for name, t in (("lse", result.lse), ("entropy", result.entropy), ("lse_low", result.lse_low),
+                    ("d_logprobs", d_logprobs), ("d_entropy", d_entropy)):
+        if t is None and (name.startswith("d_") or name == "lse_low"):
             continue
         _on_cuda(logits.device, t, name)
         if t.dtype != torch.float32 or t.shape != logits.shape[:-1] or not t.is_contiguous():
@@ -414,8 +416,8 @@ def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=N
     if out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' shape and dtype")
     a.ldd = _rows(out, a.vocab, "out")[1]
-    a.lse, a.entropy, a.d_logprobs, a.d_entropy, a.d_logits = map(
-        _ptr, (result.lse, result.entropy, d_logprobs, d_entropy, out))
+    a.lse, a.entropy, a.lse_low, a.d_logprobs, a.d_entropy, a.d_logits = map(
+        _ptr, (result.lse, result.entropy, result.lse_low, d_logprobs, d_entropy, out))
     if a.rows:
         dev = logits.device
         stream = _stream(dev)

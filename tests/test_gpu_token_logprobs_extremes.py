@@ -141,3 +141,59 @@ def test_nan_ranks_first_from_the_first_column_on(dt, t, v, k):
         picked = y.float().gather(1, want)
         assert (torch.isnan(r.top_logprobs.cpu()) == (picked != -INF)).all()
         assert (r.top_logprobs.cpu()[picked == -INF] == -INF).all()
+
+
+def gradient_within_bounds(x, tokens, dt):
+    """The gradient against its formula, and its sum over each row."""
+    t, v = x.shape
+    r, want = check(x, tokens, 0)
+    gen = torch.Generator().manual_seed(5)
+    gl, gh = torch.randn(t, generator=gen), torch.randn(t, generator=gen)
+    p, lp = want["p"], want["lp"]
+    plp = torch.where(p > 0, p * lp, torch.zeros_like(p))
+    for a, b in ((gl, gh), (gl, None), (None, gh)):
+        d = sg.token_logprobs_backward(x, tokens, r, None if a is None else a.cuda(),
+                                       None if b is None else b.cuda()).double().cpu()
+        l64 = (torch.zeros(t) if a is None else a).double()
+        h64 = (torch.zeros(t) if b is None else b).double()
+        exact = -l64[:, None] * p - h64[:, None] * (plp + p * want["entropy"][:, None])
+        exact[torch.arange(t), tokens.cpu()] += l64
+        # As in test_gpu_token_logprobs.py, plus the roundings of g and g_H (x - p) themselves.
+        tol = 2.0 ** -18 * (l64.abs()[:, None] * (p + (p > 0.5))
+                            + h64.abs()[:, None] * (plp.abs() + p * (want["entropy"] + 13)[:, None])) + 1e-30
+        u = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dt]
+        tol = tol + u * (exact.abs() + tol) + (2.0 ** -24 if dt == "f16" else 1e-38)
+        assert ((d - exact).abs() <= tol).all(), float(((d - exact).abs() / tol).max())
+        assert (d.sum(1).abs() <= tol.sum(1) + exact.sum(1).abs()).all()
+
+
+@pytest.mark.parametrize("t,v", SHAPES, ids=str)
+@pytest.mark.parametrize("value", ["lowest", "highest", -1e30, -1e10, -5e6, 1e4, 1e6, 1e10, 1e30])
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_gradient_of_rows_of_one_value(dt, value, t, v):
+    info = torch.finfo(DT[dt])
+    value = {"lowest": info.min, "highest": info.max}.get(value, value)
+    if abs(value) > info.max:
+        pytest.skip("beyond the type")
+    x = torch.full((t, v), value).to(DT[dt]).cuda()
+    gradient_within_bounds(x, torch.full((t,), v // 2, device="cuda"), dt)
+
+
+@pytest.mark.parametrize("t,v", SHAPES, ids=str)
+@pytest.mark.parametrize("offset", [1e4, -1e4, 1e6, -1e6, 1e7])
+def test_gradient_of_rows_far_from_zero(offset, t, v):
+    x, tokens = normal(t, v, seed=6)
+    gradient_within_bounds((x + offset).cuda(), tokens, "f32")
+
+
+def test_a_result_without_the_low_part_is_taken():
+    # Five fields, lse alone: as precise as fp32 holds it.
+    x, tokens = normal(7, 1000, seed=7)
+    r, want = check(x.cuda(), tokens, 0)
+    g = torch.rand(7, generator=torch.Generator().manual_seed(8))
+    old = sg.TokenLogprobs(*r[:5])
+    a = sg.token_logprobs_backward(x.cuda(), tokens, r, g.cuda(), g.cuda()).double().cpu()
+    b = sg.token_logprobs_backward(x.cuda(), tokens, old, g.cuda(), g.cuda()).double().cpu()
+    # lse (below 16) rounds within 2^-21, log p L (below 30) within 2^-20 of p's value either way
+    p, lp, h, g = want["p"], want["lp"].abs(), want["entropy"][:, None], g.double()[:, None]
+    assert ((a - b).abs() <= 2.0 ** -17 * g * p * (2 + lp + h) + 2.0 ** -23 * a.abs() + 1e-30).all()
