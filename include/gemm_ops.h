@@ -4,10 +4,10 @@
  * of a gradient, and the log probabilities of tokens with their gradient.
  *
  * Sizes vary from call to call (a prompt's length, a batch), so these
- * operators take no plan for a problem: one gemm_ops_t per device and stream
- * holds what persists between calls (a status word and the synchronisation
- * flags of split tiles, a few KiB), and a call's large buffers come from the
- * caller: *_workspace says how many bytes a call needs.
+ * operators take no plan for a problem: one gemm_ops_t per device holds what
+ * persists between calls (limits of the device and a status word), and a
+ * call's buffers come from the caller: *_workspace says how many bytes a call
+ * needs.
  *
  * Pointers are device pointers on the handle's device; matrices are
  * row-major.  A workspace starts 256-byte aligned, holds nothing between calls, and
@@ -17,8 +17,11 @@
  * Errors are gemm.h's: argument errors are found on the host before anything
  * is launched, nothing throws, and a device-side wait that runs out of time
  * is recorded in the handle's status word (gemm_ops_check).  Calls are
- * asynchronous, may be captured into a CUDA graph, and one handle may be
- * used by one host thread at a time and on one stream at a time.
+ * asynchronous and may be captured into a CUDA graph.  One handle serves any
+ * number of streams and host threads, but for gemm_ops_configure and
+ * gemm_ops_destroy, which need it to themselves.  Calls, and graphs that
+ * captured calls, may run beside one another as long as their workspaces,
+ * `kept` buffers and outputs are different ones.
  */
 #ifndef SPGEMM_GEMM_OPS_H_
 #define SPGEMM_GEMM_OPS_H_

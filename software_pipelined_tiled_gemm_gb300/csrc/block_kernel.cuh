@@ -556,6 +556,8 @@ __global__ void __launch_bounds__(kernel_threads(kG), 1)
   } else {
     // --------------------------------------------------------- epilogue --
     ptx::pdl_wait_prior_grid();
+    if (blockIdx.x == 0)
+      for (int i = static_cast<int>(threadIdx.x) - 64; i < p.zero_flags; i += 128 * kG) p.sk_flags[i] = 0;
     const int q = warp & 3;         // TMEM lane quarter
     const int ew = (warp - 2) & 3;  // index of the quarter's staging, partials and flags
     const int g = (warp - 2) >> 2;  // which of the quarter's warps

@@ -44,6 +44,7 @@ struct BlockParams : Params {
   int walkers;         // CTAs, or CTA pairs
   int epi;             // epilogue warps per TMEM lane quarter, 1 or 2
   int splits;          // > 1: each tile's K is split over a cluster of this many single CTAs
+  int zero_flags;      // > 0: this launch needs no flags and zeroes so many for the next ones
   int symmetric;       // 1: only tiles on and above the diagonal run; each off-diagonal one is
                        // also written transposed (square output)
   int out_bf16;        // type of the 16-bit output(s)

@@ -22,7 +22,7 @@ struct Ffn {
   float* pre;
   uint16_t* h;         // M x I, pitch Ip
   uint16_t* dgu;       // backward: M x 2 I, pitch round8(2 I)
-  float* partials;
+  BlockScratch scratch;
   Matrix x, w_in, w_out, dy;
   bool few_first, few_second;  // forward products that go over the weights as they lie (few_tokens.cu)
   PackJobs pack;
@@ -110,7 +110,7 @@ size_t layout(const gemm_ops* ops, const gemm_ffn_args_t* a, bool backward, void
   f->w_in = {a->w_in, 2 * f->I, f->D, f->D, 0};
   f->w_out = {a->w_out, f->D, f->I, f->I, 0};
   Carver c(workspace);
-  f->partials = static_cast<float*>(c.take(block_workspace(ops)));
+  f->scratch = take_scratch(ops, c);
   f->pre = static_cast<float*>(a->kept);
   if (a->kept)
     f->h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a->kept) + pre_bytes(f->M, f->I));
@@ -212,7 +212,7 @@ gemm_status_t gemm_ffn_run(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* w
     g.out0 = {f.h, f.M, f.Ip, f.Ip, 0};
     g.pre = f.pre;
     g.stream_b = true;
-    st = run_block(ops, g, f.partials, stream);
+    st = run_block(ops, g, f.scratch, stream);
     if (st != GEMM_OK) return st;
   }
 
@@ -239,7 +239,7 @@ gemm_status_t gemm_ffn_run(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* w
   y.bf16 = y.out_bf16 = f.bf16;
   y.out0 = {args->y, f.M, f.D, f.D, 0};
   y.stream_b = true;
-  return run_block(ops, y, f.partials, stream);
+  return run_block(ops, y, f.scratch, stream);
 }
 
 gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* workspace,
@@ -274,7 +274,7 @@ gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, vo
     g.out0 = {f.dgu, M, I, Gp, 0};      // side by side in one row
     g.out1 = {f.dgu + I, M, I, Gp, 0};
     g.pre = f.pre;
-    st = run_block(ops, g, f.partials, stream);
+    st = run_block(ops, g, f.scratch, stream);
     if (st != GEMM_OK) return st;
   }
   BlockProblem p;
@@ -287,7 +287,7 @@ gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, vo
     p.a = {f.dgu, M, 2 * I, Gp, 0};
     p.b = f.w_in;
     p.out0 = {args->dx, M, D, D, 0};
-    st = run_block(ops, p, f.partials, stream);
+    st = run_block(ops, p, f.scratch, stream);
     if (st != GEMM_OK) return st;
   }
   p.kind = BlockProblem::kTN;
@@ -298,7 +298,7 @@ gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, vo
     p.a = {f.dgu, M, 2 * I, Gp, 0};
     p.b = f.x;
     p.out0 = {args->dw_in, 2 * I, D, D, 0};
-    st = run_block(ops, p, f.partials, stream);
+    st = run_block(ops, p, f.scratch, stream);
     if (st != GEMM_OK) return st;
   }
   if (args->dw_out) {
@@ -307,7 +307,7 @@ gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, vo
     p.a = f.dy;
     p.b = {f.h, M, I, f.Ip, 0};
     p.out0 = {args->dw_out, D, I, I, 0};
-    st = run_block(ops, p, f.partials, stream);
+    st = run_block(ops, p, f.scratch, stream);
   }
   return st;
 }

@@ -103,6 +103,29 @@ BlockOut describe_out(const Matrix& m, int64_t N, int64_t batch) {
   return o;
 }
 
+constexpr int kZeroThreads = 256;
+
+// Flags of a call whose first product already needs them.  The product starts
+// beside this kernel and waits for it.
+__global__ void __launch_bounds__(kZeroThreads) zero_flags_kernel(int* flags, int count) {
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  for (int i = threadIdx.x; i < count; i += kZeroThreads) flags[i] = 0;
+}
+
+cudaError_t launch_zero_flags(const BlockScratch& s, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(1, 1, 1);
+  cfg.blockDim = dim3(kZeroThreads, 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, zero_flags_kernel, s.flags, s.count);
+}
+
 constexpr size_t kStagingBytes = 4u * 2u * kStoreBuf;
 
 size_t block_smem(int cg, int stages, int a_rows) {
@@ -113,12 +136,16 @@ size_t block_smem(int cg, int stages, int a_rows) {
 
 }  // namespace
 
-size_t block_workspace(const gemm_ops* ops) {
-  return static_cast<size_t>(ops->sm_count) *
-         std::max(block_partial_bytes(1), block_partial_bytes(2));
+BlockScratch take_scratch(const gemm_ops* ops, Carver& c) {
+  BlockScratch s;
+  s.partials = static_cast<float*>(
+      c.take(ops->sm_count * std::max(block_partial_bytes(1), block_partial_bytes(2))));
+  s.count = 4 * ops->sm_count;
+  s.flags = static_cast<int*>(c.take(s.count * sizeof(int)));
+  return s;
 }
 
-gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, cudaStream_t stream) {
+gemm_status_t run_block(const gemm_ops* ops, const BlockProblem& pr, BlockScratch& scratch, cudaStream_t stream) {
   const bool gated = pr.kind == BlockProblem::kGated;
   const bool a_t = pr.kind == BlockProblem::kTN;
   const bool use_d = pr.kind == BlockProblem::kDiagOut || pr.kind == BlockProblem::kDiagRows ||
@@ -218,8 +245,9 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   p.splits = splits;
   p.sk_tiles = static_cast<int>(sk);
   p.dp_tiles = static_cast<int>(nt - sk);
-  p.sk_ws = partials;
-  p.sk_flags = ops->d_flags;
+  p.sk_ws = scratch.partials;
+  p.sk_flags = scratch.flags;
+  p.zero_flags = scratch.zeroed || sk > 0 ? 0 : scratch.count;
   p.a_box_rows = a_rows;
   p.b_stream = pr.stream_b && tm == 1 ? 1 : 0;
   p.l2_prefetch_first = p.b_stream;
@@ -268,7 +296,10 @@ gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, 
   if (st != GEMM_OK) return st;
 
   const int grid = static_cast<int>(walkers) * cg;
-  cudaError_t e;
+  cudaError_t e = cudaSuccess;
+  if (sk > 0 && !scratch.zeroed) e = launch_zero_flags(scratch, stream);
+  if (e != cudaSuccess) return ops_cuda_fail(e, "flag clearing launch");
+  scratch.zeroed = true;
   switch (pr.kind) {
     case BlockProblem::kNT: e = block_launch_nt(maps, p, cg, grid, smem, stream); break;
     case BlockProblem::kNN: e = block_launch_nn(maps, p, cg, grid, smem, stream); break;
@@ -318,11 +349,8 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
   if (e == cudaSuccess) e = logprobs_set_smem();
   if (e == cudaSuccess) e = small_newton_init(ops);
   if (e == cudaSuccess) e = few_tokens_init(ops);
-  const size_t flags = static_cast<size_t>(ops->sm_count) * 4 * sizeof(int);
   if (e == cudaSuccess) e = cudaMalloc(&ops->d_status, 4 * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(ops->d_status, 0, 4 * sizeof(int));
-  if (e == cudaSuccess) e = cudaMalloc(&ops->d_flags, flags);
-  if (e == cudaSuccess) e = cudaMemset(ops->d_flags, 0, flags);
   // cudaMemset runs on the default stream; another stream's first call must not overtake it.
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) {
@@ -338,7 +366,6 @@ void gemm_ops_destroy(gemm_ops_t* ops) {
   OpsDevice guard(ops->device);
   cudaDeviceSynchronize();
   if (ops->d_status) cudaFree(ops->d_status);
-  if (ops->d_flags) cudaFree(ops->d_flags);
   delete ops;
 }
 
@@ -363,9 +390,6 @@ gemm_status_t gemm_ops_check(gemm_ops_t* ops, int32_t* device_status, int32_t* d
   int h[4] = {0, 0, 0, 0};
   e = cudaMemcpy(h, ops->d_status, sizeof(h), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(ops->d_status, 0, sizeof(h));
-  // A launch that gave up part-way may have left partial-ready flags raised.
-  if (e == cudaSuccess && h[0] != 0)
-    e = cudaMemset(ops->d_flags, 0, static_cast<size_t>(ops->sm_count) * 4 * sizeof(int));
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) return ops_cuda_fail(e, "read or clear the status word");
   *device_status = h[0];

@@ -16,8 +16,8 @@ namespace spgemm {
 constexpr int kSmallCluster = 8;  // CTAs of a cluster of the on-chip iteration, at most
 }
 
-// What persists between calls: the device status word and the
-// partial-ready flags of split tiles (raised and reset within a launch).
+// What persists between calls: limits of the device and its status word.  Calls
+// only read it, so that it serves any streams, captured graphs among them.
 struct gemm_ops {
   int device = 0;
   int sm_count = 0;
@@ -30,7 +30,6 @@ struct gemm_ops {
   unsigned long long timeout_ns = 0;
   int debug_fault = 0;
   int* d_status = nullptr;       // [0] code, [1] detail
-  int* d_flags = nullptr;        // 4 per CTA
 };
 
 namespace spgemm {
@@ -110,11 +109,20 @@ struct BlockProblem {
   bool stream_b = false;         // B is read once: evict-first copies
 };
 
-// Workspace for the fp32 partials of split tiles, enough for any product.
-size_t block_workspace(const gemm_ops* ops);
+// A call's workspace for its products' split tiles: fp32 partials, and the flags
+// that say they are there (4 per CTA, raised and reset within a launch).  They
+// are a call's own, because calls on other streams and replayed graphs may run
+// beside it.  Whatever runs first in a call and needs no flags zeroes them.
+struct BlockScratch {
+  float* partials = nullptr;
+  int* flags = nullptr;
+  int count = 0;         // flags
+  bool zeroed = false;   // by what was launched before
+};
+BlockScratch take_scratch(const gemm_ops* ops, Carver& c);  // enough for any product
 
 cudaError_t logprobs_set_smem();  // logprobs.cu
 
-gemm_status_t run_block(gemm_ops* ops, const BlockProblem& pr, float* partials, cudaStream_t stream);
+gemm_status_t run_block(const gemm_ops* ops, const BlockProblem& pr, BlockScratch& scratch, cudaStream_t stream);
 
 }  // namespace spgemm

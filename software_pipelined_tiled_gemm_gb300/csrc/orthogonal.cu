@@ -57,6 +57,8 @@ struct NormArgs {
   uint16_t* x;
   int64_t ldx;
   float eps;
+  int* flags;          // zeroed for the products (BlockScratch)
+  int flag_count;
 };
 
 // Row and first column of a matrix's vector v.
@@ -70,6 +72,8 @@ __global__ void __launch_bounds__(kNormThreads) sum_squares_kernel(const NormArg
   __shared__ double shared[kNormThreads / 32];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait_prior_grid();
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < a.flag_count; i += kNormThreads) a.flags[i] = 0;
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.batch_stride;
   SquareSum sum;
   auto pass = [&](auto&& add) {
@@ -162,7 +166,7 @@ cudaError_t normalize(const NormArgs& a, int64_t batch, int blocks, cudaStream_t
 }
 
 struct Layout {
-  float* partials;
+  BlockScratch scratch;
   double* norms;
   uint16_t* x[2];
   uint16_t* a;
@@ -196,7 +200,7 @@ Layout layout(const gemm_ops* ops, const gemm_orthogonalize_args_t* g, void* wor
       1, std::min<int64_t>(steps, kNormBlocks / std::max<int64_t>(1, std::min<int64_t>(g->batch, kNormBlocks)))));
   const size_t x = static_cast<size_t>(g->batch) * g->m * l.np * 2;
   const size_t a = static_cast<size_t>(g->batch) * l.s * l.sp * 2;
-  l.partials = static_cast<float*>(c.take(block_workspace(ops)));
+  l.scratch = take_scratch(ops, c);
   l.norms = static_cast<double*>(c.take(static_cast<size_t>(g->batch) * l.blocks * sizeof(double)));
   l.x[0] = static_cast<uint16_t*>(c.take(x));
   l.x[1] = static_cast<uint16_t*>(c.take(x));
@@ -258,7 +262,7 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
   gemm_status_t st = check(args);
   if (st != GEMM_OK || args->batch == 0 || args->m == 0 || args->n == 0) return st;
   const int64_t m = args->m, n = args->n, batch = args->batch;
-  const Layout l = layout(ops, args, workspace);
+  Layout l = layout(ops, args, workspace);
   if ((!workspace && l.bytes > 0) || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < l.bytes)
     return ops_fail(GEMM_ERR_INVALID_ARG, "workspace NULL, not 256-byte aligned or below %zu bytes", l.bytes);
   const size_t g_bytes = (static_cast<size_t>(batch - 1) * (batch > 1 ? args->batch_stride : 0) +
@@ -311,6 +315,9 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
   na.x = l.x[0];
   na.ldx = l.np;
   na.eps = args->eps;
+  na.flags = l.scratch.flags;
+  na.flag_count = l.scratch.count;
+  l.scratch.zeroed = true;
   cudaError_t e;
   if (args->dtype == GEMM_IN_F32)
     e = normalize<float>(na, batch, l.blocks, stream);
@@ -335,7 +342,7 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
     p.alpha = inv * inv;
     p.out0 = A;  // the padded row is the iterate's own
     p.out0.cols = l.sp;
-    st = run_block(ops, p, l.partials, stream);
+    st = run_block(ops, p, l.scratch, stream);
     if (st != GEMM_OK) return st;
 
     p.kind = BlockProblem::kDiagOut;  // B = c A A^T + b A
@@ -347,7 +354,7 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
     p.out0.cols = l.sp;
     p.diag = l.diag;
     p.diag_batch = l.diag_batch;
-    st = run_block(ops, p, l.partials, stream);
+    st = run_block(ops, p, l.scratch, stream);
     if (st != GEMM_OK) return st;
 
     const bool last = it + 1 == args->steps;
@@ -368,7 +375,7 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t* ops, const gemm_orthogonalize_args_
     p.beta = last ? inv * args->a : args->a;
     p.out_bf16 = last;
     p.out0 = last ? Matrix{args->out, m, n, n, m * n} : Matrix{Y.ptr, m, l.np, l.np, m * l.np};
-    st = run_block(ops, p, l.partials, stream);
+    st = run_block(ops, p, l.scratch, stream);
     if (st != GEMM_OK) return st;
     std::swap(X, Y);
   }

@@ -6,8 +6,8 @@ A thin ctypes binding over ``include/gemm_ops.h``.  As in :func:`matmul_nt`,
 tensors are CUDA tensors, work goes to the current stream of their device,
 nothing synchronises, and there is no fallback.  What a call needs besides
 its outputs (a workspace) comes from PyTorch's allocator on that stream.
-One library handle is kept per device and stream; :func:`check_operators`
-reports what a kernel recorded in them.
+One library handle is kept per device; :func:`check_operators` reports what
+a kernel recorded in them.
 """
 from __future__ import annotations
 
@@ -106,17 +106,16 @@ def _stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _handle(device, stream):
-    """The handle of a device and stream (one handle serves one stream)."""
-    key = (device.index, stream)
-    h = _handles.get(key)
+def _handle(device):
+    """The handle of a device."""
+    h = _handles.get(device.index)
     if h is None:
         with _lock:
-            h = _handles.get(key)
+            h = _handles.get(device.index)
             if h is None:
                 out = _vp()
                 _check(_lib().gemm_ops_create(ctypes.byref(out), device.index), "gemm_ops_create")
-                h = _handles[key] = out.value
+                h = _handles[device.index] = out.value
     return h
 
 
@@ -134,10 +133,8 @@ def check_operators() -> None:
 
 
 def _configure(device, timeout_ns=0, debug_fault=0) -> None:
-    """gemm_ops_configure for the handle of the device's current stream (tests)."""
-    stream = _stream(device)
-    _check(_lib().gemm_ops_configure(_handle(device, stream), timeout_ns, debug_fault),
-           "gemm_ops_configure")
+    """gemm_ops_configure for the device's handle (tests)."""
+    _check(_lib().gemm_ops_configure(_handle(device), timeout_ns, debug_fault), "gemm_ops_configure")
 
 
 def close_operators() -> None:
@@ -219,7 +216,7 @@ def _run(name, query, run, args, device, *which):
     """Workspace from the caching allocator of the current stream, then the call."""
     import torch
     stream = _stream(device)
-    h = _handle(device, stream)
+    h = _handle(device)
     ref, need = ctypes.byref(args), _sz()
     status = query(h, ref, *which, ctypes.byref(need))
     if not status:
@@ -386,7 +383,7 @@ def token_logprobs(logits, tokens=None, top_k=0):
     a.logprobs = _ptr(logprobs)
     if a.rows:
         stream = _stream(dev)
-        _check(_lib().gemm_token_logprobs(_handle(dev, stream), ctypes.byref(a), stream),
+        _check(_lib().gemm_token_logprobs(_handle(dev), ctypes.byref(a), stream),
                "gemm_token_logprobs")
     return TokenLogprobs(logprobs, entropy, lse, top_lp, top_ids, lse_low)
 
@@ -421,6 +418,6 @@ def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=N
     if a.rows:
         dev = logits.device
         stream = _stream(dev)
-        _check(_lib().gemm_token_logprobs_backward(_handle(dev, stream), ctypes.byref(a), stream),
+        _check(_lib().gemm_token_logprobs_backward(_handle(dev), ctypes.byref(a), stream),
                "gemm_token_logprobs_backward")
     return out
