@@ -56,6 +56,7 @@ struct Args {
   int64_t ldw;
   int m, rows, k;
   int share;           // warps of a group
+  int x_shifted;       // rows of tokens are not 16-byte aligned
   int weights_ready;   // the previous kernel on the stream has waited for what writes w
   uint16_t* out;       // M x rows
   int64_t ldo;
@@ -123,8 +124,9 @@ struct Window {
   }
 };
 
-// kTiles: groups of eight tokens.  kShifted: rows of weights or tokens that
-// are not 16-byte aligned, or of no multiple of eight elements.
+// kTiles: groups of eight tokens.  kShifted: rows of weights that are not
+// 16-byte aligned, or of no multiple of eight elements.  The tokens are read
+// once, however they lie, so that theirs need no instance.
 template <bool kBf16, int kTiles, bool kGated, bool kShifted>
 __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
   constexpr int kGroup = kGated ? 8 : 16;  // rows of a group
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const Args a) {
   ptx::pdl_launch_dependents();
   if (rounds > 0 && !a.weights_ready) load(0, s0);
   const int pitch = token_pitch(a.k);
-  if constexpr (kShifted) {
+  if (kShifted || a.x_shifted) {
     const uint16_t* x_end = a.x + (a.m - 1) * a.ldx + a.k;
 #pragma unroll 4
     for (int i = threadIdx.x; i < a.m * vecs; i += kThreads) {
@@ -310,6 +312,9 @@ Kernel kernel_of(bool bf16, bool gated, bool shifted, int64_t m) {
 
 }  // namespace
 
+// Whether whole 16-byte words of the rows can be read where they lie.
+bool aligned_rows(const Matrix& m) { return m.cols % 8 == 0 && copyable(m); }
+
 size_t token_bytes(int64_t m, int64_t k) { return static_cast<size_t>(m) * token_pitch(static_cast<int>(k)) * 16; }
 
 // Shared memory for the tokens, beside the partials.
@@ -323,16 +328,21 @@ size_t token_limit(int64_t m) {
 // then bound by those: 9 to 16 tokens up to 256 MB of weights (us here and on
 // tiles: 36 and 51 where gate and up are 108 MB, 73 and 74 at 268 MB, 135 to
 // 159 and 132 at 537 MB), 17 to 32 up to 48 MB (23 and 27 at 34 MB, 90 and 74
-// at 268 MB).  Rows that are not 16-byte aligned cost twice the loads, but on
-// tiles a padded copy of all weights (1 token of 2049 / 4095 24 and 51, 16
-// tokens 36 and 52); more than eight tokens of long rows do not gain (16 of
-// 6045 / 1617 68 and 57).
-bool few_tokens_fits(const gemm_ops* ops, int64_t m, int64_t k, int64_t rows) {
-  const int64_t limit = int64_t{1} << 20;
-  const int64_t most = m <= 8 ? kOpsMaxDim * limit : m <= 16 ? 256 * limit : 48 * limit;
-  if (k % 8 != 0 && m > 8 && token_bytes(m, k) > 128 * 1024) return false;
-  return 2 * rows * k <= most && m >= 1 && m <= kFewTokens && k <= kOpsMaxDim - 64 && ops->smem_optin >= 227 * 1024 &&
-         token_bytes(m, k) <= token_limit(m);
+// at 268 MB).
+//
+// Rows of weights that are not 16-byte aligned cost twice the loads here, and a
+// padded copy of all weights on tiles: up to eight tokens always gain (1 of
+// 2049 / 2051 23 and 45, of 4095 / 8193 81 and 122), 9 to 16 where what they
+// fill of shared memory is below 160 KB (16 of 4095 / 4097, 132 KB, 68 and 80;
+// 12 of 6045 / 1617, 146 KB, 52 and 63; 16 of those, 195 KB, 76 and 63), 17 to
+// 32 there up to 32 MB of weights (17 tokens where gate and up are 25 MB 44 and
+// 53, 39 MB 64 and 61, 49 MB 72 and 67).
+bool few_tokens_fits(const gemm_ops* ops, int64_t m, int64_t rows, const Matrix& w) {
+  const int64_t k = w.cols, limit = int64_t{1} << 20;
+  const bool aligned = aligned_rows(w);
+  const int64_t most = m <= 8 ? kOpsMaxDim * limit : m <= 16 ? 256 * limit : (aligned ? 48 : 32) * limit;
+  if (m < 1 || m > kFewTokens || k > kOpsMaxDim - 64 || ops->smem_optin < 227 * 1024) return false;
+  return 2 * rows * k <= most && token_bytes(m, k) <= (aligned || m <= 8 ? token_limit(m) : 160 * 1024);
 }
 
 cudaError_t few_tokens_init(const gemm_ops* ops) {
@@ -367,7 +377,8 @@ cudaError_t few_tokens_launch(const gemm_ops* ops, const FewTokens& f, cudaStrea
   a.share = 1;
   while (a.share < kWarps && groups * a.share * 2 <= kWarps && ceil_div(f.x.cols, 32) >= a.share * 2)
     a.share *= 2;
-  const bool shifted = f.x.cols % 8 != 0 || !copyable(f.x) || !copyable(f.w);
+  const bool shifted = !aligned_rows(f.w);
+  a.x_shifted = aligned_rows(f.x) ? 0 : 1;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(ops->sm_count, 1, 1);

@@ -24,8 +24,8 @@ struct FewTokens {
   int act;
 };
 
-// m tokens, weights of `rows` rows of k (gated: of both halves).
-bool few_tokens_fits(const gemm_ops* ops, int64_t m, int64_t k, int64_t rows);
+// m tokens, `rows` rows of weights w (gated: of both halves).
+bool few_tokens_fits(const gemm_ops* ops, int64_t m, int64_t rows, const Matrix& w);
 cudaError_t few_tokens_init(const gemm_ops* ops);
 cudaError_t few_tokens_launch(const gemm_ops* ops, const FewTokens& f, cudaStream_t stream);
 

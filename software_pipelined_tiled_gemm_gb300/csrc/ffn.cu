@@ -131,8 +131,8 @@ size_t layout(const gemm_ops* ops, const gemm_ffn_args_t* a, bool backward, void
   };
   // (The fault hook withholds a copy, of which that path has none.)
   const bool few = !backward && ops->debug_fault == 0;
-  f->few_first = few && few_tokens_fits(ops, f->M, f->D, 2 * f->I);
-  f->few_second = few && few_tokens_fits(ops, f->M, f->I, f->D);
+  f->few_first = few && few_tokens_fits(ops, f->M, 2 * f->I, f->w_in);
+  f->few_second = few && few_tokens_fits(ops, f->M, f->D, f->w_out);
   if (!f->few_second) padded(&f->w_out);
   if (!f->few_first && (!backward || a->dx)) padded(&f->w_in);
   if (!f->few_first && (!backward || a->dw_in)) padded(&f->x);
