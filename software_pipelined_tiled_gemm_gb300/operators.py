@@ -121,15 +121,21 @@ def _handle(device):
 
 def check_operators() -> None:
     """Synchronise and raise :class:`GemmError` if a kernel of any operator
-    recorded an error (a wait that ran out of time)."""
-    from . import GemmError, gemm_wait_detail_string
+    recorded an error (a wait that ran out of time).  Every device's record is
+    read and cleared; the first error is raised."""
+    from . import GemmError, gemm_last_error, gemm_wait_detail_string
     with _lock:
         handles = list(_handles.values())
+    errors = []
     for h in handles:
         ds, detail = ctypes.c_int32(0), ctypes.c_int32(0)
-        _check(_lib().gemm_ops_check(h, ctypes.byref(ds), ctypes.byref(detail)), "gemm_ops_check")
-        if ds.value:
-            raise GemmError(ds.value, "operators", gemm_wait_detail_string(detail.value))
+        status = _lib().gemm_ops_check(h, ctypes.byref(ds), ctypes.byref(detail))
+        if status:
+            errors.append(GemmError(status, "gemm_ops_check", gemm_last_error()))
+        elif ds.value:
+            errors.append(GemmError(ds.value, "operators", gemm_wait_detail_string(detail.value)))
+    if errors:
+        raise errors[0]
 
 
 def _configure(device, timeout_ns=0, debug_fault=0) -> None:
