@@ -109,8 +109,12 @@ size_t layout(const gemm_ops* ops, const gemm_ffn_args_t* a, bool backward, void
   f->dy = {a->dy, f->M, f->D, a->lddy, 0};
   f->w_in = {a->w_in, 2 * f->I, f->D, f->D, 0};
   f->w_out = {a->w_out, f->D, f->I, f->I, 0};
+  // (The fault hook withholds a copy, of which the path for few tokens has none.)
+  const bool few = !backward && ops->debug_fault == 0;
+  f->few_first = few && few_tokens_fits(ops, f->M, 2 * f->I, f->w_in);
+  f->few_second = few && few_tokens_fits(ops, f->M, f->D, f->w_out);
   Carver c(workspace);
-  f->scratch = take_scratch(ops, c);
+  f->scratch = f->few_first && f->few_second ? BlockScratch() : take_scratch(ops, c);
   f->pre = static_cast<float*>(a->kept);
   if (a->kept)
     f->h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a->kept) + pre_bytes(f->M, f->I));
@@ -129,10 +133,6 @@ size_t layout(const gemm_ops* ops, const gemm_ffn_args_t* a, bool backward, void
     m->ptr = dst;
     m->ld = ldp;
   };
-  // (The fault hook withholds a copy, of which that path has none.)
-  const bool few = !backward && ops->debug_fault == 0;
-  f->few_first = few && few_tokens_fits(ops, f->M, 2 * f->I, f->w_in);
-  f->few_second = few && few_tokens_fits(ops, f->M, f->D, f->w_out);
   if (!f->few_second) padded(&f->w_out);
   if (!f->few_first && (!backward || a->dx)) padded(&f->w_in);
   if (!f->few_first && (!backward || a->dw_in)) padded(&f->x);
@@ -149,7 +149,7 @@ gemm_status_t prepare(gemm_ops_t* ops, const gemm_ffn_args_t* a, bool backward, 
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return ops_fail(GEMM_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
   const size_t need = layout(ops, a, backward, workspace, f);
-  if (a->tokens > 0 && (!workspace || bytes < need))
+  if (a->tokens > 0 && need > 0 && (!workspace || bytes < need))
     return ops_fail(GEMM_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? bytes : 0,
                     need);
   return check_overlap(a, backward, workspace, need);
