@@ -158,7 +158,7 @@ def _rows(t, cols, name):
     rows = t.numel() // cols
     if t.is_contiguous():
         return rows, cols
-    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < cols:
+    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
         raise ValueError("%s must be contiguous, or a matrix of contiguous rows" % name)
     return rows, t.stride(0)
 
@@ -311,8 +311,9 @@ def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
     b, m, n = (1,) * (3 - g.dim()) + tuple(g.shape)
     ld, bs = n, m * n
     if not g.is_contiguous():
-        ld, bs = g.stride(-2), (g.stride(0) if g.dim() == 3 else 0)
-        if g.stride(-1) != 1 or ld < n or (b > 1 and bs < 0):
+        # Strides along a single row or column lead nowhere.
+        ld, bs = g.stride(-2) if m > 1 else n, (g.stride(0) if g.dim() == 3 else 0)
+        if (n > 1 and g.stride(-1) != 1) or ld < n or (b > 1 and bs < 0):
             raise ValueError("g must have contiguous rows")
     y = _output(out, g.shape, torch.bfloat16, g.device)
     a = OrthogonalizeArgs(batch=b, m=m, n=n, dtype=_inputs[g.dtype], g=g.data_ptr(), ldg=ld,
