@@ -56,7 +56,8 @@ gemm_status_t gemm_ops_check(gemm_ops_t* ops, int32_t* device_status, int32_t* d
  * X: tokens x d_model, row pitch ldx.  w_in: 2 d_inner x d_model, the rows
  * of Wg followed by those of Wu.  w_out: d_model x d_inner.  Y: tokens x
  * d_model.  All in `dtype`; Y, w_in and w_out dense.  G and U stay in fp32;
- * H is rounded to `dtype` once, being the second product's operand. */
+ * H is rounded to `dtype` once, being the second product's operand (in fp16
+ * an element beyond 65504 becomes infinite). */
 typedef enum { GEMM_ACT_SILU = 0, GEMM_ACT_GELU_TANH = 1, GEMM_ACT_RELU = 2 } gemm_act_t;
 
 typedef struct {
@@ -95,7 +96,7 @@ gemm_status_t gemm_ffn_run(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* w
  *   dH = dY Wo,  dG = dH * U * act'(G),  dU = dH * act(G)
  *   dX = [dG dU] w_in,  dw_in = [dG dU]^T X,  dw_out = dY^T H
  * in `dtype`, each rounded once; dG and dU are rounded to `dtype` as the
- * products' operands.  With no tokens the weights' gradients are zero. */
+ * products' operands, with the same range.  With no tokens the weights' gradients are zero. */
 gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
@@ -112,7 +113,7 @@ gemm_status_t gemm_ffn_backward(gemm_ops_t* ops, const gemm_ffn_args_t* args, vo
 typedef enum { GEMM_IN_F16 = 0, GEMM_IN_BF16 = 1, GEMM_IN_F32 = 2 } gemm_in_t;
 
 typedef struct {
-  int64_t batch, m, n;   /* each >= 0 */
+  int64_t batch, m, n;   /* each >= 0; batch <= 65535 */
   gemm_in_t dtype;       /* of g */
   const void* g;
   int64_t ldg;           /* row pitch of g, elements, >= n */

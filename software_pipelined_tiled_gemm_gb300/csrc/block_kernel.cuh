@@ -1,7 +1,7 @@
 // block_kernel.cuh -- the products of the gated feed-forward block and of the
 // Newton-Schulz iteration, on the roles of gemm_kernel.cuh (one TMA producer
-// thread, one tcgen05.mma issuer thread, four epilogue warps; see there for
-// the ring and accumulator protocol).  What differs:
+// thread, one tcgen05.mma issuer thread, four or eight epilogue warps; see
+// there for the ring and accumulator protocol).  What differs:
 //
 //   operands    each K-major (rows of K) or MN-major (stored K x M / K x N).
 //               An MN-major slice of 64 K rows arrives as boxes of 64 columns
@@ -269,7 +269,7 @@ __device__ __forceinline__ void gated_bwd16(const uint32_t (&dh)[16], const floa
 }
 
 // CG: 2 for CTA pairs, 1 for single CTAs.  kAT: A stored K x M.  kBN: B
-// stored K x N.  kEpi: the epilogue (kEpiLinear, kEpiGated, kEpiGatedBwd).
+// stored K x N.  kEpi: the epilogue (block_params.h).
 // kG: epilogue warps per TMEM lane quarter.  With two, they share the
 // quarter's staging buffers and each takes 32 of a chunk's 64 columns.
 template <int CG, bool kAT, bool kBN, int kEpi, int kG>

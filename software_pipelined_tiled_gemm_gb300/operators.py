@@ -6,6 +6,8 @@ A thin ctypes binding over ``include/gemm_ops.h``.  As in :func:`matmul_nt`,
 tensors are CUDA tensors, work goes to the current stream of their device,
 nothing synchronises, and there is no fallback.  What a call needs besides
 its outputs (a workspace) comes from PyTorch's allocator on that stream.
+Nothing is recorded for autograd: outputs have no graph, even where inputs
+require gradients; the *_backward functions give those.
 One library handle is kept per device; :func:`check_operators` reports what
 a kernel recorded in them.
 """
@@ -243,6 +245,11 @@ def gated_ffn(x, w_in, w_out, act="silu", out=None, save=False):
     dtype (``out`` if given), or ``(y, kept)`` with ``save=True``, kept being
     what :func:`gated_ffn_backward` needs (10 bytes per token and inner
     feature: the projections stay in fp32).
+
+    act(x Wg^T) * (x Wu^T) is rounded to x's dtype before the second product,
+    so in float16 an element of it beyond 65504 becomes infinite.  No autograd
+    graph: for gradients pass ``save=True`` and call
+    :func:`gated_ffn_backward`.
     """
     import torch
     lib = _lib()
@@ -264,7 +271,9 @@ def gated_ffn_backward(dy, x, w_in, w_out, kept, need=(True, True, True), out=(N
     """Gradients (dx, dw_in, dw_out) of :func:`gated_ffn` from dy and what
     the forward pass kept, with the same x, w_in and w_out.
 
-    dy: x's shape and dtype, contiguous or a matrix of contiguous rows.
+    dy: x's shape and dtype, contiguous or a matrix of contiguous rows.  The
+    gradients of the projections are rounded to that dtype as operands of the
+    products (in float16 infinite beyond 65504).
     need: which of the three to compute (None in the place of the others).
     out: tensors to write them to.
     """
@@ -294,8 +303,9 @@ def orthogonalize(g, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, out=None):
     """The orthogonalised form of a matrix, by Newton-Schulz products.
 
     X = g / max(|g|_F, eps), then `steps` times X <- a X + (b A + c A^2) X
-    with A = X X^T (on the shorter side).  g: (m, n) or a batch (b, m, n),
-    float32, float16 or bfloat16, rows contiguous.  Returns bfloat16 of g's
+    with A = X X^T (on the shorter side).  g: (m, n) or a batch (b, m, n) of
+    up to 65535 matrices, float32, float16 or bfloat16, rows contiguous.  The
+    iterates are float16 whatever g is.  Returns bfloat16 of g's
     shape (``out`` if given): the update of a weight whose gradient or
     momentum is g.
     """
@@ -359,7 +369,8 @@ def token_logprobs(logits, tokens=None, top_k=0):
     """Log probabilities of `tokens` under rows of logits, in fp32.
 
     logits: (..., vocab), float32, float16 or bfloat16, contiguous or a
-    matrix of contiguous rows (a slice of a padded vocabulary).  tokens:
+    matrix of contiguous rows (a slice of a padded vocabulary); no autograd
+    graph, see :func:`token_logprobs_backward`.  tokens:
     int64 (...), or None; a negative one marks a position that does not
     count (log probability 0).  top_k: how many of the best columns to
     return, at most 64, equal ones by the lowest column.
