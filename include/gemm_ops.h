@@ -1,7 +1,8 @@
 /*
  * gemm_ops.h -- C ABI of the operators built around the GEMM (gemm.h): the
  * gated feed-forward block with its backward pass, the orthogonalised update
- * of a gradient, and the log probabilities of tokens with their gradient.
+ * of a gradient, the log probabilities of tokens with their gradient, and
+ * products grouped by expert with their gradients.
  *
  * Sizes vary from call to call (a prompt's length, a batch), so these
  * operators take no plan for a problem: one gemm_ops_t per device holds what
@@ -167,6 +168,42 @@ gemm_status_t gemm_token_logprobs(gemm_ops_t* ops, const gemm_logprobs_args_t* a
  * forward pass's lse, lse_low (and entropy). */
 gemm_status_t gemm_token_logprobs_backward(gemm_ops_t* ops, const gemm_logprobs_args_t* args,
                                            void* stream);
+
+/* ---- Products grouped by expert ---------------------------------------------
+ * Group e is the rows offsets[e] .. offsets[e + 1] - 1 of x:
+ *   y_r = W_e x_r,  dx_r = W_e^T dy_r,  dW_e = sum_r dy_r x_r^T
+ * x: rows x k, w: groups x n x k, y: rows x n; sums in fp32, each output
+ * rounded to `dtype` once.  The offsets are read on the device, so a call
+ * needs no host copy of them.  They may not decrease nor leave [0, rows];
+ * where they do, nothing is written to y, dx and dw and gemm_ops_check
+ * reports GEMM_ERR_INVALID_ARG (GEMM_CHECK_OFFSETS).  Rows of no group are
+ * not read: what they hold, NaN and infinities too, reaches no output. */
+#define GEMM_GROUPED_MAX_GROUPS 4096
+#define GEMM_CHECK_OFFSETS ((0 << 16) | 17) /* detail of the status word */
+
+typedef struct {
+  int64_t rows, groups, n, k;  /* rows >= 0, n, k >= 1, groups 1 .. GEMM_GROUPED_MAX_GROUPS */
+  gemm_dtype_t dtype;
+  const int64_t* offsets;      /* groups + 1, on the device */
+  const void* x;
+  int64_t ldx;                 /* row pitch, elements, >= k */
+  const void* w;               /* dense */
+  void* y;                     /* forward only: rows x n, dense */
+  int zero_rest;               /* 1: rows of no group of y and dx become zero; 0: they are left
+                                  as they were */
+  const void* dy;              /* backward only: rows x n, row pitch lddy */
+  int64_t lddy;
+  void* dx;                    /* rows x k, dense; each gradient may be NULL */
+  void* dw;                    /* groups x n x k; zero for an empty group */
+} gemm_grouped_args_t;
+
+/* Workspace of gemm_grouped_run (backward 0) or gemm_grouped_backward (1). */
+gemm_status_t gemm_grouped_workspace(gemm_ops_t* ops, const gemm_grouped_args_t* args, int backward,
+                                     size_t* bytes);
+gemm_status_t gemm_grouped_run(gemm_ops_t* ops, const gemm_grouped_args_t* args, void* workspace,
+                               size_t workspace_bytes, void* stream);
+gemm_status_t gemm_grouped_backward(gemm_ops_t* ops, const gemm_grouped_args_t* args,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -49,7 +49,8 @@ __all__ = [
     "GEMM_PIPELINED", "GEMM_SINGLE_BUFFER",
     "gated_ffn", "gated_ffn_backward", "GatedKept", "orthogonalize", "NEWTON_SCHULZ",
     "token_logprobs", "token_logprobs_backward", "TokenLogprobs", "MAX_TOP_K",
-    "check_operators", "close_operators", "FfnArgs", "OrthogonalizeArgs", "LogprobsArgs",
+    "grouped_matmul", "grouped_matmul_backward", "MAX_GROUPS",
+    "check_operators", "close_operators", "FfnArgs", "OrthogonalizeArgs", "LogprobsArgs", "GroupedArgs",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -533,6 +534,6 @@ def matmul_nt(A, B, epilogue=None, stages: int = 6, variant: str = "pipelined", 
 
 
 from .operators import (  # noqa: E402 - they use the binding above
-    FfnArgs, GatedKept, LogprobsArgs, MAX_TOP_K, NEWTON_SCHULZ, OrthogonalizeArgs, TokenLogprobs,
-    check_operators, close_operators, gated_ffn, gated_ffn_backward, orthogonalize, token_logprobs,
-    token_logprobs_backward)
+    FfnArgs, GatedKept, GroupedArgs, LogprobsArgs, MAX_GROUPS, MAX_TOP_K, NEWTON_SCHULZ,
+    OrthogonalizeArgs, TokenLogprobs, check_operators, close_operators, gated_ffn, gated_ffn_backward,
+    grouped_matmul, grouped_matmul_backward, orthogonalize, token_logprobs, token_logprobs_backward)

@@ -32,12 +32,6 @@ size_t pre_bytes(int64_t tokens, int64_t inner) {
   return align256(static_cast<size_t>(2) * ceil_div(tokens, 32) * 32 * inner * sizeof(float));
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || !na || !nb) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
 gemm_status_t check(const gemm_ffn_args_t* a, bool backward) {
   if (!a) return ops_fail(GEMM_ERR_INVALID_ARG, "args is NULL");
   if (a->tokens < 0 || a->d_model < 1 || a->d_inner < 1)

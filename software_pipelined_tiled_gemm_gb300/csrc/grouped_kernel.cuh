@@ -1,0 +1,418 @@
+// grouped_kernel.cuh -- matrix products of many groups of rows, each with a
+// weight of its own, on the roles of gemm_kernel.cuh (one TMA producer thread,
+// one tcgen05.mma issuer thread, eight epilogue warps; see there for the ring
+// and accumulator protocol).  What differs:
+//
+//   sizes       The groups' offsets are read on the device.  Every CTA loads
+//               them, checks them and counts the tiles of each group, so the
+//               launch needs no more than an upper bound and the host no copy.
+//   tiles       256 x n on a CTA pair, n a multiple of 32 up to 256.  The
+//               weights' features lie along the MMA's M side and a group's
+//               tokens along its N side, so a tile is as wide as the group's
+//               rows need: a group of 300 rows costs the products of 320, not
+//               of 512, and a few tokens cost what their weights' bytes do.
+//               A group's rows are cut into tiles of nearly equal width.
+//   epilogue    A lane holds one feature, a column one token: neighbouring
+//               lanes exchange halves, and a warp writes 64 contiguous bytes
+//               of two tokens with each store.  A group's last rows need no
+//               clipping by the copy engine, whose box would reach into the
+//               next group, and no staging memory: the ring has all of it.
+//   dW          The sum runs over a group's tokens, any number of them.  MMA
+//               steps of 16 tokens that are all the group's read x and dy
+//               where they lie; the last 1 to 15 come from a copy padded with
+//               zeros (grouped.cu): the next group's rows would be products'
+//               operands otherwise, and zero times their NaN is NaN.
+//
+// Every sum has a fixed order, so results repeat bit for bit.
+#pragma once
+
+#include "../../include/gemm_ops.h"
+#include "gemm_kernel.cuh"
+#include "grouped_params.h"
+#include "ptx_block.cuh"
+
+namespace spgemm {
+
+struct GroupedTile {
+  int group;
+  int lane0;        // first feature
+  int row0;         // first output row: of the tokens, or of dW_e
+  int rows;         // output rows that exist
+  int width;        // the MMA's columns
+  int first;        // kWeight: first token of the group
+  int full, part, tail;  // kWeight: whole slots of 64 tokens, whole steps after them, a last partial step
+  __device__ int slots(const GroupedParams& p, int kind) const {
+    if (kind != kGroupedWeight) return (p.reduce + kBK - 1) / kBK;
+    return full + (part > 0) + tail;
+  }
+};
+
+// Tile i of `tiles` (the least number of them) along `extent` columns: widths
+// are multiples of 32 and differ by one unit at most.
+__device__ __forceinline__ void grouped_split(int extent, int tiles, int i, int& at, int& width) {
+  const int units = (extent + kGroupedUnit - 1) / kGroupedUnit;
+  const int u0 = static_cast<int>(static_cast<int64_t>(units) * i / tiles);
+  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (i + 1) / tiles);
+  at = u0 * kGroupedUnit;
+  width = (u1 - u0) * kGroupedUnit;
+}
+
+// Tile t.  `offsets` and `first_tile` (tiles along the tokens before each
+// group) are this CTA's tables.
+template <int kKind>
+__device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedParams& p, const int* offsets,
+                                                    const int* first_tile) {
+  GroupedTile x{};
+  if constexpr (kKind == kGroupedWeight) {
+    const int tiles = (p.cols + p.cap - 1) / p.cap;
+    const int per = p.tiles_lane * tiles;
+    x.group = t / per;
+    const int r = t - x.group * per;
+    x.lane0 = (r / tiles) * kGroupedLanes;
+    int at;
+    grouped_split(p.cols, tiles, r % tiles, at, x.width);
+    x.row0 = at;
+    x.rows = min(x.width, p.cols - at);
+    x.first = offsets[x.group];
+    const int m = offsets[x.group + 1] - x.first;
+    x.full = m / kBK;
+    x.part = (m % kBK) / kGroupedTail;
+    x.tail = m % kGroupedTail != 0;
+  } else {
+    int lo = 0, hi = p.groups;  // the last group whose first tile is not after t
+    const int row = t / p.tiles_lane;  // (a group's tiles are tiles_lane times as many)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first_tile[mid] <= row)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    x.group = lo;
+    const int tiles = first_tile[lo + 1] - first_tile[lo];
+    const int r = t - first_tile[lo] * p.tiles_lane;
+    // Eight tiles of tokens at a time, lane tile by lane tile: their rows stay
+    // in L2 while the weights pass once.
+    const int g = r / (8 * p.tiles_lane);
+    const int high = min(8, tiles - 8 * g);
+    const int s = r - g * 8 * p.tiles_lane;
+    x.lane0 = (s / high) * kGroupedLanes;
+    int at;
+    const int m = offsets[lo + 1] - offsets[lo];
+    grouped_split(m, tiles, 8 * g + s % high, at, x.width);
+    x.row0 = offsets[lo] + at;
+    x.rows = min(x.width, m - at);
+  }
+  return x;
+}
+
+// Rows of no group become zero: this warp's share.
+__device__ __forceinline__ void grouped_zero_rest(const GroupedParams& p, int first, int last, int worker,
+                                                  int workers, int lane) {
+  const int rest = first + (p.rows - last);
+  for (int i = worker; i < rest; i += workers) {
+    const int row = i < first ? i : last + (i - first);
+    uint16_t* dst = p.out + row * p.ldo;
+    for (int c = lane; c < p.lanes; c += 32) dst[c] = 0;
+  }
+}
+
+template <int kKind>
+__global__ void __launch_bounds__(kGroupedThreads, 1)
+    grouped_kernel(const __grid_constant__ GroupedMaps maps, const __grid_constant__ GroupedParams p) {
+  constexpr bool kAN = kKind != kGroupedForward;   // A stored (sum) x (lanes)
+  constexpr bool kBN = kKind == kGroupedWeight;    // B stored (sum) x (columns)
+  constexpr uint32_t kBoxBytes = 64u * kBK * 2u;   // MN-major box: 64 columns x 64 rows of the sum
+  constexpr uint32_t kTailBytes = 64u * kGroupedTail * 2u;
+  constexpr uint32_t tmem_cols = 2u * kGroupedCols;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const int S = p.stages;
+  const uint32_t ring_bytes = static_cast<uint32_t>(S) * kGroupedSlot;
+  const uint32_t bar_base = sbase + ring_bytes;
+  constexpr uint32_t kBars = 8u * (2 * kGroupedStages + 5);
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (kGroupedStages + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * kGroupedStages + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * kGroupedStages + 2 + a); };
+  const uint32_t done_bar = bar_base + 8u * (2 * kGroupedStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + ring_bytes + kBars);
+  int* offsets = reinterpret_cast<int*>(smem + ring_bytes + kBars + 16u);
+  int* first_tile = offsets + p.groups + 1;
+  if (SPGEMM_OUT_OF_BOUNDS(S >= 1 && S <= kGroupedStages &&
+                               (sbase - raw_addr) + ring_bytes + kBars + 16u + 8u * (p.groups + 1) <=
+                                   ptx::dynamic_smem_bytes(),
+                           p, kCheckSmemLayout))
+    return;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int walker = static_cast<int>(blockIdx.x) / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(tfull_bar(a), 1);
+      ptx::mbar_init(tempty_bar(a), 2 * 8);
+    }
+    ptx::mbar_init(done_bar, 1);
+    ptx::fence_barrier_init();
+    ptx::tma_prefetch_desc(&maps.a);
+    ptx::tma_prefetch_desc(&maps.b[0]);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc<2>(ptx::smem_addr(tmem_slot), tmem_cols);
+    ptx::tmem_relinquish<2>();
+  }
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+
+  // The groups' offsets and, for tiles along the tokens, how many come before each group.
+  int bad = 0;
+  for (int e = threadIdx.x; e <= p.groups; e += kGroupedThreads) {
+    const int64_t at = __ldg(p.offsets + e);
+    const int64_t next = e < p.groups ? __ldg(p.offsets + e + 1) : static_cast<int64_t>(p.rows);
+    bad |= at < 0 || at > next || next > p.rows;
+    offsets[e] = static_cast<int>(at);
+  }
+  bad = __syncthreads_or(bad);
+  if constexpr (kKind != kGroupedWeight) {
+    if (warp == 0 && !bad) {
+      int before = 0;
+      for (int e0 = 0; e0 < p.groups; e0 += 32) {
+        const int e = e0 + lane;
+        const int m = e < p.groups ? offsets[e + 1] - offsets[e] : 0;
+        int n = (m + p.cap - 1) / p.cap;
+        for (int d = 1; d < 32; d *= 2) {
+          const int up = __shfl_up_sync(0xffffffffu, n, d);
+          if (lane >= d) n += up;
+        }
+        if (e < p.groups) first_tile[e + 1] = before + n;
+        before += __shfl_sync(0xffffffffu, n, 31);
+      }
+      if (lane == 0) first_tile[0] = 0;
+    }
+  }
+  ptx::tc_fence_before_sync();
+  ptx::cluster_sync();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  int total = 0;
+  if (!bad)
+    total = p.tiles_lane * (kKind == kGroupedWeight ? p.groups * ((p.cols + p.cap - 1) / p.cap)
+                                                    : first_tile[p.groups]);
+  else if (blockIdx.x == 0 && threadIdx.x == 0)
+    record_error(p.status, static_cast<int>(GEMM_ERR_INVALID_ARG), GEMM_CHECK_OFFSETS);
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0, issued_parity = 0;
+      bool ok = true;
+      for (int t = walker; ok && t < total; t += p.pairs) {
+        const GroupedTile x = grouped_tile<kKind>(t, p, offsets, first_tile);
+        if (SPGEMM_OUT_OF_BOUNDS(x.group >= 0 && x.group < p.groups && x.width >= kGroupedUnit &&
+                                     x.width <= kGroupedCols && x.rows > 0 && x.lane0 >= 0 && x.lane0 < p.lanes,
+                                 p, kCheckTile)) {
+          ok = false;
+          break;
+        }
+        const int half = x.width / 2;  // columns this CTA copies
+        const int a0 = x.lane0 + static_cast<int>(rank) * kBM;
+        const int b0 = x.row0 + static_cast<int>(rank) * half;
+        // kWeight: 64-column boxes; otherwise the smallest box of rows that holds them.
+        const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        const int boxes = (half + 63) / 64;
+        const int slots = x.slots(p, kKind);
+        for (int s = 0; s < slots; ++s) {
+          if (!wait_bounded(empty_bar(stage), phase ^ 1u, p, kDetailProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          const bool tail = kBN && x.tail && s == slots - 1;
+          const uint32_t bytes = !kBN ? kStageA + (static_cast<uint32_t>(kGroupedTail) << box) * (kBK * 2u)
+                                      : (tail ? kTailBytes : kBoxBytes) * static_cast<uint32_t>(2 + boxes);
+          const uint32_t da = sbase + stage * kGroupedSlot, db = da + kStageA;
+          const uint32_t fb = ptx::map_shared_rank(full_bar(stage), 0);
+          if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
+          // Test hook: the first slot of the first CTA is announced but never copied.
+          const bool skip = p.inject_fault == 1 && blockIdx.x == 0 && issued == 0;
+          if (!skip) {
+            if constexpr (!kBN) {
+              const int kx = s * kBK;
+              if constexpr (kAN) {
+                ptx::tma_load_3d_pair(da, &maps.a, a0, kx, x.group, fb);
+                ptx::tma_load_3d_pair(da + kBoxBytes, &maps.a, a0 + 64, kx, x.group, fb);
+              } else {
+                ptx::tma_load_3d_pair(da, &maps.a, kx, a0, x.group, fb);
+              }
+              ptx::tma_load_3d_pair(db, &maps.b[box], kx, b0, 0, fb);
+            } else {
+              const int at = tail ? 0 : x.first + s * kBK;
+              const int z = tail ? x.group : 0;
+              const CUtensorMap* ma = tail ? &maps.b[1] : &maps.a;
+              const CUtensorMap* mb = tail ? &maps.b[2] : &maps.b[0];
+              ptx::tma_load_3d_pair(da, ma, a0, at, z, fb);
+              ptx::tma_load_3d_pair(da + kBoxBytes, ma, a0 + 64, at, z, fb);
+              ptx::tma_load_3d_pair(db, mb, b0, at, z, fb);
+              if (boxes > 1) ptx::tma_load_3d_pair(db + kBoxBytes, mb, b0 + 64, at, z, fb);
+            }
+          }
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every copy this pair started must have landed before it exits.
+      if (leader) {
+        for (int s = 0; s < S; ++s)
+          if (issued & (1u << s))
+            wait_bounded(full_bar(s), (issued_parity >> s) & 1u, p, kDetailProducerDrain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer --
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int t = walker; ok && t < total; t += p.pairs) {
+        const GroupedTile x = grouped_tile<kKind>(t, p, offsets, first_tile);
+        const int slots = x.slots(p, kKind);
+        if (slots == 0) continue;  // an empty group's dW: the epilogue writes zeros
+        if (!wait_bounded_cluster<2>(tempty_bar(acc), acc_phase ^ 1u, p, kDetailMmaAccEmpty)) break;
+        ptx::tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kGroupedCols);
+        const uint32_t idesc = ptx::instr_desc_f16(kGroupedLanes, x.width, p.bf16 != 0, kBN) |
+                               (kAN ? 1u << 15 : 0u);
+        for (int s = 0; s < slots; ++s) {
+          if (!wait_bounded(full_bar(stage), phase, p, kDetailMmaFull) ||
+              SPGEMM_OUT_OF_BOUNDS(stage >= 0 && stage < S, p, kCheckMmaSlot)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after_sync();
+          const uint32_t sa = sbase + stage * kGroupedSlot, sb = sa + kStageA;
+          const uint64_t a_desc = kAN ? ptx::smem_desc_mn_sw128(sa, kBoxBytes, 1024u) : ptx::smem_desc_k_sw128(sa);
+          const uint64_t b_desc = kBN ? ptx::smem_desc_mn_sw128(sb, kBoxBytes, 1024u) : ptx::smem_desc_k_sw128(sb);
+          constexpr uint32_t a_step = kAN ? 2048u / 16u : 2u, b_step = kBN ? 2048u / 16u : 2u;
+          int steps = kBK / kUmmaK;
+          if (kBN && s >= x.full) steps = s == x.full && x.part > 0 ? x.part : 1;
+#pragma unroll
+          for (int k = 0; k < kBK / kUmmaK; ++k)
+            if (k < steps)
+              ptx::mma_f16_ss<2>(d_tmem, a_desc + a_step * k, b_desc + b_step * k, idesc, (s | k) != 0 ? 1u : 0u);
+          ptx::mma_commit_multicast_pair(empty_bar(stage), 0x3);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::mma_commit_multicast_pair(tfull_bar(acc), 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      ptx::mma_commit<2>(done_bar);
+      wait_bounded(done_bar, 0, p, kDetailMmaDrain);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------- epilogue --
+    const int q = warp & 3;         // TMEM lane quarter
+    const int g = (warp - 2) >> 2;  // which of the quarter's two warps
+    const bool bf16 = p.bf16 != 0, odd = lane & 1;
+    if (kKind != kGroupedWeight && p.zero_rest && !bad)
+      grouped_zero_rest(p, offsets[0], offsets[p.groups], static_cast<int>(blockIdx.x) * 8 + warp - 2,
+                        static_cast<int>(gridDim.x) * 8, lane);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = walker; t < total; t += p.pairs) {
+      const GroupedTile x = grouped_tile<kKind>(t, p, offsets, first_tile);
+      const bool some = x.slots(p, kKind) > 0;
+      if (some) {
+        int ready = 1;
+        if (lane == 0) ready = wait_bounded<true>(tfull_bar(acc), acc_phase, p, kDetailEpiFull) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, ready, 0)) break;
+        ptx::tc_fence_after_sync();
+      }
+      const uint32_t t_row =
+          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kGroupedCols);
+      const int f = x.lane0 + static_cast<int>(rank) * kBM + q * 32 + lane;  // this lane's feature
+      uint16_t* base = p.out + (kKind == kGroupedWeight ? x.group * p.out_group : 0) + x.row0 * p.ldo;
+      if (x.lane0 + static_cast<int>(rank) * kBM + q * 32 < p.lanes) {
+#pragma unroll 1
+        for (int c = 32 * g; c < x.rows; c += 64) {
+          uint32_t v[32];
+          if (some) {
+            ptx::tmem_ld_32x32b_x32(t_row + c, v);
+            ptx::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0u;
+          }
+          const int left = x.rows - c;
+          if (p.wide) {
+            // Two tokens of one feature a word -> two features of one token: even lanes
+            // store token 2j, odd lanes token 2j + 1.
+            uint16_t* dst = base + (c + (odd ? 1 : 0)) * p.ldo + (f & ~1);
+            const bool in = (f & ~1) < p.lanes;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t w = pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), bf16);
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, w, 1);
+              const uint32_t word = odd ? __byte_perm(got, w, 0x7632) : __byte_perm(w, got, 0x5410);
+              if (in && 2 * j + (odd ? 1 : 0) < left) *reinterpret_cast<uint32_t*>(dst) = word;
+              dst += 2 * p.ldo;
+            }
+          } else {
+            uint16_t* dst = base + c * p.ldo + f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (f < p.lanes && j < left)
+                *dst = static_cast<uint16_t>(pack2(__uint_as_float(v[j]), 0.0f, bf16));
+              dst += p.ldo;
+            }
+          }
+        }
+      }
+      if (!some) continue;
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_shared_rank(tempty_bar(acc), 0));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    __syncwarp();
+  }
+
+  ptx::tc_fence_before_sync();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc<2>(tmem_base, tmem_cols);
+  }
+}
+
+}  // namespace spgemm

@@ -11,6 +11,7 @@
 #include <new>
 
 #include "few_tokens.h"
+#include "grouped_params.h"
 #include "ops_internal.h"
 #include "orthogonal_small.h"
 #include "ptx.cuh"
@@ -66,30 +67,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// A batch of row-major 16-bit matrices as a 3-D map, box `box_cols` x
-// `box_rows` of one matrix, 128-byte swizzle.
-gemm_status_t encode(CUtensorMap* map, bool bf16, const Matrix& m, int64_t batch, uint32_t box_cols,
-                     uint32_t box_rows, CUtensorMapL2promotion l2) {
-  const EncodeTiledFn enc = encode_fn();
-  if (!enc) return ops_fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
-  const int64_t step = batch > 1 ? m.batch_stride : m.rows * m.ld;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
-                              static_cast<cuuint64_t>(batch)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(m.ld) * 2u,
-                                 static_cast<cuuint64_t>(step) * 2u};
-  const cuuint32_t box[3] = {box_cols, box_rows, 1};
-  const cuuint32_t estride[3] = {1, 1, 1};
-  const CUresult r =
-      enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-          const_cast<void*>(m.ptr), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return ops_fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for %lld x %lld x %lld",
-                    static_cast<int>(r), static_cast<long long>(batch),
-                    static_cast<long long>(m.rows), static_cast<long long>(m.cols));
-  return GEMM_OK;
-}
-
 // The bulk-store path needs every row (and matrix) of the output 16-byte
 // aligned.  A bulk store is clipped to whole 16-byte units (loads to single
 // elements), so the output must also own its rows (Matrix::cols) up to the
@@ -135,6 +112,28 @@ size_t block_smem(int cg, int stages, int a_rows) {
 }
 
 }  // namespace
+
+gemm_status_t encode_map(CUtensorMap* map, bool bf16, const Matrix& m, int64_t batch, uint32_t box_cols,
+                     uint32_t box_rows, CUtensorMapL2promotion l2) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return ops_fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const int64_t step = batch > 1 ? m.batch_stride : m.rows * m.ld;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(m.ld) * 2u,
+                                 static_cast<cuuint64_t>(step) * 2u};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r =
+      enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+          const_cast<void*>(m.ptr), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return ops_fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for %lld x %lld x %lld",
+                    static_cast<int>(r), static_cast<long long>(batch),
+                    static_cast<long long>(m.rows), static_cast<long long>(m.cols));
+  return GEMM_OK;
+}
 
 BlockScratch take_scratch(const gemm_ops* ops, Carver& c) {
   BlockScratch s;
@@ -282,17 +281,17 @@ gemm_status_t run_block(const gemm_ops* ops, const BlockProblem& pr, BlockScratc
   const CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   const CUtensorMapL2promotion none = CU_TENSOR_MAP_L2_PROMOTION_NONE;
   const uint32_t b_rows = gated && cg == 1 ? block_bn(1) / 2 : block_bn(cg) / cg;
-  gemm_status_t st = encode(&maps.a, pr.bf16, pr.a, pr.batch, kBK,
+  gemm_status_t st = encode_map(&maps.a, pr.bf16, pr.a, pr.batch, kBK,
                             a_t ? kBK : static_cast<uint32_t>(a_rows), l2);
-  if (st == GEMM_OK) st = encode(&maps.b, pr.bf16, pr.b, pr.batch, kBK, b_n ? kBK : b_rows, l2);
+  if (st == GEMM_OK) st = encode_map(&maps.b, pr.bf16, pr.b, pr.batch, kBK, b_n ? kBK : b_rows, l2);
   Matrix o0 = pr.out0, o1 = pr.out1;
   o0.rows = o1.rows = pr.M;
   o0.cols = o1.cols = pr.N;
   maps.c0 = maps.c1 = maps.d = maps.a;  // valid maps where a product has no such operand
-  if (st == GEMM_OK && p.out0.tma) st = encode(&maps.c0, pr.out_bf16, o0, pr.batch, 64, 32, none);
+  if (st == GEMM_OK && p.out0.tma) st = encode_map(&maps.c0, pr.out_bf16, o0, pr.batch, 64, 32, none);
   if (st == GEMM_OK && p.out1.ptr && p.out1.tma)
-    st = encode(&maps.c1, pr.out_bf16, o1, pr.batch, 64, 32, none);
-  if (st == GEMM_OK && use_d) st = encode(&maps.d, false, pr.d, pr.batch, 64, 32, none);
+    st = encode_map(&maps.c1, pr.out_bf16, o1, pr.batch, 64, 32, none);
+  if (st == GEMM_OK && use_d) st = encode_map(&maps.d, false, pr.d, pr.batch, 64, 32, none);
   if (st != GEMM_OK) return st;
 
   const int grid = static_cast<int>(walkers) * cg;
@@ -347,6 +346,7 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
                    block_set_smem_gated_bwd})
     if (e == cudaSuccess) e = set(ops->smem_optin);
   if (e == cudaSuccess) e = logprobs_set_smem();
+  if (e == cudaSuccess) e = grouped_set_smem(ops->smem_optin);
   if (e == cudaSuccess) e = small_newton_init(ops);
   if (e == cudaSuccess) e = few_tokens_init(ops);
   if (e == cudaSuccess) e = cudaMalloc(&ops->d_status, 4 * sizeof(int));

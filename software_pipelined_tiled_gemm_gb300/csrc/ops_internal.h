@@ -79,6 +79,18 @@ inline bool copyable(const Matrix& m) {
   return (reinterpret_cast<uintptr_t>(m.ptr) & 15u) == 0 && m.ld % 8 == 0;
 }
 
+// A batch of row-major 16-bit matrices as a 3-D map, box `box_cols` x
+// `box_rows` of one matrix, 128-byte swizzle.
+gemm_status_t encode_map(CUtensorMap* map, bool bf16, const Matrix& m, int64_t batch, uint32_t box_cols,
+                         uint32_t box_rows, CUtensorMapL2promotion l2);
+
+// Whether two ranges of bytes share one (NULL or empty ones share none).
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || !na || !nb) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
 // Up to kPackJobs matrices copied to rows of a 16-byte multiple, in one launch.
 constexpr int kPackJobs = 4;
 struct PackJob {

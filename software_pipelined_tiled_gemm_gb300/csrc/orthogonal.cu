@@ -237,11 +237,6 @@ gemm_status_t check(const gemm_orthogonalize_args_t* g) {
   return GEMM_OK;
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
 }  // namespace
 
 extern "C" {

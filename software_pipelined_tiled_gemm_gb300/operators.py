@@ -1,6 +1,7 @@
 """The operators built around the GEMM: the gated feed-forward block with its
-backward pass, the orthogonalised update of a gradient, and the log
-probabilities of tokens with their gradient.
+backward pass, the orthogonalised update of a gradient, the log
+probabilities of tokens with their gradient, and products grouped by expert
+with their gradients.
 
 A thin ctypes binding over ``include/gemm_ops.h``.  As in :func:`matmul_nt`,
 tensors are CUDA tensors, work goes to the current stream of their device,
@@ -20,7 +21,8 @@ import threading
 __all__ = [
     "gated_ffn", "gated_ffn_backward", "GatedKept", "orthogonalize", "check_operators",
     "close_operators", "FfnArgs", "OrthogonalizeArgs", "NEWTON_SCHULZ", "token_logprobs",
-    "token_logprobs_backward", "TokenLogprobs", "LogprobsArgs", "MAX_TOP_K",
+    "token_logprobs_backward", "TokenLogprobs", "LogprobsArgs", "MAX_TOP_K", "grouped_matmul",
+    "grouped_matmul_backward", "GroupedArgs", "MAX_GROUPS",
 ]
 
 _vp, _i64, _ci, _f, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
@@ -56,7 +58,15 @@ class LogprobsArgs(ctypes.Structure):
                 ("d_entropy", _vp), ("d_logits", _vp), ("ldd", _i64), ("lse_low", _vp)]
 
 
-MAX_TOP_K = 64   # GEMM_LOGPROBS_MAX_TOP_K
+class GroupedArgs(ctypes.Structure):
+    """gemm_grouped_args_t"""
+    _fields_ = [("rows", _i64), ("groups", _i64), ("n", _i64), ("k", _i64), ("dtype", _ci),
+                ("offsets", _vp), ("x", _vp), ("ldx", _i64), ("w", _vp), ("y", _vp),
+                ("zero_rest", _ci), ("dy", _vp), ("lddy", _i64), ("dx", _vp), ("dw", _vp)]
+
+
+MAX_TOP_K = 64      # GEMM_LOGPROBS_MAX_TOP_K
+MAX_GROUPS = 4096   # GEMM_GROUPED_MAX_GROUPS
 
 _bound = None
 _handles: dict = {}
@@ -87,7 +97,10 @@ def _lib():
             "gemm_orthogonalize_workspace": [_vp, ctypes.POINTER(OrthogonalizeArgs), psz],
             "gemm_orthogonalize": [_vp, ctypes.POINTER(OrthogonalizeArgs), _vp, _sz, _vp],
             "gemm_token_logprobs": [_vp, ctypes.POINTER(LogprobsArgs), _vp],
-            "gemm_token_logprobs_backward": [_vp, ctypes.POINTER(LogprobsArgs), _vp]}.items():
+            "gemm_token_logprobs_backward": [_vp, ctypes.POINTER(LogprobsArgs), _vp],
+            "gemm_grouped_workspace": [_vp, ctypes.POINTER(GroupedArgs), _ci, psz],
+            "gemm_grouped_run": [_vp, ctypes.POINTER(GroupedArgs), _vp, _sz, _vp],
+            "gemm_grouped_backward": [_vp, ctypes.POINTER(GroupedArgs), _vp, _sz, _vp]}.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, _ci
     lib.gemm_ops_destroy.argtypes, lib.gemm_ops_destroy.restype = [_vp], None
@@ -439,3 +452,82 @@ def token_logprobs_backward(logits, tokens, result, d_logprobs=None, d_entropy=N
         _check(_lib().gemm_token_logprobs_backward(_handle(dev), ctypes.byref(a), stream),
                "gemm_token_logprobs_backward")
     return out
+
+
+# ------------------------------------------------ products grouped by expert --
+
+def _grouped_args(x, w, offsets):
+    import torch
+    device = getattr(x, "device", None)
+    _on_cuda(device, x, "x")
+    _on_cuda(device, w, "w")
+    _on_cuda(device, offsets, "offsets")
+    _lib()
+    code = _sixteen.get(x.dtype)
+    if code is None:
+        raise TypeError("x must be float16 or bfloat16, got %s" % x.dtype)
+    if w.dtype != x.dtype:
+        raise TypeError("x and w must have the same dtype")
+    if w.dim() != 3 or not w.is_contiguous():
+        raise ValueError("w must be a contiguous (groups, n, k) tensor")
+    e, n, k = w.shape
+    if n == 0 or k == 0 or not 1 <= e <= MAX_GROUPS:
+        raise ValueError("w must have 1 to %d groups, and n and k at least 1" % MAX_GROUPS)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    if offsets.dtype != torch.int64:
+        raise TypeError("offsets must be int64, got %s" % offsets.dtype)
+    if offsets.shape != (e + 1,) or not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous, one more than there are groups")
+    rows, ldx = _rows(x, k, "x")
+    return GroupedArgs(rows, e, n, k, code, offsets.data_ptr(), x.data_ptr(), ldx, w.data_ptr(),
+                       lddy=n)
+
+
+def grouped_matmul(x, w, offsets, out=None):
+    """y_r = w[e] x_r for the rows r of each group e, on the current CUDA stream.
+
+    x: (rows, k), float16 or bfloat16, rows contiguous (with any pitch).  w:
+    (groups, n, k), contiguous, of x's dtype: the experts' weights.  offsets:
+    int64 (groups + 1) on the GPU: group e is x[offsets[e]:offsets[e + 1]], any
+    number of rows; it is read there, so nothing synchronises.  Returns y
+    (rows, n) of x's dtype (``out`` if given).
+
+    Rows before the first group and behind the last are not read; in y they
+    are zero, or, where ``out`` is given, left as they were.  Offsets that
+    decrease or leave x are found on the GPU: nothing is then written to y and
+    :func:`check_operators` raises.  No autograd graph, see
+    :func:`grouped_matmul_backward`.
+    """
+    lib = _lib()
+    a = _grouped_args(x, w, offsets)
+    y = _output(out, (a.rows, a.n), x.dtype, x.device)
+    a.y, a.zero_rest = y.data_ptr(), out is None
+    if a.rows:
+        _run("gemm_grouped_run", lib.gemm_grouped_workspace, lib.gemm_grouped_run, a, x.device, 0)
+    return y
+
+
+def grouped_matmul_backward(dy, x, w, offsets, need=(True, True), out=(None, None)):
+    """Gradients (dx, dw) of :func:`grouped_matmul` from dy, with the same x,
+    w and offsets: dx_r = w[e]^T dy_r, dw[e] = sum over its rows of dy_r x_r^T.
+
+    dy: (rows, n), of x's dtype, rows contiguous.  need: which of the two to
+    compute (None in the place of the other).  out: tensors to write them to.
+    Rows of no group are zero in dx (in a given one left as they were) and
+    add nothing to dw, whatever they hold; an empty group's dw is zero.
+    """
+    lib = _lib()
+    a = _grouped_args(x, w, offsets)
+    _on_cuda(x.device, dy, "dy")
+    if dy.dtype != x.dtype or tuple(dy.shape) != (a.rows, a.n):
+        raise ValueError("dy must be (rows, n), of x's dtype")
+    a.dy, a.lddy = dy.data_ptr(), _rows(dy, a.n, "dy")[1]
+    shapes = ((x.shape, "dx"), (w.shape, "dw"))
+    grads = [_output(o, shape, x.dtype, x.device, name) if want else None
+             for want, o, (shape, name) in zip(need, out, shapes)]
+    a.dx, a.dw = map(_ptr, grads)
+    a.zero_rest = out[0] is None
+    if any(need):
+        _run("gemm_grouped_backward", lib.gemm_grouped_workspace, lib.gemm_grouped_backward, a, x.device, 1)
+    return tuple(grads)
