@@ -1,8 +1,9 @@
 /*
  * gemm_ops.h -- C ABI of the operators built around the GEMM (gemm.h): the
  * gated feed-forward block with its backward pass, the orthogonalised update
- * of a gradient, the log probabilities of tokens with their gradient, and
- * products grouped by expert with their gradients.
+ * of a gradient, the log probabilities of tokens with their gradient,
+ * products grouped by expert with their gradients, and layer norm with its
+ * gradients.
  *
  * Sizes vary from call to call (a prompt's length, a batch), so these
  * operators take no plan for a problem: one gemm_ops_t per device holds what
@@ -204,6 +205,41 @@ gemm_status_t gemm_grouped_run(gemm_ops_t* ops, const gemm_grouped_args_t* args,
                                size_t workspace_bytes, void* stream);
 gemm_status_t gemm_grouped_backward(gemm_ops_t* ops, const gemm_grouped_args_t* args,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Layer norm ---------------------------------------------------------------
+ * For each row x (rows x cols), in fp32:
+ *   y = h weight + bias,  h = (x - mean) rstd,  rstd = 1 / sqrt(var + eps)
+ * var being the mean of (x - mean)^2.  The mean is held in two floats, so that
+ * a row far from zero keeps its differences.  A row that holds NaN or an
+ * infinity becomes NaN. */
+typedef struct {
+  int64_t rows, cols;       /* rows >= 0, cols >= 1 */
+  gemm_in_t dtype;          /* of x, y, dy and dx */
+  gemm_in_t weight_dtype;   /* of weight, bias and their gradients: dtype, or GEMM_IN_F32 */
+  const void* x;
+  int64_t ldx;              /* row pitch, elements, >= cols */
+  const void* weight;       /* cols; NULL: ones */
+  const void* bias;         /* cols; NULL: zeros.  Forward only */
+  float eps;                /* >= 0 */
+  void* y;                  /* forward only: rows x cols, dense; may be x itself (ldx == cols) */
+  float* stats;             /* 3 x rows: mean, what its rounding to fp32 lost, rstd.  Written by
+                               the forward pass (NULL: not kept), read by the backward pass */
+  const void* dy;           /* backward only: rows x cols, row pitch lddy */
+  int64_t lddy;
+  void* dx;                 /* rows x cols, dense; may be dy itself (lddy == cols) */
+  void* dweight;            /* cols; each gradient may be NULL */
+  void* dbias;
+} gemm_layer_norm_args_t;
+
+gemm_status_t gemm_layer_norm(gemm_ops_t* ops, const gemm_layer_norm_args_t* args, void* stream);
+
+/* With g = dy weight and <.> the mean of a row:
+ *   dx = rstd (g - <g> - h <g h>),  dweight = sum_rows dy h,  dbias = sum_rows dy
+ * The sums over rows have a fixed order.  With no rows they are zero. */
+gemm_status_t gemm_layer_norm_backward_workspace(gemm_ops_t* ops, const gemm_layer_norm_args_t* args,
+                                                 size_t* bytes);
+gemm_status_t gemm_layer_norm_backward(gemm_ops_t* ops, const gemm_layer_norm_args_t* args,
+                                       void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -134,6 +134,7 @@ struct BlockScratch {
 BlockScratch take_scratch(const gemm_ops* ops, Carver& c);  // enough for any product
 
 cudaError_t logprobs_set_smem();  // logprobs.cu
+cudaError_t layer_norm_set_smem(size_t smem);  // layer_norm.cu
 
 gemm_status_t run_block(const gemm_ops* ops, const BlockProblem& pr, BlockScratch& scratch, cudaStream_t stream);
 

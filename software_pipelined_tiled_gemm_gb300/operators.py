@@ -1,7 +1,7 @@
 """The operators built around the GEMM: the gated feed-forward block with its
 backward pass, the orthogonalised update of a gradient, the log
-probabilities of tokens with their gradient, and products grouped by expert
-with their gradients.
+probabilities of tokens with their gradient, products grouped by expert with
+their gradients, and layer norm with its gradients.
 
 A thin ctypes binding over ``include/gemm_ops.h``.  As in :func:`matmul_nt`,
 tensors are CUDA tensors, work goes to the current stream of their device,
@@ -22,7 +22,8 @@ __all__ = [
     "gated_ffn", "gated_ffn_backward", "GatedKept", "orthogonalize", "check_operators",
     "close_operators", "FfnArgs", "OrthogonalizeArgs", "NEWTON_SCHULZ", "token_logprobs",
     "token_logprobs_backward", "TokenLogprobs", "LogprobsArgs", "MAX_TOP_K", "grouped_matmul",
-    "grouped_matmul_backward", "GroupedArgs", "MAX_GROUPS",
+    "grouped_matmul_backward", "GroupedArgs", "MAX_GROUPS", "layer_norm", "layer_norm_backward",
+    "LayerNormKept", "LayerNormArgs",
 ]
 
 _vp, _i64, _ci, _f, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
@@ -65,6 +66,14 @@ class GroupedArgs(ctypes.Structure):
                 ("zero_rest", _ci), ("dy", _vp), ("lddy", _i64), ("dx", _vp), ("dw", _vp)]
 
 
+class LayerNormArgs(ctypes.Structure):
+    """gemm_layer_norm_args_t"""
+    _fields_ = [("rows", _i64), ("cols", _i64), ("dtype", _ci), ("weight_dtype", _ci), ("x", _vp),
+                ("ldx", _i64), ("weight", _vp), ("bias", _vp), ("eps", _f), ("y", _vp),
+                ("stats", _vp), ("dy", _vp), ("lddy", _i64), ("dx", _vp), ("dweight", _vp),
+                ("dbias", _vp)]
+
+
 MAX_TOP_K = 64      # GEMM_LOGPROBS_MAX_TOP_K
 MAX_GROUPS = 4096   # GEMM_GROUPED_MAX_GROUPS
 
@@ -100,7 +109,10 @@ def _lib():
             "gemm_token_logprobs_backward": [_vp, ctypes.POINTER(LogprobsArgs), _vp],
             "gemm_grouped_workspace": [_vp, ctypes.POINTER(GroupedArgs), _ci, psz],
             "gemm_grouped_run": [_vp, ctypes.POINTER(GroupedArgs), _vp, _sz, _vp],
-            "gemm_grouped_backward": [_vp, ctypes.POINTER(GroupedArgs), _vp, _sz, _vp]}.items():
+            "gemm_grouped_backward": [_vp, ctypes.POINTER(GroupedArgs), _vp, _sz, _vp],
+            "gemm_layer_norm": [_vp, ctypes.POINTER(LayerNormArgs), _vp],
+            "gemm_layer_norm_backward_workspace": [_vp, ctypes.POINTER(LayerNormArgs), psz],
+            "gemm_layer_norm_backward": [_vp, ctypes.POINTER(LayerNormArgs), _vp, _sz, _vp]}.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, _ci
     lib.gemm_ops_destroy.argtypes, lib.gemm_ops_destroy.restype = [_vp], None
@@ -530,4 +542,94 @@ def grouped_matmul_backward(dy, x, w, offsets, need=(True, True), out=(None, Non
     a.zero_rest = out[0] is None
     if any(need):
         _run("gemm_grouped_backward", lib.gemm_grouped_workspace, lib.gemm_grouped_backward, a, x.device, 1)
+    return tuple(grads)
+
+
+# ----------------------------------------------------------------- layer norm --
+
+# What a forward pass keeps for the backward pass: (3, rows) float32, each
+# row's mean, what its rounding to fp32 lost, and 1 / sqrt(var + eps).
+LayerNormKept = collections.namedtuple("LayerNormKept", "stats rows cols dtype")
+
+
+def _layer_norm_args(x, weight, bias):
+    device = getattr(x, "device", None)
+    _on_cuda(device, x, "x")
+    _lib()
+    code = _inputs.get(x.dtype)
+    if code is None:
+        raise TypeError("x must be float32, float16 or bfloat16, got %s" % x.dtype)
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must have at least one column")
+    cols = x.shape[-1]
+    rows, ldx = _rows(x, cols, "x")
+    wcode = code
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        _on_cuda(device, t, name)
+        if t.shape != (cols,) or not t.is_contiguous():
+            raise ValueError("%s must be contiguous, one for each column" % name)
+        if _inputs.get(t.dtype) not in (code, 2):
+            raise TypeError("%s must be of x's dtype or float32, got %s" % (name, t.dtype))
+        wcode = _inputs[t.dtype]
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same dtype")
+    return LayerNormArgs(rows, cols, code, wcode, x.data_ptr(), ldx, _ptr(weight), _ptr(bias))
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, save=False):
+    """y = (x - mean) / sqrt(var + eps) * weight + bias over the last dimension.
+
+    x: (..., cols), float32, float16 or bfloat16, contiguous or a matrix of
+    contiguous rows.  weight, bias: (cols), of x's dtype or float32, or None
+    (ones, zeros).  Returns y of x's shape and dtype (``out`` if given, which
+    may be x itself), or ``(y, kept)`` with ``save=True``, kept being what
+    :func:`layer_norm_backward` needs.  Sums are fp32, and the mean is kept in
+    two parts, so that rows far from zero keep their differences.  No autograd
+    graph, see :func:`layer_norm_backward`.
+    """
+    import torch
+    a = _layer_norm_args(x, weight, bias)
+    if not eps >= 0:
+        raise ValueError("eps must be at least 0")
+    a.eps = eps
+    y = _output(out, x.shape, x.dtype, x.device)
+    a.y = y.data_ptr()
+    kept = None
+    if save:
+        kept = LayerNormKept(torch.empty((3, a.rows), dtype=torch.float32, device=x.device), a.rows, a.cols, x.dtype)
+        a.stats = kept.stats.data_ptr()
+    if a.rows:
+        stream = _stream(x.device)
+        _check(_lib().gemm_layer_norm(_handle(x.device), ctypes.byref(a), stream), "gemm_layer_norm")
+    return (y, kept) if save else y
+
+
+def layer_norm_backward(dy, x, weight, kept, need=(True, True, True), out=(None, None, None)):
+    """Gradients (dx, dweight, dbias) of :func:`layer_norm` from dy and what
+    the forward pass kept, with the same x and weight (None: ones).
+
+    dy: x's shape and dtype, contiguous or a matrix of contiguous rows.
+    dweight and dbias have weight's dtype (x's without a weight).  need: which
+    of the three to compute (None in the place of the others).  out: tensors
+    to write them to; dx may be written over dy.
+    """
+    if not isinstance(kept, LayerNormKept):
+        raise TypeError("kept must come from layer_norm(..., save=True)")
+    lib = _lib()
+    a = _layer_norm_args(x, weight, None)
+    _on_cuda(x.device, dy, "dy")
+    if dy.dtype != x.dtype or dy.shape != x.shape:
+        raise ValueError("dy must have x's shape and dtype")
+    if (a.rows, a.cols, x.dtype) != kept[1:] or kept.stats.device != x.device:
+        raise ValueError("kept belongs to a forward pass of other sizes, dtype or device")
+    a.dy, a.lddy = dy.data_ptr(), _rows(dy, a.cols, "dy")[1]
+    a.stats = kept.stats.data_ptr()
+    wdtype = x.dtype if weight is None else weight.dtype
+    shapes = ((x.shape, x.dtype, "dx"), ((a.cols,), wdtype, "dweight"), ((a.cols,), wdtype, "dbias"))
+    grads = [_output(o, shape, dtype, x.device, name) if want else None
+             for want, o, (shape, dtype, name) in zip(need, out, shapes)]
+    a.dx, a.dweight, a.dbias = map(_ptr, grads)
+    _run("gemm_layer_norm_backward", lib.gemm_layer_norm_backward_workspace, lib.gemm_layer_norm_backward, a, x.device)
     return tuple(grads)
