@@ -2,8 +2,8 @@
  * gemm_ops.h -- C ABI of the operators built around the GEMM (gemm.h): the
  * gated feed-forward block with its backward pass, the orthogonalised update
  * of a gradient, the log probabilities of tokens with their gradient,
- * products grouped by expert with their gradients, and layer norm with its
- * gradients.
+ * products grouped by expert with their gradients, layer norm with its
+ * gradients, and the AdamW step of many tensors.
  *
  * Sizes vary from call to call (a prompt's length, a batch), so these
  * operators take no plan for a problem: one gemm_ops_t per device holds what
@@ -240,6 +240,59 @@ gemm_status_t gemm_layer_norm_backward_workspace(gemm_ops_t* ops, const gemm_lay
                                                  size_t* bytes);
 gemm_status_t gemm_layer_norm_backward(gemm_ops_t* ops, const gemm_layer_norm_args_t* args,
                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- AdamW step ------------------------------------------------------------------
+ * For every element of every tensor, with g = scale grad and t the step's
+ * number (1 for the first), in fp32:
+ *   m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
+ *   p <- p - lr weight_decay p - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * The parameters are updated in place (16-bit ones rounded to nearest), and
+ * `copy` receives them in its type.  The states of all tensors lie in one
+ * buffer each, in the tensors' order, each tensor's beginning at a multiple
+ * of GEMM_ADAMW_BLOCK elements.
+ *   bits 32: m and v in fp32.
+ *   bits 8: in e4m3, times a scale for each block of GEMM_ADAMW_BLOCK elements:
+ *     s = max(2^-120, largest magnitude / 448); m is rounded to nearest.  Of v
+ *     the square root r is held.  It moves by far less than half a step of the
+ *     format in one call, so that rounding to nearest would never let it
+ *     fall: it is rounded down after adding u steps, u = (a j + b t) mod 2^32,
+ *     its upper 20 bits as a fraction (element j of the buffer, a =
+ *     0xC13FA9A9, b = 0x91E10DA5), which over the steps is evenly spread in
+ *     [0, 1); r > 0 is held as 2^-9 s at least.  (A root without gradients
+ *     that beta2 = 0.999 takes to 0.47 in 1500 steps is then at 0.43.)  A NaN
+ *     or an infinity makes its block NaN.
+ * The update itself uses m and v as computed, before they are rounded. */
+#define GEMM_ADAMW_BLOCK 256
+
+typedef struct {
+  void* param;
+  const void* grad;
+  void* copy;               /* or NULL */
+  int64_t numel;            /* >= 0 */
+  int param_type;           /* gemm_in_t, each */
+  int grad_type;
+  int copy_type;            /* GEMM_IN_F16 or GEMM_IN_BF16 */
+  float weight_decay;
+} gemm_adamw_tensor_t;
+
+typedef struct {
+  const gemm_adamw_tensor_t* tensors;  /* on the host; not needed after the call */
+  int64_t count;
+  int bits;                 /* of the states: 32 or 8 */
+  void* exp_avg;            /* fp32 or e4m3, gemm_adamw_state_elements of them, 16-byte aligned */
+  void* exp_avg_sq;
+  float* scales;            /* bits 8: 2 x blocks, of exp_avg and of exp_avg_sq */
+  int64_t* step;            /* on the device: steps made so far; the call adds one */
+  double lr;                /* used where lr_device is NULL */
+  const float* lr_device;
+  double beta1, beta2;      /* in [0, 1) */
+  double eps;               /* >= 0 */
+  const float* scale;       /* on the device; NULL: 1 */
+} gemm_adamw_args_t;
+
+/* Elements of each state buffer. */
+int64_t gemm_adamw_state_elements(const gemm_adamw_tensor_t* tensors, int64_t count);
+gemm_status_t gemm_adamw(gemm_ops_t* ops, const gemm_adamw_args_t* args, void* stream);
 
 #ifdef __cplusplus
 }

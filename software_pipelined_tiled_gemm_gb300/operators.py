@@ -1,7 +1,8 @@
 """The operators built around the GEMM: the gated feed-forward block with its
 backward pass, the orthogonalised update of a gradient, the log
 probabilities of tokens with their gradient, products grouped by expert with
-their gradients, and layer norm with its gradients.
+their gradients, layer norm with its gradients, and the AdamW step of many
+tensors.
 
 A thin ctypes binding over ``include/gemm_ops.h``.  As in :func:`matmul_nt`,
 tensors are CUDA tensors, work goes to the current stream of their device,
@@ -16,6 +17,9 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
+import itertools
+import struct
 import threading
 
 __all__ = [
@@ -23,11 +27,12 @@ __all__ = [
     "close_operators", "FfnArgs", "OrthogonalizeArgs", "NEWTON_SCHULZ", "token_logprobs",
     "token_logprobs_backward", "TokenLogprobs", "LogprobsArgs", "MAX_TOP_K", "grouped_matmul",
     "grouped_matmul_backward", "GroupedArgs", "MAX_GROUPS", "layer_norm", "layer_norm_backward",
-    "LayerNormKept", "LayerNormArgs",
+    "LayerNormKept", "LayerNormArgs", "adamw", "adamw_state", "AdamWState", "AdamWTensor",
+    "AdamWArgs", "ADAMW_BLOCK",
 ]
 
-_vp, _i64, _ci, _f, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
-                           ctypes.c_size_t)
+_vp, _i64, _ci, _f, _sz, _d = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
+                               ctypes.c_size_t, ctypes.c_double)
 
 GEMM_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 1, "relu": 2}
 
@@ -74,6 +79,20 @@ class LayerNormArgs(ctypes.Structure):
                 ("dbias", _vp)]
 
 
+class AdamWTensor(ctypes.Structure):
+    """gemm_adamw_tensor_t"""
+    _fields_ = [("param", _vp), ("grad", _vp), ("copy", _vp), ("numel", _i64), ("param_type", _ci),
+                ("grad_type", _ci), ("copy_type", _ci), ("weight_decay", _f)]
+
+
+class AdamWArgs(ctypes.Structure):
+    """gemm_adamw_args_t"""
+    _fields_ = [("tensors", _vp), ("count", _i64), ("bits", _ci), ("exp_avg", _vp),
+                ("exp_avg_sq", _vp), ("scales", _vp), ("step", _vp), ("lr", _d),
+                ("lr_device", _vp), ("beta1", _d), ("beta2", _d), ("eps", _d), ("scale", _vp)]
+
+
+ADAMW_BLOCK = 256   # GEMM_ADAMW_BLOCK
 MAX_TOP_K = 64      # GEMM_LOGPROBS_MAX_TOP_K
 MAX_GROUPS = 4096   # GEMM_GROUPED_MAX_GROUPS
 
@@ -112,7 +131,8 @@ def _lib():
             "gemm_grouped_backward": [_vp, ctypes.POINTER(GroupedArgs), _vp, _sz, _vp],
             "gemm_layer_norm": [_vp, ctypes.POINTER(LayerNormArgs), _vp],
             "gemm_layer_norm_backward_workspace": [_vp, ctypes.POINTER(LayerNormArgs), psz],
-            "gemm_layer_norm_backward": [_vp, ctypes.POINTER(LayerNormArgs), _vp, _sz, _vp]}.items():
+            "gemm_layer_norm_backward": [_vp, ctypes.POINTER(LayerNormArgs), _vp, _sz, _vp],
+            "gemm_adamw": [_vp, ctypes.POINTER(AdamWArgs), _vp]}.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, _ci
     lib.gemm_ops_destroy.argtypes, lib.gemm_ops_destroy.restype = [_vp], None
@@ -633,3 +653,136 @@ def layer_norm_backward(dy, x, weight, kept, need=(True, True, True), out=(None,
     a.dx, a.dweight, a.dbias = map(_ptr, grads)
     _run("gemm_layer_norm_backward", lib.gemm_layer_norm_backward_workspace, lib.gemm_layer_norm_backward, a, x.device)
     return tuple(grads)
+
+
+# ----------------------------------------------------------------- AdamW step --
+
+# The states of a list of tensors: step, int64 () on the GPU, the steps made so
+# far; exp_avg and exp_avg_sq, one buffer each, every tensor's elements from
+# the next multiple of ADAMW_BLOCK on; scales, None (float32 states) or
+# float32 (2, blocks).  In 8 bits the states are float8_e4m3fn, to be
+# multiplied by their block's scale; exp_avg_sq then holds square roots.
+AdamWState = collections.namedtuple("AdamWState", "step exp_avg exp_avg_sq scales")
+
+
+def adamw_state(params, bits=32):
+    """New (zero) states for :func:`adamw` of these tensors, in 32 or 8 bits."""
+    import torch
+    if bits not in (32, 8):
+        raise ValueError("bits must be 32 or 8")
+    if not params:
+        raise ValueError("params must have at least one tensor")
+    device = getattr(params[0], "device", None)
+    for p in params:
+        _on_cuda(device, p, "params")
+    blocks = sum(-(-p.numel() // ADAMW_BLOCK) for p in params)
+    size = blocks * ADAMW_BLOCK
+
+    def state():
+        return torch.zeros(size, dtype=torch.float32 if bits == 32 else torch.uint8, device=device)
+    m, v = state(), state()
+    scales = None
+    if bits == 8:
+        m, v = m.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn)
+        scales = torch.zeros((2, blocks), dtype=torch.float32, device=device)
+    return AdamWState(torch.zeros((), dtype=torch.int64, device=device), m, v, scales)
+
+
+@functools.lru_cache(maxsize=64)
+def _table(count):
+    """Packs `count` gemm_adamw_tensor_t."""
+    return struct.Struct("=" + "QQQqiiif" * count)
+
+
+def _adamw_list(tensors, name, index, types):
+    """(pointers, type codes, shapes) of a list of tensors."""
+    try:
+        on = [t.get_device() for t in tensors]
+        contiguous = all([t.is_contiguous() for t in tensors])
+        codes = [types.get(t.dtype, -1) for t in tensors]
+    except AttributeError:
+        raise ValueError("%s must be CUDA tensors" % name) from None
+    if on != [index] * len(on):
+        raise ValueError("%s must be CUDA tensors on the same device as the states" % name)
+    if not contiguous:
+        raise ValueError("%s must be contiguous" % name)
+    if -1 in codes:
+        raise TypeError("%s must be %s" % (name, " or ".join(str(t)[6:] for t in types)))
+    return [t.data_ptr() for t in tensors], codes, [t.shape for t in tensors]
+
+
+def adamw(params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None,
+          scale=None):
+    """One AdamW step of many tensors, in place, on the current CUDA stream.
+
+    With g = scale * grad, m <- b1 m + (1 - b1) g, v <- b2 v + (1 - b2) g^2 and
+    p <- p - lr weight_decay p - lr m' / (sqrt(v') + eps), m' and v' being m and
+    v over 1 - b^t; all in fp32.
+
+    params, grads: lists of contiguous tensors, float32, float16 or bfloat16
+    (16-bit parameters are rounded to nearest after every step, so that a step
+    below half of their last bit is lost).  state: :func:`adamw_state` of
+    these params; its step is on the GPU and counted there.  lr: a number, or
+    a float32 tensor () on the GPU.  weight_decay: a number, or one for each
+    tensor.  copies: 16-bit tensors that receive the new parameters, or None
+    in the place of one or of all.  scale: float32 tensor () on the GPU that
+    every gradient is multiplied by (1 / loss scale, or that of a clipped
+    norm); None: 1.  Nothing may overlap what is written.
+
+    In 8 bits each block of ADAMW_BLOCK elements has a scale, its largest
+    magnitude over 448.  m is rounded to nearest; sqrt(v), which moves by less
+    than half a step of the format, up or down, in turns that are spread
+    evenly over the steps (so results repeat bit for bit), and never to 0.
+    NaN or an infinity makes its whole block NaN.  Elements of the buffers
+    between tensors become zero.
+    """
+    import torch
+    lib = _lib()
+    step, m, v, scales = state
+    _on_cuda(getattr(step, "device", None), step, "state")
+    device = step.device
+    n = len(params)
+    if len(grads) != n or (copies is not None and len(copies) != n):
+        raise ValueError("params, grads and copies must have the same length")
+    index = device.index
+    p_at, p_type, shapes = _adamw_list(params, "params", index, _inputs)
+    g_at, g_type, g_shapes = _adamw_list(grads, "grads", index, _inputs)
+    if shapes != g_shapes:
+        raise ValueError("grads must have the shapes of params")
+    c_at, c_type = itertools.repeat(0), itertools.repeat(0)
+    if copies is not None:
+        there = [i for i, c in enumerate(copies) if c is not None]
+        at, codes, c_shapes = _adamw_list([copies[i] for i in there], "copies", index, _sixteen)
+        if c_shapes != [shapes[i] for i in there]:
+            raise ValueError("copies must have the shapes of params")
+        c_at, c_type = [0] * n, [0] * n
+        for i, a, c in zip(there, at, codes):
+            c_at[i], c_type[i] = a, c
+    decay = itertools.repeat(float(weight_decay)) if isinstance(weight_decay, (int, float)) else weight_decay
+    if not isinstance(decay, itertools.repeat) and len(decay) != n:
+        raise ValueError("weight_decay must be a number, or one for each tensor")
+    sizes = [s.numel() for s in shapes]
+    blocks = sum([(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes])
+    if scales is None:
+        want = ((m, torch.float32, (blocks * ADAMW_BLOCK,)), (v, torch.float32, (blocks * ADAMW_BLOCK,)))
+    else:
+        want = ((m, torch.float8_e4m3fn, (blocks * ADAMW_BLOCK,)), (v, torch.float8_e4m3fn, (blocks * ADAMW_BLOCK,)),
+                (scales, torch.float32, (2, blocks)))
+    for t, dtype, shape in want + ((step, torch.int64, ()),):
+        _on_cuda(device, t, "state")
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError("state belongs to other tensors (see adamw_state)")
+    rate = None
+    if isinstance(lr, torch.Tensor):
+        rate, lr = lr, 0.0
+    for t, name in ((rate, "lr"), (scale, "scale")):
+        if t is not None:
+            _on_cuda(device, t, name)
+            if t.dtype != torch.float32 or t.numel() != 1:
+                raise ValueError("%s must be one float32" % name)
+    table = _table(n).pack(*itertools.chain.from_iterable(
+        zip(p_at, g_at, c_at, sizes, p_type, g_type, c_type, decay)))
+    a = AdamWArgs(ctypes.cast(table, _vp), n, 32 if scales is None else 8, m.data_ptr(), v.data_ptr(), _ptr(scales),
+                  step.data_ptr(), lr, _ptr(rate), betas[0], betas[1], eps, _ptr(scale))
+    stream = _stream(device)
+    _check(lib.gemm_adamw(_handle(device), ctypes.byref(a), stream), "gemm_adamw")
