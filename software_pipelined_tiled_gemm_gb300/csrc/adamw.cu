@@ -7,9 +7,14 @@
 //
 // The states of 256 neighbouring elements are a block; a warp takes a block at
 // a time, a lane eight elements, so a block's largest magnitude takes one
-// reduction instruction and no shared memory.  The elements of a lane lie
-// side by side where the tensor's addresses allow 16-byte vectors, and are
-// read one by one elsewhere and in a tensor's last block.
+// reduction instruction.  A thread block has a chunk of one tensor, whose
+// addresses are found once; its warps fetch their next blocks to shared memory
+// while they compute.  Tensors whose addresses allow no 16-byte vectors, and a
+// tensor's last block, are read element by element.
+//
+// With 8-bit states the arithmetic (some 400 instructions a lane and block,
+// a fifth of them for square roots in full precision) takes about as long as
+// the memory, so it is done on pairs of values where it can be.
 //
 // 8 bits: e4m3 times the block's scale, the average's and the second moment's
 // root's.  The root (not v) halves the range of exponents that the format has
@@ -25,6 +30,7 @@
 #include <vector>
 
 #include "ops_internal.h"
+#include "packed_f32.cuh"
 #include "ptx.cuh"
 
 using namespace spgemm;
@@ -33,7 +39,15 @@ namespace {
 
 constexpr int kBlock = GEMM_ADAMW_BLOCK;
 constexpr int kEach = 8;                 // elements of a lane: 32 lanes, one block
+constexpr int kPairs = kEach / 2;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+// Blocks of a warp on their way or in work, thread blocks of an SM, and
+// blocks of a warp in a chunk at most.  Measured, in us (252 M elements with
+// 8-bit states; 106 M with 32-bit ones):
+//   8 bits    3, 3 and 1 / 3 / 4 / 5 / 8:  816 / 612 / 605 / 704 / 697;  2, 4 and 4: 632;  4, 2 and 16: 642
+//   32 bits   2, 4 and 2: 429;  2, 3 and 2 / 3 / 4: 430 / 435 / 440;  1, 4 and 2 / 4: 437 / 450;  3, 2 and 4: 433
+constexpr int kSlots8 = 3, kOcc8 = 3, kMostEach8 = 4;
+constexpr int kSlots32 = 2, kOcc32 = 4, kMostEach32 = 2;
 // Types of an entry: parameter, gradient, copy (3: none), two bits each, and
 // whether its addresses allow vectors.
 constexpr uint32_t kNoCopy = 3u, kVectors = 1u << 6;
@@ -44,7 +58,7 @@ struct Entry {
   void* copy;
   int64_t numel;
   int64_t state;         // first element of the states
-  uint32_t first_block;  // of this launch
+  uint32_t first_chunk;  // of this launch
   uint32_t kinds;
   float decay;           // weight decay
 };
@@ -56,7 +70,7 @@ template <int kTensors>
 struct Job {
   Entry entry[kTensors];
   int count;
-  uint32_t blocks;
+  uint32_t chunk;         // blocks of a thread block, all of one tensor
   void* exp_avg;
   void* exp_avg_sq;
   float* scales;          // of exp_avg, then (scale_step later) of exp_avg_sq
@@ -64,41 +78,44 @@ struct Job {
   const int64_t* step;
   const float* lr_device;
   const float* scale;
-  float lr, beta1, beta2, one_less1, one_less2, ln_beta1, ln_beta2, eps;
+  float lr, beta1, beta2, one_less1, one_less2, ln_beta1, ln_beta2, eps, one;
 };
 
-// Eight fp32 values from fp16, bf16 or fp32 at p.
-__device__ __forceinline__ void load8(const void* p, uint32_t kind, float (&v)[kEach]) {
+// Eight fp32 values, in pairs, from fp16, bf16 or fp32 at p.
+__device__ __forceinline__ void load8(const void* p, uint32_t kind, F32x2 (&v)[kPairs]) {
   if (kind == GEMM_IN_F32) {
-    const float4 a = __ldcs(static_cast<const float4*>(p)), b = __ldcs(static_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    const ulonglong2 a = static_cast<const ulonglong2*>(p)[0], b = static_cast<const ulonglong2*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     return;
   }
-  const uint4 raw = __ldcs(static_cast<const uint4*>(p));
+  const uint4 raw = *static_cast<const uint4*>(p);
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = kind == GEMM_IN_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]))
-                                          : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+  for (int i = 0; i < kPairs; ++i) {
+    if (kind == GEMM_IN_BF16) {  // a bf16 is the upper half of its fp32
+      v[i] = pack_f32(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[i] = pack_f32(f.x, f.y);
+    }
   }
 }
 
-__device__ __forceinline__ void store8(void* p, uint32_t kind, const float (&v)[kEach]) {
+__device__ __forceinline__ void store8(void* p, uint32_t kind, const F32x2 (&v)[kPairs]) {
   if (kind == GEMM_IN_F32) {
-    __stcs(static_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(static_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    __stcs(static_cast<ulonglong2*>(p), make_ulonglong2(v[0], v[1]));
+    __stcs(static_cast<ulonglong2*>(p) + 1, make_ulonglong2(v[2], v[3]));
     return;
   }
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPairs; ++i) {
+    const float2 f = unpack_f32(v[i]);
     if (kind == GEMM_IN_BF16) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
       memcpy(&w[i], &h, 4);
     } else {
-      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      const __half2 h = __floats2half2_rn(f.x, f.y);
       memcpy(&w[i], &h, 4);
     }
   }
@@ -129,24 +146,40 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
   return __half22float2(__half2(h));
 }
 
-// The e4m3 code of y in [0, 448] rounded down after adding u 2^-20 steps.  A
-// normal value's step is 2^20 units of its fp32 bits, so the sum of the bits
-// and u carries into the next code by itself; below 2^-6 the step is 2^-9.
-__device__ __forceinline__ uint32_t e4m3_dithered(float y, uint32_t u) {
-  if (y < 0.015625f) return static_cast<uint32_t>(fmaf(y, 512.0f, static_cast<float>(u) * 9.5367431640625e-07f));
-  return ((__float_as_uint(y) + u) >> 20) - 960u;
+// The largest magnitude of three values, NaN if one is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) { return fminf(fminf(a, b), c); }
+
+// 1 / x to one unit in the last place; x is 0 or normal (a sum of eps and a
+// square root of an fp32 number).
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// Largest of non-negative floats over the warp, NaN above all: their order is that of their bits.
-__device__ __forceinline__ float warp_max(float v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))); }
+// Four e4m3 codes of y rounded down after adding u 2^-20 steps, from s = the
+// bits of 2^-120 y as fp32, plus u.  With that factor fp32's exponent is
+// e4m3's, and the fp32 numbers below its normal range are e4m3's below its
+// own: in both a step of the code is 2^20 units of the bits, so the sum's
+// upper bits are the code.  (Only the largest, 448 plus rounding, can carry
+// into the code of NaN, from which it is taken back.)
+__device__ __forceinline__ uint32_t dithered_codes(uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3) {
+  const uint32_t w = (s0 >> 20) | (s1 >> 20) << 8 | (s2 >> 20) << 16 | (s3 >> 20) << 24;
+  return w - (((w + 0x01010101u) & 0x80808080u) >> 7);
+}
 
-// Entry of block b: the last whose first block is not after it.
+// Entry of chunk c: the last whose first chunk is not after it.
 template <typename J>
-__device__ __forceinline__ int find_entry(const J& job, uint32_t b) {
+__device__ __forceinline__ int find_entry(const J& job, uint32_t c) {
   int lo = 0, hi = job.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (job.entry[mid].first_block <= b)
+    if (job.entry[mid].first_chunk <= c)
       lo = mid;
     else
       hi = mid;
@@ -154,119 +187,246 @@ __device__ __forceinline__ int find_entry(const J& job, uint32_t b) {
   return lo;
 }
 
-template <int kBits, int kTensors>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Job<kTensors> job) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (b >= job.blocks) return;
-  const Entry& e = job.entry[find_entry(job, b)];
-  const int64_t at = static_cast<int64_t>(b - e.first_block) * kBlock + lane * kEach;  // in the tensor
-  const int64_t state = e.state + at;
-  const uint32_t kp = e.kinds & 3u, kg = (e.kinds >> 2) & 3u, kc = (e.kinds >> 4) & 3u;
-  const int left = static_cast<int>(min(static_cast<int64_t>(kEach), e.numel - at));  // may be negative
-  // A tensor's last block may end inside: elements that do not exist count as zeros, and
-  // so do their states, which are written all the same (they are the buffer's own).
-  const bool whole = (e.kinds & kVectors) != 0 && left == kEach;
-  const int psize = kp == GEMM_IN_F32 ? 4 : 2, gsize = kg == GEMM_IN_F32 ? 4 : 2;
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem), "l"(src) : "memory");
+}
 
-  float p[kEach], g[kEach], m[kEach], v[kEach];
-  if (whole) {
-    load8(static_cast<const uint8_t*>(e.param) + at * psize, kp, p);
-    load8(static_cast<const uint8_t*>(e.grad) + at * gsize, kg, g);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      p[i] = i < left ? load1(e.param, kp, at + i) : 0.0f;
-      g[i] = i < left ? load1(e.grad, kg, at + i) : 0.0f;
+// A warp's ring: the blocks that it works on next are on their way while it
+// works on one.  Of a block: parameters and gradients (1 KiB each where they
+// are fp32), the two states, their scales.
+template <int kBits>
+struct Ring {
+  static constexpr uint32_t kState = kBlock * kBits / 8;
+  static constexpr uint32_t kGrad = 1024u, kM = 2048u, kV = kM + kState, kScales = kV + kState;
+  static constexpr uint32_t kSlot = kScales + (kBits == 8 ? 16u : 0u);
+  static constexpr int kSlots = kBits == 8 ? kSlots8 : kSlots32;
+  static constexpr size_t kBytes = static_cast<size_t>(kWarps) * kSlots * kSlot;
+};
+
+template <int kBits, int kTensors>
+__global__ void __launch_bounds__(kThreads, kBits == 8 ? kOcc8 : kOcc32) adamw_kernel(const __grid_constant__ Job<kTensors> job) {
+  using R = Ring<kBits>;
+  extern __shared__ __align__(16) uint8_t ring[];
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Entry& e = job.entry[find_entry(job, blockIdx.x)];
+  const uint32_t kp = e.kinds & 3u, kg = (e.kinds >> 2) & 3u, kc = (e.kinds >> 4) & 3u;
+  const int psize = kp == GEMM_IN_F32 ? 4 : 2, gsize = kg == GEMM_IN_F32 ? 4 : 2;
+  // This warp's blocks: every eighth of the chunk.
+  const int64_t first = static_cast<int64_t>(blockIdx.x - e.first_chunk) * job.chunk + warp;
+  const int64_t blocks = (e.numel + kBlock - 1) / kBlock;  // of the tensor
+  const int count = static_cast<int>(min(static_cast<int64_t>(job.chunk - warp + kWarps - 1), blocks - first + kWarps - 1)) / kWarps;
+  // Of those, the ones that are all the tensor's and whose addresses allow vectors.
+  const int whole = (e.kinds & kVectors) == 0 ? 0 : first + static_cast<int64_t>(count - 1) * kWarps < e.numel / kBlock ? count : count - 1;
+  uint8_t* mine = ring + warp * (R::kSlots * R::kSlot);
+
+  const int64_t at0 = first * kBlock, state0 = e.state + at0;
+  const uint8_t* from_p = static_cast<const uint8_t*>(e.param) + at0 * psize + lane * 16;
+  const uint8_t* from_g = static_cast<const uint8_t*>(e.grad) + at0 * gsize + lane * 16;
+  const uint8_t* from_m = static_cast<const uint8_t*>(job.exp_avg) + state0 * (kBits / 8) + lane * 16;
+  const uint8_t* from_v = static_cast<const uint8_t*>(job.exp_avg_sq) + state0 * (kBits / 8) + lane * 16;
+  if (kBits == 8 && lane >= 16) from_m = from_v - 256;
+  const float* from_s = kBits == 8 ? job.scales + (lane & 1) * job.scale_step + state0 / kBlock : nullptr;
+  auto fetch = [&](int i, int slot) {
+    if (i < whole) {
+      const uint32_t to = ptx::smem_addr(mine + slot * R::kSlot) + lane * 16;
+      const int64_t skip = static_cast<int64_t>(i) * (kWarps * kBlock);
+      copy_async16(to, from_p + skip * psize);
+      if (kp == GEMM_IN_F32) copy_async16(to + 512, from_p + skip * 4 + 512);
+      copy_async16(to + R::kGrad, from_g + skip * gsize);
+      if (kg == GEMM_IN_F32) copy_async16(to + R::kGrad + 512, from_g + skip * 4 + 512);
+      if constexpr (kBits == 32) {
+        copy_async16(to + R::kM, from_m + skip * 4);
+        copy_async16(to + R::kM + 512, from_m + skip * 4 + 512);
+        copy_async16(to + R::kV, from_v + skip * 4);
+        copy_async16(to + R::kV + 512, from_v + skip * 4 + 512);
+      } else {
+        copy_async16(to + R::kM, from_m + skip);  // m, and v by the upper lanes
+        if (lane < 2) copy_async4(to + R::kScales - lane * 12, from_s + i * kWarps);
+      }
     }
-  }
-  const int64_t scale_at = state / kBlock;
-  if constexpr (kBits == 32) {
-    load8(static_cast<const float*>(job.exp_avg) + state, GEMM_IN_F32, m);
-    load8(static_cast<const float*>(job.exp_avg_sq) + state, GEMM_IN_F32, v);
-  } else {
-    const uint2 cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(job.exp_avg) + state));
-    const uint2 cv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(job.exp_avg_sq) + state));
-    const float sm = job.scales[scale_at], sv = job.scales[job.scale_step + scale_at];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t wm = i < 2 ? cm.x : cm.y, wv = i < 2 ? cv.x : cv.y;
-      const float2 fm = from_e4m3x2((wm >> (16 * (i & 1))) & 0xffffu), fv = from_e4m3x2((wv >> (16 * (i & 1))) & 0xffffu);
-      m[2 * i] = fm.x * sm;
-      m[2 * i + 1] = fm.y * sm;
-      v[2 * i] = (fv.x * sv) * (fv.x * sv);
-      v[2 * i + 1] = (fv.y * sv) * (fv.y * sv);
-    }
-  }
+  for (int i = 0; i < R::kSlots - 1; ++i) fetch(i, i);
+
   // 1 - beta^t = -expm1(t ln beta), which keeps its bits where beta^t is near 1.
   const int64_t t = *job.step + 1;
   const float lr = job.lr_device ? *job.lr_device : job.lr;
   const float factor = job.scale ? *job.scale : 1.0f;
   const float rate = lr / -expm1f(static_cast<float>(t) * job.ln_beta1);
   const float unbias = rsqrtf(-expm1f(static_cast<float>(t) * job.ln_beta2));
-  const float decay = lr * e.decay;
-  float r[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    g[i] *= factor;
-    m[i] = fmaf(job.beta1, m[i], job.one_less1 * g[i]);
-    v[i] = fmaf(job.beta2, v[i], job.one_less2 * (g[i] * g[i]));
-    r[i] = __fsqrt_rn(v[i]);
-    // (The quotient is within 2 units of its last place, and p is larger.)
-    p[i] = (p[i] - decay * p[i]) - rate * __fdividef(m[i], fmaf(r[i], unbias, job.eps));
-  }
-  if (whole) {
-    store8(static_cast<uint8_t*>(e.param) + at * psize, kp, p);
-    if (kc != kNoCopy) store8(static_cast<uint16_t*>(e.copy) + at, kc, p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (i < left) {
-        store1(e.param, kp, at + i, p[i]);
-        if (kc != kNoCopy) store1(e.copy, kc, at + i, p[i]);
+  const F32x2 keep = both_f32(-lr * e.decay), step_size = both_f32(-rate), unbiases = both_f32(unbias);
+  const F32x2 factors = both_f32(factor), beta1 = both_f32(job.beta1), beta2 = both_f32(job.beta2);
+  const F32x2 less1 = both_f32(job.one_less1), less2 = both_f32(job.one_less2), eps = both_f32(job.eps);
+  // A sum below is the product with a one that the assembler does not know, plus the rest:
+  // it merges a packed product and the packed sum that follows into one rounding.
+  const F32x2 one = both_f32(job.one);
+  int slot = 0;
+  for (int n = 0; n < count; ++n) {
+    fetch(n + R::kSlots - 1, slot == 0 ? R::kSlots - 1 : slot - 1);
+    const int64_t at = at0 + static_cast<int64_t>(n) * (kWarps * kBlock) + lane * kEach;  // in the tensor
+    const int64_t state = e.state + at;
+    F32x2 p[kPairs], g[kPairs], m[kPairs], v[kPairs];
+    uint2 cm, cv;
+    float sm_old, sv_old;
+    int left = kEach;  // elements that exist
+    if (n < whole) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(R::kSlots - 1) : "memory");
+      __syncwarp();  // lanes read what others copied
+      const uint8_t* from = mine + slot * R::kSlot;
+      load8(from + lane * kEach * psize, kp, p);
+      load8(from + R::kGrad + lane * kEach * gsize, kg, g);
+      if constexpr (kBits == 32) {
+        load8(from + R::kM + lane * 32, GEMM_IN_F32, m);
+        load8(from + R::kV + lane * 32, GEMM_IN_F32, v);
       } else {
-        m[i] = v[i] = r[i] = 0.0f;
+        cm = *reinterpret_cast<const uint2*>(from + R::kM + lane * 8);
+        cv = *reinterpret_cast<const uint2*>(from + R::kV + lane * 8);
+        const float2 s = *reinterpret_cast<const float2*>(from + R::kScales);
+        sm_old = s.x;
+        sv_old = s.y;
       }
-  }
-  if constexpr (kBits == 32) {
-    store8(static_cast<float*>(job.exp_avg) + state, GEMM_IN_F32, m);
-    store8(static_cast<float*>(job.exp_avg_sq) + state, GEMM_IN_F32, v);
-  } else {
-    float top_m = 0.0f, top_r = 0.0f;
+      __syncwarp();  // before the slot is filled again
+    } else {
+      // A tensor's last block may end inside: elements that do not exist count as zeros, and
+      // so do their states, which are written all the same (they are the buffer's own).
+      left = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(kEach), e.numel - at)));
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      top_m = __uint_as_float(max(__float_as_uint(top_m), __float_as_uint(fabsf(m[i]))));
-      top_r = __uint_as_float(max(__float_as_uint(top_r), __float_as_uint(r[i])));
+      for (int i = 0; i < kPairs; ++i) {
+        const int j = 2 * i;
+        p[i] = pack_f32(j < left ? load1(e.param, kp, at + j) : 0.0f, j + 1 < left ? load1(e.param, kp, at + j + 1) : 0.0f);
+        g[i] = pack_f32(j < left ? load1(e.grad, kg, at + j) : 0.0f, j + 1 < left ? load1(e.grad, kg, at + j + 1) : 0.0f);
+      }
+      if constexpr (kBits == 32) {
+        load8(static_cast<const float*>(job.exp_avg) + state, GEMM_IN_F32, m);
+        load8(static_cast<const float*>(job.exp_avg_sq) + state, GEMM_IN_F32, v);
+      } else {
+        cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(job.exp_avg) + state);
+        cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(job.exp_avg_sq) + state);
+        sm_old = job.scales[state / kBlock];
+        sv_old = job.scales[job.scale_step + state / kBlock];
+      }
     }
-    top_m = warp_max(top_m);
-    top_r = warp_max(top_r);
-    // (A NaN stays one: it is larger than 2^-120 as bits.)
-    const uint32_t least = 0x03800000u;  // 2^-120
-    const float sm = __uint_as_float(max(__float_as_uint(__fdiv_rn(top_m, 448.0f)), least));
-    const float sv = __uint_as_float(max(__float_as_uint(__fdiv_rn(top_r, 448.0f)), least));
-    const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
-    const uint32_t lost = sv <= 3.4028235e38f ? 0u : 0x7fu;  // an infinite or NaN root: all of the block NaN
-    uint32_t wm[2] = {0u, 0u}, wv[2] = {0u, 0u};
-    const uint32_t dither = static_cast<uint32_t>(state) * 0xC13FA9A9u + static_cast<uint32_t>(t) * 0x91E10DA5u;
+    slot = slot == R::kSlots - 1 ? 0 : slot + 1;
+    if constexpr (kBits == 8) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const float y = fminf(r[i] * iv, 448.0f);
-      uint32_t code = e4m3_dithered(y, (dither + static_cast<uint32_t>(i) * 0xC13FA9A9u) >> 12);
-      if (r[i] > 0.0f) code = max(code, 1u);
-      wv[i >> 2] |= (code | lost) << (8 * (i & 3));
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 fm = from_e4m3x2((i < 2 ? cm.x : cm.y) >> (16 * (i & 1)));
+        const float2 fv = from_e4m3x2((i < 2 ? cv.x : cv.y) >> (16 * (i & 1)));
+        m[i] = mul_f32x2(pack_f32(fm.x, fm.y), both_f32(sm_old));
+        const F32x2 r = mul_f32x2(pack_f32(fv.x, fv.y), both_f32(sv_old));
+        v[i] = mul_f32x2(r, r);
+      }
     }
+    // Each operation on the states is rounded by itself (no fused multiply-add):
+    // whoever evaluates the formulas in fp32 step by step gets the same bits,
+    // and in 8 bits, where a last bit can decide a code, the same codes.
+    float r[kEach];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wm[i >> 1] |= e4m3x2(m[2 * i] * im, m[2 * i + 1] * im) << (16 * (i & 1));
-    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(job.exp_avg) + state), make_uint2(wm[0], wm[1]));
-    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(job.exp_avg_sq) + state), make_uint2(wv[0], wv[1]));
-    if (lane == 0) {
-      job.scales[scale_at] = sm;
-      job.scales[job.scale_step + scale_at] = sv;
+    for (int i = 0; i < kPairs; ++i) {
+      g[i] = mul_f32x2(g[i], factors);
+      m[i] = fma_f32x2(mul_f32x2(beta1, m[i]), one, mul_f32x2(less1, g[i]));
+      v[i] = fma_f32x2(mul_f32x2(beta2, v[i]), one, mul_f32x2(less2, mul_f32x2(g[i], g[i])));
+      const float2 vi = unpack_f32(v[i]);
+      r[2 * i] = __fsqrt_rn(vi.x);
+      r[2 * i + 1] = __fsqrt_rn(vi.y);
+      const float2 d = unpack_f32(fma_f32x2(pack_f32(r[2 * i], r[2 * i + 1]), unbiases, eps));
+      // (The quotient is within 2 units of its last place, and p is larger.)
+      const F32x2 q = mul_f32x2(m[i], pack_f32(reciprocal(d.x), reciprocal(d.y)));
+      p[i] = fma_f32x2(step_size, q, fma_f32x2(keep, p[i], p[i]));
+    }
+    if (n < whole) {
+      store8(static_cast<uint8_t*>(e.param) + at * psize, kp, p);
+      if (kc != kNoCopy) store8(static_cast<uint16_t*>(e.copy) + at, kc, p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const float2 pi = unpack_f32(p[i / 2]);
+        if (i < left) {
+          store1(e.param, kp, at + i, i % 2 ? pi.y : pi.x);
+          if (kc != kNoCopy) store1(e.copy, kc, at + i, i % 2 ? pi.y : pi.x);
+        } else {
+          float2 mi = unpack_f32(m[i / 2]), vi = unpack_f32(v[i / 2]);
+          (i % 2 ? mi.y : mi.x) = 0.0f;
+          (i % 2 ? vi.y : vi.x) = 0.0f;
+          m[i / 2] = pack_f32(mi.x, mi.y);
+          v[i / 2] = pack_f32(vi.x, vi.y);
+          r[i] = 0.0f;
+        }
+      }
+    }
+    if constexpr (kBits == 32) {
+      store8(static_cast<float*>(job.exp_avg) + state, GEMM_IN_F32, m);
+      store8(static_cast<float*>(job.exp_avg_sq) + state, GEMM_IN_F32, v);
+    } else {
+      float top_m = 0.0f, top_r = 0.0f, least_r = r[0];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 mi = unpack_f32(m[i]);
+        top_m = max3_abs(top_m, mi.x, mi.y);
+        top_r = max3_abs(top_r, r[2 * i], r[2 * i + 1]);
+        least_r = min3(least_r, r[2 * i], r[2 * i + 1]);
+      }
+      // Magnitudes order as their bits, NaN above all.
+      const uint32_t bm = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m) & 0x7fffffffu);
+      const uint32_t br = __reduce_max_sync(0xffffffffu, __float_as_uint(top_r) & 0x7fffffffu);
+      constexpr float kLeast = 7.52316384526264e-37f;  // 2^-120
+      const float sm = bm <= 0x7f800000u ? fmaxf(__fmul_rn(__uint_as_float(bm), 1.0f / 448.0f), kLeast) : __uint_as_float(bm);
+      const float sv = br <= 0x7f800000u ? fmaxf(__fmul_rn(__uint_as_float(br), 1.0f / 448.0f), kLeast) : __uint_as_float(br);
+      const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
+      const F32x2 ims = both_f32(im), ivs = both_f32(iv), down = both_f32(kLeast);
+      const uint32_t dither = static_cast<uint32_t>(state) * 0xC13FA9A9u + static_cast<uint32_t>(t) * 0x91E10DA5u;
+      uint32_t wm[2] = {0u, 0u}, s[kEach];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 y = unpack_f32(mul_f32x2(mul_f32x2(pack_f32(r[2 * i], r[2 * i + 1]), ivs), down));
+        s[2 * i] = __float_as_uint(y.x) + ((dither + static_cast<uint32_t>(2 * i) * 0xC13FA9A9u) >> 12);
+        s[2 * i + 1] = __float_as_uint(y.y) + ((dither + static_cast<uint32_t>(2 * i + 1) * 0xC13FA9A9u) >> 12);
+        const float2 mi = unpack_f32(mul_f32x2(m[i], ims));
+        wm[i >> 1] |= e4m3x2(mi.x, mi.y) << (16 * (i & 1));
+      }
+      // Nothing but 0 becomes 0: a root below a step of the smallest codes, 2^-9 sv.
+      if (least_r * iv < 0.001953125f) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) s[i] = r[i] > 0.0f ? max(s[i], 1u << 20) : 0u;
+      }
+      uint32_t wv[2] = {dithered_codes(s[0], s[1], s[2], s[3]), dithered_codes(s[4], s[5], s[6], s[7])};
+      if (!(sv <= 3.4028235e38f)) wv[0] = wv[1] = 0x7f7f7f7fu;  // an infinite or NaN root: all of the block NaN
+      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(job.exp_avg) + state), make_uint2(wm[0], wm[1]));
+      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(job.exp_avg_sq) + state), make_uint2(wv[0], wv[1]));
+      if (lane == 0) {
+        __stcs(job.scales + state / kBlock, sm);
+        __stcs(job.scales + job.scale_step + state / kBlock, sv);
+      }
     }
   }
 }
 
-__global__ void count_kernel(int64_t* step) { *step += 1; }
+__global__ void count_kernel(int64_t* step) {
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  *step += 1;
+}
+
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), unsigned blocks, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 int64_t padded(int64_t n) { return (n + kBlock - 1) / kBlock * kBlock; }
 
@@ -346,10 +506,15 @@ gemm_status_t check_overlap(const gemm_adamw_args_t* a) {
 }
 
 template <int kBits, int kTensors>
-cudaError_t run(const gemm_adamw_args_t* a, int64_t first, int64_t count, int64_t state, int64_t total, cudaStream_t stream) {
+cudaError_t run(const gemm_ops* ops, const gemm_adamw_args_t* a, int64_t first, int64_t count, int64_t state, int64_t total, cudaStream_t stream) {
   Job<kTensors> job;
   job.count = 0;
-  uint64_t blocks = 0;
+  // Chunks of eight blocks (one a warp), longer ones where there are many: a
+  // chunk's first loads are waited for.
+  uint64_t blocks = 0, chunks = 0;
+  for (int64_t i = first; i < first + count; ++i) blocks += static_cast<uint64_t>(padded(a->tensors[i].numel) / kBlock);
+  const uint64_t resident = static_cast<uint64_t>(ops->sm_count) * (kBits == 8 ? kOcc8 : kOcc32);
+  job.chunk = static_cast<uint32_t>(kWarps * std::max<uint64_t>(1, std::min<uint64_t>(kBits == 8 ? kMostEach8 : kMostEach32, blocks / (kWarps * 4 * resident))));
   for (int64_t i = first; i < first + count; ++i) {
     const gemm_adamw_tensor_t& t = a->tensors[i];
     if (t.numel == 0) continue;
@@ -359,17 +524,16 @@ cudaError_t run(const gemm_adamw_args_t* a, int64_t first, int64_t count, int64_
     e.copy = t.copy;
     e.numel = t.numel;
     e.state = state;
-    e.first_block = static_cast<uint32_t>(blocks);
+    e.first_chunk = static_cast<uint32_t>(chunks);
     e.kinds = static_cast<uint32_t>(t.param_type) | static_cast<uint32_t>(t.grad_type) << 2 |
               (t.copy ? static_cast<uint32_t>(t.copy_type) : kNoCopy) << 4;
     if (((reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad) | reinterpret_cast<uintptr_t>(t.copy)) & 15u) == 0)
       e.kinds |= kVectors;
     e.decay = t.weight_decay;
     state += padded(t.numel);
-    blocks += static_cast<uint64_t>(padded(t.numel) / kBlock);
+    chunks += (static_cast<uint64_t>(padded(t.numel) / kBlock) + job.chunk - 1) / job.chunk;
   }
   if (job.count == 0) return cudaSuccess;
-  job.blocks = static_cast<uint32_t>(blocks);
   job.exp_avg = a->exp_avg;
   job.exp_avg_sq = a->exp_avg_sq;
   job.scales = a->scales;
@@ -385,11 +549,28 @@ cudaError_t run(const gemm_adamw_args_t* a, int64_t first, int64_t count, int64_
   job.ln_beta1 = static_cast<float>(std::log(a->beta1));  // beta 0: -inf, and beta^t = 0
   job.ln_beta2 = static_cast<float>(std::log(a->beta2));
   job.eps = static_cast<float>(a->eps);
-  adamw_kernel<kBits, kTensors><<<static_cast<unsigned>((blocks + kWarps - 1) / kWarps), kThreads, 0, stream>>>(job);
-  return cudaGetLastError();
+  job.one = 1.0f;
+  return launch(adamw_kernel<kBits, kTensors>, static_cast<unsigned>(chunks), kThreads, Ring<kBits>::kBytes, stream, job);
 }
 
 }  // namespace
+
+namespace spgemm {
+
+cudaError_t adamw_set_smem() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel, size_t bytes) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  };
+  set(adamw_kernel<32, kFewTensors>, Ring<32>::kBytes);
+  set(adamw_kernel<32, kMostTensors>, Ring<32>::kBytes);
+  set(adamw_kernel<8, kFewTensors>, Ring<8>::kBytes);
+  set(adamw_kernel<8, kMostTensors>, Ring<8>::kBytes);
+  return e;
+}
+
+}  // namespace spgemm
 
 extern "C" {
 
@@ -421,16 +602,15 @@ gemm_status_t gemm_adamw(gemm_ops_t* ops, const gemm_adamw_args_t* args, void* s
     const int64_t count = std::min<int64_t>(kMostTensors, args->count - first);
     const bool few = count <= kFewTensors;
     if (args->bits == 32)
-      e = few ? run<32, kFewTensors>(args, first, count, state, total, stream)
-              : run<32, kMostTensors>(args, first, count, state, total, stream);
+      e = few ? run<32, kFewTensors>(ops, args, first, count, state, total, stream)
+              : run<32, kMostTensors>(ops, args, first, count, state, total, stream);
     else
-      e = few ? run<8, kFewTensors>(args, first, count, state, total, stream)
-              : run<8, kMostTensors>(args, first, count, state, total, stream);
+      e = few ? run<8, kFewTensors>(ops, args, first, count, state, total, stream)
+              : run<8, kMostTensors>(ops, args, first, count, state, total, stream);
     state += gemm_adamw_state_elements(args->tensors + first, count);
   }
   if (e != cudaSuccess) return ops_cuda_fail(e, "AdamW launch");
-  count_kernel<<<1, 1, 0, stream>>>(args->step);
-  e = cudaGetLastError();
+  e = launch(count_kernel, 1, 1, 0, stream, args->step);
   return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "AdamW step count launch");
 }
 

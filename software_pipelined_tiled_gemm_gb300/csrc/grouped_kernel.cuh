@@ -51,10 +51,9 @@ struct GroupedTile {
 // are multiples of 32 and differ by one unit at most.
 __device__ __forceinline__ void grouped_split(int extent, int tiles, int i, int& at, int& width) {
   const int units = (extent + kGroupedUnit - 1) / kGroupedUnit;
-  const int u0 = static_cast<int>(static_cast<int64_t>(units) * i / tiles);
-  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (i + 1) / tiles);
-  at = u0 * kGroupedUnit;
-  width = (u1 - u0) * kGroupedUnit;
+  const int each = units / tiles, more = units - each * tiles;
+  at = (i * each + min(i, more)) * kGroupedUnit;
+  width = (each + (i < more ? 1 : 0)) * kGroupedUnit;
 }
 
 // Tile t.  `offsets` and `first_tile` (tiles along the tokens before each

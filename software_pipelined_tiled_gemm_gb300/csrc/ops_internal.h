@@ -135,6 +135,7 @@ BlockScratch take_scratch(const gemm_ops* ops, Carver& c);  // enough for any pr
 
 cudaError_t logprobs_set_smem();  // logprobs.cu
 cudaError_t layer_norm_set_smem(size_t smem);  // layer_norm.cu
+cudaError_t adamw_set_smem();  // adamw.cu
 
 gemm_status_t run_block(const gemm_ops* ops, const BlockProblem& pr, BlockScratch& scratch, cudaStream_t stream);
 
