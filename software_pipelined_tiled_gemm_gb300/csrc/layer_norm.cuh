@@ -1,0 +1,804 @@
+// layer_norm.cuh -- layer norm over the rows of a matrix, and its gradients:
+// kernels and launches (layer_norm_*.cu: one type of rows each; layer_norm.cu:
+// argument checks).
+//
+// Bound by memory: the forward pass reads x and writes y, the backward pass
+// reads x and dy and writes dx.  A row belongs to a group of threads, from a
+// warp to a block, each thread holding the same columns (up to 32) of every row
+// it meets:
+//
+//   mean  = sum x / n, then d = x - mean, low = sum d / n,
+//   var   = sum d^2 / n - low^2,  h = (d - low) rstd.
+//
+// The second sum costs no pass of its own and takes out what the rounding of
+// the mean to fp32 left in the differences, so that a row far from zero loses
+// nothing but its own bits; the backward pass gets both parts of the mean.  A
+// sum or a sum of squares that leaves fp32's range is taken again, of x / n or
+// of 2^-64 d.
+//
+// Groups loop over rows.  Where rows are 16-byte aligned a thread copies its
+// own vectors of the next rows to shared memory asynchronously (nobody else
+// reads them, so no barrier is needed), which keeps rows of every group on
+// their way while one is reduced.  Rows that are not aligned are read element
+// by element, lanes side by side.  The arithmetic runs on pairs of values, and
+// a thread has many columns, so that the reductions over a row (some 25
+// instructions each) cost little: 16384 rows of 4096, forward, took 89 us with
+// scalars and 16 columns a thread, 41 us so (7 TB/s would be 38).
+//
+// The weights' gradients: a thread sums its columns over its rows in fp32
+// registers; each block leaves one partial, and a second kernel adds those in
+// block order.  The sums repeat bit for bit.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "layer_norm.h"
+#include "packed_f32.cuh"
+#include "ptx_block.cuh"
+
+namespace spgemm {
+namespace {
+
+constexpr int kAhead = 3;        // rows of a group on their way or in work, at most
+constexpr int kItems = 32;       // columns of a thread, at most
+constexpr int kSingles = 8;      // where they are read one by one
+constexpr int kMinThreads = 256; // of a block: smaller groups share one
+constexpr float kDown = 5.421010862427522e-20f;  // 2^-64
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v) {
+  if constexpr (std::is_same_v<T, __half>) return __half2float(v);
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) return __bfloat162float(v);
+  if constexpr (std::is_same_v<T, float>) return v;
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float v) {
+  if constexpr (std::is_same_v<T, __half>) return __float2half_rn(v);
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) return __float2bfloat16_rn(v);
+  if constexpr (std::is_same_v<T, float>) return v;
+}
+
+// Two values as they lie in memory, to a pair and back.
+template <typename T>
+__device__ __forceinline__ F32x2 pair_of(uint32_t w) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>)  // a bf16 is the upper half of its fp32
+    return pack_f32(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_f32(f.x, f.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t word_of(F32x2 v) {
+  const float2 f = unpack_f32(v);
+  uint32_t w;
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    memcpy(&w, &h, 4);
+  } else {
+    const __half2 h = __floats2half2_rn(f.x, f.y);
+    memcpy(&w, &h, 4);
+  }
+  return w;
+}
+
+// kN neighbouring columns from p (16-byte aligned, or kN 1), in pairs; a
+// single column has its pair's other value 0.
+template <typename T, int kN>
+__device__ __forceinline__ void load_cols(const T* p, F32x2 (&v)[(kN + 1) / 2]) {
+  if constexpr (kN == 1) {
+    v[0] = pack_f32(to_float(*p), 0.0f);
+  } else if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i) {
+      const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[i];
+      v[2 * i] = a.x;
+      v[2 * i + 1] = a.y;
+    }
+  } else {
+    static_assert(kN == 8);
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    v[0] = pair_of<T>(a.x);
+    v[1] = pair_of<T>(a.y);
+    v[2] = pair_of<T>(a.z);
+    v[3] = pair_of<T>(a.w);
+  }
+}
+template <typename T, int kN>
+__device__ __forceinline__ void store_cols(T* p, const F32x2 (&v)[(kN + 1) / 2]) {
+  if constexpr (kN == 1) {
+    *p = from_float<T>(unpack_f32(v[0]).x);
+  } else if constexpr (std::is_same_v<T, float>) {
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(word_of<T>(v[0]), word_of<T>(v[1]), word_of<T>(v[2]), word_of<T>(v[3]));
+  }
+}
+
+__device__ __forceinline__ void copy_async16(void* smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the newest ahead - 1 groups have landed.
+__device__ __forceinline__ void copy_async_wait(int ahead) {
+  static_assert(kAhead == 3);
+  if (ahead == 3)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (ahead == 2)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+constexpr int block_threads(int group) { return group < kMinThreads ? kMinThreads : group; }
+
+__device__ __forceinline__ F32x2 from_lane(F32x2 v, int d) { return __shfl_xor_sync(0xffffffffu, v, d); }
+__device__ __forceinline__ float from_lane(float v, int d) { return __shfl_xor_sync(0xffffffffu, v, d); }
+__device__ __forceinline__ F32x2 sum_of(F32x2 a, F32x2 b) { return add_f32x2(a, b); }
+__device__ __forceinline__ float sum_of(float a, float b) { return a + b; }
+
+// The sum over the group of one value or a pair, the same in every thread:
+// over the lanes, then over the warps, each as a tree.  `red`: 2 x warps of
+// the group, used in turn.
+template <int kGroup, typename V>
+__device__ __forceinline__ V group_sum(V a, F32x2* red, int& turn) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) a = sum_of(a, from_lane(a, d));
+  if constexpr (kGroup > 32) {
+    constexpr int kWarps = kGroup / 32;
+    V* mine = reinterpret_cast<V*>(red + turn * kWarps);
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) mine[(threadIdx.x % kGroup) >> 5] = a;
+    if constexpr (kGroup < kMinThreads)
+      ptx::named_barrier_sync(1 + threadIdx.x / kGroup, kGroup);
+    else
+      __syncthreads();
+    a = mine[threadIdx.x % kWarps];
+#pragma unroll
+    for (int d = kWarps / 2; d > 0; d /= 2) a = sum_of(a, from_lane(a, d));
+  }
+  return a;
+}
+__device__ __forceinline__ float both(F32x2 v) {
+  const float2 f = unpack_f32(v);
+  return f.x + f.y;
+}
+
+// 1 / sqrt(sum / n + eps) from the sums over n of d and d^2; `again` gives the
+// sum of (2^-64 d)^2 over n.  Rows of NaN give NaN.
+template <typename F>
+__device__ __forceinline__ float row_rstd(float low, float squares, float eps, F again) {
+  if (squares <= 3.4028235e38f) return rsqrtf(fmaxf(squares - low * low, 0.0f) + eps);
+  if (squares != squares) return squares;
+  const float s = again();  // the same in all threads of the group
+  return s <= 3.4028235e38f ? rsqrtf(s) * kDown : __int_as_float(0x7fc00000);
+}
+
+// How a kernel meets its weights.
+constexpr int kInRegisters = 0, kInShared = 1, kInMemory = 2;
+// fp32 weights: registers, and two blocks an SM, where a block's registers
+// hold them.  16-bit ones: shared memory and three blocks.  (16384 x 4096, fp32
+// weights: 41 and 60 us; 8192 x 8192, bf16 weights: 45 and 41 us.)  Four bytes a
+// column of 32768 columns fit no shared memory: read from L2.
+template <typename W>
+constexpr int weights_at(int group) {
+  if (group == 1024) return kInMemory;
+  return group == 32 || (group <= 256 && sizeof(W) == 4) ? kInRegisters : kInShared;
+}
+
+// fp32 weights of columns [col, col + kN), in pairs.
+template <typename W, int kN>
+__device__ __forceinline__ void weights_of(const void* base, int col, float otherwise, F32x2 (&out)[(kN + 1) / 2]) {
+  if (base == nullptr) {
+#pragma unroll
+    for (int j = 0; j < (kN + 1) / 2; ++j) out[j] = both_f32(otherwise);
+  } else if constexpr (kN == 4 && !std::is_same_v<W, float>) {
+    static_assert(kN != 4, "rows of fp32 have fp32 weights");
+  } else {
+    load_cols<W, kN>(static_cast<const W*>(base) + col, out);
+  }
+}
+
+template <typename T, typename W, int kVec, int kGroup, int kCols, int kBlocks>
+__global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel(const LayerNormJob p) {
+  constexpr int kVecs = kCols / kVec;           // vectors of a thread
+  constexpr int kPairs = (kVec + 1) / 2;        // pairs of a vector
+  constexpr int kGroups = block_threads(kGroup) / kGroup;
+  constexpr int kWeights = weights_at<W>(kGroup);
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ F32x2 red_all[kGroup > 32 ? 2 * block_threads(kGroup) / 32 : 1];
+  ptx::pdl_launch_dependents();
+  const int tid = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
+  F32x2* red = red_all + (kGroup > 32 ? group * 2 * (kGroup / 32) : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  const int vecs = p.cols / kVec;                                   // of a row
+  const int used = (vecs + kGroup - 1) / kGroup;                    // of a thread
+  const T* x = static_cast<const T*>(p.x);
+  const W* weights = nullptr;  // kInShared: columns as in memory
+  const W* biases = nullptr;
+  uint8_t* rows = ring;
+  ptx::pdl_wait_prior_grid();
+  F32x2 w[kWeights == kInRegisters ? kVecs : 1][kPairs], b[kWeights == kInRegisters ? kVecs : 1][kPairs];
+  if constexpr (kWeights == kInRegisters) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (tid + i * kGroup < vecs) {
+        weights_of<W, kVec>(p.weight, (tid + i * kGroup) * kVec, 1.0f, w[i]);
+        weights_of<W, kVec>(p.bias, (tid + i * kGroup) * kVec, 0.0f, b[i]);
+      }
+  }
+  if constexpr (kWeights == kInShared) {
+    // (Each thread reads back what it wrote itself.)
+    W* to = reinterpret_cast<W*>(ring);
+    weights = to;
+    biases = to + p.cols;
+    auto bring = [&](W* dst, const void* base) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int c = (tid + i * kGroup) * kVec;
+        if (c >= p.cols) continue;
+        if constexpr (kVec == 1) {
+          dst[c] = static_cast<const W*>(base)[c];
+        } else {
+#pragma unroll
+          for (int j = 0; j < kVec * static_cast<int>(sizeof(W)) / 16; ++j)
+            *reinterpret_cast<uint4*>(dst + c + j * (16 / sizeof(W))) =
+                *reinterpret_cast<const uint4*>(static_cast<const W*>(base) + c + j * (16 / sizeof(W)));
+        }
+      }
+    };
+    if (p.weight) bring(to, p.weight);
+    if (p.bias) bring(to + p.cols, p.bias);
+    rows += p.weight_bytes;
+  }
+  T* mine = reinterpret_cast<T*>(rows) + (static_cast<size_t>(group) * p.ahead * used * kGroup + tid) * kVec;
+  int turn = 0;
+
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  auto fetch = [&](int64_t r, int slot) {
+    if (r < p.rows) {
+      const T* src = x + r * p.ldx + tid * kVec;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (tid + i * kGroup < vecs) copy_async16(mine + (slot * used + i) * (kGroup * kVec), src + i * (kGroup * kVec));
+    }
+    copy_async_commit();
+  };
+  if constexpr (kVec > 1)
+    for (int s = 0; s < p.ahead - 1; ++s) fetch(row + s * step, s);
+
+  for (int slot = 0; row < p.rows; row += step) {
+    F32x2 v[kVecs][kPairs];
+    const T* from;
+    if constexpr (kVec > 1) {
+      fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
+      copy_async_wait(p.ahead);
+      from = mine + slot * used * (kGroup * kVec);
+      slot = slot == p.ahead - 1 ? 0 : slot + 1;
+    } else {
+      from = x + row * p.ldx + tid;
+    }
+    F32x2 sum = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      if (tid + i * kGroup < vecs) {
+        load_cols<T, kVec>(from + i * (kGroup * kVec), v[i]);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) sum = add_f32x2(sum, v[i][j]);
+      }
+    }
+    float mean = group_sum<kGroup>(both(sum), red, turn) * p.inv;
+    if (!(fabsf(mean) <= 3.4028235e38f)) {  // beyond fp32's range, or NaN: the same in all threads
+      sum = 0;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (tid + i * kGroup < vecs)
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) sum = fma_f32x2(v[i][j], both_f32(p.inv), sum);
+      mean = group_sum<kGroup>(both(sum), red, turn);
+    }
+    F32x2 lows = 0, squares = 0;
+    const F32x2 minus = both_f32(-mean);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (tid + i * kGroup < vecs) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          if constexpr (kVec == 1)  // the pair's other value stays 0
+            v[i][j] = pack_f32(unpack_f32(v[i][j]).x - mean, 0.0f);
+          else
+            v[i][j] = add_f32x2(v[i][j], minus);
+          lows = add_f32x2(lows, v[i][j]);
+          squares = fma_f32x2(v[i][j], v[i][j], squares);
+        }
+      }
+    const float2 sums = unpack_f32(group_sum<kGroup>(pack_f32(both(lows), both(squares)), red, turn));
+    const float low = sums.x * p.inv;
+    const float rstd = row_rstd(low, sums.y * p.inv, p.eps, [&]() {
+      F32x2 s = 0;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (tid + i * kGroup < vecs)
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            const F32x2 d = mul_f32x2(v[i][j], both_f32(kDown));
+            s = fma_f32x2(mul_f32x2(d, both_f32(p.inv)), d, s);
+          }
+      return group_sum<kGroup>(both(s), red, turn);
+    });
+    if (p.stats != nullptr && tid == 0) {
+      p.stats[row] = mean;
+      p.stats[p.rows + row] = low;
+      p.stats[2 * p.rows + row] = rstd;
+    }
+    T* out = static_cast<T*>(p.out) + row * p.cols + tid * kVec;
+    const F32x2 scale = both_f32(rstd), shift = both_f32(-low * rstd);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (tid + i * kGroup < vecs) {
+        F32x2 wi[kPairs], bi[kPairs], y[kPairs];
+        const int col = (tid + i * kGroup) * kVec;
+        if constexpr (kWeights == kInShared) {
+          weights_of<W, kVec>(p.weight ? weights : nullptr, col, 1.0f, wi);
+          weights_of<W, kVec>(p.bias ? biases : nullptr, col, 0.0f, bi);
+        } else if constexpr (kWeights == kInMemory) {
+          weights_of<W, kVec>(p.weight, col, 1.0f, wi);
+          weights_of<W, kVec>(p.bias, col, 0.0f, bi);
+        }
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const F32x2 h = fma_f32x2(v[i][j], scale, shift);
+          y[j] = kWeights == kInRegisters ? fma_f32x2(h, w[i][j], b[i][j]) : fma_f32x2(h, wi[j], bi[j]);
+        }
+        store_cols<T, kVec>(out + i * (kGroup * kVec), y);
+      }
+  }
+}
+
+template <typename W>
+__device__ __forceinline__ float weight_at(const void* base, int col, float otherwise) {
+  return base ? to_float(__ldg(static_cast<const W*>(base) + col)) : otherwise;
+}
+
+// Rows of more columns than a block holds: read three times, the second and
+// third mostly from L2.
+template <typename T, typename W>
+__global__ void __launch_bounds__(1024) forward_long_kernel(const LayerNormJob p) {
+  __shared__ F32x2 red[2 * 32];
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    float sum = 0.0f;
+    for (int c = threadIdx.x; c < p.cols; c += 1024) sum = fmaf(to_float(x[c]), p.inv, sum);
+    const float mean = group_sum<1024>(sum, red, turn);
+    float low = 0.0f, squares = 0.0f;
+    for (int c = threadIdx.x; c < p.cols; c += 1024) {
+      const float d = to_float(x[c]) - mean;
+      low = fmaf(d, p.inv, low);
+      squares = fmaf(d * p.inv, d, squares);
+    }
+    const float2 both = unpack_f32(group_sum<1024>(pack_f32(low, squares), red, turn));
+    low = both.x;
+    const float rstd = row_rstd(low, both.y, p.eps, [&]() {
+      float s = 0.0f;
+      for (int c = threadIdx.x; c < p.cols; c += 1024) {
+        const float d = (to_float(x[c]) - mean) * kDown;
+        s = fmaf(d * p.inv, d, s);
+      }
+      return group_sum<1024>(s, red, turn);
+    });
+    if (p.stats != nullptr && threadIdx.x == 0) {
+      p.stats[row] = mean;
+      p.stats[p.rows + row] = low;
+      p.stats[2 * p.rows + row] = rstd;
+    }
+    T* out = static_cast<T*>(p.out) + row * p.cols;
+    for (int c = threadIdx.x; c < p.cols; c += 1024) {
+      const float w = weight_at<W>(p.weight, c, 1.0f), b = weight_at<W>(p.bias, c, 0.0f);
+      out[c] = from_float<T>(fmaf((to_float(x[c]) - mean - low) * rstd, w, b));
+    }
+  }
+}
+
+template <typename T, typename W, int kVec, int kGroup, int kCols, int kBlocks>
+__global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kernel(const LayerNormJob p) {
+  constexpr int kVecs = kCols / kVec;
+  constexpr int kPairs = (kVec + 1) / 2;
+  constexpr int kGroups = block_threads(kGroup) / kGroup;
+  constexpr bool kHeld = kGroup <= 256;  // weights in registers
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ F32x2 red_all[kGroup > 32 ? 2 * block_threads(kGroup) / 32 : 1];
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  const int tid = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
+  F32x2* red = red_all + (kGroup > 32 ? group * 2 * (kGroup / 32) : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  const int vecs = p.cols / kVec;
+  const int used = (vecs + kGroup - 1) / kGroup;
+  // [slot][x, dy][vector][thread]
+  T* mine = reinterpret_cast<T*>(ring) + (static_cast<size_t>(group) * p.ahead * 2 * used * kGroup + tid) * kVec;
+  const T* x = static_cast<const T*>(p.x);
+  const T* dy = static_cast<const T*>(p.dy);
+  int turn = 0;
+  F32x2 dw[kVecs][kPairs], db[kVecs][kPairs], w[kHeld ? kVecs : 1][kPairs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) dw[i][j] = db[i][j] = 0;
+    if (kHeld && tid + i * kGroup < vecs) weights_of<W, kVec>(p.weight, (tid + i * kGroup) * kVec, 1.0f, w[kHeld ? i : 0]);
+  }
+
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  auto fetch = [&](int64_t r, int slot) {
+    if (r < p.rows) {
+      const T* sx = x + r * p.ldx + tid * kVec;
+      const T* sd = dy + r * p.lddy + tid * kVec;
+      T* to = mine + slot * 2 * used * (kGroup * kVec);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (tid + i * kGroup < vecs) {
+          copy_async16(to + i * (kGroup * kVec), sx + i * (kGroup * kVec));
+          copy_async16(to + (used + i) * (kGroup * kVec), sd + i * (kGroup * kVec));
+        }
+    }
+    copy_async_commit();
+  };
+  float next_mean = 0.0f, next_low = 0.0f, next_rstd = 0.0f;
+  auto fetch_stats = [&](int64_t r) {
+    if (r < p.rows) {
+      next_mean = __ldg(p.stats + r);
+      next_low = __ldg(p.stats + p.rows + r);
+      next_rstd = __ldg(p.stats + 2 * p.rows + r);
+    }
+  };
+  if constexpr (kVec > 1)
+    for (int s = 0; s < p.ahead - 1; ++s) fetch(row + s * step, s);
+  fetch_stats(row);
+
+  for (int slot = 0; row < p.rows; row += step) {
+    const float rstd = next_rstd;
+    const F32x2 minus = both_f32(-next_mean), scale = both_f32(rstd), shift = both_f32(-next_low * rstd);
+    fetch_stats(row + step);
+    const T *from_x, *from_d;
+    T ex[kVec == 1 ? kVecs : 1], ed[kVec == 1 ? kVecs : 1];
+    if constexpr (kVec > 1) {
+      fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
+      copy_async_wait(p.ahead);
+      from_x = mine + slot * 2 * used * (kGroup * kVec);
+      from_d = from_x + used * (kGroup * kVec);
+      slot = slot == p.ahead - 1 ? 0 : slot + 1;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (tid + i * kGroup < vecs) {
+          ex[i] = x[row * p.ldx + tid + i * kGroup];
+          ed[i] = dy[row * p.lddy + tid + i * kGroup];
+        }
+    }
+    // dy, h and g of this thread's vector i; both passes over the row take them from
+    // shared memory (or the elements' registers), which costs less than holding them.
+    auto values = [&](int i, F32x2 (&d)[kPairs], F32x2 (&h)[kPairs], F32x2 (&g)[kPairs]) {
+      if constexpr (kVec > 1) {
+        load_cols<T, kVec>(from_x + i * (kGroup * kVec), h);
+        load_cols<T, kVec>(from_d + i * (kGroup * kVec), d);
+      } else {
+        h[0] = pack_f32(to_float(ex[i]), 0.0f);
+        d[0] = pack_f32(to_float(ed[i]), 0.0f);
+      }
+      if constexpr (!kHeld) weights_of<W, kVec>(p.weight, (tid + i * kGroup) * kVec, 1.0f, g);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        h[j] = fma_f32x2(add_f32x2(h[j], minus), scale, shift);  // (one column: the other value is multiplied by d's 0)
+        g[j] = mul_f32x2(kHeld ? w[kHeld ? i : 0][j] : g[j], d[j]);
+      }
+    };
+    F32x2 gs = 0, ghs = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (tid + i * kGroup < vecs) {
+        F32x2 d[kPairs], h[kPairs], g[kPairs];
+        values(i, d, h, g);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          dw[i][j] = fma_f32x2(d[j], h[j], dw[i][j]);
+          db[i][j] = add_f32x2(db[i][j], d[j]);
+          gs = add_f32x2(gs, g[j]);
+          ghs = fma_f32x2(g[j], h[j], ghs);
+        }
+      }
+    if (p.out != nullptr) {
+      const float2 sums = unpack_f32(group_sum<kGroup>(pack_f32(both(gs), both(ghs)), red, turn));
+      // rstd (g - <g> - h <g h>)
+      const F32x2 m1 = both_f32(-sums.x * p.inv * rstd), m2 = both_f32(-sums.y * p.inv * rstd);
+      T* out = static_cast<T*>(p.out) + row * p.cols + tid * kVec;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (tid + i * kGroup < vecs) {
+          F32x2 d[kPairs], h[kPairs], g[kPairs];
+          values(i, d, h, g);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) d[j] = fma_f32x2(h[j], m2, fma_f32x2(g[j], scale, m1));
+          store_cols<T, kVec>(out + i * (kGroup * kVec), d);
+        }
+    }
+  }
+
+  if (p.partial == nullptr) return;
+  float* to = p.partial + static_cast<size_t>(blockIdx.x) * 2 * p.cols;
+  auto each = [&](auto&& f) {  // this thread's sums, by column
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (tid + i * kGroup < vecs)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const float2 a = unpack_f32(dw[i][j]), c = unpack_f32(db[i][j]);
+          const int col = (tid + i * kGroup) * kVec + 2 * j;
+          f(col, a.x, c.x);
+          if (kVec > 1) f(col + 1, a.y, c.y);
+        }
+  };
+  if constexpr (kGroups > 1) {
+    // The block's groups one after another, each adding to the sum before it.
+    float* sums = reinterpret_cast<float*>(ring);
+    copy_async_wait(1);
+    for (int turn_of = 0; turn_of < kGroups; ++turn_of) {
+      __syncthreads();
+      if (turn_of != group) continue;
+      each([&](int col, float a, float c) {
+        sums[col] = group == 0 ? a : sums[col] + a;
+        sums[p.cols + col] = group == 0 ? c : sums[p.cols + col] + c;
+      });
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.cols; c += block_threads(kGroup)) to[c] = sums[c];
+  } else {
+    each([&](int col, float a, float c) {
+      to[col] = a;
+      to[p.cols + col] = c;
+    });
+  }
+}
+
+// Rows of more columns than a block holds: a block sums a share of the rows
+// into its own partial in memory.
+template <typename T, typename W>
+__global__ void __launch_bounds__(1024) backward_long_kernel(const LayerNormJob p) {
+  __shared__ F32x2 red[2 * 32];
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  int turn = 0;
+  float* to = p.partial ? p.partial + static_cast<size_t>(blockIdx.x) * 2 * p.cols : nullptr;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+    const float mean = __ldg(p.stats + row), low = __ldg(p.stats + p.rows + row);
+    const float rstd = __ldg(p.stats + 2 * p.rows + row);
+    float gs = 0.0f, ghs = 0.0f;
+    for (int c = threadIdx.x; c < p.cols; c += 1024) {
+      const float d = to_float(dy[c]), h = ((to_float(x[c]) - mean) - low) * rstd;
+      const float w = weight_at<W>(p.weight, c, 1.0f);
+      gs = fmaf(d * w, p.inv, gs);
+      ghs = fmaf(d * w * p.inv, h, ghs);
+      if (to) {  // the thread's own columns
+        const bool first = row == blockIdx.x;
+        to[c] = first ? d * h : to[c] + d * h;
+        to[p.cols + c] = first ? d : to[p.cols + c] + d;
+      }
+    }
+    if (p.out == nullptr) continue;
+    const float2 means = unpack_f32(group_sum<1024>(pack_f32(gs, ghs), red, turn));
+    T* out = static_cast<T*>(p.out) + row * p.cols;
+    for (int c = threadIdx.x; c < p.cols; c += 1024) {
+      const float w = weight_at<W>(p.weight, c, 1.0f);
+      const float d = to_float(dy[c]), h = ((to_float(x[c]) - mean) - low) * rstd;
+      out[c] = from_float<T>(rstd * (d * w - means.x - h * means.y));
+    }
+  }
+}
+
+// The blocks' partials in order: 32 columns a block, its warps sharing the
+// partials, then the warps in order.
+constexpr int kSumThreads = 1024;
+template <typename W>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const float* partial, int blocks, int cols, W* dweight, W* dbias) {
+  __shared__ float sums[32][33];
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait_prior_grid();
+  W* out = blockIdx.y == 0 ? dweight : dbias;
+  if (out == nullptr) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  const int each = (blocks + 31) / 32;
+  const float* src = partial + static_cast<size_t>(blockIdx.y) * cols + col;
+  float s = 0.0f;
+  if (col < cols) {
+    const int end = min(blocks, (warp + 1) * each);
+    constexpr int kFlight = 10;  // loads on their way: all of a warp's where there are two blocks an SM
+    for (int b = warp * each; b < end; b += kFlight) {
+      float v[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) v[i] = b + i < end ? __ldcg(src + static_cast<size_t>(b + i) * 2 * cols) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) s += v[i];
+    }
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || col >= cols) return;
+  float total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) total += sums[w][lane];
+  out[col] = from_float<W>(total);
+}
+
+// Threads that share a row and the columns each has.
+template <int kVec, typename F>
+cudaError_t by_group(int64_t cols, F f) {
+  using std::integral_constant;
+  constexpr int kEach = kVec == 1 ? kSingles : kItems;
+  if (cols <= 32 * kEach) return f(integral_constant<int, 32>(), integral_constant<int, kEach>());
+  if (cols <= 64 * kEach) return f(integral_constant<int, 64>(), integral_constant<int, kEach>());
+  if (cols <= 128 * kEach) return f(integral_constant<int, 128>(), integral_constant<int, kEach>());
+  if (cols <= 256 * kEach) return f(integral_constant<int, 256>(), integral_constant<int, kEach>());
+  if (cols <= 512 * kEach) return f(integral_constant<int, 512>(), integral_constant<int, kEach>());
+  if (cols <= 1024 * kEach) return f(integral_constant<int, 1024>(), integral_constant<int, kEach>());
+  return f(integral_constant<int, 1024>(), integral_constant<int, kItems>());
+}
+
+// Blocks of an SM that the registers are shared out for.
+template <typename W>
+constexpr int forward_blocks(int group, int vec) {
+  if (group >= 512) return 1;
+  return vec == 1 || weights_at<W>(group) == kInShared ? 3 : 2;
+}
+constexpr int backward_blocks(int group, int vec) { return vec == 1 && group <= 256 ? 2 : 1; }
+
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int grid_of(const gemm_ops* ops, int64_t rows, int groups, int per_sm) {
+  return static_cast<int>(std::min<int64_t>(ceil_div(rows, int64_t{groups}), static_cast<int64_t>(ops->sm_count) * per_sm));
+}
+
+// The ring's depth: p->ahead rows of `row` bytes a block beside `beside` bytes,
+// so that `per_sm` blocks fit an SM with two rows each if they can.  False: not one row fits.
+bool ring_of(const gemm_ops* ops, LayerNormJob* p, size_t row, size_t beside, int per_sm, size_t* smem) {
+  const size_t most = ops->smem_optin - kLayerNormStatic;
+  p->ahead = kAhead;
+  while (p->ahead > 2 && (p->ahead * row + beside + kLayerNormStatic) * per_sm > ops->smem_optin) --p->ahead;
+  while (p->ahead > 1 && p->ahead * row + beside > most) --p->ahead;
+  *smem = p->ahead * row + beside;
+  return *smem <= most;
+}
+
+template <typename T, typename W, int kVec>
+cudaError_t forward_vec(const gemm_ops* ops, LayerNormJob p, cudaStream_t stream) {
+  return by_group<kVec>(p.cols, [&](auto g, auto c) {
+    constexpr int kGroup = g(), kCols = c(), kBlocks = forward_blocks<W>(kGroup, kVec), kThreads = block_threads(kGroup);
+    const size_t row = kVec == 1 ? 0 : static_cast<size_t>(kThreads) * ceil_div(p.cols / kVec, int64_t{kGroup}) * 16;
+    p.weight_bytes = weights_at<W>(kGroup) == kInShared ? static_cast<int>((2 * sizeof(W) * p.cols + 15) / 16 * 16) : 0;
+    size_t smem;
+    if (!ring_of(ops, &p, row, p.weight_bytes, kBlocks, &smem)) return cudaErrorInvalidValue;
+    return launch(forward_kernel<T, W, kVec, kGroup, kCols, kBlocks>,
+                  dim3(grid_of(ops, p.rows, kThreads / kGroup, kBlocks)), kThreads, smem, stream, p);
+  });
+}
+
+template <int kVec>
+int backward_grid(const gemm_ops* ops, int64_t rows, int64_t cols) {
+  if (cols > kLayerNormMaxCols) return static_cast<int>(std::min<int64_t>(rows, 2 * ops->sm_count));
+  int n = 0;
+  by_group<kVec>(cols, [&](auto g, auto) {
+    n = grid_of(ops, rows, block_threads(g()) / g(), backward_blocks(g(), kVec));
+    return cudaSuccess;
+  });
+  return n;
+}
+
+// False where not one row of x and dy fits the ring.
+template <typename T>
+bool backward_fits(const gemm_ops* ops, int64_t cols) {
+  constexpr int kVec = 16 / sizeof(T);
+  bool fits = true;
+  by_group<kVec>(cols, [&](auto g, auto) {
+    fits = static_cast<size_t>(block_threads(g())) * 2 * ceil_div(cols / kVec, int64_t{g()}) * 16 <= ops->smem_optin - kLayerNormStatic;
+    return cudaSuccess;
+  });
+  return fits;
+}
+
+template <typename T, typename W, int kVec>
+cudaError_t backward_vec(const gemm_ops* ops, LayerNormJob p, int blocks, cudaStream_t stream) {
+  return by_group<kVec>(p.cols, [&](auto g, auto c) {
+    constexpr int kGroup = g(), kCols = c(), kBlocks = backward_blocks(kGroup, kVec), kThreads = block_threads(kGroup);
+    const size_t row = kVec == 1 ? 0 : static_cast<size_t>(kThreads) * 2 * ceil_div(p.cols / kVec, int64_t{kGroup}) * 16;
+    size_t smem;
+    if (!ring_of(ops, &p, row, 0, kBlocks, &smem)) return cudaErrorInvalidValue;
+    if (kThreads > kGroup) smem = std::max(smem, static_cast<size_t>(p.cols) * 2 * sizeof(float));
+    return launch(backward_kernel<T, W, kVec, kGroup, kCols, kBlocks>, dim3(blocks), kThreads, smem, stream, p);
+  });
+}
+
+template <typename T, typename W>
+cudaError_t forward(const gemm_ops* ops, const LayerNormJob& p, bool vec, cudaStream_t stream) {
+  if (p.cols > kLayerNormMaxCols)
+    return launch(forward_long_kernel<T, W>, dim3(static_cast<unsigned>(std::min<int64_t>(p.rows, 2 * ops->sm_count))),
+                  1024, 0, stream, p);
+  return vec ? forward_vec<T, W, 16 / sizeof(T)>(ops, p, stream) : forward_vec<T, W, 1>(ops, p, stream);
+}
+
+template <typename T, typename W>
+cudaError_t backward(const gemm_ops* ops, const LayerNormJob& p, bool vec, void* dweight, void* dbias, cudaStream_t stream) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (p.cols <= kLayerNormMaxCols && !backward_fits<T>(ops, p.cols)) vec = false;
+  const int blocks = vec ? backward_grid<kVec>(ops, p.rows, p.cols) : backward_grid<1>(ops, p.rows, p.cols);
+  cudaError_t e;
+  if (p.cols > kLayerNormMaxCols)
+    e = launch(backward_long_kernel<T, W>, dim3(blocks), 1024, 0, stream, p);
+  else
+    e = vec ? backward_vec<T, W, kVec>(ops, p, blocks, stream) : backward_vec<T, W, 1>(ops, p, blocks, stream);
+  if (e != cudaSuccess || !p.partial) return e;
+  return launch(sum_kernel<W>, dim3(static_cast<unsigned>(ceil_div(p.cols, int64_t{32})), 2), kSumThreads, 0, stream,
+                static_cast<const float*>(p.partial), blocks, p.cols, static_cast<W*>(dweight), static_cast<W*>(dbias));
+}
+
+template <typename T, typename W, int kVec>
+cudaError_t set_smem(size_t smem) {
+  const int bytes = static_cast<int>(smem - kLayerNormStatic);
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto g, auto c) {
+    constexpr int kGroup = g(), kCols = c();
+    const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(forward_kernel<T, W, kVec, kGroup, kCols, forward_blocks<W>(kGroup, kVec)>, attr, bytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(backward_kernel<T, W, kVec, kGroup, kCols, backward_blocks(kGroup, kVec)>, attr, bytes);
+    return e;
+  };
+  for (int64_t cols = 256; cols <= kLayerNormMaxCols; cols *= 2) by_group<kVec>(cols, set);
+  return e;
+}
+
+}  // namespace
+}  // namespace spgemm
+
+#define SPGEMM_DEFINE_LAYER_NORM(NAME, T)                                                                       \
+  namespace spgemm {                                                                                            \
+  cudaError_t layer_norm_set_smem_##NAME(size_t smem) {                                                         \
+    cudaError_t e = set_smem<T, T, 16 / sizeof(T)>(smem);                                                       \
+    if (e == cudaSuccess) e = set_smem<T, float, 16 / sizeof(T)>(smem);                                         \
+    if (e == cudaSuccess) e = set_smem<T, T, 1>(smem);                                                          \
+    if (e == cudaSuccess) e = set_smem<T, float, 1>(smem);                                                      \
+    return e;                                                                                                   \
+  }                                                                                                             \
+  cudaError_t layer_norm_forward_##NAME(const gemm_ops* ops, const LayerNormJob& p, bool vec, bool wide,        \
+                                        cudaStream_t stream) {                                                  \
+    return wide ? forward<T, float>(ops, p, vec, stream) : forward<T, T>(ops, p, vec, stream);                  \
+  }                                                                                                             \
+  cudaError_t layer_norm_backward_##NAME(const gemm_ops* ops, const LayerNormJob& p, bool vec, bool wide,       \
+                                         void* dweight, void* dbias, cudaStream_t stream) {                     \
+    return wide ? backward<T, float>(ops, p, vec, dweight, dbias, stream)                                       \
+                : backward<T, T>(ops, p, vec, dweight, dbias, stream);                                          \
+  }                                                                                                             \
+  int layer_norm_backward_grid_##NAME(const gemm_ops* ops, int64_t rows, int64_t cols) {                        \
+    return std::max(backward_grid<16 / sizeof(T)>(ops, rows, cols), backward_grid<1>(ops, rows, cols));         \
+  }                                                                                                             \
+  }
