@@ -180,7 +180,10 @@ gemm_status_t gemm_token_logprobs_backward(gemm_ops_t* ops, const gemm_logprobs_
  * reports GEMM_ERR_INVALID_ARG (GEMM_CHECK_OFFSETS).  Rows of no group are
  * not read: what they hold, NaN and infinities too, reaches no output. */
 #define GEMM_GROUPED_MAX_GROUPS 4096
-#define GEMM_CHECK_OFFSETS ((0 << 16) | 17) /* detail of the status word */
+/* Details of the status word. */
+#define GEMM_CHECK_OFFSETS ((0 << 16) | 17)  /* offsets that decrease or leave the rows */
+#define GEMM_WAIT_NEXT_TILE ((3 << 16) | 5)  /* a role waiting for its CTA pair's next tile */
+#define GEMM_WAIT_NEXT_FREE ((3 << 16) | 6)  /* the scheduler waiting for the roles to take one */
 
 typedef struct {
   int64_t rows, groups, n, k;  /* rows >= 0, n, k >= 1, groups 1 .. GEMM_GROUPED_MAX_GROUPS */

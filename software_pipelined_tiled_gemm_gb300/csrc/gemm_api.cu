@@ -347,6 +347,8 @@ const char* gemm_wait_detail_string(int32_t detail) {
     case GEMM_WAIT_SK_COPY: return "stream-K owner waiting for the partial's bytes";
     case GEMM_WAIT_SK_FREE: return "cluster split contributor waiting for the owner's ring";
     case GEMM_CHECK_SMEM_LAYOUT: return "ring, staging and barriers exceed the launch's shared memory";
+    case GEMM_WAIT_NEXT_TILE: return "grouped product waiting for a CTA pair's next tile";
+    case GEMM_WAIT_NEXT_FREE: return "grouped product's scheduler waiting for a tile to be taken";
     case GEMM_CHECK_OFFSETS: return "group offsets decrease or leave the rows";
     case GEMM_CHECK_TILE: return "tile index or tile coordinates out of range";
     case GEMM_CHECK_K_SLICE: return "K slot outside the unit's range or the K extent";

@@ -55,6 +55,20 @@ __global__ void __launch_bounds__(kTailThreads)
   }
 }
 
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct Grouped {
   const gemm_grouped_args_t* a;
   Matrix x, w, dy, tail_x, tail_dy;
@@ -127,7 +141,7 @@ gemm_status_t check_overlap(const gemm_grouped_args_t* a, bool backward, const v
 
 // Lays out the workspace (with a null base: only measures it).  An operand
 // the copy engine cannot read is replaced by a padded copy.
-size_t layout(const gemm_grouped_args_t* a, bool backward, void* workspace, Grouped* g) {
+size_t layout(const gemm_ops* ops, const gemm_grouped_args_t* a, bool backward, void* workspace, Grouped* g) {
   g->a = a;
   g->x = {a->x, a->rows, a->k, a->ldx, 0};
   g->w = {a->w, a->groups * a->n, a->k, a->k, 0};
@@ -168,7 +182,7 @@ gemm_status_t prepare(gemm_ops_t* ops, const gemm_grouped_args_t* a, bool backwa
   if (st != GEMM_OK) return st;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return ops_fail(GEMM_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
-  const size_t need = layout(a, backward, workspace, g);
+  const size_t need = layout(ops, a, backward, workspace, g);
   if (need > 0 && (!workspace || bytes < need))
     return ops_fail(GEMM_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? bytes : 0, need);
   return check_overlap(a, backward, workspace, need);
@@ -196,17 +210,27 @@ gemm_status_t run_product(const gemm_ops* ops, const Grouped& g, int kind, void*
   p.timeout_ns = ops->timeout_ns;
   p.inject_fault = ops->debug_fault;
 
+  if (ops->pairs < 1) return ops_fail(GEMM_ERR_UNSUPPORTED, "no CTA pair fits the device");
   p.cap = kGroupedCols;
-  const int64_t tiles =
-      kind == kGroupedWeight ? a->groups * p.tiles_lane * ceil_div(a->n, int64_t{p.cap})
-                             : p.tiles_lane * (a->rows / p.cap + std::min(a->groups, a->rows));
-  p.pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ops->pairs, tiles)));
+  int64_t tiles = p.tiles_lane * (a->rows / grouped_cap(kGroupedCaps - 1) + std::min(a->groups, a->rows));  // at most
+  if (kind == kGroupedWeight) {
+    const int slots = static_cast<int>(a->rows / a->groups / kBK) + 2, strips = static_cast<int>(a->groups) * p.tiles_lane;
+    float best = -1.0f;
+    for (int i = 0; i < kGroupedCaps; ++i) {
+      const int cap = grouped_cap(i), n = strips * grouped_tiles(p.cols, cap);
+      const float clocks = grouped_clocks(static_cast<float>(strips) * grouped_strip_clocks(p.cols, cap, slots), n, cap, slots, ops->pairs);
+      if (best >= 0.0f && clocks >= best) continue;
+      best = clocks;
+      tiles = n;
+      p.cap = cap;
+    }
+  }
+  p.pairs = static_cast<int>(std::min<int64_t>(ops->pairs, tiles));
 
   p.stages = kGroupedStages;
   while (p.stages > 1 && grouped_smem_bytes(p.stages, p.groups) > ops->smem_optin) --p.stages;
   const size_t smem = grouped_smem_bytes(p.stages, p.groups);
   if (smem > ops->smem_optin) return ops_fail(GEMM_ERR_SMEM_BUDGET, "no ring fits shared memory");
-  if (ops->pairs < 1) return ops_fail(GEMM_ERR_UNSUPPORTED, "no CTA pair fits the device");
 
   const CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   gemm_status_t st;
@@ -276,7 +300,7 @@ gemm_status_t gemm_grouped_workspace(gemm_ops_t* ops, const gemm_grouped_args_t*
   const gemm_status_t st = check(args, backward != 0);
   if (st != GEMM_OK) return st;
   Grouped g;
-  *bytes = layout(args, backward != 0, nullptr, &g);
+  *bytes = layout(ops, args, backward != 0, nullptr, &g);
   return GEMM_OK;
 }
 
@@ -318,16 +342,8 @@ gemm_status_t gemm_grouped_backward(gemm_ops_t* ops, const gemm_grouped_args_t* 
                      static_cast<uint16_t*>(const_cast<void*>(to[i]->ptr)), from[i]->ld, to[i]->ld,
                      static_cast<int>(from[i]->cols)};
     const int64_t blocks = ceil_div(kGroupedTail * ceil_div(std::max(args->n, args->k), int64_t{8}), int64_t{4 * kTailThreads});
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(args->groups), static_cast<unsigned>(std::min<int64_t>(blocks, 64)), 2);
-    cfg.blockDim = dim3(kTailThreads, 1, 1);
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tail_kernel, jobs, args->offsets, args->rows);
+    e = launch(tail_kernel, dim3(static_cast<unsigned>(args->groups), static_cast<unsigned>(std::min<int64_t>(blocks, 64)), 2),
+               kTailThreads, stream, jobs, args->offsets, args->rows);
     if (e != cudaSuccess) return ops_cuda_fail(e, "group tails launch");
   }
   if (args->dx) st = run_product(ops, g, kGroupedInput, args->dx, stream);

@@ -6,12 +6,19 @@
 //   sizes       The groups' offsets are read on the device.  Every CTA loads
 //               them, checks them and counts the tiles of each group, so the
 //               launch needs no more than an upper bound and the host no copy.
+//   producers   One thread issues a copy in some 50 to 90 clocks, and a slot takes
+//               two to four: A's and B's come from a warp each (dW of 32768 x
+//               4096 x 2048: see grouped.cu's figures).
+//   schedule    Finding a tile's place takes some hundred instructions, and the
+//               producer is never far ahead of the tensor cores (a slot's copies
+//               take about as long as the ring's other slots last), so an
+//               eleventh warp describes a CTA's tiles ahead of time: the other
+//               roles read eight words (found by each role itself: 1 us a tile).
 //   tiles       256 x n on a CTA pair, n a multiple of 32 up to 256.  The
 //               weights' features lie along the MMA's M side and a group's
 //               tokens along its N side, so a tile is as wide as the group's
 //               rows need: a group of 300 rows costs the products of 320, not
 //               of 512, and a few tokens cost what their weights' bytes do.
-//               A group's rows are cut into tiles of nearly equal width.
 //   epilogue    A lane holds one feature, a column one token: neighbouring
 //               lanes exchange halves, and a warp writes 64 contiguous bytes
 //               of two tokens with each store.  A group's last rows need no
@@ -32,51 +39,42 @@
 #include "ptx_block.cuh"
 
 namespace spgemm {
-
-struct GroupedTile {
+// What a CTA's scheduler tells the other roles of a tile.
+struct alignas(16) GroupedTile {
+  int rows;         // output rows that exist; 0: there are no more tiles
   int group;
   int lane0;        // first feature
   int row0;         // first output row: of the tokens, or of dW_e
-  int rows;         // output rows that exist
   int width;        // the MMA's columns
+  int slots;        // ring slots of the sum
   int first;        // kWeight: first token of the group
-  int full, part, tail;  // kWeight: whole slots of 64 tokens, whole steps after them, a last partial step
-  __device__ int slots(const GroupedParams& p, int kind) const {
-    if (kind != kGroupedWeight) return (p.reduce + kBK - 1) / kBK;
-    return full + (part > 0) + tail;
-  }
+  int full;         // kWeight: whole slots of 64 tokens
+  int part;         // kWeight: whole steps after them
+  int tail;         // kWeight: 1 where a last partial step follows
+  int pad[2];
 };
-
-// Tile i of `tiles` (the least number of them) along `extent` columns: widths
-// are multiples of 32 and differ by one unit at most.
-__device__ __forceinline__ void grouped_split(int extent, int tiles, int i, int& at, int& width) {
-  const int units = (extent + kGroupedUnit - 1) / kGroupedUnit;
-  const int each = units / tiles, more = units - each * tiles;
-  at = (i * each + min(i, more)) * kGroupedUnit;
-  width = (each + (i < more ? 1 : 0)) * kGroupedUnit;
-}
+static_assert(sizeof(GroupedTile) == 48);
 
 // Tile t.  `offsets` and `first_tile` (tiles along the tokens before each
 // group) are this CTA's tables.
 template <int kKind>
 __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedParams& p, const int* offsets,
-                                                    const int* first_tile) {
+                                                    const int* first_tile, int cap) {
   GroupedTile x{};
   if constexpr (kKind == kGroupedWeight) {
-    const int tiles = (p.cols + p.cap - 1) / p.cap;
+    const int tiles = grouped_tiles(p.cols, cap);
     const int per = p.tiles_lane * tiles;
     x.group = t / per;
     const int r = t - x.group * per;
     x.lane0 = (r / tiles) * kGroupedLanes;
-    int at;
-    grouped_split(p.cols, tiles, r % tiles, at, x.width);
-    x.row0 = at;
-    x.rows = min(x.width, p.cols - at);
+    x.row0 = (r % tiles) * cap;
+    x.rows = min(cap, p.cols - x.row0);
     x.first = offsets[x.group];
     const int m = offsets[x.group + 1] - x.first;
     x.full = m / kBK;
     x.part = (m % kBK) / kGroupedTail;
-    x.tail = m % kGroupedTail != 0;
+    x.tail = m % kGroupedTail != 0 ? 1 : 0;
+    x.slots = x.full + (x.part > 0 ? 1 : 0) + x.tail;
   } else {
     int lo = 0, hi = p.groups;  // the last group whose first tile is not after t
     const int row = t / p.tiles_lane;  // (a group's tiles are tiles_lane times as many)
@@ -96,12 +94,12 @@ __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedParams& 
     const int high = min(8, tiles - 8 * g);
     const int s = r - g * 8 * p.tiles_lane;
     x.lane0 = (s / high) * kGroupedLanes;
-    int at;
-    const int m = offsets[lo + 1] - offsets[lo];
-    grouped_split(m, tiles, 8 * g + s % high, at, x.width);
+    const int at = (8 * g + s % high) * cap;
     x.row0 = offsets[lo] + at;
-    x.rows = min(x.width, m - at);
+    x.rows = min(cap, offsets[lo + 1] - x.row0);
+    x.slots = (p.reduce + kBK - 1) / kBK;
   }
+  x.width = (x.rows + kGroupedUnit - 1) / kGroupedUnit * kGroupedUnit;
   return x;
 }
 
@@ -132,17 +130,22 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   const int S = p.stages;
   const uint32_t ring_bytes = static_cast<uint32_t>(S) * kGroupedSlot;
   const uint32_t bar_base = sbase + ring_bytes;
-  constexpr uint32_t kBars = 8u * (2 * kGroupedStages + 5);
+  constexpr uint32_t kBars = 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead);
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (kGroupedStages + s); };
   auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * kGroupedStages + a); };
   auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * kGroupedStages + 2 + a); };
   const uint32_t done_bar = bar_base + 8u * (2 * kGroupedStages + 4);
+  auto next_full_bar = [&](int d) { return bar_base + 8u * (2 * kGroupedStages + 5 + d); };
+  auto next_empty_bar = [&](int d) { return bar_base + 8u * (2 * kGroupedStages + 5 + kGroupedAhead + d); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + ring_bytes + kBars);
-  int* offsets = reinterpret_cast<int*>(smem + ring_bytes + kBars + 16u);
+  int* cap_slot = reinterpret_cast<int*>(tmem_slot + 1);
+  // (the queue of tiles 16-byte aligned)
+  GroupedTile* queue = reinterpret_cast<GroupedTile*>(smem + ((ring_bytes + kBars + 8u + 15u) & ~15u));
+  int* offsets = reinterpret_cast<int*>(queue + kGroupedAhead);
   int* first_tile = offsets + p.groups + 1;
   if (SPGEMM_OUT_OF_BOUNDS(S >= 1 && S <= kGroupedStages &&
-                               (sbase - raw_addr) + ring_bytes + kBars + 16u + 8u * (p.groups + 1) <=
+                               (sbase - raw_addr) + ring_bytes + kBars + 24u + 48u * kGroupedAhead + 8u * (p.groups + 1) <=
                                    ptx::dynamic_smem_bytes(),
                            p, kCheckSmemLayout))
     return;
@@ -163,6 +166,10 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       ptx::mbar_init(tempty_bar(a), 2 * 8);
     }
     ptx::mbar_init(done_bar, 1);
+    for (int d = 0; d < kGroupedAhead; ++d) {
+      ptx::mbar_init(next_full_bar(d), 1);
+      ptx::mbar_init(next_empty_bar(d), leader ? 11 : 10);  // producers, MMA issuer, epilogue warps
+    }
     ptx::fence_barrier_init();
     ptx::tma_prefetch_desc(&maps.a);
     ptx::tma_prefetch_desc(&maps.b[0]);
@@ -185,11 +192,37 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   bad = __syncthreads_or(bad);
   if constexpr (kKind != kGroupedWeight) {
     if (warp == 0 && !bad) {
+      // The width of full tiles that takes the least time.
+      const int slots = (p.reduce + kBK - 1) / kBK;
+      int tiles[kGroupedCaps] = {};
+      float clocks[kGroupedCaps] = {};
+      for (int e = lane; e < p.groups; e += 32) {
+        const int m = offsets[e + 1] - offsets[e];
+#pragma unroll
+        for (int i = 0; i < kGroupedCaps; ++i) {
+          tiles[i] += grouped_tiles(m, grouped_cap(i));
+          clocks[i] += grouped_strip_clocks(m, grouped_cap(i), slots);
+        }
+      }
+      uint32_t best = 0xffffffffu;
+#pragma unroll
+      for (int i = 0; i < kGroupedCaps; ++i) {
+        const int n = __reduce_add_sync(0xffffffffu, tiles[i]) * p.tiles_lane;
+        float c = clocks[i];
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) c += __shfl_xor_sync(0xffffffffu, c, d);
+        c = grouped_clocks(c * static_cast<float>(p.tiles_lane), n, grouped_cap(i), slots, p.pairs);
+        // Positive floats order as their bits; two of those make room for the width.
+        best = min(best, (__float_as_uint(c) & ~3u) | static_cast<uint32_t>(i));
+      }
+      const int cap = grouped_cap(best & 3u);
+      static_assert(kGroupedCaps == 4);
+      if (lane == 0) *cap_slot = cap;
       int before = 0;
       for (int e0 = 0; e0 < p.groups; e0 += 32) {
         const int e = e0 + lane;
         const int m = e < p.groups ? offsets[e + 1] - offsets[e] : 0;
-        int n = (m + p.cap - 1) / p.cap;
+        int n = grouped_tiles(m, cap);
         for (int d = 1; d < 32; d *= 2) {
           const int up = __shfl_up_sync(0xffffffffu, n, d);
           if (lane >= d) n += up;
@@ -205,24 +238,41 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   ptx::tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
+  const int cap = kKind == kGroupedWeight ? p.cap : *cap_slot;
   int total = 0;
   if (!bad)
-    total = p.tiles_lane * (kKind == kGroupedWeight ? p.groups * ((p.cols + p.cap - 1) / p.cap)
-                                                    : first_tile[p.groups]);
+    total = p.tiles_lane * (kKind == kGroupedWeight ? p.groups * grouped_tiles(p.cols, cap) : first_tile[p.groups]);
   else if (blockIdx.x == 0 && threadIdx.x == 0)
     record_error(p.status, static_cast<int>(GEMM_ERR_INVALID_ARG), GEMM_CHECK_OFFSETS);
 
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer --
+  // The next tile for one thread of a role that has met `n` tiles so far; rows 0: none.
+  auto next_of = [&](int& n) -> GroupedTile {
+    const int d = n % kGroupedAhead;
+    const uint32_t parity = static_cast<uint32_t>(n / kGroupedAhead) & 1u;
+    ++n;
+    GroupedTile x{};
+    if (!wait_bounded(next_full_bar(d), parity, p, GEMM_WAIT_NEXT_TILE)) return x;
+    const uint32_t at = ptx::smem_addr(queue + d);
+    const uint4 v0 = ptx::ld_shared_v4(at), v1 = ptx::ld_shared_v4(at + 16u), v2 = ptx::ld_shared_v4(at + 32u);
+    memcpy(&x, &v0, 16);
+    memcpy(&x.width, &v1, 16);
+    memcpy(&x.part, &v2, 16);
+    ptx::mbar_arrive(next_empty_bar(d));
+    return x;
+  };
+
+  if (warp == 0 || warp == 11) {
+    // ----------------------------------------------------- TMA producers --
+    const bool for_a = warp == 0;  // the other brings B
     if (lane == 0) {
+      int met = 0;
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued = 0, issued_parity = 0;
       bool ok = true;
-      for (int t = walker; ok && t < total; t += p.pairs) {
-        const GroupedTile x = grouped_tile<kKind>(t, p, offsets, first_tile);
+      for (GroupedTile x = next_of(met); x.rows > 0; x = next_of(met)) {
         if (SPGEMM_OUT_OF_BOUNDS(x.group >= 0 && x.group < p.groups && x.width >= kGroupedUnit &&
-                                     x.width <= kGroupedCols && x.rows > 0 && x.lane0 >= 0 && x.lane0 < p.lanes,
+                                     x.width <= kGroupedCols && x.lane0 >= 0 && x.lane0 < p.lanes,
                                  p, kCheckTile)) {
           ok = false;
           break;
@@ -231,53 +281,52 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         const int a0 = x.lane0 + static_cast<int>(rank) * kBM;
         const int b0 = x.row0 + static_cast<int>(rank) * half;
         // kWeight: 64-column boxes; otherwise the smallest box of rows that holds them.
-        const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        const int box = grouped_box(x.width);
         const int boxes = (half + 63) / 64;
-        const int slots = x.slots(p, kKind);
-        for (int s = 0; s < slots; ++s) {
+        for (int s = 0; s < x.slots; ++s) {
           if (!wait_bounded(empty_bar(stage), phase ^ 1u, p, kDetailProducerEmpty)) {
             ok = false;
             break;
           }
-          const bool tail = kBN && x.tail && s == slots - 1;
-          const uint32_t bytes = !kBN ? kStageA + (static_cast<uint32_t>(kGroupedTail) << box) * (kBK * 2u)
-                                      : (tail ? kTailBytes : kBoxBytes) * static_cast<uint32_t>(2 + boxes);
+          const bool tail = kBN && x.tail && s == x.slots - 1;
           const uint32_t da = sbase + stage * kGroupedSlot, db = da + kStageA;
           const uint32_t fb = ptx::map_shared_rank(full_bar(stage), 0);
-          if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
-          // Test hook: the first slot of the first CTA is announced but never copied.
-          const bool skip = p.inject_fault == 1 && blockIdx.x == 0 && issued == 0;
-          if (!skip) {
-            if constexpr (!kBN) {
-              const int kx = s * kBK;
-              if constexpr (kAN) {
-                ptx::tma_load_3d_pair(da, &maps.a, a0, kx, x.group, fb);
-                ptx::tma_load_3d_pair(da + kBoxBytes, &maps.a, a0 + 64, kx, x.group, fb);
+          if (for_a) {
+            const uint32_t bytes = !kBN ? kStageA + (static_cast<uint32_t>(kGroupedTail) << box) * (kBK * 2u)
+                                        : (tail ? kTailBytes : kBoxBytes) * static_cast<uint32_t>(2 + boxes);
+            if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
+            // Test hook: the first slot of the first CTA is announced but never copied.
+            if (p.inject_fault != 1 || blockIdx.x != 0 || issued != 0) {
+              if constexpr (!kAN) {
+                ptx::tma_load_3d_pair(da, &maps.a, s * kBK, a0, x.group, fb);
               } else {
-                ptx::tma_load_3d_pair(da, &maps.a, kx, a0, x.group, fb);
+                const int at = !kBN ? s * kBK : tail ? 0 : x.first + s * kBK;
+                const int z = !kBN || tail ? x.group : 0;
+                const CUtensorMap* map = kBN && tail ? &maps.b[1] : &maps.a;
+                ptx::tma_load_3d_pair(da, map, a0, at, z, fb);
+                ptx::tma_load_3d_pair(da + kBoxBytes, map, a0 + 64, at, z, fb);
               }
-              ptx::tma_load_3d_pair(db, &maps.b[box], kx, b0, 0, fb);
-            } else {
-              const int at = tail ? 0 : x.first + s * kBK;
-              const int z = tail ? x.group : 0;
-              const CUtensorMap* ma = tail ? &maps.b[1] : &maps.a;
-              const CUtensorMap* mb = tail ? &maps.b[2] : &maps.b[0];
-              ptx::tma_load_3d_pair(da, ma, a0, at, z, fb);
-              ptx::tma_load_3d_pair(da + kBoxBytes, ma, a0 + 64, at, z, fb);
-              ptx::tma_load_3d_pair(db, mb, b0, at, z, fb);
-              if (boxes > 1) ptx::tma_load_3d_pair(db + kBoxBytes, mb, b0 + 64, at, z, fb);
             }
+            issued |= 1u << stage;
+            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          } else if constexpr (!kBN) {
+            ptx::tma_load_3d_pair(db, &maps.b[box], s * kBK, b0, 0, fb);
+          } else {
+            const int at = tail ? 0 : x.first + s * kBK;
+            const int z = tail ? x.group : 0;
+            const CUtensorMap* map = tail ? &maps.b[2] : &maps.b[0];
+            ptx::tma_load_3d_pair(db, map, b0, at, z, fb);
+            if (boxes > 1) ptx::tma_load_3d_pair(db + kBoxBytes, map, b0 + 64, at, z, fb);
           }
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
+        if (!ok) break;
       }
       // Every copy this pair started must have landed before it exits.
-      if (leader) {
+      if (leader && for_a) {
         for (int s = 0; s < S; ++s)
           if (issued & (1u << s))
             wait_bounded(full_bar(s), (issued_parity >> s) & 1u, p, kDetailProducerDrain);
@@ -292,9 +341,9 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int t = walker; ok && t < total; t += p.pairs) {
-        const GroupedTile x = grouped_tile<kKind>(t, p, offsets, first_tile);
-        const int slots = x.slots(p, kKind);
+      int met = 0;
+      for (GroupedTile x = next_of(met); ok && x.rows > 0; x = next_of(met)) {
+        const int slots = x.slots;
         if (slots == 0) continue;  // an empty group's dW: the epilogue writes zeros
         if (!wait_bounded_cluster<2>(tempty_bar(acc), acc_phase ^ 1u, p, kDetailMmaAccEmpty)) break;
         ptx::tc_fence_after_sync();
@@ -335,6 +384,22 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       wait_bounded(done_bar, 0, p, kDetailMmaDrain);
     }
     __syncwarp();
+  } else if (warp == 10) {
+    // -------------------------------------------------------- scheduler --
+    if (lane == 0) {
+      int n = 0;
+      for (int t = walker;; t += p.pairs, ++n) {
+        const int d = n % kGroupedAhead;
+        const uint32_t parity = static_cast<uint32_t>(n / kGroupedAhead) & 1u;
+        GroupedTile x{};
+        if (t < total) x = grouped_tile<kKind>(t, p, offsets, first_tile, cap);
+        if (!wait_bounded(next_empty_bar(d), parity ^ 1u, p, GEMM_WAIT_NEXT_FREE)) break;
+        queue[d] = x;
+        ptx::mbar_arrive(next_full_bar(d));
+        if (t >= total) break;
+      }
+    }
+    __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue --
     const int q = warp & 3;         // TMEM lane quarter
@@ -343,11 +408,20 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     if (kKind != kGroupedWeight && p.zero_rest && !bad)
       grouped_zero_rest(p, offsets[0], offsets[p.groups], static_cast<int>(blockIdx.x) * 8 + warp - 2,
                         static_cast<int>(gridDim.x) * 8, lane);
-    int acc = 0;
+    int acc = 0, met = 0;
     uint32_t acc_phase = 0;
-    for (int t = walker; t < total; t += p.pairs) {
-      const GroupedTile x = grouped_tile<kKind>(t, p, offsets, first_tile);
-      const bool some = x.slots(p, kKind) > 0;
+    auto next_of_warp = [&]() {
+      GroupedTile x{};
+      if (lane == 0) x = next_of(met);
+      x.rows = __shfl_sync(0xffffffffu, x.rows, 0);
+      x.group = __shfl_sync(0xffffffffu, x.group, 0);
+      x.lane0 = __shfl_sync(0xffffffffu, x.lane0, 0);
+      x.row0 = __shfl_sync(0xffffffffu, x.row0, 0);
+      x.slots = __shfl_sync(0xffffffffu, x.slots, 0);
+      return x;
+    };
+    for (GroupedTile x = next_of_warp(); x.rows > 0; x = next_of_warp()) {
+      const bool some = x.slots > 0;
       if (some) {
         int ready = 1;
         if (lane == 0) ready = wait_bounded<true>(tfull_bar(acc), acc_phase, p, kDetailEpiFull) ? 1 : 0;

@@ -25,7 +25,35 @@ constexpr int kGroupedCols = 256;     // and at most this
 constexpr int kGroupedTail = 16;      // tokens of one MMA step
 constexpr int kGroupedStages = 7;     // ring slots at most
 constexpr uint32_t kGroupedSlot = 2u * kStageA;  // A and B: 128 rows (or columns) x 64 each
-constexpr int kGroupedThreads = 64 + 128 * 2;
+constexpr int kGroupedThreads = 64 + 128 * 2 + 64;
+constexpr int kGroupedAhead = 4;      // tiles that a CTA's scheduler describes ahead
+
+// What a tile costs, in clocks of a CTA pair.  A ring slot: 64 a unit of 32
+// columns for the tensor cores, or what its copies take at the 64 bytes a clock
+// that an SM receives: 16 KiB of one operand and a box of 16 to 128 rows of the
+// other.  So a tile of 224 columns costs one of 256, and one of 32 more than
+// half of that; a group's rows make full tiles and one for the rest.  A tile's
+// start and end: 1500.
+__host__ __device__ constexpr int grouped_box(int width) { return width <= 32 ? 0 : width <= 64 ? 1 : width <= 128 ? 2 : 3; }
+__host__ __device__ constexpr float grouped_tile_clocks(int width, int slots) {
+  const int math = 2 * width, copies = 256 + (32 << grouped_box(width));
+  return static_cast<float>(slots) * static_cast<float>(math > copies ? math : copies) + 1500.0f;
+}
+// Widths of full tiles to choose from.
+constexpr int kGroupedCaps = 4;
+__host__ __device__ constexpr int grouped_cap(int i) { return kGroupedCols >> i; }
+// Tiles of a strip of `extent` columns, and their clocks.
+__host__ __device__ constexpr int grouped_tiles(int extent, int cap) { return (extent + cap - 1) / cap; }
+__host__ __device__ constexpr float grouped_strip_clocks(int extent, int cap, int slots) {
+  const int full = extent / cap, rest = extent - full * cap;
+  return static_cast<float>(full) * grouped_tile_clocks(cap, slots) + (rest > 0 ? grouped_tile_clocks(rest, slots) : 0.0f);
+}
+// Clocks of `tiles` tiles that take `clocks` in all on `pairs` walkers: an even
+// share, and what the last round leaves idle.
+__host__ __device__ constexpr float grouped_clocks(float clocks, int tiles, int cap, int slots, int pairs) {
+  const int idle = (tiles + pairs - 1) / pairs * pairs - tiles;
+  return (clocks + static_cast<float>(idle) * grouped_tile_clocks(cap, slots)) / static_cast<float>(pairs);
+}
 
 struct GroupedParams : Params {  // of Params: stages, bf16, status, timeout_ns, inject_fault
   const int64_t* offsets;
@@ -35,7 +63,7 @@ struct GroupedParams : Params {  // of Params: stages, bf16, status, timeout_ns,
   int lanes;           // extent along the lanes
   int cols;            // kWeight: rows n of dW_e
   int tiles_lane;      // tiles along the lanes
-  int cap;             // columns of a tile at most
+  int cap;             // kWeight: columns of a tile at most (the other kinds choose on the device)
   int zero_rest;
   int pairs;           // CTA pairs of the launch
   uint16_t* out;
@@ -53,7 +81,7 @@ struct GroupedMaps {
 // Shared memory beside the ring: the groups' offsets and first tile rows.
 inline size_t grouped_table_bytes(int groups) { return 2u * sizeof(int) * static_cast<size_t>(groups + 1); }
 inline size_t grouped_smem_bytes(int stages, int groups) {
-  return kAlignSlack + static_cast<size_t>(stages) * kGroupedSlot + 8u * (2 * kGroupedStages + 5) + 16u +
+  return kAlignSlack + static_cast<size_t>(stages) * kGroupedSlot + 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead) + 16u + 48u * kGroupedAhead + 16u +
          grouped_table_bytes(groups);
 }
 
