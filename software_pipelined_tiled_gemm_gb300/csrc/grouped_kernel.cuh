@@ -6,9 +6,11 @@
 //   sizes       The groups' offsets are read on the device.  Every CTA loads
 //               them, checks them and counts the tiles of each group, so the
 //               launch needs no more than an upper bound and the host no copy.
-//   producers   One thread issues a copy in some 50 to 90 clocks, and a slot takes
-//               two to four: A's and B's come from a warp each (dW of 32768 x
-//               4096 x 2048: see grouped.cu's figures).
+//   copies      A copy costs some 90 clocks beside its bytes, whoever issues it, so
+//               an operand stored along the sum comes as boxes of 64 columns x 128
+//               rows, two slices of 64 in a slot (boxes of 64 rows: dW took a tenth
+//               longer; boxes of two panels, 3- or 4-dimensional, longer still).
+//               A's and B's are issued by a warp each.
 //   schedule    Finding a tile's place takes some hundred instructions, and the
 //               producer is never far ahead of the tensor cores (a slot's copies
 //               take about as long as the ring's other slots last), so an
@@ -48,7 +50,7 @@ struct alignas(16) GroupedTile {
   int width;        // the MMA's columns
   int slots;        // ring slots of the sum
   int first;        // kWeight: first token of the group
-  int full;         // kWeight: whole slots of 64 tokens
+  int full;         // kWeight: slots whose tokens are all the group's
   int part;         // kWeight: whole steps after them
   int tail;         // kWeight: 1 where a last partial step follows
   int pad[2];
@@ -71,8 +73,8 @@ __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedParams& 
     x.rows = min(cap, p.cols - x.row0);
     x.first = offsets[x.group];
     const int m = offsets[x.group + 1] - x.first;
-    x.full = m / kBK;
-    x.part = (m % kBK) / kGroupedTail;
+    x.full = m / (kBK * p.slices);
+    x.part = (m % (kBK * p.slices)) / kGroupedTail;
     x.tail = m % kGroupedTail != 0 ? 1 : 0;
     x.slots = x.full + (x.part > 0 ? 1 : 0) + x.tail;
   } else {
@@ -97,7 +99,7 @@ __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedParams& 
     const int at = (8 * g + s % high) * cap;
     x.row0 = offsets[lo] + at;
     x.rows = min(cap, offsets[lo + 1] - x.row0);
-    x.slots = (p.reduce + kBK - 1) / kBK;
+    x.slots = (p.reduce + kBK * p.slices - 1) / (kBK * p.slices);
   }
   x.width = (x.rows + kGroupedUnit - 1) / kGroupedUnit * kGroupedUnit;
   return x;
@@ -119,7 +121,9 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     grouped_kernel(const __grid_constant__ GroupedMaps maps, const __grid_constant__ GroupedParams p) {
   constexpr bool kAN = kKind != kGroupedForward;   // A stored (sum) x (lanes)
   constexpr bool kBN = kKind == kGroupedWeight;    // B stored (sum) x (columns)
-  constexpr uint32_t kBoxBytes = 64u * kBK * 2u;   // MN-major box: 64 columns x 64 rows of the sum
+  // MN-major box: 64 columns x 64 (or, two slices a slot, 128) rows of the sum.
+  const uint32_t box_bytes = 64u * kBK * 2u * static_cast<uint32_t>(p.slices);
+  const uint32_t slot_a = kStageA * static_cast<uint32_t>(p.slices), slot_bytes = 2u * slot_a;
   constexpr uint32_t kTailBytes = 64u * kGroupedTail * 2u;
   constexpr uint32_t tmem_cols = 2u * kGroupedCols;
 
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const uint32_t sbase = ptx::smem_addr(smem);
   const int S = p.stages;
-  const uint32_t ring_bytes = static_cast<uint32_t>(S) * kGroupedSlot;
+  const uint32_t ring_bytes = static_cast<uint32_t>(S) * slot_bytes;
   const uint32_t bar_base = sbase + ring_bytes;
   constexpr uint32_t kBars = 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead);
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
@@ -289,34 +293,37 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             break;
           }
           const bool tail = kBN && x.tail && s == x.slots - 1;
-          const uint32_t da = sbase + stage * kGroupedSlot, db = da + kStageA;
+          const uint32_t da = sbase + stage * slot_bytes, db = da + slot_a;
           const uint32_t fb = ptx::map_shared_rank(full_bar(stage), 0);
           if (for_a) {
-            const uint32_t bytes = !kBN ? kStageA + (static_cast<uint32_t>(kGroupedTail) << box) * (kBK * 2u)
-                                        : (tail ? kTailBytes : kBoxBytes) * static_cast<uint32_t>(2 + boxes);
+            const uint32_t bytes =
+                !kBN ? slot_a + (static_cast<uint32_t>(kGroupedTail) << box) * (kBK * 2u) * static_cast<uint32_t>(p.slices)
+                     : (tail ? kTailBytes : box_bytes) * static_cast<uint32_t>(2 + boxes);
             if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
             // Test hook: the first slot of the first CTA is announced but never copied.
             if (p.inject_fault != 1 || blockIdx.x != 0 || issued != 0) {
               if constexpr (!kAN) {
-                ptx::tma_load_3d_pair(da, &maps.a, s * kBK, a0, x.group, fb);
+                for (int i = 0; i < p.slices; ++i)
+                  ptx::tma_load_3d_pair(da + i * kStageA, &maps.a, (s * p.slices + i) * kBK, a0, x.group, fb);
               } else {
-                const int at = !kBN ? s * kBK : tail ? 0 : x.first + s * kBK;
+                const int at = !kBN ? s * kBK * p.slices : tail ? 0 : x.first + s * kBK * p.slices;
                 const int z = !kBN || tail ? x.group : 0;
                 const CUtensorMap* map = kBN && tail ? &maps.b[1] : &maps.a;
                 ptx::tma_load_3d_pair(da, map, a0, at, z, fb);
-                ptx::tma_load_3d_pair(da + kBoxBytes, map, a0 + 64, at, z, fb);
+                ptx::tma_load_3d_pair(da + box_bytes, map, a0 + 64, at, z, fb);
               }
             }
             issued |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           } else if constexpr (!kBN) {
-            ptx::tma_load_3d_pair(db, &maps.b[box], s * kBK, b0, 0, fb);
+            for (int i = 0; i < p.slices; ++i)
+              ptx::tma_load_3d_pair(db + i * kStageA, &maps.b[box], (s * p.slices + i) * kBK, b0, 0, fb);
           } else {
-            const int at = tail ? 0 : x.first + s * kBK;
+            const int at = tail ? 0 : x.first + s * kBK * p.slices;
             const int z = tail ? x.group : 0;
             const CUtensorMap* map = tail ? &maps.b[2] : &maps.b[0];
             ptx::tma_load_3d_pair(db, map, b0, at, z, fb);
-            if (boxes > 1) ptx::tma_load_3d_pair(db + kBoxBytes, map, b0 + 64, at, z, fb);
+            if (boxes > 1) ptx::tma_load_3d_pair(db + box_bytes, map, b0 + 64, at, z, fb);
           }
           if (++stage == S) {
             stage = 0;
@@ -357,16 +364,20 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             break;
           }
           ptx::tc_fence_after_sync();
-          const uint32_t sa = sbase + stage * kGroupedSlot, sb = sa + kStageA;
-          const uint64_t a_desc = kAN ? ptx::smem_desc_mn_sw128(sa, kBoxBytes, 1024u) : ptx::smem_desc_k_sw128(sa);
-          const uint64_t b_desc = kBN ? ptx::smem_desc_mn_sw128(sb, kBoxBytes, 1024u) : ptx::smem_desc_k_sw128(sb);
-          constexpr uint32_t a_step = kAN ? 2048u / 16u : 2u, b_step = kBN ? 2048u / 16u : 2u;
-          int steps = kBK / kUmmaK;
+          const uint32_t sa = sbase + stage * slot_bytes, sb = sa + slot_a;
+          const uint64_t a_desc = kAN ? ptx::smem_desc_mn_sw128(sa, box_bytes, 1024u) : ptx::smem_desc_k_sw128(sa);
+          const uint64_t b_desc = kBN ? ptx::smem_desc_mn_sw128(sb, box_bytes, 1024u) : ptx::smem_desc_k_sw128(sb);
+          int steps = p.slices * (kBK / kUmmaK);
           if (kBN && s >= x.full) steps = s == x.full && x.part > 0 ? x.part : 1;
+          // A step: 32 bytes of a K-major row, the slices 16 KiB apart, or two atoms of 8 rows of the sum.
 #pragma unroll
-          for (int k = 0; k < kBK / kUmmaK; ++k)
+          for (int k = 0; k < kGroupedSlices * (kBK / kUmmaK); ++k) {
+            constexpr uint32_t kRows = 2048u / 16u, kSlice = kStageA / 16u;
+            const uint32_t along = static_cast<uint32_t>(k) / 4u * kSlice + static_cast<uint32_t>(k) % 4u * 2u;
             if (k < steps)
-              ptx::mma_f16_ss<2>(d_tmem, a_desc + a_step * k, b_desc + b_step * k, idesc, (s | k) != 0 ? 1u : 0u);
+              ptx::mma_f16_ss<2>(d_tmem, a_desc + (kAN ? kRows * k : along), b_desc + (kBN ? kRows * k : along), idesc,
+                                 (s | k) != 0 ? 1u : 0u);
+          }
           ptx::mma_commit_multicast_pair(empty_bar(stage), 0x3);
           if (++stage == S) {
             stage = 0;

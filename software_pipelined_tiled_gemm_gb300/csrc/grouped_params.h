@@ -24,16 +24,17 @@ constexpr int kGroupedUnit = 32;      // a tile's columns are a multiple of this
 constexpr int kGroupedCols = 256;     // and at most this
 constexpr int kGroupedTail = 16;      // tokens of one MMA step
 constexpr int kGroupedStages = 7;     // ring slots at most
-constexpr uint32_t kGroupedSlot = 2u * kStageA;  // A and B: 128 rows (or columns) x 64 each
+constexpr uint32_t kGroupedSlice = 2u * kStageA;  // A and B: 128 rows (or columns) x 64 of the sum each
+constexpr int kGroupedSlices = 2;     // of a ring slot at most
 constexpr int kGroupedThreads = 64 + 128 * 2 + 64;
 constexpr int kGroupedAhead = 4;      // tiles that a CTA's scheduler describes ahead
 
-// What a tile costs, in clocks of a CTA pair.  A ring slot: 64 a unit of 32
-// columns for the tensor cores, or what its copies take at the 64 bytes a clock
-// that an SM receives: 16 KiB of one operand and a box of 16 to 128 rows of the
-// other.  So a tile of 224 columns costs one of 256, and one of 32 more than
-// half of that; a group's rows make full tiles and one for the rest.  A tile's
-// start and end: 1500.
+// What a tile costs, in clocks of a CTA pair.  A slice of 64 of the sum: 64 a
+// unit of 32 columns for the tensor cores, or what its copies take at the 64
+// bytes a clock that an SM receives: 16 KiB of one operand and a box of 16 to
+// 128 rows of the other.  So a tile of 224 columns costs one of 256, and one of
+// 32 more than half of that; a group's rows make full tiles and one for the
+// rest.  A tile's start and end: 1500.
 __host__ __device__ constexpr int grouped_box(int width) { return width <= 32 ? 0 : width <= 64 ? 1 : width <= 128 ? 2 : 3; }
 __host__ __device__ constexpr float grouped_tile_clocks(int width, int slots) {
   const int math = 2 * width, copies = 256 + (32 << grouped_box(width));
@@ -65,6 +66,7 @@ struct GroupedParams : Params {  // of Params: stages, bf16, status, timeout_ns,
   int tiles_lane;      // tiles along the lanes
   int cap;             // kWeight: columns of a tile at most (the other kinds choose on the device)
   int zero_rest;
+  int slices;          // of 64 of the sum, in a ring slot
   int pairs;           // CTA pairs of the launch
   uint16_t* out;
   int64_t ldo;         // row pitch of the output; kWeight: of dW_e
@@ -80,8 +82,8 @@ struct GroupedMaps {
 
 // Shared memory beside the ring: the groups' offsets and first tile rows.
 inline size_t grouped_table_bytes(int groups) { return 2u * sizeof(int) * static_cast<size_t>(groups + 1); }
-inline size_t grouped_smem_bytes(int stages, int groups) {
-  return kAlignSlack + static_cast<size_t>(stages) * kGroupedSlot + 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead) + 16u + 48u * kGroupedAhead + 16u +
+inline size_t grouped_smem_bytes(int stages, int slices, int groups) {
+  return kAlignSlack + static_cast<size_t>(stages) * slices * kGroupedSlice + 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead) + 16u + 48u * kGroupedAhead + 16u +
          grouped_table_bytes(groups);
 }
 
