@@ -211,12 +211,10 @@ gemm_status_t run_product(const gemm_ops* ops, const Grouped& g, int kind, void*
   p.inject_fault = ops->debug_fault;
 
   if (ops->pairs < 1) return ops_fail(GEMM_ERR_UNSUPPORTED, "no CTA pair fits the device");
-  // Few rows a group: the weights' bytes count, and more slots are on their way in half the size.
-  p.slices = a->rows >= 128 * a->groups ? kGroupedSlices : 1;
   p.cap = kGroupedCols;
   int64_t tiles = p.tiles_lane * (a->rows / grouped_cap(kGroupedCaps - 1) + std::min(a->groups, a->rows));  // at most
   if (kind == kGroupedWeight) {
-    const int slots = static_cast<int>(a->rows / a->groups / kBK) + 2, strips = static_cast<int>(a->groups) * p.tiles_lane;
+    const int slots = static_cast<int>(a->rows / a->groups / kGroupedK) + 2, strips = static_cast<int>(a->groups) * p.tiles_lane;
     float best = -1.0f;
     for (int i = 0; i < kGroupedCaps; ++i) {
       const int cap = grouped_cap(i), n = strips * grouped_tiles(p.cols, cap);
@@ -229,22 +227,22 @@ gemm_status_t run_product(const gemm_ops* ops, const Grouped& g, int kind, void*
   }
   p.pairs = static_cast<int>(std::min<int64_t>(ops->pairs, tiles));
 
-  p.stages = kGroupedStages / p.slices;
-  while (p.stages > 1 && grouped_smem_bytes(p.stages, p.slices, p.groups) > ops->smem_optin) --p.stages;
-  const size_t smem = grouped_smem_bytes(p.stages, p.slices, p.groups);
+  p.stages = kGroupedStages;
+  while (p.stages > 1 && grouped_smem_bytes(p.stages, p.groups) > ops->smem_optin) --p.stages;
+  const size_t smem = grouped_smem_bytes(p.stages, p.groups);
   if (smem > ops->smem_optin) return ops_fail(GEMM_ERR_SMEM_BUDGET, "no ring fits shared memory");
 
   const CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   gemm_status_t st;
   if (kind == kGroupedWeight) {
-    st = encode_map(&maps.a, bf16, g.x, 1, 64, kBK * p.slices, l2);
-    if (st == GEMM_OK) st = encode_map(&maps.b[0], bf16, g.dy, 1, 64, kBK * p.slices, l2);
+    st = encode_map(&maps.a, bf16, g.x, 1, 64, kGroupedK, l2);
+    if (st == GEMM_OK) st = encode_map(&maps.b[0], bf16, g.dy, 1, 64, kGroupedK, l2);
     if (st == GEMM_OK) st = encode_map(&maps.b[1], bf16, g.tail_x, a->groups, 64, kGroupedTail, l2);
     if (st == GEMM_OK) st = encode_map(&maps.b[2], bf16, g.tail_dy, a->groups, 64, kGroupedTail, l2);
     maps.b[3] = maps.b[0];
   } else {
     st = kind == kGroupedForward ? encode_map(&maps.a, bf16, g.w, a->groups, kBK, kBM, l2)
-                                 : encode_map(&maps.a, bf16, g.w, a->groups, 64, kBK * p.slices, l2);
+                                 : encode_map(&maps.a, bf16, g.w, a->groups, 64, kGroupedK, l2);
     for (int i = 0; i < 4 && st == GEMM_OK; ++i)
       st = encode_map(&maps.b[i], bf16, kind == kGroupedForward ? g.x : g.dy, 1, kBK, kGroupedTail << i, l2);
   }

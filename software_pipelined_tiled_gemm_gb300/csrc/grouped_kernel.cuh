@@ -15,7 +15,10 @@
 //               producer is never far ahead of the tensor cores (a slot's copies
 //               take about as long as the ring's other slots last), so an
 //               eleventh warp describes a CTA's tiles ahead of time: the other
-//               roles read eight words (found by each role itself: 1 us a tile).
+//               roles read some words (found by each role itself: 1 us a tile).
+//               Pairs take tiles in turn: handed out from a counter as pairs become
+//               free they ended 1 to 2 % sooner where groups differ, and 17 % later
+//               where all pairs had the same number of equal tiles.
 //   tiles       256 x n on a CTA pair, n a multiple of 32 up to 256.  The
 //               weights' features lie along the MMA's M side and a group's
 //               tokens along its N side, so a tile is as wide as the group's
@@ -73,8 +76,8 @@ __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedParams& 
     x.rows = min(cap, p.cols - x.row0);
     x.first = offsets[x.group];
     const int m = offsets[x.group + 1] - x.first;
-    x.full = m / (kBK * p.slices);
-    x.part = (m % (kBK * p.slices)) / kGroupedTail;
+    x.full = m / kGroupedK;
+    x.part = (m % kGroupedK) / kGroupedTail;
     x.tail = m % kGroupedTail != 0 ? 1 : 0;
     x.slots = x.full + (x.part > 0 ? 1 : 0) + x.tail;
   } else {
@@ -99,7 +102,7 @@ __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedParams& 
     const int at = (8 * g + s % high) * cap;
     x.row0 = offsets[lo] + at;
     x.rows = min(cap, offsets[lo + 1] - x.row0);
-    x.slots = (p.reduce + kBK * p.slices - 1) / (kBK * p.slices);
+    x.slots = (p.reduce + kGroupedK - 1) / kGroupedK;
   }
   x.width = (x.rows + kGroupedUnit - 1) / kGroupedUnit * kGroupedUnit;
   return x;
@@ -121,9 +124,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     grouped_kernel(const __grid_constant__ GroupedMaps maps, const __grid_constant__ GroupedParams p) {
   constexpr bool kAN = kKind != kGroupedForward;   // A stored (sum) x (lanes)
   constexpr bool kBN = kKind == kGroupedWeight;    // B stored (sum) x (columns)
-  // MN-major box: 64 columns x 64 (or, two slices a slot, 128) rows of the sum.
-  const uint32_t box_bytes = 64u * kBK * 2u * static_cast<uint32_t>(p.slices);
-  const uint32_t slot_a = kStageA * static_cast<uint32_t>(p.slices), slot_bytes = 2u * slot_a;
+  constexpr uint32_t kBoxBytes = 64u * kGroupedK * 2u;  // MN-major box: 64 columns x 128 rows of the sum
   constexpr uint32_t kTailBytes = 64u * kGroupedTail * 2u;
   constexpr uint32_t tmem_cols = 2u * kGroupedCols;
 
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const uint32_t sbase = ptx::smem_addr(smem);
   const int S = p.stages;
-  const uint32_t ring_bytes = static_cast<uint32_t>(S) * slot_bytes;
+  const uint32_t ring_bytes = static_cast<uint32_t>(S) * kGroupedSlot;
   const uint32_t bar_base = sbase + ring_bytes;
   constexpr uint32_t kBars = 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead);
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   if constexpr (kKind != kGroupedWeight) {
     if (warp == 0 && !bad) {
       // The width of full tiles that takes the least time.
-      const int slots = (p.reduce + kBK - 1) / kBK;
+      const int slots = (p.reduce + kGroupedK - 1) / kGroupedK;
       int tiles[kGroupedCaps] = {};
       float clocks[kGroupedCaps] = {};
       for (int e = lane; e < p.groups; e += 32) {
@@ -293,37 +294,39 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             break;
           }
           const bool tail = kBN && x.tail && s == x.slots - 1;
-          const uint32_t da = sbase + stage * slot_bytes, db = da + slot_a;
+          const uint32_t da = sbase + stage * kGroupedSlot, db = da + kGroupedOperand;
           const uint32_t fb = ptx::map_shared_rank(full_bar(stage), 0);
           if (for_a) {
             const uint32_t bytes =
-                !kBN ? slot_a + (static_cast<uint32_t>(kGroupedTail) << box) * (kBK * 2u) * static_cast<uint32_t>(p.slices)
-                     : (tail ? kTailBytes : box_bytes) * static_cast<uint32_t>(2 + boxes);
+                !kBN ? kGroupedOperand + (static_cast<uint32_t>(kGroupedTail) << box) * (kGroupedK * 2u)
+                     : (tail ? kTailBytes : kBoxBytes) * static_cast<uint32_t>(2 + boxes);
             if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), 2u * bytes);
             // Test hook: the first slot of the first CTA is announced but never copied.
             if (p.inject_fault != 1 || blockIdx.x != 0 || issued != 0) {
               if constexpr (!kAN) {
-                for (int i = 0; i < p.slices; ++i)
-                  ptx::tma_load_3d_pair(da + i * kStageA, &maps.a, (s * p.slices + i) * kBK, a0, x.group, fb);
+#pragma unroll
+                for (int i = 0; i < kGroupedSlices; ++i)
+                  ptx::tma_load_3d_pair(da + i * kStageA, &maps.a, s * kGroupedK + i * kBK, a0, x.group, fb);
               } else {
-                const int at = !kBN ? s * kBK * p.slices : tail ? 0 : x.first + s * kBK * p.slices;
+                const int at = !kBN ? s * kGroupedK : tail ? 0 : x.first + s * kGroupedK;
                 const int z = !kBN || tail ? x.group : 0;
                 const CUtensorMap* map = kBN && tail ? &maps.b[1] : &maps.a;
                 ptx::tma_load_3d_pair(da, map, a0, at, z, fb);
-                ptx::tma_load_3d_pair(da + box_bytes, map, a0 + 64, at, z, fb);
+                ptx::tma_load_3d_pair(da + kBoxBytes, map, a0 + 64, at, z, fb);
               }
             }
             issued |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           } else if constexpr (!kBN) {
-            for (int i = 0; i < p.slices; ++i)
-              ptx::tma_load_3d_pair(db + i * kStageA, &maps.b[box], (s * p.slices + i) * kBK, b0, 0, fb);
+#pragma unroll
+            for (int i = 0; i < kGroupedSlices; ++i)
+              ptx::tma_load_3d_pair(db + i * kStageA, &maps.b[box], s * kGroupedK + i * kBK, b0, 0, fb);
           } else {
-            const int at = tail ? 0 : x.first + s * kBK * p.slices;
+            const int at = tail ? 0 : x.first + s * kGroupedK;
             const int z = tail ? x.group : 0;
             const CUtensorMap* map = tail ? &maps.b[2] : &maps.b[0];
             ptx::tma_load_3d_pair(db, map, b0, at, z, fb);
-            if (boxes > 1) ptx::tma_load_3d_pair(db + box_bytes, map, b0 + 64, at, z, fb);
+            if (boxes > 1) ptx::tma_load_3d_pair(db + kBoxBytes, map, b0 + 64, at, z, fb);
           }
           if (++stage == S) {
             stage = 0;
@@ -364,14 +367,14 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             break;
           }
           ptx::tc_fence_after_sync();
-          const uint32_t sa = sbase + stage * slot_bytes, sb = sa + slot_a;
-          const uint64_t a_desc = kAN ? ptx::smem_desc_mn_sw128(sa, box_bytes, 1024u) : ptx::smem_desc_k_sw128(sa);
-          const uint64_t b_desc = kBN ? ptx::smem_desc_mn_sw128(sb, box_bytes, 1024u) : ptx::smem_desc_k_sw128(sb);
-          int steps = p.slices * (kBK / kUmmaK);
+          const uint32_t sa = sbase + stage * kGroupedSlot, sb = sa + kGroupedOperand;
+          const uint64_t a_desc = kAN ? ptx::smem_desc_mn_sw128(sa, kBoxBytes, 1024u) : ptx::smem_desc_k_sw128(sa);
+          const uint64_t b_desc = kBN ? ptx::smem_desc_mn_sw128(sb, kBoxBytes, 1024u) : ptx::smem_desc_k_sw128(sb);
+          int steps = kGroupedK / kUmmaK;
           if (kBN && s >= x.full) steps = s == x.full && x.part > 0 ? x.part : 1;
           // A step: 32 bytes of a K-major row, the slices 16 KiB apart, or two atoms of 8 rows of the sum.
 #pragma unroll
-          for (int k = 0; k < kGroupedSlices * (kBK / kUmmaK); ++k) {
+          for (int k = 0; k < kGroupedK / kUmmaK; ++k) {
             constexpr uint32_t kRows = 2048u / 16u, kSlice = kStageA / 16u;
             const uint32_t along = static_cast<uint32_t>(k) / 4u * kSlice + static_cast<uint32_t>(k) % 4u * 2u;
             if (k < steps)

@@ -23,21 +23,23 @@ constexpr int kGroupedLanes = 256;    // of a CTA pair
 constexpr int kGroupedUnit = 32;      // a tile's columns are a multiple of this (16 a CTA)
 constexpr int kGroupedCols = 256;     // and at most this
 constexpr int kGroupedTail = 16;      // tokens of one MMA step
-constexpr int kGroupedStages = 7;     // ring slots at most
-constexpr uint32_t kGroupedSlice = 2u * kStageA;  // A and B: 128 rows (or columns) x 64 of the sum each
-constexpr int kGroupedSlices = 2;     // of a ring slot at most
+constexpr int kGroupedStages = 3;     // ring slots
+constexpr int kGroupedSlices = 2;     // of 64 of the sum, in a slot
+constexpr int kGroupedK = kGroupedSlices * kBK;
+constexpr uint32_t kGroupedOperand = kGroupedSlices * kStageA;  // 128 rows (or columns) of A or B
+constexpr uint32_t kGroupedSlot = 2u * kGroupedOperand;
 constexpr int kGroupedThreads = 64 + 128 * 2 + 64;
 constexpr int kGroupedAhead = 4;      // tiles that a CTA's scheduler describes ahead
 
-// What a tile costs, in clocks of a CTA pair.  A slice of 64 of the sum: 64 a
+// What a tile costs, in clocks of a CTA pair.  A slot: 128 a
 // unit of 32 columns for the tensor cores, or what its copies take at the 64
-// bytes a clock that an SM receives: 16 KiB of one operand and a box of 16 to
+// bytes a clock that an SM receives: 32 KiB of one operand and boxes of 16 to
 // 128 rows of the other.  So a tile of 224 columns costs one of 256, and one of
 // 32 more than half of that; a group's rows make full tiles and one for the
 // rest.  A tile's start and end: 1500.
 __host__ __device__ constexpr int grouped_box(int width) { return width <= 32 ? 0 : width <= 64 ? 1 : width <= 128 ? 2 : 3; }
 __host__ __device__ constexpr float grouped_tile_clocks(int width, int slots) {
-  const int math = 2 * width, copies = 256 + (32 << grouped_box(width));
+  const int math = 4 * width, copies = 512 + (64 << grouped_box(width));
   return static_cast<float>(slots) * static_cast<float>(math > copies ? math : copies) + 1500.0f;
 }
 // Widths of full tiles to choose from.
@@ -66,7 +68,6 @@ struct GroupedParams : Params {  // of Params: stages, bf16, status, timeout_ns,
   int tiles_lane;      // tiles along the lanes
   int cap;             // kWeight: columns of a tile at most (the other kinds choose on the device)
   int zero_rest;
-  int slices;          // of 64 of the sum, in a ring slot
   int pairs;           // CTA pairs of the launch
   uint16_t* out;
   int64_t ldo;         // row pitch of the output; kWeight: of dW_e
@@ -82,8 +83,8 @@ struct GroupedMaps {
 
 // Shared memory beside the ring: the groups' offsets and first tile rows.
 inline size_t grouped_table_bytes(int groups) { return 2u * sizeof(int) * static_cast<size_t>(groups + 1); }
-inline size_t grouped_smem_bytes(int stages, int slices, int groups) {
-  return kAlignSlack + static_cast<size_t>(stages) * slices * kGroupedSlice + 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead) + 16u + 48u * kGroupedAhead + 16u +
+inline size_t grouped_smem_bytes(int stages, int groups) {
+  return kAlignSlack + static_cast<size_t>(stages) * kGroupedSlot + 8u * (2 * kGroupedStages + 5 + 2 * kGroupedAhead) + 16u + 48u * kGroupedAhead + 16u +
          grouped_table_bytes(groups);
 }
 
