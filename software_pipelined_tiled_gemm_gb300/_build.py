@@ -36,7 +36,7 @@ SOURCES = ["gemm_api.cu", "gemm_bn64.cu", "gemm_bn128.cu", "gemm_bn256.cu", "gem
            "gemm_pair256.cu", "pad.cu", "fill.cu", "noalloc.cu", "ops_api.cu", "block_nt.cu",
            "block_nn.cu", "block_tn.cu", "block_diag_out.cu", "block_diag_rows.cu",
            "block_diag_cols.cu", "block_gated.cu", "block_gated_bwd.cu", "pack.cu", "ffn.cu", "few_tokens.cu",
-           "orthogonal.cu", "orthogonal_small.cu", "logprobs.cu", "grouped.cu",
+           "orthogonal.cu", "orthogonal_small.cu", "logprobs.cu", "grouped.cu", "grouped_few.cu",
            "layer_norm.cu", "layer_norm_f16.cu",
            "layer_norm_bf16.cu", "layer_norm_f32.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

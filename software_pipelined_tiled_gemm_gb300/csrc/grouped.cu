@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "grouped_few.h"
 #include "ops_internal.h"
 
 using namespace spgemm;
@@ -157,6 +158,7 @@ size_t layout(const gemm_ops* ops, const gemm_grouped_args_t* a, bool backward, 
     m->ld = ldp;
   };
   if (a->rows == 0) return 0;
+  if (!backward && grouped_few_fits(ops, a)) return 0;  // goes over the operands as they lie
   if (!backward || a->dw) padded(&g->x);
   if (!backward || a->dx) padded(&g->w);
   if (backward && (a->dx || a->dw)) padded(&g->dy);
@@ -312,7 +314,12 @@ gemm_status_t gemm_grouped_run(gemm_ops_t* ops, const gemm_grouped_args_t* args,
   OpsDevice guard(ops->device);
   if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
-  const cudaError_t e = launch_pack(g.pack, ops->sm_count, stream);
+  cudaError_t e;
+  if (grouped_few_fits(ops, args)) {
+    e = grouped_few_launch(ops, args, stream);
+    return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "grouped product launch");
+  }
+  e = launch_pack(g.pack, ops->sm_count, stream);
   if (e != cudaSuccess) return ops_cuda_fail(e, "padding copy launch");
   return run_product(ops, g, kGroupedForward, args->y, stream);
 }

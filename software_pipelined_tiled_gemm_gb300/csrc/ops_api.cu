@@ -11,6 +11,7 @@
 #include <new>
 
 #include "few_tokens.h"
+#include "grouped_few.h"
 #include "grouped_params.h"
 #include "ops_internal.h"
 #include "orthogonal_small.h"
@@ -351,6 +352,7 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
   if (e == cudaSuccess) e = adamw_set_smem();
   if (e == cudaSuccess) e = small_newton_init(ops);
   if (e == cudaSuccess) e = few_tokens_init(ops);
+  if (e == cudaSuccess) e = grouped_few_init(ops);
   if (e == cudaSuccess) e = cudaMalloc(&ops->d_status, 4 * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(ops->d_status, 0, 4 * sizeof(int));
   // cudaMemset runs on the default stream; another stream's first call must not overtake it.

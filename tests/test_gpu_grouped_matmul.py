@@ -103,6 +103,35 @@ def test_product_and_gradients(size, dt):
     sg.check_operators()
 
 
+# Few rows a group: passes over the weights as they lie.  Shares of blocks that span several groups,
+# groups without rows, more rows in a group than are held at a time, rows too long for eight tokens.
+FEW = [
+    ([1, 0, 1, 1], 2048, 512), ([0] * 7 + [2], 300, 1000), ([1] * 60, 16, 72), ([0, 3, 0, 0, 1], 1000, 257),
+    ([9] + [0] * 7, 136, 1000), ([33] + [0] * 31 + [1], 200, 640), ([40, 1] + [0] * 20, 57, 333),
+    ([2, 1], 40, 20001), ([1, 2, 0, 1], 24, 24000), ([70] + [1] * 9, 33, 129),
+]
+
+
+@pytest.mark.parametrize("size", FEW, ids=str)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_few_rows_a_group(size, dt):
+    sizes, n, k = size
+    for before, after in ((0, 0), (2, 3)):
+        x, w, dy, off = inputs(sizes, n, k, dt, sum(sizes) + n, before, after)
+        want = reference(x, w, dy, off, dt)["y"]
+        y = sg.grouped_matmul(x, w, off)
+        assert_within(y, want, before)
+        assert torch.equal(y, sg.grouped_matmul(x, w, off))
+        odd = torch.full((w.numel() + 8,), float("nan"), dtype=w.dtype, device="cuda")[1:1 + w.numel()].view(w.shape)
+        odd.copy_(w)
+        out = torch.full_like(y, 7.0)
+        assert_within(sg.grouped_matmul(x, odd, off)[before:len(x) - after], tuple(t[before:len(x) - after] for t in want), "odd")
+        sg.grouped_matmul(x, w, off, out=out)
+        assert (out[:before] == 7).all() and (out[len(x) - after:] == 7).all()
+        assert torch.equal(out[before:len(x) - after], y[before:len(x) - after])
+    sg.check_operators()
+
+
 def test_many_groups():
     sizes = [(i * 7) % 5 for i in range(1000)]
     ts = inputs(sizes, 40, 96, "bf16", seed=2, after=2)
@@ -171,10 +200,12 @@ def test_each_gradient_alone():
     assert sg.grouped_matmul_backward(dy, x, w, off, need=(False, False)) == (None, None)
 
 
+@pytest.mark.parametrize("groups", [2, 5])      # tiles, and passes over the weights
 @pytest.mark.parametrize("off", [[0, 4, 3], [-1, 4, 8], [0, 4, 9], [2, 1, 8], [0, 1 << 40, 8]])
-def test_wrong_offsets_are_reported_and_write_nothing(off):
+def test_wrong_offsets_are_reported_and_write_nothing(off, groups):
+    off = off + off[-1:] * (groups - 2)
     x = torch.randn(8, 64, device="cuda").bfloat16()
-    w = torch.randn(2, 32, 64, device="cuda").bfloat16()
+    w = torch.randn(groups, 32, 64, device="cuda").bfloat16()
     dy = torch.randn(8, 32, device="cuda").bfloat16()
     off = torch.tensor(off, device="cuda")
     y, dx, dw = (torch.full_like(t, 7.0) for t in (dy, x, w))
