@@ -281,11 +281,12 @@ typedef struct {
 typedef struct {
   const gemm_adamw_tensor_t* tensors;  /* on the host; not needed after the call */
   int64_t count;
+  int64_t state_elements;   /* of exp_avg and of exp_avg_sq: gemm_adamw_state_elements */
   int bits;                 /* of the states: 32 or 8 */
-  void* exp_avg;            /* fp32 or e4m3, gemm_adamw_state_elements of them, 16-byte aligned */
+  void* exp_avg;            /* fp32 or e4m3, 16-byte aligned */
   void* exp_avg_sq;
   float* scales;            /* bits 8: 2 x blocks, of exp_avg and of exp_avg_sq */
-  int64_t* step;            /* on the device: steps made so far; the call adds one */
+  int64_t* step;            /* on the device: steps made so far, below 2^32; the call adds one */
   double lr;                /* used where lr_device is NULL */
   const float* lr_device;
   double beta1, beta2;      /* in [0, 1) */

@@ -75,7 +75,8 @@ struct Job {
   void* exp_avg_sq;
   float* scales;          // of exp_avg, then (scale_step later) of exp_avg_sq
   int64_t scale_step;
-  const int64_t* step;
+  unsigned long long* step;
+  int last;               // 1: the call's last launch, which counts the step
   const float* lr_device;
   const float* scale;
   float lr, beta1, beta2, one_less1, one_less2, ln_beta1, ln_beta2, eps, one;
@@ -255,7 +256,13 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? kOcc8 : kOcc32) adamw_k
   for (int i = 0; i < R::kSlots - 1; ++i) fetch(i, i);
 
   // 1 - beta^t = -expm1(t ln beta), which keeps its bits where beta^t is near 1.
-  const int64_t t = *job.step + 1;
+  const uint32_t t = static_cast<uint32_t>(*job.step) + 1u;
+  if (job.last) {
+    // Thread blocks that have read the step are counted above its 32 bits; the
+    // last one to read it counts the step, and the kernel needs it no more.
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(job.step, 1ull << 32) >> 32 == gridDim.x - 1) *job.step = t;
+  }
   const float lr = job.lr_device ? *job.lr_device : job.lr;
   const float factor = job.scale ? *job.scale : 1.0f;
   const float rate = lr / -expm1f(static_cast<float>(t) * job.ln_beta1);
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? kOcc8 : kOcc32) adamw_k
       const float sv = br <= 0x7f800000u ? fmaxf(__fmul_rn(__uint_as_float(br), 1.0f / 448.0f), kLeast) : __uint_as_float(br);
       const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
       const F32x2 ims = both_f32(im), ivs = both_f32(iv), down = both_f32(kLeast);
-      const uint32_t dither = static_cast<uint32_t>(state) * 0xC13FA9A9u + static_cast<uint32_t>(t) * 0x91E10DA5u;
+      const uint32_t dither = static_cast<uint32_t>(state) * 0xC13FA9A9u + t * 0x91E10DA5u;
       uint32_t wm[2] = {0u, 0u}, s[kEach];
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
@@ -407,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? kOcc8 : kOcc32) adamw_k
   }
 }
 
+// The step of a call whose tensors are all empty.
 __global__ void count_kernel(int64_t* step) {
   ptx::pdl_launch_dependents();
   ptx::pdl_wait_prior_grid();
@@ -455,6 +463,9 @@ gemm_status_t check(const gemm_adamw_args_t* a) {
       return ops_fail(GEMM_ERR_INVALID_ARG, "tensor %lld is not aligned to its elements", at);
   }
   if (total > kBlock * kOpsMaxDim) return ops_fail(GEMM_ERR_INVALID_ARG, "more than 2^39 elements");
+  if (a->state_elements != total)
+    return ops_fail(GEMM_ERR_INVALID_ARG, "state buffers of %lld elements, %lld needed", (long long)a->state_elements,
+                    (long long)total);
   if (total > 0) {
     if (!a->exp_avg || !a->exp_avg_sq || (a->bits == 8 && !a->scales)) return ops_fail(GEMM_ERR_INVALID_ARG, "a state is NULL");
     if ((reinterpret_cast<uintptr_t>(a->exp_avg) | reinterpret_cast<uintptr_t>(a->exp_avg_sq)) & 15u)
@@ -506,7 +517,8 @@ gemm_status_t check_overlap(const gemm_adamw_args_t* a) {
 }
 
 template <int kBits, int kTensors>
-cudaError_t run(const gemm_ops* ops, const gemm_adamw_args_t* a, int64_t first, int64_t count, int64_t state, int64_t total, cudaStream_t stream) {
+cudaError_t run(const gemm_ops* ops, const gemm_adamw_args_t* a, int64_t first, int64_t count, int64_t state, int64_t total,
+                bool last, cudaStream_t stream) {
   Job<kTensors> job;
   job.count = 0;
   // Chunks of eight blocks (one a warp), longer ones where there are many: a
@@ -538,7 +550,8 @@ cudaError_t run(const gemm_ops* ops, const gemm_adamw_args_t* a, int64_t first, 
   job.exp_avg_sq = a->exp_avg_sq;
   job.scales = a->scales;
   job.scale_step = total / kBlock;
-  job.step = a->step;
+  job.step = reinterpret_cast<unsigned long long*>(a->step);
+  job.last = last ? 1 : 0;
   job.lr_device = a->lr_device;
   job.scale = a->scale;
   job.lr = static_cast<float>(a->lr);
@@ -596,21 +609,23 @@ gemm_status_t gemm_adamw(gemm_ops_t* ops, const gemm_adamw_args_t* args, void* s
   if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
   const int64_t total = gemm_adamw_state_elements(args->tensors, args->count);
-  int64_t state = 0;
+  int64_t state = 0, done = 0;
   cudaError_t e = cudaSuccess;
-  for (int64_t first = 0; first < args->count && e == cudaSuccess; first += kMostTensors) {
+  for (int64_t first = 0; first < args->count && done < total && e == cudaSuccess; first += kMostTensors) {
     const int64_t count = std::min<int64_t>(kMostTensors, args->count - first);
     const bool few = count <= kFewTensors;
+    done += gemm_adamw_state_elements(args->tensors + first, count);
+    const bool last = done == total;  // (later tensors are empty)
     if (args->bits == 32)
-      e = few ? run<32, kFewTensors>(ops, args, first, count, state, total, stream)
-              : run<32, kMostTensors>(ops, args, first, count, state, total, stream);
+      e = few ? run<32, kFewTensors>(ops, args, first, count, state, total, last, stream)
+              : run<32, kMostTensors>(ops, args, first, count, state, total, last, stream);
     else
-      e = few ? run<8, kFewTensors>(ops, args, first, count, state, total, stream)
-              : run<8, kMostTensors>(ops, args, first, count, state, total, stream);
-    state += gemm_adamw_state_elements(args->tensors + first, count);
+      e = few ? run<8, kFewTensors>(ops, args, first, count, state, total, last, stream)
+              : run<8, kMostTensors>(ops, args, first, count, state, total, last, stream);
+    state = done;
   }
   if (e != cudaSuccess) return ops_cuda_fail(e, "AdamW launch");
-  e = launch(count_kernel, 1, 1, 0, stream, args->step);
+  if (total == 0) e = launch(count_kernel, 1, 1, 0, stream, args->step);
   return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "AdamW step count launch");
 }
 

@@ -35,6 +35,9 @@
 //               zeros (grouped.cu): the next group's rows would be products'
 //               operands otherwise, and zero times their NaN is NaN.
 //
+// Under the power cap a busy wait costs clocks, so all of them suspend (1 % of
+// long calls back to back).
+//
 // Every sum has a fixed order, so results repeat bit for bit.
 #pragma once
 
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         const int box = grouped_box(x.width);
         const int boxes = (half + 63) / 64;
         for (int s = 0; s < x.slots; ++s) {
-          if (!wait_bounded(empty_bar(stage), phase ^ 1u, p, kDetailProducerEmpty)) {
+          if (!wait_bounded<true>(empty_bar(stage), phase ^ 1u, p, kDetailProducerEmpty)) {
             ok = false;
             break;
           }
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         const uint32_t idesc = ptx::instr_desc_f16(kGroupedLanes, x.width, p.bf16 != 0, kBN) |
                                (kAN ? 1u << 15 : 0u);
         for (int s = 0; s < slots; ++s) {
-          if (!wait_bounded(full_bar(stage), phase, p, kDetailMmaFull) ||
+          if (!wait_bounded<true>(full_bar(stage), phase, p, kDetailMmaFull) ||
               SPGEMM_OUT_OF_BOUNDS(stage >= 0 && stage < S, p, kCheckMmaSlot)) {
             ok = false;
             break;
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         const uint32_t parity = static_cast<uint32_t>(n / kGroupedAhead) & 1u;
         GroupedTile x{};
         if (t < total) x = grouped_tile<kKind>(t, p, offsets, first_tile, cap);
-        if (!wait_bounded(next_empty_bar(d), parity ^ 1u, p, GEMM_WAIT_NEXT_FREE)) break;
+        if (!wait_bounded<true>(next_empty_bar(d), parity ^ 1u, p, GEMM_WAIT_NEXT_FREE)) break;
         queue[d] = x;
         ptx::mbar_arrive(next_full_bar(d));
         if (t >= total) break;

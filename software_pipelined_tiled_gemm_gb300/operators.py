@@ -19,6 +19,7 @@ import collections
 import ctypes
 import functools
 import itertools
+import operator
 import struct
 import threading
 
@@ -87,7 +88,7 @@ class AdamWTensor(ctypes.Structure):
 
 class AdamWArgs(ctypes.Structure):
     """gemm_adamw_args_t"""
-    _fields_ = [("tensors", _vp), ("count", _i64), ("bits", _ci), ("exp_avg", _vp),
+    _fields_ = [("tensors", _vp), ("count", _i64), ("state_elements", _i64), ("bits", _ci), ("exp_avg", _vp),
                 ("exp_avg_sq", _vp), ("scales", _vp), ("step", _vp), ("lr", _d),
                 ("lr_device", _vp), ("beta1", _d), ("beta2", _d), ("eps", _d), ("scale", _vp)]
 
@@ -694,21 +695,28 @@ def _table(count):
     return struct.Struct("=" + "QQQqiiif" * count)
 
 
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
 def _adamw_list(tensors, name, index, types):
-    """(pointers, type codes, shapes) of a list of tensors."""
+    """(pointers, type codes, shapes) of a list of tensors.  (map, not a loop: a
+    step of many small tensors is bound by what the host does for each.)"""
+    import torch
+    t = torch.Tensor
     try:
-        on = [t.get_device() for t in tensors]
-        contiguous = all([t.is_contiguous() for t in tensors])
-        codes = [types.get(t.dtype, -1) for t in tensors]
-    except AttributeError:
+        on = set(map(t.get_device, tensors))
+        contiguous = all(map(t.is_contiguous, tensors))
+        dtypes = list(map(_dtype_of, tensors))
+        at, shapes = list(map(t.data_ptr, tensors)), list(map(_shape_of, tensors))
+    except TypeError:
         raise ValueError("%s must be CUDA tensors" % name) from None
-    if on != [index] * len(on):
+    if on and on != {index}:
         raise ValueError("%s must be CUDA tensors on the same device as the states" % name)
     if not contiguous:
         raise ValueError("%s must be contiguous" % name)
-    if -1 in codes:
-        raise TypeError("%s must be %s" % (name, " or ".join(str(t)[6:] for t in types)))
-    return [t.data_ptr() for t in tensors], codes, [t.shape for t in tensors]
+    if not types.keys() >= set(dtypes):
+        raise TypeError("%s must be %s" % (name, " or ".join(str(d)[6:] for d in types)))
+    return at, map(types.get, dtypes), shapes
 
 
 def adamw(params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None,
@@ -761,13 +769,14 @@ def adamw(params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0
     decay = itertools.repeat(float(weight_decay)) if isinstance(weight_decay, (int, float)) else weight_decay
     if not isinstance(decay, itertools.repeat) and len(decay) != n:
         raise ValueError("weight_decay must be a number, or one for each tensor")
-    sizes = [s.numel() for s in shapes]
-    blocks = sum([(s + ADAMW_BLOCK - 1) // ADAMW_BLOCK for s in sizes])
+    sizes = list(map(torch.Size.numel, shapes))
+    _on_cuda(device, m, "state")
+    size = m.numel()
     if scales is None:
-        want = ((m, torch.float32, (blocks * ADAMW_BLOCK,)), (v, torch.float32, (blocks * ADAMW_BLOCK,)))
+        want = ((m, torch.float32, (size,)), (v, torch.float32, (size,)))
     else:
-        want = ((m, torch.float8_e4m3fn, (blocks * ADAMW_BLOCK,)), (v, torch.float8_e4m3fn, (blocks * ADAMW_BLOCK,)),
-                (scales, torch.float32, (2, blocks)))
+        want = ((m, torch.float8_e4m3fn, (size,)), (v, torch.float8_e4m3fn, (size,)),
+                (scales, torch.float32, (2, size // ADAMW_BLOCK)))
     for t, dtype, shape in want + ((step, torch.int64, ()),):
         _on_cuda(device, t, "state")
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
@@ -782,7 +791,7 @@ def adamw(params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0
                 raise ValueError("%s must be one float32" % name)
     table = _table(n).pack(*itertools.chain.from_iterable(
         zip(p_at, g_at, c_at, sizes, p_type, g_type, c_type, decay)))
-    a = AdamWArgs(ctypes.cast(table, _vp), n, 32 if scales is None else 8, m.data_ptr(), v.data_ptr(), _ptr(scales),
+    a = AdamWArgs(ctypes.cast(table, _vp), n, size, 32 if scales is None else 8, m.data_ptr(), v.data_ptr(), _ptr(scales),
                   step.data_ptr(), lr, _ptr(rate), betas[0], betas[1], eps, _ptr(scale))
     stream = _stream(device)
     _check(lib.gemm_adamw(_handle(device), ctypes.byref(a), stream), "gemm_adamw")

@@ -331,6 +331,19 @@ def test_streams_and_graph(bits):
         assert torch.equal(x.float(), y.float())
 
 
+def test_no_elements_still_count_the_step():
+    empty = [torch.empty(0, device="cuda"), torch.empty(3, 0, device="cuda")]
+    state = sg.adamw_state(empty)
+    for i in range(3):
+        sg.adamw(empty, empty, state, 1e-2)
+        assert int(state.step) == i + 1
+    # Empty tensors at the end of a list longer than a launch's table.
+    case = Case([(5,)] * 512 + [(0,)] * 20, bits=32, seed=12)
+    want, t = case.want(1e-2)
+    sg.adamw(case.params, case.grads, case.state, 1e-2)
+    case.check(want, t)
+
+
 def test_refusals():
     case = Case([(300,), (20, 20)], copy="bf16", bits=8, seed=11)
     p, g, s, c = case.params, case.grads, case.state, case.copies
@@ -347,7 +360,7 @@ def test_refusals():
     refuse(ValueError, "length", p, g[:1], s, 1e-2)
     refuse(ValueError, "shapes", p, [g[0], g[1].view(-1)], s, 1e-2)
     refuse(ValueError, "contiguous", p, [g[0], g[1].t()], s, 1e-2)
-    refuse(ValueError, "state", p[:1], g[:1], s, 1e-2)
+    refuse(sg.GemmError, "state", p[:1], g[:1], s, 1e-2)
     refuse(ValueError, "state", p, g, s._replace(scales=None), 1e-2)
     refuse(ValueError, "CUDA", [p[0].cpu(), p[1]], g, s, 1e-2)
     refuse(ValueError, "lr", p, g, s, torch.tensor([1.0, 2.0], device="cuda"))
