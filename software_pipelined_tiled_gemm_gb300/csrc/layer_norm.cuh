@@ -45,7 +45,7 @@
 namespace spgemm {
 namespace {
 
-constexpr int kAhead = 3;        // rows of a group on their way or in work, at most
+constexpr int kAhead = 3;        // rows of a group on their way or in work, at most (six: no faster)
 constexpr int kItems = 32;       // columns of a thread, at most
 constexpr int kSingles = 8;      // where they are read one by one
 constexpr int kMinThreads = 256; // of a block: smaller groups share one
@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
   constexpr int kPairs = (kVec + 1) / 2;
   constexpr int kGroups = block_threads(kGroup) / kGroup;
   constexpr bool kHeld = kGroup <= 256;  // weights in registers
+  constexpr bool kKept = kGroup <= 256 && kVec > 1;  // and h and g between the two passes over a row
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ F32x2 red_all[kGroup > 32 ? 2 * block_threads(kGroup) / 32 : 1];
   ptx::pdl_launch_dependents();
@@ -481,8 +482,9 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
           ed[i] = dy[row * p.lddy + tid + i * kGroup];
         }
     }
-    // dy, h and g of this thread's vector i; both passes over the row take them from
-    // shared memory (or the elements' registers), which costs less than holding them.
+    // dy, h and g of this thread's vector i, from shared memory (or the elements'
+    // registers).  The second pass over the row finds h and g in registers where one
+    // block an SM leaves it enough of them (16384 x 4096: 78 us, 72 us so).
     auto values = [&](int i, F32x2 (&d)[kPairs], F32x2 (&h)[kPairs], F32x2 (&g)[kPairs]) {
       if constexpr (kVec > 1) {
         load_cols<T, kVec>(from_x + i * (kGroup * kVec), h);
@@ -499,6 +501,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
       }
     };
     F32x2 gs = 0, ghs = 0;
+    F32x2 hs[kKept ? kVecs : 1][kPairs], gk[kKept ? kVecs : 1][kPairs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
       if (tid + i * kGroup < vecs) {
@@ -506,6 +509,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
         values(i, d, h, g);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
+          if (kKept) hs[kKept ? i : 0][j] = h[j], gk[kKept ? i : 0][j] = g[j];
           dw[i][j] = fma_f32x2(d[j], h[j], dw[i][j]);
           db[i][j] = add_f32x2(db[i][j], d[j]);
           gs = add_f32x2(gs, g[j]);
@@ -521,9 +525,11 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
       for (int i = 0; i < kVecs; ++i)
         if (tid + i * kGroup < vecs) {
           F32x2 d[kPairs], h[kPairs], g[kPairs];
-          values(i, d, h, g);
+          if (!kKept) values(i, d, h, g);
 #pragma unroll
-          for (int j = 0; j < kPairs; ++j) d[j] = fma_f32x2(h[j], m2, fma_f32x2(g[j], scale, m1));
+          for (int j = 0; j < kPairs; ++j)
+            d[j] = kKept ? fma_f32x2(hs[kKept ? i : 0][j], m2, fma_f32x2(gk[kKept ? i : 0][j], scale, m1))
+                         : fma_f32x2(h[j], m2, fma_f32x2(g[j], scale, m1));
           store_cols<T, kVec>(out + i * (kGroup * kVec), d);
         }
     }
