@@ -63,8 +63,8 @@ struct Entry {
   float decay;           // weight decay
 };
 
-// Tables of two sizes: a launch's arguments cost time to send (a table of 512
-// entries 3 us more than one of 32).
+// Tables of two sizes: a launch's arguments cost the host time (the call of 98
+// tensors takes it 4.8 us with 512 entries, 4.2 us with 128).
 constexpr int kFewTensors = 32, kMostTensors = 512;
 template <int kTensors>
 struct Job {
