@@ -142,7 +142,7 @@ gemm_status_t gemm_layer_norm_backward_workspace(gemm_ops_t* ops, const gemm_lay
   if (st != GEMM_OK) return st;
   *bytes = 0;
   if (args->rows > 0 && (args->dweight || args->dbias))
-    *bytes = static_cast<size_t>(layer_norm_backward_grid_f32(ops, args->rows, args->cols)) * 2 * args->cols * sizeof(float);
+    *bytes = static_cast<size_t>(layer_norm_backward_blocks(ops, args->rows, args->cols)) * 2 * args->cols * sizeof(float);
   return GEMM_OK;
 }
 

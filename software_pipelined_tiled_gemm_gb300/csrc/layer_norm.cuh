@@ -16,15 +16,20 @@
 // sum or a sum of squares that leaves fp32's range is taken again, of x / n or
 // of 2^-64 d.
 //
-// Groups loop over rows.  Where rows are 16-byte aligned a thread copies its
-// own vectors of the next rows to shared memory asynchronously (nobody else
-// reads them, so no barrier is needed), which keeps rows of every group on
-// their way while one is reduced.  Rows that are not aligned are read element
-// by element, lanes side by side.  The arithmetic runs on pairs of values, and
-// a thread has many columns, so that the reductions over a row (some 25
-// instructions each) cost little: 16384 rows of 4096 bf16, forward, took 89 us
-// with scalars and 16 columns a thread, 45 us so (one call, cold; in a stream of
-// calls forward and backward take 117 us, 672 MB, 5.7 TB/s).
+// Groups loop over rows.  A thread copies its vectors of the next rows to shared
+// memory asynchronously, which keeps rows of every group on their way while one
+// is reduced; nobody else reads them, so no barrier is needed.  Rows that are not
+// 16-byte aligned, or of no whole number of vectors (kShifted), go by the aligned
+// vectors that cover them: a group's rows are a multiple of 8 (fp32: 4) apart, so
+// all of them begin at the same place of a vector, and a thread has the same
+// columns in each, as with aligned rows.  Only what a row's first and last vector
+// holds of other rows is cleared, and its own elements there are written one by
+// one.  (A matrix whose rows begin elsewhere in a vector than x's is read or
+// written element by element.)  The arithmetic runs on pairs of values, and a
+// thread has many columns, so that the reductions over a row (some 25
+// instructions each) cost little.
+//
+// FIGURES
 //
 // The weights' gradients: a thread sums its columns over its rows in fp32
 // registers; each block leaves one partial, and a second kernel adds those in
@@ -48,7 +53,6 @@ namespace {
 
 constexpr int kAhead = 3;        // rows of a group on their way or in work, at most
 constexpr int kItems = 32;       // columns of a thread, at most
-constexpr int kSingles = 8;      // where they are read one by one
 constexpr int kMinThreads = 256; // of a block: smaller groups share one
 constexpr float kDown = 5.421010862427522e-20f;  // 2^-64
 
@@ -87,38 +91,45 @@ __device__ __forceinline__ uint32_t word_of(F32x2 v) {
   return w;
 }
 
-// kN neighbouring columns from p (16-byte aligned, or kN 1), in pairs; a
-// single column has its pair's other value 0.
-template <typename T, int kN>
-__device__ __forceinline__ void load_cols(const T* p, F32x2 (&v)[(kN + 1) / 2]) {
-  if constexpr (kN == 1) {
-    v[0] = pack_f32(to_float(*p), 0.0f);
-  } else if constexpr (std::is_same_v<T, float>) {
-#pragma unroll
-    for (int i = 0; i < kN / 4; ++i) {
-      const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[i];
-      v[2 * i] = a.x;
-      v[2 * i + 1] = a.y;
-    }
+// Elements of 16 bytes.
+template <typename T>
+constexpr int kVecOf = 16 / static_cast<int>(sizeof(T));
+
+template <typename T>
+__device__ __forceinline__ void from_words(uint4 a, F32x2 (&v)[kVecOf<T> / 2]) {
+  if constexpr (std::is_same_v<T, float>) {
+    v[0] = pack_f32(__uint_as_float(a.x), __uint_as_float(a.y));
+    v[1] = pack_f32(__uint_as_float(a.z), __uint_as_float(a.w));
   } else {
-    static_assert(kN == 8);
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
     v[0] = pair_of<T>(a.x);
     v[1] = pair_of<T>(a.y);
     v[2] = pair_of<T>(a.z);
     v[3] = pair_of<T>(a.w);
   }
 }
-template <typename T, int kN>
-__device__ __forceinline__ void store_cols(T* p, const F32x2 (&v)[(kN + 1) / 2]) {
-  if constexpr (kN == 1) {
-    *p = from_float<T>(unpack_f32(v[0]).x);
-  } else if constexpr (std::is_same_v<T, float>) {
-    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
+template <typename T>
+__device__ __forceinline__ uint4 to_words(const F32x2 (&v)[kVecOf<T> / 2]) {
+  if constexpr (std::is_same_v<T, float>) {
+    const float2 a = unpack_f32(v[0]), b = unpack_f32(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(word_of<T>(v[0]), word_of<T>(v[1]), word_of<T>(v[2]), word_of<T>(v[3]));
+    return make_uint4(word_of<T>(v[0]), word_of<T>(v[1]), word_of<T>(v[2]), word_of<T>(v[3]));
   }
 }
+// kN neighbouring columns from p (16-byte aligned), in pairs.
+template <typename W, int kN>
+__device__ __forceinline__ void load_cols(const W* p, F32x2 (&v)[kN / 2]) {
+  constexpr int kEach = kVecOf<W>;
+#pragma unroll
+  for (int i = 0; i < kN / kEach; ++i) {
+    F32x2 part[kEach / 2];
+    from_words<W>(reinterpret_cast<const uint4*>(p)[i], part);
+#pragma unroll
+    for (int j = 0; j < kEach / 2; ++j) v[i * (kEach / 2) + j] = part[j];
+  }
+}
+
+__device__ __forceinline__ int bytes_past(const void* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u); }
 
 __device__ __forceinline__ void copy_async16(void* smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(smem)), "l"(src) : "memory");
@@ -134,6 +145,80 @@ __device__ __forceinline__ void copy_async_wait(int ahead) {
   else
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
+
+// A thread's vectors of its group's rows.
+template <typename T, bool kShifted, int kGroup>
+struct Share {
+  static constexpr int kVec = kVecOf<T>;
+  int tid, cols;
+  int back;   // elements of a row's first vector before the row
+  int vecs;   // of a row
+  int used;   // of a thread at most, in any group
+
+  // `row`: the group's first
+  __device__ __forceinline__ Share(int tid_, int cols_, const T* row) : tid(tid_), cols(cols_) {
+    back = kShifted ? bytes_past(row) / static_cast<int>(sizeof(T)) : 0;
+    vecs = (back + cols + kVec - 1) / kVec;
+    used = (cols + (kShifted ? kVec - 1 : 0) + kVec * kGroup - 1) / (kVec * kGroup);
+  }
+  __device__ __forceinline__ bool has(int i) const { return tid + i * kGroup < vecs; }
+  __device__ __forceinline__ int col(int i) const { return (tid + i * kGroup) * kVec - back; }  // of vector i's first element
+  __device__ __forceinline__ bool partial(int i) const { return kShifted && (col(i) < 0 || col(i) + kVec > cols); }
+  __device__ __forceinline__ bool in(int c) const { return !kShifted || (c >= 0 && c < cols); }
+  __device__ __forceinline__ bool fits(const T* row) const { return !kShifted || bytes_past(row) == back * static_cast<int>(sizeof(T)); }
+
+  // Elements of vector i that are not the row's become zero.
+  template <int kPairs>
+  __device__ __forceinline__ void clear(int i, F32x2 (&v)[kPairs]) const {
+    if (!partial(i)) return;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const float2 f = unpack_f32(v[j]);
+      v[j] = pack_f32(in(col(i) + 2 * j) ? f.x : 0.0f, in(col(i) + 2 * j + 1) ? f.y : 0.0f);
+    }
+  }
+
+  // Copies a row to its place in the ring (`to`: this thread's).  Nothing behind
+  // the row is read, nor anything before the matrix.
+  template <int kVecs>
+  __device__ __forceinline__ void fetch(uint4* to, const T* row, const T* matrix, bool fit) const {
+    const T* src = row + (tid * kVec - back);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      if (!has(i)) continue;
+      if constexpr (!kShifted) {
+        copy_async16(to + i * kGroup, src + i * (kGroup * kVec));
+      } else if (fit && (i > 0 || src >= matrix)) {
+        const int bytes = min(16, (cols - col(i)) * static_cast<int>(sizeof(T)));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(to + i * kGroup)),
+                     "l"(src + i * (kGroup * kVec)), "r"(bytes)
+                     : "memory");
+      } else {
+        T* one = reinterpret_cast<T*>(to + i * kGroup);
+        for (int j = 0; j < kVec; ++j) one[j] = in(col(i) + j) ? row[col(i) + j] : from_float<T>(0.0f);
+      }
+    }
+  }
+
+  // Vector i of a row of results.
+  __device__ __forceinline__ void store(int i, T* row, bool fit, const F32x2 (&v)[kVec / 2]) const {
+    const uint4 y = to_words<T>(v);
+    T* to = row + (tid * kVec - back) + i * (kGroup * kVec);
+    if (!kShifted || (fit && !partial(i))) {
+      *reinterpret_cast<uint4*>(to) = y;
+      return;
+    }
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      if (!in(col(i) + j)) continue;
+      if constexpr (sizeof(T) == 2)
+        reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+      else
+        reinterpret_cast<uint32_t*>(to)[j] = w[j];
+    }
+  }
+};
 
 constexpr int block_threads(int group) { return group < kMinThreads ? kMinThreads : group; }
 
@@ -191,23 +276,28 @@ constexpr int weights_at(int group) {
   return group == 32 || (group <= 256 && sizeof(W) == 4) ? kInRegisters : kInShared;
 }
 
-// fp32 weights of columns [col, col + kN), in pairs.
+// fp32 weights of columns [col, col + kN), in pairs; `cols`: of the row, which may
+// not have all of them (0: it has, and they are aligned).
 template <typename W, int kN>
-__device__ __forceinline__ void weights_of(const void* base, int col, float otherwise, F32x2 (&out)[(kN + 1) / 2]) {
+__device__ __forceinline__ void weights_of(const void* base, int col, int cols, float otherwise, F32x2 (&out)[kN / 2]) {
+  const W* w = static_cast<const W*>(base) + col;
   if (base == nullptr) {
 #pragma unroll
-    for (int j = 0; j < (kN + 1) / 2; ++j) out[j] = both_f32(otherwise);
-  } else if constexpr (kN == 4 && !std::is_same_v<W, float>) {
-    static_assert(kN != 4, "rows of fp32 have fp32 weights");
-  } else {
-    load_cols<W, kN>(static_cast<const W*>(base) + col, out);
+    for (int j = 0; j < kN / 2; ++j) out[j] = both_f32(otherwise);
+  } else if (cols > 0 && (col < 0 || col + kN > cols || bytes_past(w) != 0)) {
+    auto at = [&](int j) { return col + j >= 0 && col + j < cols ? to_float(w[j]) : 0.0f; };
+#pragma unroll
+    for (int j = 0; j < kN / 2; ++j) out[j] = pack_f32(at(2 * j), at(2 * j + 1));
+  } else if constexpr (kN >= kVecOf<W>) {  // (rows of fp32 have fp32 weights)
+    load_cols<W, kN>(w, out);
   }
 }
 
-template <typename T, typename W, int kVec, int kGroup, int kCols, int kBlocks>
+template <typename T, typename W, bool kShifted, int kGroup, int kBlocks>
 __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel(const LayerNormJob p) {
-  constexpr int kVecs = kCols / kVec;           // vectors of a thread
-  constexpr int kPairs = (kVec + 1) / 2;        // pairs of a vector
+  constexpr int kVec = kVecOf<T>;
+  constexpr int kVecs = kItems / kVec;          // vectors of a thread
+  constexpr int kPairs = kVec / 2;              // pairs of a vector
   constexpr int kGroups = block_threads(kGroup) / kGroup;
   constexpr int kWeights = weights_at<W>(kGroup);
   extern __shared__ __align__(16) uint8_t ring[];
@@ -216,9 +306,10 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
   const int tid = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
   F32x2* red = red_all + (kGroup > 32 ? group * 2 * (kGroup / 32) : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-  const int vecs = p.cols / kVec;                                   // of a row
-  const int used = (vecs + kGroup - 1) / kGroup;                    // of a thread
+  const int edge = kShifted ? p.cols : 0;
   const T* x = static_cast<const T*>(p.x);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  const Share<T, kShifted, kGroup> share(tid, p.cols, x + row * p.ldx);
   const W* weights = nullptr;  // kInShared: columns as in memory
   const W* biases = nullptr;
   uint8_t* rows = ring;
@@ -227,67 +318,60 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
   if constexpr (kWeights == kInRegisters) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if (tid + i * kGroup < vecs) {
-        weights_of<W, kVec>(p.weight, (tid + i * kGroup) * kVec, 1.0f, w[i]);
-        weights_of<W, kVec>(p.bias, (tid + i * kGroup) * kVec, 0.0f, b[i]);
+      if (share.has(i)) {
+        weights_of<W, kVec>(p.weight, share.col(i), edge, 1.0f, w[i]);
+        weights_of<W, kVec>(p.bias, share.col(i), edge, 0.0f, b[i]);
       }
   }
   if constexpr (kWeights == kInShared) {
-    // (Each thread reads back what it wrote itself.)
-    W* to = reinterpret_cast<W*>(ring);
+    // (Each thread reads back what it wrote itself, or another group wrote there too.)
+    const int wide = kShifted ? share.used * kGroup * kVec : p.cols;
+    W* to = reinterpret_cast<W*>(ring) + (kShifted ? group * 2 * wide : 0);
     weights = to;
-    biases = to + p.cols;
+    biases = to + wide;
     auto bring = [&](W* dst, const void* base) {
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
-        const int c = (tid + i * kGroup) * kVec;
-        if (c >= p.cols) continue;
-        if constexpr (kVec == 1) {
-          dst[c] = static_cast<const W*>(base)[c];
+        if (!share.has(i)) continue;
+        const W* src = static_cast<const W*>(base) + share.col(i);
+        W* own = dst + (tid + i * kGroup) * kVec;
+        if (kShifted && (share.partial(i) || bytes_past(src) != 0)) {
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) own[j] = share.in(share.col(i) + j) ? src[j] : from_float<W>(0.0f);
         } else {
 #pragma unroll
           for (int j = 0; j < kVec * static_cast<int>(sizeof(W)) / 16; ++j)
-            *reinterpret_cast<uint4*>(dst + c + j * (16 / sizeof(W))) =
-                *reinterpret_cast<const uint4*>(static_cast<const W*>(base) + c + j * (16 / sizeof(W)));
+            reinterpret_cast<uint4*>(own)[j] = reinterpret_cast<const uint4*>(src)[j];
         }
       }
     };
     if (p.weight) bring(to, p.weight);
-    if (p.bias) bring(to + p.cols, p.bias);
+    if (p.bias) bring(to + wide, p.bias);
     rows += p.weight_bytes;
   }
-  T* mine = reinterpret_cast<T*>(rows) + (static_cast<size_t>(group) * p.ahead * used * kGroup + tid) * kVec;
+  const int row_vecs = share.used * kGroup;  // in the ring
+  uint4* mine = reinterpret_cast<uint4*>(rows) + group * p.ahead * row_vecs + tid;
   int turn = 0;
+  const bool fit = share.fits(static_cast<const T*>(p.out) + row * p.cols);
 
-  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
   auto fetch = [&](int64_t r, int slot) {
-    if (r < p.rows) {
-      const T* src = x + r * p.ldx + tid * kVec;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (tid + i * kGroup < vecs) copy_async16(mine + (slot * used + i) * (kGroup * kVec), src + i * (kGroup * kVec));
-    }
+    if (r < p.rows) share.template fetch<kVecs>(mine + slot * row_vecs, x + r * p.ldx, x, true);
     copy_async_commit();
   };
-  if constexpr (kVec > 1)
-    for (int s = 0; s < p.ahead - 1; ++s) fetch(row + s * step, s);
+  for (int s = 0; s < p.ahead - 1; ++s) fetch(row + s * step, s);
 
   for (int slot = 0; row < p.rows; row += step) {
     F32x2 v[kVecs][kPairs];
-    const T* from;
-    if constexpr (kVec > 1) {
-      fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
-      copy_async_wait(p.ahead);
-      from = mine + slot * used * (kGroup * kVec);
-      slot = slot == p.ahead - 1 ? 0 : slot + 1;
-    } else {
-      from = x + row * p.ldx + tid;
-    }
+    fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
+    copy_async_wait(p.ahead);
+    const uint4* from = mine + slot * row_vecs;
+    slot = slot == p.ahead - 1 ? 0 : slot + 1;
     F32x2 sum = 0;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      if (tid + i * kGroup < vecs) {
-        load_cols<T, kVec>(from + i * (kGroup * kVec), v[i]);
+      if (share.has(i)) {
+        from_words<T>(from[i * kGroup], v[i]);
+        share.clear(i, v[i]);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) sum = add_f32x2(sum, v[i][j]);
       }
@@ -297,7 +381,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
       sum = 0;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
-        if (tid + i * kGroup < vecs)
+        if (share.has(i))
 #pragma unroll
           for (int j = 0; j < kPairs; ++j) sum = fma_f32x2(v[i][j], both_f32(p.inv), sum);
       mean = group_sum<kGroup>(both(sum), red, turn);
@@ -306,13 +390,12 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
     const F32x2 minus = both_f32(-mean);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if (tid + i * kGroup < vecs) {
+      if (share.has(i)) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) v[i][j] = add_f32x2(v[i][j], minus);
+        share.clear(i, v[i]);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          if constexpr (kVec == 1)  // the pair's other value stays 0
-            v[i][j] = pack_f32(unpack_f32(v[i][j]).x - mean, 0.0f);
-          else
-            v[i][j] = add_f32x2(v[i][j], minus);
           lows = add_f32x2(lows, v[i][j]);
           squares = fma_f32x2(v[i][j], v[i][j], squares);
         }
@@ -323,7 +406,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
       F32x2 s = 0;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
-        if (tid + i * kGroup < vecs)
+        if (share.has(i))
 #pragma unroll
           for (int j = 0; j < kPairs; ++j) {
             const F32x2 d = mul_f32x2(v[i][j], both_f32(kDown));
@@ -336,26 +419,25 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
       p.stats[p.rows + row] = low;
       p.stats[2 * p.rows + row] = rstd;
     }
-    T* out = static_cast<T*>(p.out) + row * p.cols + tid * kVec;
+    T* out = static_cast<T*>(p.out) + row * p.cols;
     const F32x2 scale = both_f32(rstd), shift = both_f32(-low * rstd);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if (tid + i * kGroup < vecs) {
+      if (share.has(i)) {
         F32x2 wi[kPairs], bi[kPairs], y[kPairs];
-        const int col = (tid + i * kGroup) * kVec;
         if constexpr (kWeights == kInShared) {
-          weights_of<W, kVec>(p.weight ? weights : nullptr, col, 1.0f, wi);
-          weights_of<W, kVec>(p.bias ? biases : nullptr, col, 0.0f, bi);
+          weights_of<W, kVec>(p.weight ? weights : nullptr, (tid + i * kGroup) * kVec, 0, 1.0f, wi);
+          weights_of<W, kVec>(p.bias ? biases : nullptr, (tid + i * kGroup) * kVec, 0, 0.0f, bi);
         } else if constexpr (kWeights == kInMemory) {
-          weights_of<W, kVec>(p.weight, col, 1.0f, wi);
-          weights_of<W, kVec>(p.bias, col, 0.0f, bi);
+          weights_of<W, kVec>(p.weight, share.col(i), edge, 1.0f, wi);
+          weights_of<W, kVec>(p.bias, share.col(i), edge, 0.0f, bi);
         }
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const F32x2 h = fma_f32x2(v[i][j], scale, shift);
           y[j] = kWeights == kInRegisters ? fma_f32x2(h, w[i][j], b[i][j]) : fma_f32x2(h, wi[j], bi[j]);
         }
-        store_cols<T, kVec>(out + i * (kGroup * kVec), y);
+        share.store(i, out, fit, y);
       }
   }
 }
@@ -407,13 +489,12 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const LayerNormJob p
   }
 }
 
-template <typename T, typename W, int kVec, int kGroup, int kCols, int kBlocks>
-__global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kernel(const LayerNormJob p) {
-  constexpr int kVecs = kCols / kVec;
-  constexpr int kPairs = (kVec + 1) / 2;
+template <typename T, typename W, bool kShifted, int kGroup>
+__global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(const LayerNormJob p) {
+  constexpr int kVec = kVecOf<T>, kVecs = kItems / kVec, kPairs = kVec / 2;
   constexpr int kGroups = block_threads(kGroup) / kGroup;
   constexpr bool kHeld = kGroup <= 256;  // weights in registers
-  constexpr bool kKept = kGroup <= 256 && kVec > 1;  // and h and g between the two passes over a row
+  constexpr bool kKept = kGroup <= 256;  // and h and g between the two passes over a row
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ F32x2 red_all[kGroup > 32 ? 2 * block_threads(kGroup) / 32 : 1];
   ptx::pdl_launch_dependents();
@@ -421,33 +502,29 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
   const int tid = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
   F32x2* red = red_all + (kGroup > 32 ? group * 2 * (kGroup / 32) : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-  const int vecs = p.cols / kVec;
-  const int used = (vecs + kGroup - 1) / kGroup;
-  // [slot][x, dy][vector][thread]
-  T* mine = reinterpret_cast<T*>(ring) + (static_cast<size_t>(group) * p.ahead * 2 * used * kGroup + tid) * kVec;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
   const T* x = static_cast<const T*>(p.x);
   const T* dy = static_cast<const T*>(p.dy);
+  const Share<T, kShifted, kGroup> share(tid, p.cols, x + row * p.ldx);
+  const bool fit = share.fits(static_cast<const T*>(p.out) + row * p.cols), fit_dy = share.fits(dy + row * p.lddy);
+  const int edge = kShifted ? p.cols : 0;
+  // [slot][x, dy][vector][thread]
+  const int row_vecs = share.used * kGroup;
+  uint4* mine = reinterpret_cast<uint4*>(ring) + group * p.ahead * 2 * row_vecs + tid;
   int turn = 0;
   F32x2 dw[kVecs][kPairs], db[kVecs][kPairs], w[kHeld ? kVecs : 1][kPairs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) dw[i][j] = db[i][j] = 0;
-    if (kHeld && tid + i * kGroup < vecs) weights_of<W, kVec>(p.weight, (tid + i * kGroup) * kVec, 1.0f, w[kHeld ? i : 0]);
+    if (kHeld && share.has(i)) weights_of<W, kVec>(p.weight, share.col(i), edge, 1.0f, w[kHeld ? i : 0]);
   }
 
-  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
   auto fetch = [&](int64_t r, int slot) {
     if (r < p.rows) {
-      const T* sx = x + r * p.ldx + tid * kVec;
-      const T* sd = dy + r * p.lddy + tid * kVec;
-      T* to = mine + slot * 2 * used * (kGroup * kVec);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (tid + i * kGroup < vecs) {
-          copy_async16(to + i * (kGroup * kVec), sx + i * (kGroup * kVec));
-          copy_async16(to + (used + i) * (kGroup * kVec), sd + i * (kGroup * kVec));
-        }
+      uint4* to = mine + slot * 2 * row_vecs;
+      share.template fetch<kVecs>(to, x + r * p.ldx, x, true);
+      share.template fetch<kVecs>(to + row_vecs, dy + r * p.lddy, dy, fit_dy);
     }
     copy_async_commit();
   };
@@ -459,46 +536,29 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
       next_rstd = __ldg(p.stats + 2 * p.rows + r);
     }
   };
-  if constexpr (kVec > 1)
-    for (int s = 0; s < p.ahead - 1; ++s) fetch(row + s * step, s);
+  for (int s = 0; s < p.ahead - 1; ++s) fetch(row + s * step, s);
   fetch_stats(row);
 
   for (int slot = 0; row < p.rows; row += step) {
     const float rstd = next_rstd;
     const F32x2 minus = both_f32(-next_mean), scale = both_f32(rstd), shift = both_f32(-next_low * rstd);
     fetch_stats(row + step);
-    const T *from_x, *from_d;
-    T ex[kVec == 1 ? kVecs : 1], ed[kVec == 1 ? kVecs : 1];
-    if constexpr (kVec > 1) {
-      fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
-      copy_async_wait(p.ahead);
-      from_x = mine + slot * 2 * used * (kGroup * kVec);
-      from_d = from_x + used * (kGroup * kVec);
-      slot = slot == p.ahead - 1 ? 0 : slot + 1;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (tid + i * kGroup < vecs) {
-          ex[i] = x[row * p.ldx + tid + i * kGroup];
-          ed[i] = dy[row * p.lddy + tid + i * kGroup];
-        }
-    }
-    // dy, h and g of this thread's vector i, from shared memory (or the elements'
-    // registers).  The second pass over the row finds h and g in registers where one
+    fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
+    copy_async_wait(p.ahead);
+    const uint4* from = mine + slot * 2 * row_vecs;
+    slot = slot == p.ahead - 1 ? 0 : slot + 1;
+    // dy, h and g of this thread's vector i, from shared memory.  The second pass over the row finds h and g in registers where one
     // block an SM leaves it enough of them (16384 x 4096 bf16,
     // forward and backward together: 119.5 us without, 117.3 us so).
     auto values = [&](int i, F32x2 (&d)[kPairs], F32x2 (&h)[kPairs], F32x2 (&g)[kPairs]) {
-      if constexpr (kVec > 1) {
-        load_cols<T, kVec>(from_x + i * (kGroup * kVec), h);
-        load_cols<T, kVec>(from_d + i * (kGroup * kVec), d);
-      } else {
-        h[0] = pack_f32(to_float(ex[i]), 0.0f);
-        d[0] = pack_f32(to_float(ed[i]), 0.0f);
-      }
-      if constexpr (!kHeld) weights_of<W, kVec>(p.weight, (tid + i * kGroup) * kVec, 1.0f, g);
+      from_words<T>(from[i * kGroup], h);
+      from_words<T>(from[row_vecs + i * kGroup], d);
+      share.clear(i, h);
+      share.clear(i, d);
+      if constexpr (!kHeld) weights_of<W, kVec>(p.weight, share.col(i), edge, 1.0f, g);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        h[j] = fma_f32x2(add_f32x2(h[j], minus), scale, shift);  // (one column: the other value is multiplied by d's 0)
+        h[j] = fma_f32x2(add_f32x2(h[j], minus), scale, shift);
         g[j] = mul_f32x2(kHeld ? w[kHeld ? i : 0][j] : g[j], d[j]);
       }
     };
@@ -506,7 +566,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
     F32x2 hs[kKept ? kVecs : 1][kPairs], gk[kKept ? kVecs : 1][kPairs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if (tid + i * kGroup < vecs) {
+      if (share.has(i)) {
         F32x2 d[kPairs], h[kPairs], g[kPairs];
         values(i, d, h, g);
 #pragma unroll
@@ -522,17 +582,17 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
       const float2 sums = unpack_f32(group_sum<kGroup>(pack_f32(both(gs), both(ghs)), red, turn));
       // rstd (g - <g> - h <g h>)
       const F32x2 m1 = both_f32(-sums.x * p.inv * rstd), m2 = both_f32(-sums.y * p.inv * rstd);
-      T* out = static_cast<T*>(p.out) + row * p.cols + tid * kVec;
+      T* out = static_cast<T*>(p.out) + row * p.cols;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
-        if (tid + i * kGroup < vecs) {
+        if (share.has(i)) {
           F32x2 d[kPairs], h[kPairs], g[kPairs];
           if (!kKept) values(i, d, h, g);
 #pragma unroll
           for (int j = 0; j < kPairs; ++j)
             d[j] = kKept ? fma_f32x2(hs[kKept ? i : 0][j], m2, fma_f32x2(gk[kKept ? i : 0][j], scale, m1))
                          : fma_f32x2(h[j], m2, fma_f32x2(g[j], scale, m1));
-          store_cols<T, kVec>(out + i * (kGroup * kVec), d);
+          share.store(i, out, fit, d);
         }
     }
   }
@@ -542,13 +602,13 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) backward_kerne
   auto each = [&](auto&& f) {  // this thread's sums, by column
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if (tid + i * kGroup < vecs)
+      if (share.has(i))
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const float2 a = unpack_f32(dw[i][j]), c = unpack_f32(db[i][j]);
-          const int col = (tid + i * kGroup) * kVec + 2 * j;
-          f(col, a.x, c.x);
-          if (kVec > 1) f(col + 1, a.y, c.y);
+          const int col = share.col(i) + 2 * j;
+          if (share.in(col)) f(col, a.x, c.x);
+          if (share.in(col + 1)) f(col + 1, a.y, c.y);
         }
   };
   if constexpr (kGroups > 1) {
@@ -645,27 +705,24 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const float* partial, 
   out[col] = from_float<W>(total);
 }
 
-// Threads that share a row and the columns each has.
-template <int kVec, typename F>
+// Threads that share a row.
+template <typename F>
 cudaError_t by_group(int64_t cols, F f) {
   using std::integral_constant;
-  constexpr int kEach = kVec == 1 ? kSingles : kItems;
-  if (cols <= 32 * kEach) return f(integral_constant<int, 32>(), integral_constant<int, kEach>());
-  if (cols <= 64 * kEach) return f(integral_constant<int, 64>(), integral_constant<int, kEach>());
-  if (cols <= 128 * kEach) return f(integral_constant<int, 128>(), integral_constant<int, kEach>());
-  if (cols <= 256 * kEach) return f(integral_constant<int, 256>(), integral_constant<int, kEach>());
-  if (cols <= 512 * kEach) return f(integral_constant<int, 512>(), integral_constant<int, kEach>());
-  if (cols <= 1024 * kEach) return f(integral_constant<int, 1024>(), integral_constant<int, kEach>());
-  return f(integral_constant<int, 1024>(), integral_constant<int, kItems>());
+  if (cols <= 32 * kItems) return f(integral_constant<int, 32>());
+  if (cols <= 64 * kItems) return f(integral_constant<int, 64>());
+  if (cols <= 128 * kItems) return f(integral_constant<int, 128>());
+  if (cols <= 256 * kItems) return f(integral_constant<int, 256>());
+  if (cols <= 512 * kItems) return f(integral_constant<int, 512>());
+  return f(integral_constant<int, 1024>());
 }
 
 // Blocks of an SM that the registers are shared out for.
 template <typename W>
-constexpr int forward_blocks(int group, int vec) {
+constexpr int forward_blocks(int group) {
   if (group >= 512) return 1;
-  return vec == 1 || weights_at<W>(group) == kInShared ? 3 : 2;
+  return weights_at<W>(group) == kInShared ? 3 : 2;
 }
-constexpr int backward_blocks(int group, int vec) { return vec == 1 && group <= 256 ? 2 : 1; }
 
 template <typename... A>
 cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
@@ -682,8 +739,10 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cu
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A group has one row, or rows that lie a multiple of 8 apart.
 int grid_of(const gemm_ops* ops, int64_t rows, int groups, int per_sm) {
-  return static_cast<int>(std::min<int64_t>(ceil_div(rows, int64_t{groups}), static_cast<int64_t>(ops->sm_count) * per_sm));
+  const int64_t most = std::max<int64_t>(8, static_cast<int64_t>(ops->sm_count) * per_sm / 8 * 8);
+  return static_cast<int>(std::min(ceil_div(rows, int64_t{groups}), most));
 }
 
 // The ring's depth: p->ahead rows of `row` bytes a block beside `beside` bytes,
@@ -697,91 +756,100 @@ bool ring_of(const gemm_ops* ops, LayerNormJob* p, size_t row, size_t beside, in
   return *smem <= most;
 }
 
-template <typename T, typename W, int kVec>
-cudaError_t forward_vec(const gemm_ops* ops, LayerNormJob p, cudaStream_t stream) {
-  return by_group<kVec>(p.cols, [&](auto g, auto c) {
-    constexpr int kGroup = g(), kCols = c(), kBlocks = forward_blocks<W>(kGroup, kVec), kThreads = block_threads(kGroup);
-    const size_t row = kVec == 1 ? 0 : static_cast<size_t>(kThreads) * ceil_div(p.cols / kVec, int64_t{kGroup}) * 16;
-    p.weight_bytes = weights_at<W>(kGroup) == kInShared ? static_cast<int>((2 * sizeof(W) * p.cols + 15) / 16 * 16) : 0;
+// Columns that a group's threads need room for: unaligned rows may begin anywhere
+// in their first vector.
+template <typename T, bool kShifted>
+int64_t room_of(int64_t cols) {
+  return cols + (kShifted ? kVecOf<T> - 1 : 0);
+}
+// Vectors of a block's threads for a row of each group.
+template <typename T, bool kShifted>
+size_t block_vecs(int64_t cols, int group) {
+  return static_cast<size_t>(block_threads(group)) * ceil_div(room_of<T, kShifted>(cols), int64_t{kVecOf<T>} * group);
+}
+
+template <typename T, typename W, bool kShifted>
+cudaError_t forward_rows(const gemm_ops* ops, LayerNormJob p, cudaStream_t stream) {
+  return by_group(room_of<T, kShifted>(p.cols), [&](auto g) {
+    constexpr int kGroup = g(), kBlocks = forward_blocks<W>(kGroup), kThreads = block_threads(kGroup);
+    const size_t vecs = block_vecs<T, kShifted>(p.cols, kGroup);
+    p.weight_bytes = 0;
+    if (weights_at<W>(kGroup) == kInShared)
+      p.weight_bytes = static_cast<int>(2 * sizeof(W) * (kShifted ? vecs * kVecOf<T> : round8(p.cols)));
     size_t smem;
-    if (!ring_of(ops, &p, row, p.weight_bytes, kBlocks, &smem)) return cudaErrorInvalidValue;
-    return launch(forward_kernel<T, W, kVec, kGroup, kCols, kBlocks>,
-                  dim3(grid_of(ops, p.rows, kThreads / kGroup, kBlocks)), kThreads, smem, stream, p);
+    if (!ring_of(ops, &p, vecs * 16, p.weight_bytes, kBlocks, &smem)) return cudaErrorInvalidValue;
+    return launch(forward_kernel<T, W, kShifted, kGroup, kBlocks>, dim3(grid_of(ops, p.rows, kThreads / kGroup, kBlocks)),
+                  kThreads, smem, stream, p);
   });
 }
 
-template <int kVec>
+int long_grid(const gemm_ops* ops, int64_t rows) { return static_cast<int>(std::min<int64_t>(rows, 2 * ops->sm_count)); }
+
+template <typename T, bool kShifted>
 int backward_grid(const gemm_ops* ops, int64_t rows, int64_t cols) {
-  if (cols > kLayerNormMaxCols) return static_cast<int>(std::min<int64_t>(rows, 2 * ops->sm_count));
   int n = 0;
-  by_group<kVec>(cols, [&](auto g, auto) {
-    n = grid_of(ops, rows, block_threads(g()) / g(), backward_blocks(g(), kVec));
+  by_group(room_of<T, kShifted>(cols), [&](auto g) {
+    n = grid_of(ops, rows, block_threads(g()) / g(), 1);
     return cudaSuccess;
   });
   return n;
 }
 
-// False where not one row of x and dy fits the ring.
-template <typename T>
+// Whether one row of x and dy fits the ring (fp32 rows of more than 28672 columns do not).
+template <typename T, bool kShifted>
 bool backward_fits(const gemm_ops* ops, int64_t cols) {
-  constexpr int kVec = 16 / sizeof(T);
-  bool fits = true;
-  by_group<kVec>(cols, [&](auto g, auto) {
-    fits = static_cast<size_t>(block_threads(g())) * 2 * ceil_div(cols / kVec, int64_t{g()}) * 16 <= ops->smem_optin - kLayerNormStatic;
+  bool fits = room_of<T, kShifted>(cols) <= kLayerNormMaxCols;
+  by_group(room_of<T, kShifted>(cols), [&](auto g) {
+    fits = fits && block_vecs<T, kShifted>(cols, g()) * 32 <= ops->smem_optin - kLayerNormStatic;
     return cudaSuccess;
   });
   return fits;
 }
 
-template <typename T, typename W, int kVec>
-cudaError_t backward_vec(const gemm_ops* ops, LayerNormJob p, int blocks, cudaStream_t stream) {
-  return by_group<kVec>(p.cols, [&](auto g, auto c) {
-    constexpr int kGroup = g(), kCols = c(), kBlocks = backward_blocks(kGroup, kVec), kThreads = block_threads(kGroup);
-    const size_t row = kVec == 1 ? 0 : static_cast<size_t>(kThreads) * 2 * ceil_div(p.cols / kVec, int64_t{kGroup}) * 16;
+template <typename T, typename W, bool kShifted>
+cudaError_t backward_rows(const gemm_ops* ops, LayerNormJob p, int blocks, cudaStream_t stream) {
+  return by_group(room_of<T, kShifted>(p.cols), [&](auto g) {
+    constexpr int kGroup = g(), kThreads = block_threads(kGroup);
     size_t smem;
-    if (!ring_of(ops, &p, row, 0, kBlocks, &smem)) return cudaErrorInvalidValue;
+    if (!ring_of(ops, &p, block_vecs<T, kShifted>(p.cols, kGroup) * 32, 0, 1, &smem)) return cudaErrorInvalidValue;
     if (kThreads > kGroup) smem = std::max(smem, static_cast<size_t>(p.cols) * 2 * sizeof(float));
-    return launch(backward_kernel<T, W, kVec, kGroup, kCols, kBlocks>, dim3(blocks), kThreads, smem, stream, p);
+    return launch(backward_kernel<T, W, kShifted, kGroup>, dim3(blocks), kThreads, smem, stream, p);
   });
 }
 
 template <typename T, typename W>
 cudaError_t forward(const gemm_ops* ops, const LayerNormJob& p, bool vec, cudaStream_t stream) {
-  if (p.cols > kLayerNormMaxCols)
-    return launch(forward_long_kernel<T, W>, dim3(static_cast<unsigned>(std::min<int64_t>(p.rows, 2 * ops->sm_count))),
-                  1024, 0, stream, p);
-  return vec ? forward_vec<T, W, 16 / sizeof(T)>(ops, p, stream) : forward_vec<T, W, 1>(ops, p, stream);
+  if (room_of<T, true>(p.cols) > kLayerNormMaxCols && !(vec && p.cols <= kLayerNormMaxCols))
+    return launch(forward_long_kernel<T, W>, dim3(long_grid(ops, p.rows)), 1024, 0, stream, p);
+  return vec ? forward_rows<T, W, false>(ops, p, stream) : forward_rows<T, W, true>(ops, p, stream);
 }
 
 template <typename T, typename W>
 cudaError_t backward(const gemm_ops* ops, const LayerNormJob& p, bool vec, void* dweight, void* dbias, cudaStream_t stream) {
-  constexpr int kVec = 16 / sizeof(T);
-  if (p.cols <= kLayerNormMaxCols && !backward_fits<T>(ops, p.cols)) vec = false;
-  const int blocks = vec ? backward_grid<kVec>(ops, p.rows, p.cols) : backward_grid<1>(ops, p.rows, p.cols);
-  cudaError_t e;
-  if (p.cols > kLayerNormMaxCols)
-    e = launch(backward_long_kernel<T, W>, dim3(blocks), 1024, 0, stream, p);
-  else
-    e = vec ? backward_vec<T, W, kVec>(ops, p, blocks, stream) : backward_vec<T, W, 1>(ops, p, blocks, stream);
+  const bool fits = vec ? backward_fits<T, false>(ops, p.cols) : backward_fits<T, true>(ops, p.cols);
+  const int blocks = !fits ? long_grid(ops, p.rows)
+                     : vec ? backward_grid<T, false>(ops, p.rows, p.cols)
+                           : backward_grid<T, true>(ops, p.rows, p.cols);
+  const cudaError_t e = !fits ? launch(backward_long_kernel<T, W>, dim3(blocks), 1024, 0, stream, p)
+                        : vec ? backward_rows<T, W, false>(ops, p, blocks, stream)
+                              : backward_rows<T, W, true>(ops, p, blocks, stream);
   if (e != cudaSuccess || !p.partial) return e;
   return launch(sum_kernel<W>, dim3(static_cast<unsigned>(ceil_div(p.cols, int64_t{32})), 2), kSumThreads, 0, stream,
                 static_cast<const float*>(p.partial), blocks, p.cols, static_cast<W*>(dweight), static_cast<W*>(dbias));
 }
 
-template <typename T, typename W, int kVec>
+template <typename T, typename W, bool kShifted>
 cudaError_t set_smem(size_t smem) {
   const int bytes = static_cast<int>(smem - kLayerNormStatic);
   cudaError_t e = cudaSuccess;
-  auto set = [&](auto g, auto c) {
-    constexpr int kGroup = g(), kCols = c();
+  auto set = [&](auto g) {
+    constexpr int kGroup = g();
     const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(forward_kernel<T, W, kVec, kGroup, kCols, forward_blocks<W>(kGroup, kVec)>, attr, bytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(backward_kernel<T, W, kVec, kGroup, kCols, backward_blocks(kGroup, kVec)>, attr, bytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(forward_kernel<T, W, kShifted, kGroup, forward_blocks<W>(kGroup)>, attr, bytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(backward_kernel<T, W, kShifted, kGroup>, attr, bytes);
     return e;
   };
-  for (int64_t cols = 256; cols <= kLayerNormMaxCols; cols *= 2) by_group<kVec>(cols, set);
+  for (int64_t cols = 1024; cols <= kLayerNormMaxCols; cols *= 2) by_group(cols, set);
   return e;
 }
 
@@ -791,10 +859,10 @@ cudaError_t set_smem(size_t smem) {
 #define SPGEMM_DEFINE_LAYER_NORM(NAME, T)                                                                       \
   namespace spgemm {                                                                                            \
   cudaError_t layer_norm_set_smem_##NAME(size_t smem) {                                                         \
-    cudaError_t e = set_smem<T, T, 16 / sizeof(T)>(smem);                                                       \
-    if (e == cudaSuccess) e = set_smem<T, float, 16 / sizeof(T)>(smem);                                         \
-    if (e == cudaSuccess) e = set_smem<T, T, 1>(smem);                                                          \
-    if (e == cudaSuccess) e = set_smem<T, float, 1>(smem);                                                      \
+    cudaError_t e = set_smem<T, T, false>(smem);                                                                \
+    if (e == cudaSuccess) e = set_smem<T, float, false>(smem);                                                  \
+    if (e == cudaSuccess) e = set_smem<T, T, true>(smem);                                                       \
+    if (e == cudaSuccess) e = set_smem<T, float, true>(smem);                                                   \
     return e;                                                                                                   \
   }                                                                                                             \
   cudaError_t layer_norm_forward_##NAME(const gemm_ops* ops, const LayerNormJob& p, bool vec, bool wide,        \
@@ -805,8 +873,5 @@ cudaError_t set_smem(size_t smem) {
                                          void* dweight, void* dbias, cudaStream_t stream) {                     \
     return wide ? backward<T, float>(ops, p, vec, dweight, dbias, stream)                                       \
                 : backward<T, T>(ops, p, vec, dweight, dbias, stream);                                          \
-  }                                                                                                             \
-  int layer_norm_backward_grid_##NAME(const gemm_ops* ops, int64_t rows, int64_t cols) {                        \
-    return std::max(backward_grid<16 / sizeof(T)>(ops, rows, cols), backward_grid<1>(ops, rows, cols));         \
   }                                                                                                             \
   }

@@ -37,11 +37,13 @@ struct LayerNormJob {
   cudaError_t layer_norm_forward_##NAME(const gemm_ops* ops, const LayerNormJob& p, bool vec, bool wide,     \
                                         cudaStream_t stream);                                                \
   cudaError_t layer_norm_backward_##NAME(const gemm_ops* ops, const LayerNormJob& p, bool vec, bool wide,    \
-                                         void* dweight, void* dbias, cudaStream_t stream);                   \
-  int layer_norm_backward_grid_##NAME(const gemm_ops* ops, int64_t rows, int64_t cols);
+                                         void* dweight, void* dbias, cudaStream_t stream);
 SPGEMM_DECLARE_LAYER_NORM(f16)
 SPGEMM_DECLARE_LAYER_NORM(bf16)
 SPGEMM_DECLARE_LAYER_NORM(f32)
 #undef SPGEMM_DECLARE_LAYER_NORM
+
+// Blocks of a backward pass at most, each of which leaves a partial.
+int layer_norm_backward_blocks(const gemm_ops* ops, int64_t rows, int64_t cols);
 
 }  // namespace spgemm
