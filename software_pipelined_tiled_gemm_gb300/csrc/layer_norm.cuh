@@ -29,7 +29,13 @@
 // thread has many columns, so that the reductions over a row (some 25
 // instructions each) cost little.
 //
-// FIGURES
+// 16384 x 4096 bf16: forward 47 us, backward 75 us (672 MB in all, 5.5 TB/s; with
+// scalars and 16 columns a thread the forward pass took 89 us).  16384 x 4097:
+// 107 and 146 us (read element by element, without copies ahead: 300 and 494 us).
+// Rows a little wider than 1024, 2048, 4096 or 8192 columns leave half of their
+// group idle (16384 x 4104: 64 and 107 us), and the masks and element stores of
+// unaligned rows are a larger part of narrow ones (262144 x 255: 179 and 259 us,
+// x 256: 86 and 157).
 //
 // The weights' gradients: a thread sums its columns over its rows in fp32
 // registers; each block leaves one partial, and a second kernel adds those in
@@ -146,20 +152,32 @@ __device__ __forceinline__ void copy_async_wait(int ahead) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// A thread's vectors of its group's rows.
+// A thread's vectors of its group's rows.  Of kShifted rows, a group's first vector
+// may hold the end of another row and its last one another's beginning.  All threads
+// mask those two vectors (others' masks are all ones): a branch for the thread that
+// has them would keep its row's threads waiting.
 template <typename T, bool kShifted, int kGroup>
 struct Share {
   static constexpr int kVec = kVecOf<T>;
   int tid, cols;
-  int back;   // elements of a row's first vector before the row
-  int vecs;   // of a row
-  int used;   // of a thread at most, in any group
+  int back;        // elements of a row's first vector before the row
+  int vecs;        // of a row
+  int used;        // of a thread at most, in any group
+  int round;       // in which the group has the last vector
+  uint4 head, tail;    // masks of this thread's vectors 0 and `round`
+  int tail_bytes;  // of its vector `round`, up to the row's end
+  bool edge;       // whether a lane of this warp has one of the two vectors
 
   // `row`: the group's first
   __device__ __forceinline__ Share(int tid_, int cols_, const T* row) : tid(tid_), cols(cols_) {
     back = kShifted ? bytes_past(row) / static_cast<int>(sizeof(T)) : 0;
     vecs = (back + cols + kVec - 1) / kVec;
     used = (cols + (kShifted ? kVec - 1 : 0) + kVec * kGroup - 1) / (kVec * kGroup);
+    round = (vecs - 1) / kGroup;
+    tail_bytes = min(16, (cols - col(round)) * static_cast<int>(sizeof(T)));
+    head = mask_of(0);
+    tail = mask_of(round);
+    edge = kShifted && __any_sync(0xffffffffu, partial(0) || (has(round) && partial(round)));
   }
   __device__ __forceinline__ bool has(int i) const { return tid + i * kGroup < vecs; }
   __device__ __forceinline__ int col(int i) const { return (tid + i * kGroup) * kVec - back; }  // of vector i's first element
@@ -167,14 +185,41 @@ struct Share {
   __device__ __forceinline__ bool in(int c) const { return !kShifted || (c >= 0 && c < cols); }
   __device__ __forceinline__ bool fits(const T* row) const { return !kShifted || bytes_past(row) == back * static_cast<int>(sizeof(T)); }
 
-  // Elements of vector i that are not the row's become zero.
-  template <int kPairs>
-  __device__ __forceinline__ void clear(int i, F32x2 (&v)[kPairs]) const {
-    if (!partial(i)) return;
+  __device__ __forceinline__ uint4 mask_of(int i) const {
+    uint32_t m[4];
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) {
-      const float2 f = unpack_f32(v[j]);
-      v[j] = pack_f32(in(col(i) + 2 * j) ? f.x : 0.0f, in(col(i) + 2 * j + 1) ? f.y : 0.0f);
+    for (int w = 0; w < 4; ++w) {
+      if constexpr (sizeof(T) == 2)
+        m[w] = (in(col(i) + 2 * w) ? 0xffffu : 0u) | (in(col(i) + 2 * w + 1) ? 0xffff0000u : 0u);
+      else
+        m[w] = in(col(i) + w) ? ~0u : 0u;
+    }
+    return make_uint4(m[0], m[1], m[2], m[3]);
+  }
+  static __device__ __forceinline__ uint4 both_of(uint4 a, uint4 m) { return make_uint4(a.x & m.x, a.y & m.y, a.z & m.z, a.w & m.w); }
+
+  // Elements of vector i that are not the row's become zero: as they lie in memory, and in fp32.
+  __device__ __forceinline__ uint4 own(int i, uint4 a) const {
+    if constexpr (kShifted) {
+      if (i == 0) a = both_of(a, head);
+      if (i == round) a = both_of(a, tail);
+    }
+    return a;
+  }
+  static __device__ __forceinline__ void mask_pairs(F32x2 (&v)[kVec / 2], uint4 mask) {
+    const uint32_t m[4] = {mask.x, mask.y, mask.z, mask.w};
+#pragma unroll
+    for (int j = 0; j < kVec / 2; ++j) {
+      if constexpr (sizeof(T) == 2)
+        v[j] &= static_cast<F32x2>(__byte_perm(m[j], 0u, 0x3232)) << 32 | __byte_perm(m[j], 0u, 0x1010);
+      else
+        v[j] &= static_cast<F32x2>(m[2 * j + 1]) << 32 | m[2 * j];
+    }
+  }
+  __device__ __forceinline__ void own(int i, F32x2 (&v)[kVec / 2]) const {
+    if constexpr (kShifted) {
+      if (i == 0) mask_pairs(v, head);
+      if (i == round) mask_pairs(v, tail);
     }
   }
 
@@ -183,20 +228,24 @@ struct Share {
   template <int kVecs>
   __device__ __forceinline__ void fetch(uint4* to, const T* row, const T* matrix, bool fit) const {
     const T* src = row + (tid * kVec - back);
+    if (kShifted && (!fit || row - back < matrix)) {
+#pragma unroll 1
+      for (int i = 0; i < used; ++i) {
+        T* one = reinterpret_cast<T*>(to + i * kGroup);
+#pragma unroll 1
+        for (int j = 0; j < kVec; ++j) one[j] = in(col(i) + j) ? row[col(i) + j] : from_float<T>(0.0f);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       if (!has(i)) continue;
-      if constexpr (!kShifted) {
-        copy_async16(to + i * kGroup, src + i * (kGroup * kVec));
-      } else if (fit && (i > 0 || src >= matrix)) {
-        const int bytes = min(16, (cols - col(i)) * static_cast<int>(sizeof(T)));
+      if (kShifted && i == round)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(to + i * kGroup)),
-                     "l"(src + i * (kGroup * kVec)), "r"(bytes)
+                     "l"(src + i * (kGroup * kVec)), "r"(tail_bytes)
                      : "memory");
-      } else {
-        T* one = reinterpret_cast<T*>(to + i * kGroup);
-        for (int j = 0; j < kVec; ++j) one[j] = in(col(i) + j) ? row[col(i) + j] : from_float<T>(0.0f);
-      }
+      else
+        copy_async16(to + i * kGroup, src + i * (kGroup * kVec));
     }
   }
 
@@ -204,18 +253,18 @@ struct Share {
   __device__ __forceinline__ void store(int i, T* row, bool fit, const F32x2 (&v)[kVec / 2]) const {
     const uint4 y = to_words<T>(v);
     T* to = row + (tid * kVec - back) + i * (kGroup * kVec);
-    if (!kShifted || (fit && !partial(i))) {
-      *reinterpret_cast<uint4*>(to) = y;
-      return;
-    }
-    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    if (kShifted && (!fit || (edge && (i == 0 || i == round) && partial(i)))) {
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (!in(col(i) + j)) continue;
-      if constexpr (sizeof(T) == 2)
-        reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
-      else
-        reinterpret_cast<uint32_t*>(to)[j] = w[j];
+      for (int j = 0; j < kVec; ++j) {
+        if (!in(col(i) + j)) continue;
+        if constexpr (sizeof(T) == 2)
+          reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+        else
+          reinterpret_cast<uint32_t*>(to)[j] = w[j];
+      }
+    } else {
+      *reinterpret_cast<uint4*>(to) = y;
     }
   }
 };
@@ -267,13 +316,15 @@ __device__ __forceinline__ float row_rstd(float low, float squares, float eps, F
 // How a kernel meets its weights.
 constexpr int kInRegisters = 0, kInShared = 1, kInMemory = 2;
 // fp32 weights: registers, and two blocks an SM, where a block's registers
-// hold them.  16-bit ones: shared memory and three blocks.  (16384 x 4096, fp32
-// weights: 41 and 60 us; 8192 x 8192, bf16 weights: 45 and 41 us.)  Four bytes a
-// column of 32768 columns fit no shared memory: read from L2.
+// hold them.  16-bit ones: shared memory and three blocks.  (Registers and shared
+// memory, 16384 x 4096 with fp32 weights: 41 and 60 us; 8192 x 8192 with bf16
+// weights: 45 and 41 us.)  Unaligned rows, whose masks take registers: shared memory
+// and two blocks (16384 x 5001 with bf16 weights: 106 us, three blocks 124 us; 65536 x
+// 1001: 67 and 83 us).  Four bytes a column of 32768 columns fit no shared memory: read from L2.
 template <typename W>
-constexpr int weights_at(int group) {
+constexpr int weights_at(int group, bool shifted) {
   if (group == 1024) return kInMemory;
-  return group == 32 || (group <= 256 && sizeof(W) == 4) ? kInRegisters : kInShared;
+  return shifted ? kInShared : group == 32 || (group <= 256 && sizeof(W) == 4) ? kInRegisters : kInShared;
 }
 
 // fp32 weights of columns [col, col + kN), in pairs; `cols`: of the row, which may
@@ -299,7 +350,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
   constexpr int kVecs = kItems / kVec;          // vectors of a thread
   constexpr int kPairs = kVec / 2;              // pairs of a vector
   constexpr int kGroups = block_threads(kGroup) / kGroup;
-  constexpr int kWeights = weights_at<W>(kGroup);
+  constexpr int kWeights = weights_at<W>(kGroup, kShifted);
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ F32x2 red_all[kGroup > 32 ? 2 * block_threads(kGroup) / 32 : 1];
   ptx::pdl_launch_dependents();
@@ -370,8 +421,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       if (share.has(i)) {
-        from_words<T>(from[i * kGroup], v[i]);
-        share.clear(i, v[i]);
+        from_words<T>(share.own(i, from[i * kGroup]), v[i]);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) sum = add_f32x2(sum, v[i][j]);
       }
@@ -393,7 +443,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
       if (share.has(i)) {
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) v[i][j] = add_f32x2(v[i][j], minus);
-        share.clear(i, v[i]);
+        share.own(i, v[i]);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           lows = add_f32x2(lows, v[i][j]);
@@ -551,10 +601,8 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
     // block an SM leaves it enough of them (16384 x 4096 bf16,
     // forward and backward together: 119.5 us without, 117.3 us so).
     auto values = [&](int i, F32x2 (&d)[kPairs], F32x2 (&h)[kPairs], F32x2 (&g)[kPairs]) {
-      from_words<T>(from[i * kGroup], h);
-      from_words<T>(from[row_vecs + i * kGroup], d);
-      share.clear(i, h);
-      share.clear(i, d);
+      from_words<T>(share.own(i, from[i * kGroup]), h);
+      from_words<T>(share.own(i, from[row_vecs + i * kGroup]), d);
       if constexpr (!kHeld) weights_of<W, kVec>(p.weight, share.col(i), edge, 1.0f, g);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
@@ -719,9 +767,9 @@ cudaError_t by_group(int64_t cols, F f) {
 
 // Blocks of an SM that the registers are shared out for.
 template <typename W>
-constexpr int forward_blocks(int group) {
+constexpr int forward_blocks(int group, bool shifted) {
   if (group >= 512) return 1;
-  return weights_at<W>(group) == kInShared ? 3 : 2;
+  return weights_at<W>(group, shifted) == kInShared && !shifted ? 3 : 2;
 }
 
 template <typename... A>
@@ -771,10 +819,10 @@ size_t block_vecs(int64_t cols, int group) {
 template <typename T, typename W, bool kShifted>
 cudaError_t forward_rows(const gemm_ops* ops, LayerNormJob p, cudaStream_t stream) {
   return by_group(room_of<T, kShifted>(p.cols), [&](auto g) {
-    constexpr int kGroup = g(), kBlocks = forward_blocks<W>(kGroup), kThreads = block_threads(kGroup);
+    constexpr int kGroup = g(), kBlocks = forward_blocks<W>(kGroup, kShifted), kThreads = block_threads(kGroup);
     const size_t vecs = block_vecs<T, kShifted>(p.cols, kGroup);
     p.weight_bytes = 0;
-    if (weights_at<W>(kGroup) == kInShared)
+    if (weights_at<W>(kGroup, kShifted) == kInShared)
       p.weight_bytes = static_cast<int>(2 * sizeof(W) * (kShifted ? vecs * kVecOf<T> : round8(p.cols)));
     size_t smem;
     if (!ring_of(ops, &p, vecs * 16, p.weight_bytes, kBlocks, &smem)) return cudaErrorInvalidValue;
@@ -845,7 +893,7 @@ cudaError_t set_smem(size_t smem) {
   auto set = [&](auto g) {
     constexpr int kGroup = g();
     const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(forward_kernel<T, W, kShifted, kGroup, forward_blocks<W>(kGroup)>, attr, bytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(forward_kernel<T, W, kShifted, kGroup, forward_blocks<W>(kGroup, kShifted)>, attr, bytes);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(backward_kernel<T, W, kShifted, kGroup>, attr, bytes);
     return e;
   };
