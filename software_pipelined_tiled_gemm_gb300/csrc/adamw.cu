@@ -63,7 +63,7 @@ struct Entry {
   float decay;           // weight decay
 };
 
-// Tables of two sizes: a launch's arguments cost the host time (the call of 98
+// Tables of two sizes: a launch's arguments cost the host time (the call of 50
 // tensors takes it 4.8 us with 512 entries, 4.2 us with 128).
 constexpr int kFewTensors = 32, kMostTensors = 512;
 template <int kTensors>

@@ -206,6 +206,35 @@ def test_pitch_alignment_and_in_place(cols):
     assert torch.equal(sg.layer_norm(z, w, b, out=z), same["y"])
 
 
+@pytest.mark.parametrize("cols", [1, 3, 13, 61, 1019, 1531, 4099])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_share_vectors_of_memory_and_nothing_else(cols, dt):
+    """A row that begins or ends inside 16 bytes has neighbours there: rows of NaN
+    between clean ones, in every place of a vector, out of place and in place."""
+    x, w, b, dy = inputs(67, cols, dt, "f32", seed=12)
+    want = reference(x, w, b, dy)
+    clean = torch.arange(67, device="cuda") % 2 == 0
+    for at in (0, 1, 3):
+        def placed(t):
+            flat = torch.full((t.numel() + 16,), float("nan"), dtype=t.dtype, device="cuda")
+            out = flat[at:at + t.numel()].view(t.shape)
+            out.copy_(t)
+            out[~clean] = float("nan")
+            return flat, out
+        (_, px), (flat_d, pd) = placed(x), placed(dy)
+        y, kept = sg.layer_norm(px, w, b, save=True)
+        dx = sg.layer_norm_backward(pd, px, w, kept, need=(True, False, False))[0]
+        flat_x, z = placed(x)
+        sg.layer_norm(z, w, b, out=z)
+        sg.layer_norm_backward(pd, px, w, kept, need=(True, False, False), out=(pd, None, None))
+        for name, got in (("y", y), ("dx", dx), ("y", z), ("dx", pd)):
+            value, bound = want[name]
+            assert_within(got[clean], (value[clean], bound[clean]), (name, at))
+            assert got[~clean].isnan().all()
+        for flat in (flat_x, flat_d):   # beside the matrix nothing is written
+            assert flat[:at].isnan().all() and flat[at + x.numel():].isnan().all()
+
+
 def test_each_gradient_alone_and_no_rows():
     x, w, b, dy = inputs(50, 264, "f32", "f32", seed=7)
     y, kept = sg.layer_norm(x, w, b, save=True)
