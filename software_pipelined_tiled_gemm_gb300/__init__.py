@@ -50,8 +50,8 @@ __all__ = [
     "gated_ffn", "gated_ffn_backward", "GatedKept", "orthogonalize", "NEWTON_SCHULZ",
     "token_logprobs", "token_logprobs_backward", "TokenLogprobs", "MAX_TOP_K",
     "grouped_matmul", "grouped_matmul_backward", "MAX_GROUPS", "layer_norm", "layer_norm_backward",
-    "LayerNormKept", "LayerNormArgs", "adamw", "adamw_state", "AdamWState", "AdamWTensor", "AdamWArgs",
-    "ADAMW_BLOCK",
+    "LayerNormKept", "LayerNormArgs", "adamw", "adamw_state", "AdamWState", "AdamWTensor",
+    "AdamWArgs", "ADAMW_BLOCK",
     "check_operators", "close_operators", "FfnArgs", "OrthogonalizeArgs", "LogprobsArgs", "GroupedArgs",
 ]
 
@@ -536,6 +536,8 @@ def matmul_nt(A, B, epilogue=None, stages: int = 6, variant: str = "pipelined", 
 
 
 from .operators import (  # noqa: E402 - they use the binding above
-    ADAMW_BLOCK, AdamWArgs, AdamWState, AdamWTensor, FfnArgs, GatedKept, GroupedArgs, LayerNormArgs, LayerNormKept, LogprobsArgs, MAX_GROUPS, MAX_TOP_K, NEWTON_SCHULZ,
-    OrthogonalizeArgs, TokenLogprobs, adamw, adamw_state, check_operators, close_operators, gated_ffn, gated_ffn_backward,
-    grouped_matmul, grouped_matmul_backward, layer_norm, layer_norm_backward, orthogonalize, token_logprobs, token_logprobs_backward)
+    ADAMW_BLOCK, AdamWArgs, AdamWState, AdamWTensor, FfnArgs, GatedKept, GroupedArgs, LayerNormArgs,
+    LayerNormKept, LogprobsArgs, MAX_GROUPS, MAX_TOP_K, NEWTON_SCHULZ, OrthogonalizeArgs,
+    TokenLogprobs, adamw, adamw_state, check_operators, close_operators, gated_ffn,
+    gated_ffn_backward, grouped_matmul, grouped_matmul_backward, layer_norm, layer_norm_backward,
+    orthogonalize, token_logprobs, token_logprobs_backward)
