@@ -13,8 +13,8 @@
 // The second sum costs no pass of its own and takes out what the rounding of
 // the mean to fp32 left in the differences, so that a row far from zero loses
 // nothing but its own bits; the backward pass gets both parts of the mean.  A
-// sum or a sum of squares that leaves fp32's range is taken again, of x / n or
-// of 2^-64 d.
+// row whose sums leave fp32's range is taken again by itself, scaled
+// (careful_row).
 //
 // Groups loop over rows.  A thread copies its vectors of the next rows to shared
 // memory asynchronously, which keeps rows of every group on their way while one
@@ -60,7 +60,7 @@ namespace {
 constexpr int kAhead = 3;        // rows of a group on their way or in work, at most
 constexpr int kItems = 32;       // columns of a thread, at most
 constexpr int kMinThreads = 256; // of a block: smaller groups share one
-constexpr float kDown = 5.421010862427522e-20f;  // 2^-64
+constexpr float kMost = 3.4028235e38f;  // the largest fp32
 
 template <typename T>
 __device__ __forceinline__ float to_float(T v) {
@@ -276,13 +276,13 @@ __device__ __forceinline__ float from_lane(float v, int d) { return __shfl_xor_s
 __device__ __forceinline__ F32x2 sum_of(F32x2 a, F32x2 b) { return add_f32x2(a, b); }
 __device__ __forceinline__ float sum_of(float a, float b) { return a + b; }
 
-// The sum over the group of one value or a pair, the same in every thread:
-// over the lanes, then over the warps, each as a tree.  `red`: 2 x warps of
-// the group, used in turn.
-template <int kGroup, typename V>
-__device__ __forceinline__ V group_sum(V a, F32x2* red, int& turn) {
+// One value or a pair of the whole group (`op`: a sum, or the least of them), the
+// same in every thread: over the lanes, then over the warps, each as a tree.
+// `red`: 2 x warps of the group, used in turn.
+template <int kGroup, typename V, typename F>
+__device__ __forceinline__ V group_reduce(V a, F32x2* red, int& turn, F op) {
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) a = sum_of(a, from_lane(a, d));
+  for (int d = 16; d > 0; d /= 2) a = op(a, from_lane(a, d));
   if constexpr (kGroup > 32) {
     constexpr int kWarps = kGroup / 32;
     V* mine = reinterpret_cast<V*>(red + turn * kWarps);
@@ -294,23 +294,112 @@ __device__ __forceinline__ V group_sum(V a, F32x2* red, int& turn) {
       __syncthreads();
     a = mine[threadIdx.x % kWarps];
 #pragma unroll
-    for (int d = kWarps / 2; d > 0; d /= 2) a = sum_of(a, from_lane(a, d));
+    for (int d = kWarps / 2; d > 0; d /= 2) a = op(a, from_lane(a, d));
   }
   return a;
+}
+template <int kGroup, typename V>
+__device__ __forceinline__ V group_sum(V a, F32x2* red, int& turn) {
+  return group_reduce<kGroup>(a, red, turn, [](V x, V y) { return sum_of(x, y); });
+}
+// The least of each of two values.
+template <int kGroup>
+__device__ __forceinline__ float2 group_least(float a, float b, F32x2* red, int& turn) {
+  return unpack_f32(group_reduce<kGroup>(pack_f32(a, b), red, turn, [](F32x2 x, F32x2 y) {
+    const float2 f = unpack_f32(x), g = unpack_f32(y);
+    return pack_f32(fminf(f.x, g.x), fminf(f.y, g.y));
+  }));
 }
 __device__ __forceinline__ float both(F32x2 v) {
   const float2 f = unpack_f32(v);
   return f.x + f.y;
 }
 
-// 1 / sqrt(sum / n + eps) from the sums over n of d and d^2; `again` gives the
-// sum of (2^-64 d)^2 over n.  Rows of NaN give NaN.
-template <typename F>
-__device__ __forceinline__ float row_rstd(float low, float squares, float eps, F again) {
-  if (squares <= 3.4028235e38f) return rsqrtf(fmaxf(squares - low * low, 0.0f) + eps);
-  if (squares != squares) return squares;
-  const float s = again();  // the same in all threads of the group
-  return s <= 3.4028235e38f ? rsqrtf(s) * kDown : __int_as_float(0x7fc00000);
+template <typename W>
+__device__ __forceinline__ float weight_at(const void* base, int col, float otherwise) {
+  return base ? to_float(__ldg(static_cast<const W*>(base) + col)) : otherwise;
+}
+
+// This thread's elements of a row in its ring, and of one in memory, with their columns.
+template <typename T, int kGroup>
+struct InRing {
+  const uint4* from;
+  int col, cols;  // of the first vector's first element; of the row
+  template <typename F>
+  __device__ __forceinline__ void operator()(F f) const {
+#pragma unroll 1
+    for (int i = 0, c = col; c < cols; ++i, c += kGroup * kVecOf<T>)
+#pragma unroll 1
+      for (int j = 0; j < kVecOf<T>; ++j)
+        if (c + j >= 0 && c + j < cols) f(to_float(reinterpret_cast<const T*>(from + i * kGroup)[j]), c + j);
+  }
+};
+template <typename T>
+struct InMemory {
+  const T* x;
+  int cols;
+  template <typename F>
+  __device__ __forceinline__ void operator()(F f) const {
+#pragma unroll 1
+    for (int c = threadIdx.x; c < cols; c += 1024) f(to_float(x[c]), c);
+  }
+};
+
+// Whether a row's sums tell its variance: not where they left fp32's range.
+__device__ __forceinline__ bool sums_do(float squares) { return squares <= kMost; }
+
+// A row whose sums do not, by itself: its statistics and its results.  `each(f)` hands this
+// thread's elements and their columns to f.
+//
+// The row is taken times the power of two that brings its largest magnitude to [1, 2)
+// (at the ends of fp32's exponents: to [2^-23, 4)), where no sum of up to 2^29 columns
+// leaves the range.  The mean's first part is kept between the least and the greatest
+// element, so that a constant row has differences of 0, and the variance is that of
+// what both parts leave.  It is 0 or so large that it hides an eps that the scale takes
+// below fp32's range.  NaN and infinities have NaN differences, and so give NaN.
+//
+// Weights are read from memory and elements one by one, so that the loop around it needs
+// no registers for this.  (An even number of reductions: the caller's `turn` holds.)
+template <typename T, typename W, int kGroup, typename Each>
+__device__ __forceinline__ void careful_row(const Each& each, const LayerNormJob& p, int64_t row, bool keeps, F32x2* red, int turn) {
+  float2 least = make_float2(__int_as_float(0x7f800000), __int_as_float(0x7f800000));  // of x, and of -x
+  each([&](float x, int) {
+    least.x = fminf(least.x, x);
+    least.y = fminf(least.y, -x);
+  });
+  least = group_least<kGroup>(least.x, least.y, red, turn);
+  // Biased exponents of the scale, 254 - e, and of 1 / scale, e: both normal numbers.
+  const uint32_t e = min(max(__float_as_uint(fmaxf(fabsf(least.x), fabsf(least.y))) >> 23, 1u), 253u);
+  const float scale = __uint_as_float((254u - e) << 23), unscale = __uint_as_float(e << 23);
+  float sum = 0.0f;
+  each([&](float x, int) { sum += x * scale; });
+  const float mean = fminf(fmaxf(group_sum<kGroup>(sum, red, turn) * p.inv, least.x * scale), -least.y * scale);
+  sum = 0.0f;
+  each([&](float x, int) { sum += x * scale - mean; });
+  const float low = group_sum<kGroup>(sum, red, turn) * p.inv;
+  sum = 0.0f;
+  each([&](float x, int) {
+    const float d = (x * scale - mean) - low;
+    sum = fmaf(d, d, sum);
+  });
+  const float variance = group_sum<kGroup>(sum, red, turn) * p.inv;
+  // Of the scaled row, and of the row.
+  const float eps = p.eps * scale * scale;
+  float scaled = rsqrtf(variance + eps), rstd = scaled * scale;
+  if (variance == 0.0f || eps > kMost) {  // eps alone
+    rstd = rsqrtf(p.eps);
+    scaled = rstd <= kMost ? fminf(rstd * unscale, kMost) : rstd;  // (differences of 0 stay so)
+  }
+  if (p.stats != nullptr && keeps) {
+    p.stats[row] = mean * unscale;
+    p.stats[p.rows + row] = low * unscale;
+    p.stats[2 * p.rows + row] = rstd;
+  }
+  T* out = static_cast<T*>(p.out) + row * p.cols;
+  each([&](float x, int c) {
+    const float h = ((x * scale - mean) - low) * scaled;
+    out[c] = from_float<T>(fmaf(h, weight_at<W>(p.weight, c, 1.0f), weight_at<W>(p.bias, c, 0.0f)));
+  });
 }
 
 // How a kernel meets its weights.
@@ -426,16 +515,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
         for (int j = 0; j < kPairs; ++j) sum = add_f32x2(sum, v[i][j]);
       }
     }
-    float mean = group_sum<kGroup>(both(sum), red, turn) * p.inv;
-    if (!(fabsf(mean) <= 3.4028235e38f)) {  // beyond fp32's range, or NaN: the same in all threads
-      sum = 0;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (share.has(i))
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) sum = fma_f32x2(v[i][j], both_f32(p.inv), sum);
-      mean = group_sum<kGroup>(both(sum), red, turn);
-    }
+    const float mean = group_sum<kGroup>(both(sum), red, turn) * p.inv;
     F32x2 lows = 0, squares = 0;
     const F32x2 minus = both_f32(-mean);
 #pragma unroll
@@ -451,19 +531,11 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
         }
       }
     const float2 sums = unpack_f32(group_sum<kGroup>(pack_f32(both(lows), both(squares)), red, turn));
-    const float low = sums.x * p.inv;
-    const float rstd = row_rstd(low, sums.y * p.inv, p.eps, [&]() {
-      F32x2 s = 0;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (share.has(i))
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) {
-            const F32x2 d = mul_f32x2(v[i][j], both_f32(kDown));
-            s = fma_f32x2(mul_f32x2(d, both_f32(p.inv)), d, s);
-          }
-      return group_sum<kGroup>(both(s), red, turn);
-    });
+    if (!sums_do(sums.y)) {  // the same in all threads of the group
+      careful_row<T, W, kGroup>(InRing<T, kGroup>{from, share.col(0), p.cols}, p, row, tid == 0, red, turn);
+      continue;
+    }
+    const float low = sums.x * p.inv, rstd = rsqrtf(fmaxf(sums.y * p.inv - low * low, 0.0f) + p.eps);
     if (p.stats != nullptr && tid == 0) {
       p.stats[row] = mean;
       p.stats[p.rows + row] = low;
@@ -492,11 +564,6 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
   }
 }
 
-template <typename W>
-__device__ __forceinline__ float weight_at(const void* base, int col, float otherwise) {
-  return base ? to_float(__ldg(static_cast<const W*>(base) + col)) : otherwise;
-}
-
 // Rows of more columns than a block holds: read three times, the second and
 // third mostly from L2.
 template <typename T, typename W>
@@ -518,14 +585,11 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const LayerNormJob p
     }
     const float2 both = unpack_f32(group_sum<1024>(pack_f32(low, squares), red, turn));
     low = both.x;
-    const float rstd = row_rstd(low, both.y, p.eps, [&]() {
-      float s = 0.0f;
-      for (int c = threadIdx.x; c < p.cols; c += 1024) {
-        const float d = (to_float(x[c]) - mean) * kDown;
-        s = fmaf(d * p.inv, d, s);
-      }
-      return group_sum<1024>(s, red, turn);
-    });
+    if (!sums_do(both.y)) {
+      careful_row<T, W, 1024>(InMemory<T>{x, p.cols}, p, row, threadIdx.x == 0, red, turn);
+      continue;
+    }
+    const float rstd = rsqrtf(fmaxf(both.y - low * low, 0.0f) + p.eps);
     if (p.stats != nullptr && threadIdx.x == 0) {
       p.stats[row] = mean;
       p.stats[p.rows + row] = low;
