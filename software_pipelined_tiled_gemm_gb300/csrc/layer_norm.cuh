@@ -603,6 +603,18 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const LayerNormJob p
   }
 }
 
+// h = (x - mean) rstd + shift, as the backward pass takes it.  Where mean rstd leaves fp32's
+// range the row is a constant one (others' deviations are 2^-24 mean / sqrt(n) or more): h is
+// 0, also of the zeros that stand for what lies beside an unaligned row.
+struct ToNormal {
+  float minus, rstd, shift;
+  __device__ __forceinline__ ToNormal(float mean, float low, float r) {
+    minus = -mean;
+    rstd = fabsf(mean * r) > kMost / 2 ? 0.0f : r;
+    shift = -low * rstd;
+  }
+};
+
 template <typename T, typename W, bool kShifted, int kGroup>
 __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(const LayerNormJob p) {
   constexpr int kVec = kVecOf<T>, kVecs = kItems / kVec, kPairs = kVec / 2;
@@ -655,7 +667,8 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
 
   for (int slot = 0; row < p.rows; row += step) {
     const float rstd = next_rstd;
-    const F32x2 minus = both_f32(-next_mean), scale = both_f32(rstd), shift = both_f32(-next_low * rstd);
+    const ToNormal to_h(next_mean, next_low, rstd);
+    const F32x2 minus = both_f32(to_h.minus), up = both_f32(to_h.rstd), shift = both_f32(to_h.shift), scale = both_f32(rstd);
     fetch_stats(row + step);
     fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
     copy_async_wait(p.ahead);
@@ -670,7 +683,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
       if constexpr (!kHeld) weights_of<W, kVec>(p.weight, share.col(i), edge, 1.0f, g);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        h[j] = fma_f32x2(add_f32x2(h[j], minus), scale, shift);
+        h[j] = fma_f32x2(add_f32x2(h[j], minus), up, shift);
         g[j] = mul_f32x2(kHeld ? w[kHeld ? i : 0][j] : g[j], d[j]);
       }
     };

@@ -58,3 +58,20 @@ def test_differences_beyond_the_range(cols, dt):
     want = reference(x, None, None, x)["y"]
     for t in (x, odd(x)):
         assert_within(sg.layer_norm(t), want, "y")
+
+
+@pytest.mark.parametrize("cols", [64, 1024, 8192])   # (sums of equal numbers are exact)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gradient_of_unaligned_rows_whose_mean_is_large(cols, dt):
+    """What a row's first and last vector hold beside the row is no part of it, nor is its distance from the mean."""
+    x = torch.full((9, cols), 2.0 ** 121, device="cuda").to(DT[dt])
+    dy = (normal(9, cols, seed=2) + 0.5).to(DT[dt])
+    y, kept = sg.layer_norm(x, save=True)
+    want = sg.layer_norm_backward(dy, x, None, kept, need=(True, False, False))[0]
+    assert bool(torch.isfinite(want).all())
+    y, kept = sg.layer_norm(odd(x), save=True)
+    dx = sg.layer_norm_backward(odd(dy), odd(x), None, kept, need=(True, False, False))[0]
+    # Sums in another order: c(n) of |dy|, and a rounding of the output.
+    bound = 317.0 * (max(32, cols / 1024) + 48) * 2.0 ** -22 * dy.double().abs().mean(1, keepdim=True)
+    u = {"f32": 2.0 ** -23, "bf16": 2.0 ** -7}[dt]
+    assert_within(dx, (want.double(), bound + u * (want.double().abs() + bound)), "dx")
