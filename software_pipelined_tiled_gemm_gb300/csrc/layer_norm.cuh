@@ -13,8 +13,8 @@
 // The second sum costs no pass of its own and takes out what the rounding of
 // the mean to fp32 left in the differences, so that a row far from zero loses
 // nothing but its own bits; the backward pass gets both parts of the mean.  A
-// row whose sums leave fp32's range is taken again by itself, scaled
-// (careful_row).
+// row whose sums leave fp32's range, or are mostly the mean's rounding, is taken
+// again by itself, scaled (careful_row).
 //
 // Groups loop over rows.  A thread copies its vectors of the next rows to shared
 // memory asynchronously, which keeps rows of every group on their way while one
@@ -345,8 +345,12 @@ struct InMemory {
   }
 };
 
-// Whether a row's sums tell its variance: not where they left fp32's range.
-__device__ __forceinline__ bool sums_do(float squares) { return squares <= kMost; }
+// Whether a row's sums tell its variance (given with eps added): not where they left
+// fp32's range, nor where the mean's rounding, which low takes out of the squares, is
+// more than what is left (a constant row far from zero).
+__device__ __forceinline__ bool sums_do(float squares, float low, float variance) {
+  return squares <= kMost && low * low <= variance;
+}
 
 // A row whose sums do not, by itself: its statistics and its results.  `each(f)` hands this
 // thread's elements and their columns to f.
@@ -531,11 +535,12 @@ __global__ void __launch_bounds__(block_threads(kGroup), kBlocks) forward_kernel
         }
       }
     const float2 sums = unpack_f32(group_sum<kGroup>(pack_f32(both(lows), both(squares)), red, turn));
-    if (!sums_do(sums.y)) {  // the same in all threads of the group
+    const float low = sums.x * p.inv, variance = fmaxf(sums.y * p.inv - low * low, 0.0f) + p.eps;
+    if (!sums_do(sums.y, low, variance)) {  // the same in all threads of the group
       careful_row<T, W, kGroup>(InRing<T, kGroup>{from, share.col(0), p.cols}, p, row, tid == 0, red, turn);
       continue;
     }
-    const float low = sums.x * p.inv, rstd = rsqrtf(fmaxf(sums.y * p.inv - low * low, 0.0f) + p.eps);
+    const float rstd = rsqrtf(variance);
     if (p.stats != nullptr && tid == 0) {
       p.stats[row] = mean;
       p.stats[p.rows + row] = low;
@@ -585,11 +590,12 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const LayerNormJob p
     }
     const float2 both = unpack_f32(group_sum<1024>(pack_f32(low, squares), red, turn));
     low = both.x;
-    if (!sums_do(both.y)) {
+    const float variance = fmaxf(both.y - low * low, 0.0f) + p.eps;
+    if (!sums_do(both.y, low, variance)) {
       careful_row<T, W, 1024>(InMemory<T>{x, p.cols}, p, row, threadIdx.x == 0, red, turn);
       continue;
     }
-    const float rstd = rsqrtf(fmaxf(both.y - low * low, 0.0f) + p.eps);
+    const float rstd = rsqrtf(variance);
     if (p.stats != nullptr && threadIdx.x == 0) {
       p.stats[row] = mean;
       p.stats[p.rows + row] = low;

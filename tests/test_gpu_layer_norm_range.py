@@ -60,6 +60,39 @@ def test_differences_beyond_the_range(cols, dt):
         assert_within(sg.layer_norm(t), want, "y")
 
 
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_constant_rows(cols, dt):
+    """x - mean is 0 and the variance is 0, however large x is and whatever n x rounds to:
+    y is the bias, rstd 1 / sqrt(eps), and dx rstd (dy - <dy>).
+
+    h is 0 to the bit where the mean's rounding, d = x - mean, is the larger part of
+    var + eps.  Elsewhere |d| is at most sqrt(eps), in all columns the same, so low is d
+    but for its sum's error, c(n) |d|, and |h| = |d - low| rstd at most c(n)."""
+    top = 65000.0 if dt == "f16" else MOST
+    sizes = [1.5, -777.0, 64996.0] + [-10.0 ** e for e in range(6, 39, 4)] + [1e27, 3.3e28, 1e30, 1e37, MOST, -MOST]
+    x = torch.tensor(sizes, device="cuda").clamp(-top, top).to(DT[dt])[:, None].expand(-1, cols).contiguous()
+    b, dy = normal(cols).to(DT[dt]), (normal(len(sizes), cols, seed=2) + 0.5).to(DT[dt])
+    g = dy.double()
+    mean, size = g.mean(1, keepdim=True), g.abs().mean(1, keepdim=True)
+    rstd = 1e-5 ** -0.5
+    # The mean's sum, the difference, the products with rstd, and rstd itself (2^-21).
+    c = (max(32, cols / 1024) + 48) * 2.0 ** -23
+    bound = rstd * ((c + 2.0 ** -22) * size + 2.0 ** -20 * (g.abs() + mean.abs()) + c * c * size)
+    value = rstd * (g - mean)
+    u = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dt]
+    bound = bound + u * (value.abs() + bound)
+    for place in (lambda t: t, odd):
+        y, kept = sg.layer_norm(place(x), None, b, save=True)
+        near = c + 2.0 ** -23 * b.double().abs()
+        assert bool(((y.double() - b.double()).abs() <= near + u * (b.double().abs() + near)).all())
+        far = x[:, 0].abs() > 1e9   # d is 0 or at least 2^-24 x
+        assert torch.equal(y[far], b.expand_as(y)[far])
+        assert bool((kept.stats[2].double() / rstd - 1).abs().max() <= 2.0 ** -21)
+        dx = sg.layer_norm_backward(place(dy), place(x), None, kept, need=(True, False, False))[0]
+        assert_within(dx, (value, bound), "dx")
+
+
 @pytest.mark.parametrize("cols", [64, 1024, 8192])   # (sums of equal numbers are exact)
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_gradient_of_unaligned_rows_whose_mean_is_large(cols, dt):
@@ -75,3 +108,27 @@ def test_gradient_of_unaligned_rows_whose_mean_is_large(cols, dt):
     bound = 317.0 * (max(32, cols / 1024) + 48) * 2.0 ** -22 * dy.double().abs().mean(1, keepdim=True)
     u = {"f32": 2.0 ** -23, "bf16": 2.0 ** -7}[dt]
     assert_within(dx, (want.double(), bound + u * (want.double().abs() + bound)), "dx")
+
+
+@pytest.mark.parametrize("cols", [13, 61, 1019, 1531, 4099, 33000])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_such_rows_between_others(cols, dt):
+    """Each row by itself: rows of every kind in one matrix, out of place and in place."""
+    x = normal(64, cols) * 2 + 1
+    x[1::8] *= 3e37
+    x[2::8] = 1e30
+    x[3::8, cols // 2] = float("nan")
+    x[4::8, 0] = float("inf")
+    x[5::8] = x[5::8] * 1e-3 + 1e4
+    x[6::8] = 0.0
+    x = x.to(DT[dt])
+    # (One of the random rows of 33000 columns reaches beyond 3.4e38 and holds an infinity.)
+    whole = torch.isfinite(x).all(1)
+    assert not whole[3::8].any() and not whole[4::8].any() and int(whole.sum()) >= 47
+    # (A row of 1e30 or of zeros: its h is 0 to the bit, which the general bound does not ask for.)
+    value, bound = reference(x[whole], None, None, x[whole])["y"]
+    for t in (x, odd(x)):
+        y = sg.layer_norm(t)
+        assert_within(y[whole], (value, bound), "y")
+        assert y[~whole].isnan().all() and not y[2::8].any() and not y[6::8].any()
+        assert torch.equal(sg.layer_norm(t, out=t)[whole], y[whole])
