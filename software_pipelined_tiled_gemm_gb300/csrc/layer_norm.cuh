@@ -609,16 +609,22 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const LayerNormJob p
   }
 }
 
-// h = (x - mean) rstd + shift, as the backward pass takes it.  Where mean rstd leaves fp32's
-// range the row is a constant one (others' deviations are 2^-24 mean / sqrt(n) or more): h is
-// 0, also of the zeros that stand for what lies beside an unaligned row.
+// h = (x down + minus) rstd + shift, as the backward pass takes it.  Where mean rstd leaves
+// fp32's range the row is a constant one (others' deviations are 2^-24 mean / sqrt(n) or more):
+// h is 0, also of the zeros that stand for what lies beside an unaligned row.  Where the
+// deviation is so large that a difference from the mean may leave the range (2^128 in a row of
+// up to 2^29 columns: a deviation of 2^113 at least) a quarter of x and mean is taken.
 struct ToNormal {
-  float minus, rstd, shift;
+  float down, minus, rstd, shift;
   __device__ __forceinline__ ToNormal(float mean, float low, float r) {
-    minus = -mean;
+    const bool large = r < 7.888609052210118e-31f;  // 2^-100
+    down = large ? 0.25f : 1.0f;
+    minus = -mean * down;
     rstd = fabsf(mean * r) > kMost / 2 ? 0.0f : r;
     shift = -low * rstd;
+    if (large) rstd *= 4.0f;
   }
+  __device__ __forceinline__ float h(float x) const { return fmaf(fmaf(x, down, minus), rstd, shift); }
 };
 
 template <typename T, typename W, bool kShifted, int kGroup>
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
   for (int slot = 0; row < p.rows; row += step) {
     const float rstd = next_rstd;
     const ToNormal to_h(next_mean, next_low, rstd);
-    const F32x2 minus = both_f32(to_h.minus), up = both_f32(to_h.rstd), shift = both_f32(to_h.shift), scale = both_f32(rstd);
+    const F32x2 down = both_f32(to_h.down), minus = both_f32(to_h.minus), up = both_f32(to_h.rstd), shift = both_f32(to_h.shift), scale = both_f32(rstd);
     fetch_stats(row + step);
     fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
     copy_async_wait(p.ahead);
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
       if constexpr (!kHeld) weights_of<W, kVec>(p.weight, share.col(i), edge, 1.0f, g);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        h[j] = fma_f32x2(add_f32x2(h[j], minus), up, shift);
+        h[j] = fma_f32x2(fma_f32x2(h[j], down, minus), up, shift);
         g[j] = mul_f32x2(kHeld ? w[kHeld ? i : 0][j] : g[j], d[j]);
       }
     };
@@ -767,7 +773,7 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
 // Rows of more columns than a block holds: a block sums a share of the rows
 // into its own partial in memory.
 template <typename T, typename W>
-__global__ void __launch_bounds__(1024) backward_long_kernel(const LayerNormJob p) {
+__global__ void __launch_bounds__(1024, 2) backward_long_kernel(const LayerNormJob p) {
   __shared__ F32x2 red[2 * 32];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait_prior_grid();
@@ -778,9 +784,10 @@ __global__ void __launch_bounds__(1024) backward_long_kernel(const LayerNormJob 
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
     const float mean = __ldg(p.stats + row), low = __ldg(p.stats + p.rows + row);
     const float rstd = __ldg(p.stats + 2 * p.rows + row);
+    const ToNormal to_h(mean, low, rstd);
     float gs = 0.0f, ghs = 0.0f;
     for (int c = threadIdx.x; c < p.cols; c += 1024) {
-      const float d = to_float(dy[c]), h = ((to_float(x[c]) - mean) - low) * rstd;
+      const float d = to_float(dy[c]), h = to_h.h(to_float(x[c]));
       const float w = weight_at<W>(p.weight, c, 1.0f);
       gs = fmaf(d * w, p.inv, gs);
       ghs = fmaf(d * w * p.inv, h, ghs);
@@ -795,7 +802,7 @@ __global__ void __launch_bounds__(1024) backward_long_kernel(const LayerNormJob 
     T* out = static_cast<T*>(p.out) + row * p.cols;
     for (int c = threadIdx.x; c < p.cols; c += 1024) {
       const float w = weight_at<W>(p.weight, c, 1.0f);
-      const float d = to_float(dy[c]), h = ((to_float(x[c]) - mean) - low) * rstd;
+      const float d = to_float(dy[c]), h = to_h.h(to_float(x[c]));
       out[c] = from_float<T>(rstd * (d * w - means.x - h * means.y));
     }
   }

@@ -61,6 +61,20 @@ def test_differences_beyond_the_range(cols, dt):
 
 
 @pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gradients_of_rows_beyond_the_range(cols, dt):
+    x = torch.cat([normal(4, cols) * 3e37, torch.full((3, cols), -MOST, device="cuda")])
+    x[4, 0] = x[5, -1] = x[6, cols // 2] = MOST
+    x, dy = x.to(DT[dt]), (normal(7, cols, seed=2) * 1e33).to(DT[dt])
+    want = reference(x, None, None, dy)
+    for place in (lambda t: t, odd):
+        y, kept = sg.layer_norm(place(x), save=True)
+        got = sg.layer_norm_backward(place(dy), place(x), None, kept)
+        for name, t in zip(("dx", "dweight", "dbias"), got):
+            assert_within(t, want[name], name)
+
+
+@pytest.mark.parametrize("cols", COLS)
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_constant_rows(cols, dt):
     """x - mean is 0 and the variance is 0, however large x is and whatever n x rounds to:
