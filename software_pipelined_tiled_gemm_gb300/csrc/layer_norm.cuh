@@ -347,9 +347,10 @@ struct InMemory {
 
 // Whether a row's sums tell its variance (given with eps added): not where they left
 // fp32's range, nor where the mean's rounding, which low takes out of the squares, is
-// more than what is left (a constant row far from zero).
+// more than what is left (a constant row far from zero), nor where squares may have
+// been too small for fp32 and eps does not hide that.
 __device__ __forceinline__ bool sums_do(float squares, float low, float variance) {
-  return squares <= kMost && low * low <= variance;
+  return squares <= kMost && low * low <= variance && variance >= 8.271806125530277e-25f;  // 2^-80
 }
 
 // A row whose sums do not, by itself: its statistics and its results.  `each(f)` hands this

@@ -107,6 +107,21 @@ def test_constant_rows(cols, dt):
         assert_within(dx, (value, bound), "dx")
 
 
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_without_eps(cols, dt):
+    """Squares below fp32's range, which eps does not hide."""
+    x = (normal(4, cols) * torch.tensor([[1e-18], [1e-21], [1e-30], [1e-37]], device="cuda")).to(DT[dt])
+    dy = (normal(4, cols, seed=2) * 1e-10).to(DT[dt])
+    want = reference(x, None, None, dy, eps=0.0)
+    for place in (lambda t: t, odd):
+        y, kept = sg.layer_norm(place(x), eps=0.0, save=True)
+        assert_within(y, want["y"], "y")
+        got = sg.layer_norm_backward(place(dy), place(x), None, kept)
+        for name, t in zip(("dx", "dweight", "dbias"), got):
+            assert_within(t, want[name], name)
+
+
 @pytest.mark.parametrize("cols", [64, 1024, 8192])   # (sums of equal numbers are exact)
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_gradient_of_unaligned_rows_whose_mean_is_large(cols, dt):
