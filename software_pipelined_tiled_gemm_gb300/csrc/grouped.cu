@@ -43,12 +43,12 @@ __global__ void __launch_bounds__(kTailThreads)
     if (r < tail) {
       const uint16_t* src = j.src + (end - tail + r) * j.ld + 8 * v;
       if (8 * v + 8 <= j.cols) {
-        out = __ldg(reinterpret_cast<const uint4*>(src));
+        out = __ldcg(reinterpret_cast<const uint4*>(src));
       } else {
         uint32_t wd[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          if (8 * v + c < j.cols) wd[c >> 1] |= static_cast<uint32_t>(__ldg(src + c)) << ((c & 1) * 16);
+          if (8 * v + c < j.cols) wd[c >> 1] |= static_cast<uint32_t>(src[c]) << ((c & 1) * 16);
         out = make_uint4(wd[0], wd[1], wd[2], wd[3]);
       }
     }

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_few_kernel(const Args a) 
   ptx::pdl_wait_prior_grid();
   int bad = 0;
   for (int e = threadIdx.x; e <= a.groups; e += kThreads) {
-    const int64_t at = __ldg(a.offsets + e), next = e < a.groups ? __ldg(a.offsets + e + 1) : a.rows;
+    const int64_t at = a.offsets[e], next = e < a.groups ? a.offsets[e + 1] : a.rows;
     bad |= at < 0 || at > next || next > a.rows;
   }
   if (__syncthreads_or(bad)) {
@@ -73,14 +73,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_few_kernel(const Args a) 
     int count = 0;
     for (int e0 = 0; e0 < a.groups; e0 += 32) {
       const int e = e0 + lane;
-      const bool some = e < a.groups && __ldg(a.offsets + e + 1) > __ldg(a.offsets + e);
+      const bool some = e < a.groups && a.offsets[e + 1] > a.offsets[e];
       const uint32_t votes = __ballot_sync(0xffffffffu, some);
       if (some) list[count + __popc(votes & ((1u << lane) - 1u))] = e;
       count += __popc(votes);
     }
     if (lane == 0) found = count;
   } else if (a.zero_rest) {
-    const int64_t first = __ldg(a.offsets), last = __ldg(a.offsets + a.groups), rest = first + (a.rows - last);
+    const int64_t first = a.offsets[0], last = a.offsets[a.groups], rest = first + (a.rows - last);
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kWarps - 1) + warp - 1; i < rest;
          i += static_cast<int64_t>(gridDim.x) * (kWarps - 1)) {
       uint16_t* dst = a.y + (i < first ? i : last + (i - first)) * a.n;
@@ -99,8 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_few_kernel(const Args a) 
     const int last_row = static_cast<int>(min(static_cast<int64_t>(a.n), first_row + (share_end - at)));
     at += last_row - first_row;
     const int e = list[index];
-    const int64_t token0 = __ldg(a.offsets + e);
-    const int64_t token_end = __ldg(a.offsets + e + 1);
+    const int64_t token0 = a.offsets[e], token_end = a.offsets[e + 1];
     const uint16_t* we = a.w + static_cast<int64_t>(e) * a.n * a.k;
     // Warps of 16 rows: as many as the block has for them, while each has words to read.
     const int sets = (last_row - first_row + 15) / 16;

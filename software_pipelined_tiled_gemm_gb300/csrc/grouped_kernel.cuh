@@ -195,8 +195,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   // The groups' offsets and, for tiles along the tokens, how many come before each group.
   int bad = 0;
   for (int e = threadIdx.x; e <= p.groups; e += kGroupedThreads) {
-    const int64_t at = __ldg(p.offsets + e);
-    const int64_t next = e < p.groups ? __ldg(p.offsets + e + 1) : static_cast<int64_t>(p.rows);
+    const int64_t at = p.offsets[e], next = e < p.groups ? p.offsets[e + 1] : static_cast<int64_t>(p.rows);
     bad |= at < 0 || at > next || next > p.rows;
     offsets[e] = static_cast<int>(at);
   }

@@ -317,7 +317,7 @@ __device__ __forceinline__ float both(F32x2 v) {
 
 template <typename W>
 __device__ __forceinline__ float weight_at(const void* base, int col, float otherwise) {
-  return base ? to_float(__ldg(static_cast<const W*>(base) + col)) : otherwise;
+  return base ? to_float(static_cast<const W*>(base)[col]) : otherwise;
 }
 
 // This thread's elements of a row in its ring, and of one in memory, with their columns.
@@ -670,9 +670,9 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
   float next_mean = 0.0f, next_low = 0.0f, next_rstd = 0.0f;
   auto fetch_stats = [&](int64_t r) {
     if (r < p.rows) {
-      next_mean = __ldg(p.stats + r);
-      next_low = __ldg(p.stats + p.rows + r);
-      next_rstd = __ldg(p.stats + 2 * p.rows + r);
+      next_mean = p.stats[r];
+      next_low = p.stats[p.rows + r];
+      next_rstd = p.stats[2 * p.rows + r];
     }
   };
   for (int s = 0; s < p.ahead - 1; ++s) fetch(row + s * step, s);
@@ -682,9 +682,9 @@ __global__ void __launch_bounds__(block_threads(kGroup), 1) backward_kernel(cons
     const float rstd = next_rstd;
     const ToNormal to_h(next_mean, next_low, rstd);
     const F32x2 down = both_f32(to_h.down), minus = both_f32(to_h.minus), up = both_f32(to_h.rstd), shift = both_f32(to_h.shift), scale = both_f32(rstd);
-    fetch_stats(row + step);
     fetch(row + (p.ahead - 1) * step, slot == 0 ? p.ahead - 1 : slot - 1);
     copy_async_wait(p.ahead);
+    fetch_stats(row + step);
     const uint4* from = mine + slot * 2 * row_vecs;
     slot = slot == p.ahead - 1 ? 0 : slot + 1;
     // dy, h and g of this thread's vector i, from shared memory.  The second pass over the row finds h and g in registers where one
@@ -783,8 +783,8 @@ __global__ void __launch_bounds__(1024, 2) backward_long_kernel(const LayerNormJ
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-    const float mean = __ldg(p.stats + row), low = __ldg(p.stats + p.rows + row);
-    const float rstd = __ldg(p.stats + 2 * p.rows + row);
+    const float mean = p.stats[row], low = p.stats[p.rows + row];
+    const float rstd = p.stats[2 * p.rows + row];
     const ToNormal to_h(mean, low, rstd);
     float gs = 0.0f, ghs = 0.0f;
     for (int c = threadIdx.x; c < p.cols; c += 1024) {
