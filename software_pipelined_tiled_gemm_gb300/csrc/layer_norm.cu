@@ -86,6 +86,18 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+// The kernels' shared memory, set by the first layer norm of a handle: with some hundred
+// instances it takes 4 ms, which no other operator's first call should.  (Two calls at once
+// may both set it.)
+cudaError_t set_up(gemm_ops_t* ops) {
+  if (ops->layer_norm_ready.load(std::memory_order_acquire)) return cudaSuccess;
+  cudaError_t e = layer_norm_set_smem_f16(ops->smem_optin);
+  if (e == cudaSuccess) e = layer_norm_set_smem_bf16(ops->smem_optin);
+  if (e == cudaSuccess) e = layer_norm_set_smem_f32(ops->smem_optin);
+  if (e == cudaSuccess) ops->layer_norm_ready.store(true, std::memory_order_release);
+  return e;
+}
+
 LayerNormJob job_of(const gemm_layer_norm_args_t* a) {
   LayerNormJob p{};
   p.x = a->x;
@@ -100,17 +112,6 @@ LayerNormJob job_of(const gemm_layer_norm_args_t* a) {
 
 }  // namespace
 
-namespace spgemm {
-
-cudaError_t layer_norm_set_smem(size_t smem) {
-  cudaError_t e = layer_norm_set_smem_f16(smem);
-  if (e == cudaSuccess) e = layer_norm_set_smem_bf16(smem);
-  if (e == cudaSuccess) e = layer_norm_set_smem_f32(smem);
-  return e;
-}
-
-}  // namespace spgemm
-
 extern "C" {
 
 gemm_status_t gemm_layer_norm(gemm_ops_t* ops, const gemm_layer_norm_args_t* args, void* stream_handle) {
@@ -121,6 +122,8 @@ gemm_status_t gemm_layer_norm(gemm_ops_t* ops, const gemm_layer_norm_args_t* arg
   if (st != GEMM_OK || args->rows == 0) return st;
   OpsDevice guard(ops->device);
   if (guard.err != cudaSuccess) return ops_cuda_fail(guard.err, "cudaSetDevice");
+  cudaError_t e = set_up(ops);
+  if (e != cudaSuccess) return ops_cuda_fail(e, "layer norm set-up");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_handle);
   LayerNormJob p = job_of(args);
   p.bias = args->bias;
@@ -129,9 +132,9 @@ gemm_status_t gemm_layer_norm(gemm_ops_t* ops, const gemm_layer_norm_args_t* arg
   const int64_t per = args->dtype == GEMM_IN_F32 ? 4 : 8;
   const bool vec = p.cols % per == 0 && p.ldx % per == 0 && aligned16({p.x, p.out, p.weight, p.bias});
   const bool wide = args->weight_dtype == GEMM_IN_F32;
-  const cudaError_t e = args->dtype == GEMM_IN_F32   ? layer_norm_forward_f32(ops, p, vec, wide, stream)
-                        : args->dtype == GEMM_IN_F16 ? layer_norm_forward_f16(ops, p, vec, wide, stream)
-                                                     : layer_norm_forward_bf16(ops, p, vec, wide, stream);
+  e = args->dtype == GEMM_IN_F32   ? layer_norm_forward_f32(ops, p, vec, wide, stream)
+      : args->dtype == GEMM_IN_F16 ? layer_norm_forward_f16(ops, p, vec, wide, stream)
+                                   : layer_norm_forward_bf16(ops, p, vec, wide, stream);
   return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "layer norm launch");
 }
 
@@ -169,6 +172,8 @@ gemm_status_t gemm_layer_norm_backward(gemm_ops_t* ops, const gemm_layer_norm_ar
     return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "cudaMemsetAsync(weight gradients)");
   }
   if (!args->dx && !args->dweight && !args->dbias) return GEMM_OK;
+  cudaError_t e = set_up(ops);
+  if (e != cudaSuccess) return ops_cuda_fail(e, "layer norm set-up");
   LayerNormJob p = job_of(args);
   p.dy = args->dy;
   p.lddy = args->lddy;
@@ -178,9 +183,9 @@ gemm_status_t gemm_layer_norm_backward(gemm_ops_t* ops, const gemm_layer_norm_ar
   const bool vec = p.cols % per == 0 && p.ldx % per == 0 && p.lddy % per == 0 &&
                    aligned16({p.x, p.dy, p.out, p.weight});
   void *dw = args->dweight, *db = args->dbias;
-  const cudaError_t e = args->dtype == GEMM_IN_F32   ? layer_norm_backward_f32(ops, p, vec, wide, dw, db, stream)
-                        : args->dtype == GEMM_IN_F16 ? layer_norm_backward_f16(ops, p, vec, wide, dw, db, stream)
-                                                     : layer_norm_backward_bf16(ops, p, vec, wide, dw, db, stream);
+  e = args->dtype == GEMM_IN_F32   ? layer_norm_backward_f32(ops, p, vec, wide, dw, db, stream)
+      : args->dtype == GEMM_IN_F16 ? layer_norm_backward_f16(ops, p, vec, wide, dw, db, stream)
+                                   : layer_norm_backward_bf16(ops, p, vec, wide, dw, db, stream);
   return e == cudaSuccess ? GEMM_OK : ops_cuda_fail(e, "layer norm gradient launch");
 }
 

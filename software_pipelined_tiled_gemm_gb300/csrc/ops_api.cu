@@ -348,7 +348,6 @@ gemm_status_t gemm_ops_create(gemm_ops_t** out, int device) {
     if (e == cudaSuccess) e = set(ops->smem_optin);
   if (e == cudaSuccess) e = logprobs_set_smem();
   if (e == cudaSuccess) e = grouped_set_smem(ops->smem_optin);
-  if (e == cudaSuccess) e = layer_norm_set_smem(ops->smem_optin);
   if (e == cudaSuccess) e = adamw_set_smem();
   if (e == cudaSuccess) e = small_newton_init(ops);
   if (e == cudaSuccess) e = few_tokens_init(ops);

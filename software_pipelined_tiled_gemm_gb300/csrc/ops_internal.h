@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -17,7 +18,8 @@ constexpr int kSmallCluster = 8;  // CTAs of a cluster of the on-chip iteration,
 }
 
 // What persists between calls: limits of the device and its status word.  Calls
-// only read it, so that it serves any streams, captured graphs among them.
+// only read it (but for the flag), so that it serves any streams, captured graphs
+// among them.
 struct gemm_ops {
   int device = 0;
   int sm_count = 0;
@@ -30,6 +32,7 @@ struct gemm_ops {
   unsigned long long timeout_ns = 0;
   int debug_fault = 0;
   int* d_status = nullptr;       // [0] code, [1] detail
+  std::atomic<bool> layer_norm_ready{false};  // its kernels' attributes are set
 };
 
 namespace spgemm {
@@ -134,7 +137,6 @@ struct BlockScratch {
 BlockScratch take_scratch(const gemm_ops* ops, Carver& c);  // enough for any product
 
 cudaError_t logprobs_set_smem();  // logprobs.cu
-cudaError_t layer_norm_set_smem(size_t smem);  // layer_norm.cu
 cudaError_t adamw_set_smem();  // adamw.cu
 
 gemm_status_t run_block(const gemm_ops* ops, const BlockProblem& pr, BlockScratch& scratch, cudaStream_t stream);
