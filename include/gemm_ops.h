@@ -290,7 +290,7 @@ typedef struct {
   double lr;                /* used where lr_device is NULL */
   const float* lr_device;
   double beta1, beta2;      /* in [0, 1) */
-  double eps;               /* >= 0 */
+  double eps;               /* 0, or in [2^-126, 2^126] */
   const float* scale;       /* on the device; NULL: 1 */
 } gemm_adamw_args_t;
 

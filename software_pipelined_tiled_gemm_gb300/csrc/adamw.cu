@@ -154,8 +154,8 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 }
 __device__ __forceinline__ float min3(float a, float b, float c) { return fminf(fminf(a, b), c); }
 
-// 1 / x to one unit in the last place; x is 0 or normal (a sum of eps and a
-// square root of an fp32 number).
+// 1 / x to one unit in the last place; x is 0, normal or infinite (a sum of an eps
+// that is not subnormal and a square root of an fp32 number).
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -440,7 +440,10 @@ gemm_status_t check(const gemm_adamw_args_t* a) {
   if (a->bits != 32 && a->bits != 8) return ops_fail(GEMM_ERR_INVALID_ARG, "bits %d not in {8, 32}", a->bits);
   if (!(a->beta1 >= 0.0 && a->beta1 < 1.0 && a->beta2 >= 0.0 && a->beta2 < 1.0))
     return ops_fail(GEMM_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-  if (!(a->eps >= 0.0)) return ops_fail(GEMM_ERR_INVALID_ARG, "eps must be at least 0");
+  // As fp32, 0 or where the reciprocal of a sum with it is a normal number (0 / 1e-40 would be 0 times infinity).
+  const float eps = static_cast<float>(a->eps);
+  if (!(a->eps == 0.0 || (eps >= 1.1754943508222875e-38f && eps <= 8.507059173023462e+37f)))
+    return ops_fail(GEMM_ERR_INVALID_ARG, "eps must be 0 or between 2^-126 and 2^126");
   if (!a->step) return ops_fail(GEMM_ERR_INVALID_ARG, "step is NULL");
   int64_t total = 0;
   for (int64_t i = 0; i < a->count; ++i) {

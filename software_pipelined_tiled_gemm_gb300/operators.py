@@ -735,7 +735,8 @@ def adamw(params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0
     tensor.  copies: 16-bit tensors that receive the new parameters, or None
     in the place of one or of all.  scale: float32 tensor () on the GPU that
     every gradient is multiplied by (1 / loss scale, or that of a clipped
-    norm); None: 1.  Nothing may overlap what is written.
+    norm); None: 1.  eps: 0, or between 2^-126 and 2^126.  Nothing may overlap
+    what is written.
 
     In 8 bits each block of ADAMW_BLOCK elements has a scale, its largest
     magnitude over 448.  m is rounded to nearest; sqrt(v), which moves by less

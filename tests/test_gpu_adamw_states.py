@@ -133,3 +133,18 @@ def test_all_of_the_state_repeats():
         assert int(other.state.step) == 4
         for x, y in zip(a.params + a.copies + list(a.state[1:]), other.params + other.copies + list(other.state[1:])):
             assert torch.equal(x.float(), y.float())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_eps_at_the_ends_of_the_range(bits):
+    """An eps whose reciprocal fp32 does not hold is refused; the least one leaves a parameter without gradients as it was."""
+    case = Case([(300,)], bits=bits, seed=3)
+    case.state = sg.adamw_state(case.params, bits)
+    for eps in (1e-39, 1e-50, 1e38, 1e300, float("inf"), float("nan"), -1e-8):
+        with pytest.raises(sg.GemmError, match="eps"):
+            sg.adamw(case.params, case.grads, case.state, 1e-2, eps=eps)
+    assert int(case.state.step) == 0
+    before, g = case.params[0].clone(), [torch.zeros_like(case.grads[0])]
+    for eps in (2.0 ** -126, 2.0 ** 126):
+        sg.adamw(case.params, g, case.state, 1e-2, eps=eps, weight_decay=0.0)
+        assert torch.equal(case.params[0], before)
