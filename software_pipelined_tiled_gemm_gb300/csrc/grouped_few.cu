@@ -233,12 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_few_kernel(const Args a) 
 
 using Kernel = void (*)(const Args);
 
+// (Aligned weights come here with two rows a group at most: `two` is never set for them.)
 Kernel kernel_of(bool bf16, bool two, bool shifted) {
-  if (shifted)
-    return bf16 ? (two ? grouped_few_kernel<true, 2, true> : grouped_few_kernel<true, 1, true>)
-                : (two ? grouped_few_kernel<false, 2, true> : grouped_few_kernel<false, 1, true>);
-  return bf16 ? (two ? grouped_few_kernel<true, 2, false> : grouped_few_kernel<true, 1, false>)
-              : (two ? grouped_few_kernel<false, 2, false> : grouped_few_kernel<false, 1, false>);
+  if (!shifted) return bf16 ? grouped_few_kernel<true, 1, false> : grouped_few_kernel<false, 1, false>;
+  return bf16 ? (two ? grouped_few_kernel<true, 2, true> : grouped_few_kernel<true, 1, true>)
+              : (two ? grouped_few_kernel<false, 2, true> : grouped_few_kernel<false, 1, true>);
 }
 
 bool aligned_rows(const Matrix& m) { return m.cols % 8 == 0 && copyable(m); }
@@ -269,8 +268,8 @@ bool grouped_few_fits(const gemm_ops* ops, const gemm_grouped_args_t* a) {
 cudaError_t grouped_few_init(const gemm_ops* ops) {
   cudaError_t e = cudaSuccess;
   if (ops->smem_optin < 227 * 1024) return e;  // not used
-  for (int i = 0; i < 8 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(kernel_of((i & 1) != 0, (i & 2) != 0, (i & 4) != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+  for (int i = 0; i < 6 && e == cudaSuccess; ++i)
+    e = cudaFuncSetAttribute(kernel_of((i & 1) != 0, i >= 4, i >= 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(few_smem(ops)));
   return e;
 }
