@@ -186,7 +186,7 @@ gemm_status_t gemm_token_logprobs_backward(gemm_ops_t* ops, const gemm_logprobs_
 #define GEMM_WAIT_NEXT_FREE ((3 << 16) | 6)  /* the scheduler waiting for the roles to take one */
 
 typedef struct {
-  int64_t rows, groups, n, k;  /* rows >= 0, n, k >= 1, groups 1 .. GEMM_GROUPED_MAX_GROUPS */
+  int64_t rows, groups, n, k;  /* rows 0 .. 2^31 - 65536, n, k >= 1, groups 1 .. GEMM_GROUPED_MAX_GROUPS */
   gemm_dtype_t dtype;
   const int64_t* offsets;      /* groups + 1, on the device */
   const void* x;

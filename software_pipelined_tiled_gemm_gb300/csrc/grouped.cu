@@ -76,6 +76,8 @@ struct Grouped {
   PackJobs pack;
 };
 
+constexpr int64_t kMostRows = (int64_t{1} << 31) - 65536;
+
 gemm_status_t check(const gemm_grouped_args_t* a, bool backward) {
   if (!a) return ops_fail(GEMM_ERR_INVALID_ARG, "args is NULL");
   if (a->rows < 0 || a->n < 1 || a->k < 1)
@@ -84,8 +86,9 @@ gemm_status_t check(const gemm_grouped_args_t* a, bool backward) {
   if (a->groups < 1 || a->groups > GEMM_GROUPED_MAX_GROUPS)
     return ops_fail(GEMM_ERR_INVALID_ARG, "%lld groups not in 1 .. %d", (long long)a->groups,
                     GEMM_GROUPED_MAX_GROUPS);
-  if (a->rows > kOpsMaxDim || a->n > kOpsMaxDim || a->k > kOpsMaxDim)
-    return ops_fail(GEMM_ERR_INVALID_ARG, "size above 2^31-1");
+  if (a->n > kOpsMaxDim || a->k > kOpsMaxDim) return ops_fail(GEMM_ERR_INVALID_ARG, "size above 2^31-1");
+  // The kernels count rows in 32 bits, a tile's or a launch's warps beyond the last.
+  if (a->rows > kMostRows) return ops_fail(GEMM_ERR_INVALID_ARG, "more than 2^31 - 65536 rows");
   // The tiles of 32 output rows that all products could need.
   const int64_t most = std::max(ceil_div(a->n, int64_t{kGroupedLanes}), ceil_div(a->k, int64_t{kGroupedLanes}));
   if (most * (ceil_div(a->rows, int64_t{kGroupedUnit}) + a->groups) > kOpsMaxDim / 2 ||
