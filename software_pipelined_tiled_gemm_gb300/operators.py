@@ -636,6 +636,7 @@ def layer_norm_backward(dy, x, weight, kept, need=(True, True, True), out=(None,
     of the three to compute (None in the place of the others).  out: tensors
     to write them to; dx may be written over dy.
     """
+    import torch
     if not isinstance(kept, LayerNormKept):
         raise TypeError("kept must come from layer_norm(..., save=True)")
     lib = _lib()
@@ -643,10 +644,14 @@ def layer_norm_backward(dy, x, weight, kept, need=(True, True, True), out=(None,
     _on_cuda(x.device, dy, "dy")
     if dy.dtype != x.dtype or dy.shape != x.shape:
         raise ValueError("dy must have x's shape and dtype")
-    if (a.rows, a.cols, x.dtype) != kept[1:] or kept.stats.device != x.device:
-        raise ValueError("kept belongs to a forward pass of other sizes, dtype or device")
+    if (a.rows, a.cols, x.dtype) != kept[1:]:
+        raise ValueError("kept belongs to a forward pass of other sizes or dtype")
+    stats = kept.stats
+    _on_cuda(x.device, stats, "kept.stats")
+    if stats.dtype != torch.float32 or stats.shape != (3, a.rows) or not stats.is_contiguous():
+        raise ValueError("kept.stats must be contiguous float32 (3, rows)")
     a.dy, a.lddy = dy.data_ptr(), _rows(dy, a.cols, "dy")[1]
-    a.stats = kept.stats.data_ptr()
+    a.stats = stats.data_ptr()
     wdtype = x.dtype if weight is None else weight.dtype
     shapes = ((x.shape, x.dtype, "dx"), ((a.cols,), wdtype, "dweight"), ((a.cols,), wdtype, "dbias"))
     grads = [_output(o, shape, dtype, x.device, name) if want else None

@@ -36,3 +36,21 @@ def test_rows_that_32_bits_do_not_count(backward):
     for rows in ((1 << 31) - 65535, (1 << 31) - 256, (1 << 31) - 1, 1 << 31, 1 << 40):
         assert status(rows) == sg.GEMM_ERR_INVALID_ARG
         assert "rows" in sg.gemm_last_error()
+
+
+@pytest.mark.parametrize("rows,cols", [(6, 40), (200, 1531)])
+def test_kept_statistics_of_another_layout(rows, cols):
+    """The kernels read three rows of fp32; a slice of them for a part of the rows is another layout."""
+    x = torch.randn(rows, cols, device="cuda")
+    y, kept = sg.layer_norm(x, save=True)
+    half = rows // 2
+    for stats in (kept.stats[:, :half], kept.stats[:2], kept.stats.half(), kept.stats.t().contiguous(), kept.stats.view(-1),
+                  kept.stats.cpu(), None, torch.empty(3, 2 * rows, device="cuda")[:, ::2]):
+        with pytest.raises(ValueError, match="kept"):
+            sg.layer_norm_backward(y, x, None, kept._replace(stats=stats))
+    with pytest.raises(ValueError, match="kept"):
+        sg.layer_norm_backward(y[:half], x[:half], None, kept._replace(stats=kept.stats[:, :half], rows=half))
+    # A copy of the slice has the layout.
+    part = sg.LayerNormKept(kept.stats[:, :half].contiguous(), half, cols, x.dtype)
+    dx = sg.layer_norm_backward(y[:half], x[:half], None, part, need=(True, False, False))[0]
+    assert torch.equal(dx, sg.layer_norm_backward(y, x, None, kept, need=(True, False, False))[0][:half])
