@@ -177,8 +177,10 @@ gemm_status_t gemm_token_logprobs_backward(gemm_ops_t* ops, const gemm_logprobs_
  * rounded to `dtype` once.  The offsets are read on the device, so a call
  * needs no host copy of them.  They may not decrease nor leave [0, rows];
  * where they do, nothing is written to y, dx and dw and gemm_ops_check
- * reports GEMM_ERR_INVALID_ARG (GEMM_CHECK_OFFSETS).  Rows of no group are
- * not read: what they hold, NaN and infinities too, reaches no output. */
+ * reports GEMM_ERR_INVALID_ARG (GEMM_CHECK_OFFSETS).  What rows of no group
+ * hold, NaN and infinities too, reaches no output, but they may be read (with
+ * the last rows of a group, or by the copy of an operand that is not aligned):
+ * nobody else may write them during the call. */
 #define GEMM_GROUPED_MAX_GROUPS 4096
 /* Details of the status word. */
 #define GEMM_CHECK_OFFSETS ((0 << 16) | 17)  /* offsets that decrease or leave the rows */
@@ -213,8 +215,11 @@ gemm_status_t gemm_grouped_backward(gemm_ops_t* ops, const gemm_grouped_args_t* 
  * For each row x (rows x cols), in fp32:
  *   y = h weight + bias,  h = (x - mean) rstd,  rstd = 1 / sqrt(var + eps)
  * var being the mean of (x - mean)^2.  The mean is held in two floats, so that
- * a row far from zero keeps its differences.  A row that holds NaN or an
- * infinity becomes NaN. */
+ * a row far from zero keeps its differences; a constant row has a variance of
+ * 0.  Rows of finite values of any size, and variances below fp32's range with
+ * an eps of 0, have their y; rstd is kept in fp32, so the gradients of a row
+ * whose deviation is below 2^-128 with an eps of 0 are not finite.  A row that
+ * holds NaN or an infinity becomes NaN. */
 typedef struct {
   int64_t rows, cols;       /* rows >= 0, cols >= 1 */
   gemm_in_t dtype;          /* of x, y, dy and dx */
@@ -238,7 +243,8 @@ gemm_status_t gemm_layer_norm(gemm_ops_t* ops, const gemm_layer_norm_args_t* arg
 
 /* With g = dy weight and <.> the mean of a row:
  *   dx = rstd (g - <g> - h <g h>),  dweight = sum_rows dy h,  dbias = sum_rows dy
- * The sums over rows have a fixed order.  With no rows they are zero. */
+ * The sums over rows have a fixed order.  With no rows they are zero.  Where a
+ * row's sums of g or g h leave fp32's range its dx is not finite. */
 gemm_status_t gemm_layer_norm_backward_workspace(gemm_ops_t* ops, const gemm_layer_norm_args_t* args,
                                                  size_t* bytes);
 gemm_status_t gemm_layer_norm_backward(gemm_ops_t* ops, const gemm_layer_norm_args_t* args,
@@ -260,7 +266,9 @@ gemm_status_t gemm_layer_norm_backward(gemm_ops_t* ops, const gemm_layer_norm_ar
  *     format in one call, so that rounding to nearest would never let it
  *     fall: it is rounded down after adding u steps, u = (a j + b t) mod 2^32,
  *     its upper 20 bits as a fraction (element j of the buffer, a =
- *     0xC13FA9A9, b = 0x91E10DA5), which over the steps is evenly spread in
+ *     0xC13FA9A9, b = 0x91E10DA5: the additive recurrence in two dimensions of
+ *     the plastic number p, p^3 = p + 1, of which a and b are 1 / p and 1 / p^2
+ *     times 2^32, rounded down), which over the steps is evenly spread in
  *     [0, 1); r > 0 is held as 2^-9 s at least.  (A root without gradients
  *     that beta2 = 0.999 takes to 0.47 in 1500 steps is then at 0.43.)  A NaN
  *     or an infinity makes its block NaN.

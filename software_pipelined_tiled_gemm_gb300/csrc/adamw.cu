@@ -41,9 +41,10 @@ constexpr int kBlock = GEMM_ADAMW_BLOCK;
 constexpr int kEach = 8;                 // elements of a lane: 32 lanes, one block
 constexpr int kPairs = kEach / 2;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-// Blocks of a warp on their way or in work, thread blocks of an SM, and
-// blocks of a warp in a chunk at most.  Measured, in us (252 M elements with
-// 8-bit states; 106 M with 32-bit ones):
+// Blocks of a warp on their way or in work, thread blocks of an SM that the
+// registers are shared out for (of four with 32-bit states, 64 KiB of ring
+// each, three fit its shared memory), and blocks of a warp in a chunk at most.
+// Measured, in us (252 M elements with 8-bit states; 106 M with 32-bit ones):
 //   8 bits    3, 3 and 1 / 3 / 4 / 5 / 8:  816 / 612 / 605 / 704 / 697;  2, 4 and 4: 632;  4, 2 and 16: 642
 //   32 bits   2, 4 and 2: 429;  2, 3 and 2 / 3 / 4: 430 / 435 / 440;  1, 4 and 2 / 4: 437 / 450;  3, 2 and 4: 433
 constexpr int kSlots8 = 3, kOcc8 = 3, kMostEach8 = 4;
@@ -63,8 +64,8 @@ struct Entry {
   float decay;           // weight decay
 };
 
-// Tables of two sizes: a launch's arguments cost the host time (the call of 50
-// tensors takes it 4.8 us with 512 entries, 4.2 us with 128).
+// Tables of two sizes: a launch's arguments cost the host time (a call of 32 tensors
+// takes it 4.6 us, one of 33, with the larger table, 5.9).
 constexpr int kFewTensors = 32, kMostTensors = 512;
 template <int kTensors>
 struct Job {
@@ -524,8 +525,8 @@ cudaError_t run(const gemm_ops* ops, const gemm_adamw_args_t* a, int64_t first, 
   // chunk's first loads are waited for.
   uint64_t blocks = 0, chunks = 0;
   for (int64_t i = first; i < first + count; ++i) blocks += static_cast<uint64_t>(padded(a->tensors[i].numel) / kBlock);
-  const uint64_t resident = static_cast<uint64_t>(ops->sm_count) * (kBits == 8 ? kOcc8 : kOcc32);
-  job.chunk = static_cast<uint32_t>(kWarps * std::max<uint64_t>(1, std::min<uint64_t>(kBits == 8 ? kMostEach8 : kMostEach32, blocks / (kWarps * 4 * resident))));
+  const uint64_t side_by_side = static_cast<uint64_t>(ops->sm_count) * (kBits == 8 ? kOcc8 : kOcc32);
+  job.chunk = static_cast<uint32_t>(kWarps * std::max<uint64_t>(1, std::min<uint64_t>(kBits == 8 ? kMostEach8 : kMostEach32, blocks / (kWarps * 4 * side_by_side))));
   for (int64_t i = first; i < first + count; ++i) {
     const gemm_adamw_tensor_t& t = a->tensors[i];
     if (t.numel == 0) continue;

@@ -258,6 +258,10 @@ int tokens_that_fit(const gemm_ops* ops, int64_t groups, int64_t k) {
 //   16 x 2048 x 4096    1: 37, 50    2: 48, 52    4: 60, 54
 //   16 x 2047 x 4095    1: 82, 136   8: 107, 144  12: 179, 144
 //   64 x 1023 x 1021    1: 52, 72    8: 76, 80    12: 109, 80
+// That is with rows evenly spread.  The host does not know how they are: where one group has
+// all of them, each 8 (16) rows are another pass over its weights.  64 x 2048 x 4096 with 128
+// rows: 181, 170 evenly spread, 55, 21 in one group; 64 x 1023 x 1021 with 512: 70, 77 and
+// 146, 60; 1024 x 512 x 512 with 2048: 85, 99 and 471, 18.
 bool grouped_few_fits(const gemm_ops* ops, const gemm_grouped_args_t* a) {
   const Matrix w{a->w, a->groups * a->n, a->k, a->k, 0};
   const int64_t most = (aligned_rows(w) ? 2 : 8) * a->groups;

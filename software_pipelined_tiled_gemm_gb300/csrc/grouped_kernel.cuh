@@ -38,8 +38,9 @@
 //               zeros (grouped.cu): the next group's rows would be products'
 //               operands otherwise, and zero times their NaN is NaN.
 //
-// Under the power cap a busy wait costs clocks, so all of them suspend (1 % of
-// long calls back to back).
+// Under the power cap a busy wait costs clocks, so the long ones suspend: for a
+// ring slot, for a full accumulator, for room in the queue of tiles (1 % of long
+// calls back to back).
 //
 // Every sum has a fixed order, so results repeat bit for bit.
 #pragma once

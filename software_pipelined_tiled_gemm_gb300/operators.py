@@ -526,7 +526,8 @@ def grouped_matmul(x, w, offsets, out=None):
     number of rows; it is read there, so nothing synchronises.  Returns y
     (rows, n) of x's dtype (``out`` if given).
 
-    Rows before the first group and behind the last are not read; in y they
+    What rows before the first group and behind the last hold reaches no
+    output (they may be read, so nobody else may be writing them); in y they
     are zero, or, where ``out`` is given, left as they were.  Offsets that
     decrease or leave x are found on the GPU: nothing is then written to y and
     :func:`check_operators` raises.  No autograd graph, see
@@ -634,7 +635,8 @@ def layer_norm_backward(dy, x, weight, kept, need=(True, True, True), out=(None,
     dy: x's shape and dtype, contiguous or a matrix of contiguous rows.
     dweight and dbias have weight's dtype (x's without a weight).  need: which
     of the three to compute (None in the place of the others).  out: tensors
-    to write them to; dx may be written over dy.
+    to write them to; dx may be written over dy.  The sums of a row's dy weight
+    and dy weight h are fp32: where they leave its range, dx is not finite.
     """
     import torch
     if not isinstance(kept, LayerNormKept):
