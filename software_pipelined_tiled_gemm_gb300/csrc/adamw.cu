@@ -10,7 +10,8 @@
 // reduction instruction.  A thread block has a chunk of one tensor, whose
 // addresses are found once; its warps fetch their next blocks to shared memory
 // while they compute.  Tensors whose addresses allow no 16-byte vectors, and a
-// tensor's last block, are read element by element.
+// tensor's last block, are read element by element (67 M elements, bf16 gradients and
+// copies: 273 us with 32-bit states and 196 with 8-bit ones, 664 and 556 from odd addresses).
 //
 // With 8-bit states the arithmetic (some 400 instructions a lane and block,
 // a fifth of them for square roots in full precision) takes about as long as

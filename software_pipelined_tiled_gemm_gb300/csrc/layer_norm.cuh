@@ -29,13 +29,14 @@
 // thread has many columns, so that the reductions over a row (some 25
 // instructions each) cost little.
 //
-// 16384 x 4096 bf16: forward 47 us, backward 75 us (672 MB in all, 5.5 TB/s; with
-// scalars and 16 columns a thread the forward pass took 89 us).  16384 x 4097:
-// 107 and 146 us (read element by element, without copies ahead: 300 and 494 us).
-// Rows a little wider than 1024, 2048, 4096 or 8192 columns leave half of their
-// group idle (16384 x 4104: 64 and 107 us), and the masks and element stores of
-// unaligned rows are a larger part of narrow ones (262144 x 255: 179 and 259 us,
-// x 256: 86 and 157).
+// 16384 x 4096 bf16: forward 46 us, backward 76 us (672 MB in all, 5.5 TB/s; with
+// scalars and 16 columns a thread the forward pass took 89 us).  fp32: 98 and 124 us
+// (5.5 and 6.5 TB/s); 8192 x 8192 96 and 131 us, 4096 x 16384, without rows ahead, 111 and
+// 155 us.  16384 x 4097 bf16: 100 and 142 us (read element by element, without copies
+// ahead: 300 and 494 us).  Rows a little wider than 1024, 2048, 4096 or 8192 columns
+// leave half of their group idle (16384 x 4104: 66 and 110 us), and the masks and
+// element stores of unaligned rows are a larger part of narrow ones (262144 x 255: 174
+// and 258 us, x 256: 87 and 157).
 //
 // The weights' gradients: a thread sums its columns over its rows in fp32
 // registers; each block leaves one partial, and a second kernel adds those in
