@@ -161,3 +161,24 @@ def test_such_rows_between_others(cols, dt):
         assert_within(y[whole], (value, bound), "y")
         assert y[~whole].isnan().all() and not y[2::8].any() and not y[6::8].any()
         assert torch.equal(sg.layer_norm(t, out=t)[whole], y[whole])
+
+
+@pytest.mark.parametrize("cols", [5, 40, 1000, 4099, 9000, 33000])
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("eps", [1e-5, 0.0, 1e-30])
+def test_nan_and_infinities_beside_anything(cols, dt, eps):
+    """One of them makes its whole row NaN, whatever the others are: zeros, subnormal or large numbers."""
+    top = 6e4 if dt == "f16" else MOST
+    rows = [0.0, 1e-38, 1e-40, -1e-30, 1e-7, 1.0, top]
+    marks = [float("nan"), float("inf"), float("-inf")]
+    x = torch.tensor(rows, device="cuda").repeat(len(marks))[:, None].expand(-1, cols).to(DT[dt]).contiguous()
+    for i in range(len(x)):
+        x[i, (i * 7) % cols] = marks[i // len(rows)]
+    both = torch.zeros(1, cols, device="cuda", dtype=DT[dt])
+    both[0, 0], both[0, -1] = float("inf"), float("-inf")
+    x = torch.cat([x, both, torch.full_like(both, float("nan")), torch.full_like(both, float("inf"))])
+    dy = normal(len(x), cols, seed=2).to(DT[dt])
+    for place in (lambda t: t, odd):
+        y, kept = sg.layer_norm(place(x), eps=eps, save=True)
+        assert y.isnan().all()
+        assert sg.layer_norm_backward(place(dy), place(x), None, kept, need=(True, False, False))[0].isnan().all()
